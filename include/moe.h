@@ -67,7 +67,9 @@ const char* moe_last_error(void);
 /* ABI version of this library (major * 10000 + minor * 100 + patch): 1.1.0
  * adds moe_experts_forward_combine, moe_route_dispatch,
  * moe_route_sigmoid_grouped_dispatch and moe_permute_rows to 1.0.0; nothing
- * was removed or changed. */
+ * was removed or changed. The moe_mxfp4_*, moe_experts_mxfp4_*,
+ * moe_forward_mxfp4* and moe_grad_* entry points came later under the same
+ * number: a caller that has to know looks the symbols up. */
 int moe_version(void);
 
 /*
@@ -615,6 +617,190 @@ moe_status moe_experts_backward(const moe_experts* experts, const void* x_dispat
 moe_status moe_dispatch_backward(const void* dinput, moe_dtype dtype, const uint32_t* inv, int64_t T, int32_t top_k,
                                  int64_t H, void* dx, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Experts in microscaled 4-bit floating point (MXFP4, OCP Microscaling
+ * Formats v1.0: blocks of 32 E2M1 elements with one E8M0 scale). The pages
+ * have float experts only; these entry points are added beside them.
+ *
+ * Layout of an MXFP4 matrix [rows, K], K a multiple of 32:
+ *   codes    [rows, K / 2] bytes: element 2i in the low, 2i + 1 in the high
+ *            four bits of byte i; bit 3 is the sign, 0..7 stand for 0, 0.5, 1,
+ *            1.5, 2, 3, 4, 6. 16-byte aligned.
+ *   scales   [rows, moe_mxfp4_scale_pitch(K)] bytes: byte b < K / 32 of a row
+ *            is the scale 2^(byte - 127) of its elements 32b .. 32b + 31, 255
+ *            is NaN. The pitch is K / 32 rounded up to 4; the bytes past K / 32
+ *            are written as 0 and never read. 4-byte aligned.
+ * ---------------------------------------------------------------------- */
+
+/* 4 * ceil(K / 128), or 0 where K is not a positive multiple of 32. */
+int64_t moe_mxfp4_scale_pitch(int64_t K);
+
+/*
+ * moe_mxfp4_quantize - float rows to MXFP4, optionally straight into
+ * dispatched order.
+ *
+ *   x         device, [rows, K] in `dtype`, 16-byte aligned.
+ *   K         a multiple of 32, 32 .. 262144.
+ *   inv       NULL: row r is written to row r (top_k must be 1). Else device,
+ *             [rows * top_k] uint32, moe_dispatch's slot -> row map: row t is
+ *             written to the rows inv[t * top_k + j], j < top_k, and codes and
+ *             scales hold rows * top_k rows. An entry >= rows * top_k is
+ *             skipped; rows that no entry names are left as they were.
+ *   codes, scales   device, out (layout above).
+ *
+ * For a block with a = max |x_i|: byte = clamp(floor(log2 a) - 2 + 127, 0,
+ * 254) (0 where a = 0); each element is x_i / 2^(byte - 127) rounded to the
+ * nearest E2M1 value, ties to the even mantissa, saturated to 6. A block that
+ * holds a NaN or an infinity gets byte 255 and zero codes.
+ * Errors: MOE_ERR_DTYPE, MOE_ERR_SHAPE, MOE_ERR_TOP_K, MOE_ERR_NULL,
+ * MOE_ERR_ALIGNMENT.
+ */
+moe_status moe_mxfp4_quantize(const void* x, moe_dtype dtype, int64_t rows, int64_t K, const uint32_t* inv,
+                              int32_t top_k, void* codes, void* scales, void* stream);
+
+/*
+ * moe_mxfp4_dequantize - the values an MXFP4 matrix stands for, [rows, K] in
+ * `dtype` (16-byte aligned), rounded to nearest even (exact in F32 but for
+ * scales above 2^125, whose largest elements overflow to infinity).
+ */
+moe_status moe_mxfp4_dequantize(const void* codes, const void* scales, int64_t rows, int64_t K, void* out,
+                                moe_dtype dtype, void* stream);
+
+/* Opaque handle of MXFP4 expert weights. */
+typedef struct moe_experts_mxfp4 moe_experts_mxfp4;
+
+/*
+ * moe_experts_mxfp4_create - validate and wrap bias-free SwiGLU expert
+ * weights in MXFP4: gate and up [E, I, H], down [E, H, I] (as E * I, or E * H
+ * rows of the layout above).
+ *
+ *   E, H, I       1 <= E <= 1024; H and I multiples of 32, 32 .. 262144.
+ *   storage       device, moe_experts_mxfp4_storage_size(E, H, I) bytes,
+ *                 256-byte aligned: the weights' scales in the tensor cores'
+ *                 order, written by kernels enqueued on `stream`; uses of the
+ *                 handle on other streams have to be ordered after them.
+ *   out           receives the handle.
+ *
+ * The handle keeps the code pointers and `storage` (the caller keeps them
+ * alive and unchanged); the scale arrays are not used after the stream has
+ * passed the call. It is read-only and may be shared between streams; free it
+ * with moe_experts_mxfp4_destroy. Device is the current device at creation.
+ */
+size_t moe_experts_mxfp4_storage_size(int64_t E, int64_t H, int64_t I);
+moe_status moe_experts_mxfp4_create(const void* gate_codes, const void* gate_scales, const void* up_codes,
+                                    const void* up_scales, const void* down_codes, const void* down_scales, int64_t E,
+                                    int64_t H, int64_t I, void* storage, size_t storage_bytes, void* stream,
+                                    moe_experts_mxfp4** out);
+void moe_experts_mxfp4_destroy(moe_experts_mxfp4* experts);
+
+/*
+ * moe_experts_mxfp4_gate_up - h = SiLU(W_gate[e] x) * (W_up[e] x) on
+ * dispatched MXFP4 rows, FP32 accumulation.
+ *
+ *   x_codes, x_scales   device, MXFP4 [rows, H] (moe_mxfp4_quantize with inv).
+ *   offsets       device, [E + 1] uint32 (from moe_dispatch); offsets[E] must
+ *                 equal rows.
+ *   h             device, [rows, I] out in `dtype`, or NULL.
+ *   h_codes, h_scales   device, MXFP4 [rows, I] out, or both NULL: h rounded
+ *                 to `dtype` and then quantised, the same bytes as
+ *                 moe_mxfp4_quantize gives on h. At least one of the two
+ *                 outputs is needed.
+ *   dtype         MOE_F32, MOE_F16 or MOE_BF16.
+ *
+ * No workspace. Rows past offsets[E] are not written. A row with a NaN block
+ * gives NaN outputs for its token only.
+ */
+moe_status moe_experts_mxfp4_gate_up(const moe_experts_mxfp4* experts, const void* x_codes, const void* x_scales,
+                                     const uint32_t* offsets, int64_t rows, moe_dtype dtype, void* h, void* h_codes,
+                                     void* h_scales, void* stream);
+
+/* moe_experts_mxfp4_down - y = W_down[e] h on MXFP4 [rows, I] -> [rows, H] in
+ * `dtype`, FP32 accumulation. Arguments as moe_experts_mxfp4_gate_up. */
+moe_status moe_experts_mxfp4_down(const moe_experts_mxfp4* experts, const void* h_codes, const void* h_scales,
+                                  const uint32_t* offsets, int64_t rows, moe_dtype dtype, void* y, void* stream);
+
+/*
+ * moe_experts_mxfp4_forward_dispatched - both stages: h goes from gate/up to
+ * down as MXFP4 (rounded to `dtype` before). The same bits as
+ * moe_experts_mxfp4_gate_up with h_codes followed by moe_experts_mxfp4_down.
+ *   workspace     device, moe_experts_mxfp4_forward_dispatched_workspace_size
+ *                 bytes (h as MXFP4), 256-byte aligned.
+ */
+size_t moe_experts_mxfp4_forward_dispatched_workspace_size(const moe_experts_mxfp4* experts, int64_t rows);
+moe_status moe_experts_mxfp4_forward_dispatched(const moe_experts_mxfp4* experts, const void* x_codes,
+                                                const void* x_scales, const uint32_t* offsets, int64_t rows,
+                                                moe_dtype dtype, void* y, void* workspace, size_t workspace_bytes,
+                                                void* stream);
+
+/*
+ * moe_forward_mxfp4 - the whole local chain on MXFP4 experts: route +
+ * dispatch (one launch, as moe_forward), x quantised into dispatched order,
+ * the two expert products, combine. The same bits as moe_route_dispatch,
+ * moe_mxfp4_quantize (with inv), moe_experts_mxfp4_forward_dispatched and
+ * moe_combine in turn.
+ *
+ *   x, out        device, [T, H] in `dtype` (MOE_F32, MOE_F16, MOE_BF16),
+ *                 16-byte aligned; h is rounded to `dtype` before it is
+ *                 quantised.
+ *   logits, logits_dtype, T, top_k, renormalize, indices_opt, weights_opt
+ *                 as in moe_forward.
+ *   workspace     device, moe_forward_mxfp4_workspace_size(experts, T, top_k,
+ *                 dtype) bytes, 256-byte aligned.
+ */
+size_t moe_forward_mxfp4_workspace_size(const moe_experts_mxfp4* experts, int64_t T, int32_t top_k, moe_dtype dtype);
+moe_status moe_forward_mxfp4(const moe_experts_mxfp4* experts, const void* x, moe_dtype dtype, const void* logits,
+                             moe_dtype logits_dtype, int64_t T, int32_t top_k, int32_t renormalize, void* out,
+                             uint32_t* indices_opt, void* weights_opt, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* ------------------------------------------------------------------------
+ * Gradient norm and clipping over many tensors: what a training step runs
+ * between the backward (moe_experts_backward's dgate, dup, ddown and the
+ * caller's other gradients) and the optimizer. Added beside the pages'
+ * training calls.
+ * ---------------------------------------------------------------------- */
+
+/* One dense gradient of `numel` elements (0 is allowed), aligned to its
+ * element size. `dst` is used by moe_grad_clip only: where the clipped
+ * gradient goes, src itself to clip in place. */
+typedef struct {
+  const void* src;
+  void* dst;
+  int64_t numel;
+  int32_t dtype;  /* moe_dtype of src and dst */
+} moe_grad_tensor;
+
+/*
+ * moe_grad_norm - the L2 norm over all elements of n tensors.
+ *
+ *   tensors    host, n entries, read during the call only (n >= 0).
+ *   norm       device, one float out: sqrt of the sum of squares (FP64 sums;
+ *              the same bits on every run). 0 without elements; NaN or
+ *              infinity where the gradients hold one.
+ *   workspace  device, moe_grad_norm_workspace_size(n) bytes, 256-byte
+ *              aligned; contents need not be initialised. Calls that may
+ *              overlap need separate workspaces.
+ */
+size_t moe_grad_norm_workspace_size(int64_t n);
+moe_status moe_grad_norm(const moe_grad_tensor* tensors, int64_t n, float* norm, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * moe_grad_clip - dst = src * max_norm / norm for every tensor if norm is
+ * finite and larger than max_norm; otherwise dst = src (in place: nothing is
+ * written). FP32 arithmetic, rounded to the tensor's dtype.
+ *
+ *   norm       device, one float: moe_grad_norm's result, or that of a larger
+ *              set of gradients (for sharded experts, the root of the ranks'
+ *              summed squares). A NaN or infinite norm leaves the gradients as
+ *              they are: the caller sees it in *norm and skips the step.
+ *   max_norm   finite and >= 0.
+ *
+ * dst ranges must not overlap one another or another entry's src, and a dst
+ * that is not its own src must not overlap it (MOE_ERR_SHAPE).
+ */
+moe_status moe_grad_clip(const moe_grad_tensor* tensors, int64_t n, const float* norm, float max_norm, void* stream);
+
 /*
  * moe_device_status - read (and clear, if `clear` is nonzero) the device
  * status word. The expert GEMM kernels bound every pipeline wait (about one
@@ -629,7 +815,10 @@ moe_status moe_dispatch_backward(const void* dinput, moe_dtype dtype, const uint
  * down launch waiting for its expert's h rows, 0x1A the combine of
  * moe_experts_forward_combine waiting for the last down tile, 0x1B the grid
  * barrier of moe_route_dispatch and moe_route_sigmoid_grouped_dispatch (and
- * of the forward calls' routing), 0x100
+ * of the forward calls' routing), 0x21 - 0x28 the waits of the MXFP4 expert
+ * products (0x21 producer, 0x22 MMA for a loaded stage, 0x23 MMA for a drained
+ * accumulator, 0x24 epilogue, 0x25 / 0x26 teardown drains, 0x27 scale loader,
+ * 0x28 MMA for a free scale buffer), 0x100
  * moe_selftest_bounded_wait. Synchronises the current device; *code = 0 when
  * no wait has timed out.
  */

@@ -48,6 +48,12 @@ class RouterWeightOptions(ctypes.Structure):
         super().__init__(code, int(bool(renormalize)), float(scale))
 
 
+class GradTensor(ctypes.Structure):
+    """moe_grad_tensor: one dense gradient (src, dst, numel, dtype code)."""
+    _fields_ = [("src", ctypes.c_void_p), ("dst", ctypes.c_void_p), ("numel", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
+
+
 _INDEX = {torch.int32: 1, torch.int64: 2}
 if hasattr(torch, "uint32"):
     _INDEX[torch.uint32] = 0
@@ -58,6 +64,7 @@ _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_
 _OPT = ctypes.POINTER(GroupRoutingOptions)
 _ROPT = ctypes.POINTER(RouterWeightOptions)
 _FP = ctypes.c_void_p
+_GT = ctypes.POINTER(GradTensor)
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_last_error": (ctypes.c_char_p, []),
@@ -103,6 +110,23 @@ SIGNATURES = {
     "moe_experts_backward_workspace_size": (_SZ, [_P, _I64]),
     "moe_experts_backward": (ctypes.c_int, [_P, _P, _P, _I64, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "moe_dispatch_backward": (ctypes.c_int, [_P, ctypes.c_int, _P, _I64, _I32, _I64, _P, _P]),
+    "moe_mxfp4_scale_pitch": (_I64, [_I64]),
+    "moe_mxfp4_quantize": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _P, _I32, _P, _P, _P]),
+    "moe_mxfp4_dequantize": (ctypes.c_int, [_P, _P, _I64, _I64, _P, ctypes.c_int, _P]),
+    "moe_experts_mxfp4_storage_size": (_SZ, [_I64, _I64, _I64]),
+    "moe_experts_mxfp4_create": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P,
+                                                ctypes.POINTER(ctypes.c_void_p)]),
+    "moe_experts_mxfp4_destroy": (None, [_P]),
+    "moe_experts_mxfp4_gate_up": (ctypes.c_int, [_P, _P, _P, _P, _I64, ctypes.c_int, _P, _P, _P, _P]),
+    "moe_experts_mxfp4_down": (ctypes.c_int, [_P, _P, _P, _P, _I64, ctypes.c_int, _P, _P]),
+    "moe_experts_mxfp4_forward_dispatched_workspace_size": (_SZ, [_P, _I64]),
+    "moe_experts_mxfp4_forward_dispatched": (ctypes.c_int, [_P, _P, _P, _P, _I64, ctypes.c_int, _P, _P, _SZ, _P]),
+    "moe_forward_mxfp4_workspace_size": (_SZ, [_P, _I64, _I32, ctypes.c_int]),
+    "moe_forward_mxfp4": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, ctypes.c_int, _I64, _I32, _I32, _P, _P, _P, _P,
+                                         _SZ, _P]),
+    "moe_grad_norm_workspace_size": (_SZ, [_I64]),
+    "moe_grad_norm": (ctypes.c_int, [_GT, _I64, _P, _P, _SZ, _P]),
+    "moe_grad_clip": (ctypes.c_int, [_GT, _I64, _P, ctypes.c_float, _P]),
     "moe_device_status": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _I32]),
     "moe_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_uint32, _P]),
 }
@@ -660,6 +684,312 @@ def moe_dispatch_backward(dinput: torch.Tensor, inv: torch.Tensor, T: int, top_k
     dx = torch.empty(T, H, dtype=dinput.dtype, device=dinput.device)
     _check(lib.moe_dispatch_backward(_ptr(dinput), _dt(dinput), _ptr(inv), T, top_k, H, _ptr(dx), _stream(stream)))
     return dx
+
+
+# ---- experts in microscaled 4-bit floating point (MXFP4)
+
+Mxfp4 = namedtuple("Mxfp4", "codes scales")
+Mxfp4.__doc__ = """An MXFP4 matrix [.., K]: codes uint8 [.., K/2] (element 2i in the low half of byte i) and
+scales uint8 [.., moe_mxfp4_scale_pitch(K)] (E8M0, one per 32 elements)."""
+
+
+def _on_current_device(*tensors):
+    """The library launches on the current device: tensors of another one are refused."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != cur:
+            raise MoeError(7, f"a tensor is on {t.device}, the current device is cuda:{cur}")
+
+
+def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    """torch.empty on the stream the call runs on: memory that an earlier use on another stream may still touch is
+    not handed out, and scratch that the call drops is reused in that stream's order only."""
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _scratch(nbytes: int, device, workspace, stream) -> torch.Tensor:
+    if workspace is not None:
+        return workspace
+    return _empty((max(int(nbytes), 1),), torch.uint8, device, stream)
+
+
+def _mx(q, name: str) -> tuple[torch.Tensor, torch.Tensor, int]:
+    """(codes, scales, K) of an Mxfp4, checked: contiguous uint8 on the device, shapes that belong together."""
+    codes, scales = _dev_tensor(q.codes, f"{name}.codes"), _dev_tensor(q.scales, f"{name}.scales")
+    if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
+        raise MoeError(3, f"{name}: codes and scales must be uint8")
+    if codes.dim() < 1 or scales.dim() < 1:
+        raise MoeError(2, f"{name}: codes and scales need at least one dimension")
+    K = codes.shape[-1] * 2
+    if tuple(scales.shape) != tuple(codes.shape[:-1]) + (moe_mxfp4_scale_pitch(K),):
+        raise MoeError(2, f"{name}: scales {tuple(scales.shape)} do not belong to codes {tuple(codes.shape)}")
+    return codes, scales, K
+
+
+def moe_mxfp4_scale_pitch(K: int) -> int:
+    """Bytes of one row of scales: K / 32 rounded up to 4."""
+    pitch = int(load_library().moe_mxfp4_scale_pitch(K))
+    if pitch == 0:
+        raise MoeError(2, "K must be a positive multiple of 32")
+    return pitch
+
+
+def moe_mxfp4_quantize(x: torch.Tensor, *, inv: torch.Tensor | None = None, top_k: int = 1, out: Mxfp4 | None = None,
+                       stream=None) -> Mxfp4:
+    """x [.., K] in float32, float16 or bfloat16 as MXFP4 (K a multiple of 32).
+    With inv (moe_dispatch's, [T * top_k]) x is [T, K] and row t goes to the
+    rows inv[t * top_k + j] of the [T * top_k, K] result: quantised and
+    dispatched at once. Rows that no entry of inv names are left as they were
+    (not set, without `out`)."""
+    lib = load_library()
+    _dev_tensor(x, "x")
+    if x.dim() < 1:
+        raise MoeError(2, "x needs at least one dimension")
+    K = x.shape[-1]
+    lead = tuple(x.shape[:-1])
+    pitch = moe_mxfp4_scale_pitch(K)
+    rows = x.numel() // K
+    if inv is not None:
+        _dev_tensor(inv, "inv")
+        if x.dim() != 2 or inv.numel() != rows * top_k:
+            raise MoeError(2, "inv must hold one entry per slot of x [T, K]")
+        if inv.element_size() != 4:
+            raise MoeError(3, "inv must be uint32 (or its int32 view)")
+        lead = (rows * top_k,)
+    if out is None:
+        out = Mxfp4(_empty(lead + (K // 2,), torch.uint8, x.device, stream),
+                    _empty(lead + (pitch,), torch.uint8, x.device, stream))
+    codes, scales, k_out = _mx(out, "out")
+    if k_out != K or codes.numel() * 2 != (rows * top_k if inv is not None else rows) * K:
+        raise MoeError(2, "out does not have the result's shape")
+    _on_current_device(x, inv, codes, scales)
+    _check(lib.moe_mxfp4_quantize(_ptr(x), _dt(x), rows, K, _ptr(inv), top_k, _ptr(codes), _ptr(scales),
+                                  _stream(stream)))
+    return out
+
+
+def moe_mxfp4_dequantize(q: Mxfp4, dtype: torch.dtype = torch.bfloat16, *, out=None, stream=None) -> torch.Tensor:
+    """The values an MXFP4 matrix stands for, [.., K] in `dtype`."""
+    lib = load_library()
+    codes, scales, K = _mx(q, "q")
+    if out is None:
+        out = _empty(tuple(codes.shape[:-1]) + (K,), dtype, codes.device, stream)
+    _dev_tensor(out, "out")
+    if out.dtype != dtype or out.numel() != codes.numel() * 2:
+        raise MoeError(2, "out does not have the result's shape and dtype")
+    _on_current_device(codes, scales, out)
+    _check(lib.moe_mxfp4_dequantize(_ptr(codes), _ptr(scales), codes.numel() * 2 // K, K, _ptr(out), _dt(out),
+                                    _stream(stream)))
+    return out
+
+
+class ExpertsMxfp4:
+    """SwiGLU experts in MXFP4: a handle over gate/up [E, I, H] and down
+    [E, H, I] (Mxfp4 tensors; the codes are kept alive here, the scales are
+    laid out once for the tensor cores). Waits for its set-up, so that the
+    handle can be used on any stream; not to be made during a graph capture."""
+
+    def __init__(self, gate: Mxfp4, up: Mxfp4, down: Mxfp4):
+        lib = load_library()
+        (gc, gs, H), (uc, us, Hu), (dc, ds, I) = _mx(gate, "gate"), _mx(up, "up"), _mx(down, "down")
+        if gc.dim() != 3:
+            raise MoeError(2, "gate must be [E, I, H]")
+        E = gc.shape[0]
+        if (tuple(gc.shape) != (E, I, H // 2) or tuple(uc.shape) != tuple(gc.shape) or Hu != H or
+                tuple(dc.shape) != (E, H, I // 2)):
+            raise MoeError(2, "gate and up must be [E, I, H] and down [E, H, I]")
+        _on_current_device(gc, gs, uc, us, dc, ds)
+        self.E, self.H, self.I = E, H, I
+        self.device = gc.device
+        self._codes = (gc, uc, dc)
+        self._storage = torch.empty(max(1, lib.moe_experts_mxfp4_storage_size(E, H, I)), dtype=torch.uint8,
+                                    device=gc.device)
+        handle = ctypes.c_void_p()
+        _check(lib.moe_experts_mxfp4_create(_ptr(gc), _ptr(gs), _ptr(uc), _ptr(us), _ptr(dc), _ptr(ds), E, H, I,
+                                            _ptr(self._storage), self._storage.numel(), _stream(),
+                                            ctypes.byref(handle)))
+        self.handle = handle
+        torch.cuda.current_stream().synchronize()
+
+    @classmethod
+    def from_float(cls, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor) -> "ExpertsMxfp4":
+        """Quantise float gate/up [E, I, H] and down [E, H, I]."""
+        return cls(*(moe_mxfp4_quantize(t) for t in (gate, up, down)))
+
+    def __del__(self):
+        if getattr(self, "handle", None) and _lib is not None:
+            _lib.moe_experts_mxfp4_destroy(self.handle)
+            self.handle = None
+
+
+def _mx_rows(experts: ExpertsMxfp4, q: Mxfp4, name: str, K: int, offsets: torch.Tensor):
+    """(codes, scales, rows) of dispatched MXFP4 rows, with the experts' offsets checked."""
+    codes, scales, k = _mx(q, name)
+    if codes.dim() != 2 or k != K:
+        raise MoeError(2, f"{name} must be [rows, {K}]")
+    _dev_tensor(offsets, "offsets")
+    if offsets.element_size() != 4:
+        raise MoeError(3, "offsets must be uint32 (or its int32 view)")
+    if offsets.numel() != experts.E + 1:
+        raise MoeError(2, "offsets must hold E + 1 entries")
+    _on_current_device(codes, scales, offsets)
+    return codes, scales, codes.shape[0]
+
+
+def _mx_out(out, rows: int, cols: int, dtype: torch.dtype, device, stream) -> torch.Tensor:
+    if out is None:
+        return _empty((rows, cols), dtype, device, stream)
+    _dev_tensor(out, "out")
+    if out.dtype != dtype or tuple(out.shape) != (rows, cols):
+        raise MoeError(2, f"out must be [{rows}, {cols}] in {dtype}")
+    _on_current_device(out)
+    return out
+
+
+def moe_experts_mxfp4_gate_up(experts: ExpertsMxfp4, x: Mxfp4, offsets: torch.Tensor, *,
+                              dtype: torch.dtype = torch.bfloat16, quantized: bool = False, out=None, stream=None):
+    """First stage on dispatched MXFP4 rows: h [rows, I] = SiLU(x W_gate^T) *
+    (x W_up^T) per expert in `dtype`, or with quantized=True h rounded to
+    `dtype` and quantised, an Mxfp4 (what moe_mxfp4_quantize gives on h)."""
+    lib = load_library()
+    codes, scales, rows = _mx_rows(experts, x, "x", experts.H, offsets)
+    h, hc, hs = None, None, None
+    if quantized:
+        if out is None:
+            out = Mxfp4(_empty((rows, experts.I // 2), torch.uint8, codes.device, stream),
+                        _empty((rows, moe_mxfp4_scale_pitch(experts.I)), torch.uint8, codes.device, stream))
+        hc, hs, k = _mx(out, "out")
+        if k != experts.I or hc.dim() != 2 or hc.shape[0] != rows:
+            raise MoeError(2, f"out must be [{rows}, {experts.I}]")
+        _on_current_device(hc, hs)
+    else:
+        out = h = _mx_out(out, rows, experts.I, dtype, codes.device, stream)
+    if dtype not in _DTYPE:
+        raise MoeError(3, f"unsupported dtype {dtype}")
+    _check(lib.moe_experts_mxfp4_gate_up(experts.handle, _ptr(codes), _ptr(scales), _ptr(offsets), rows,
+                                         _DTYPE[dtype], _ptr(h), _ptr(hc), _ptr(hs), _stream(stream)))
+    return out
+
+
+def moe_experts_mxfp4_down(experts: ExpertsMxfp4, h: Mxfp4, offsets: torch.Tensor, *,
+                           dtype: torch.dtype = torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+    """Second stage: y [rows, H] = h W_down^T per expert, from MXFP4 h."""
+    lib = load_library()
+    codes, scales, rows = _mx_rows(experts, h, "h", experts.I, offsets)
+    y = _mx_out(out, rows, experts.H, dtype, codes.device, stream)
+    _check(lib.moe_experts_mxfp4_down(experts.handle, _ptr(codes), _ptr(scales), _ptr(offsets), rows, _dt(y), _ptr(y),
+                                      _stream(stream)))
+    return y
+
+
+def moe_experts_mxfp4_forward_dispatched(experts: ExpertsMxfp4, x: Mxfp4, offsets: torch.Tensor, *,
+                                         dtype: torch.dtype = torch.bfloat16, out=None, workspace=None,
+                                         stream=None) -> torch.Tensor:
+    """Both stages on dispatched MXFP4 rows: y [rows, H] in `dtype`; h passes
+    between them as MXFP4 (rounded to `dtype` first)."""
+    lib = load_library()
+    codes, scales, rows = _mx_rows(experts, x, "x", experts.H, offsets)
+    y = _mx_out(out, rows, experts.H, dtype, codes.device, stream)
+    need = lib.moe_experts_mxfp4_forward_dispatched_workspace_size(experts.handle, rows)
+    ws = _scratch(need, codes.device, workspace, stream)
+    _check(lib.moe_experts_mxfp4_forward_dispatched(experts.handle, _ptr(codes), _ptr(scales), _ptr(offsets), rows,
+                                                    _dt(y), _ptr(y), _ptr(ws), ws.numel(), _stream(stream)))
+    return y
+
+
+def moe_forward_mxfp4(experts: ExpertsMxfp4, x: torch.Tensor, logits: torch.Tensor, top_k: int, renormalize: bool, *,
+                      out=None, indices=None, weights=None, workspace=None, stream=None) -> torch.Tensor:
+    """The whole local chain on MXFP4 experts: x [T, H] (float32, float16 or
+    bfloat16) is routed, quantised into dispatched order, run through the
+    experts' 4-bit products and combined to out [T, H] in x's dtype."""
+    lib = load_library()
+    _dev_tensor(x, "x")
+    _dev_tensor(logits, "logits")
+    if x.dim() != 2 or x.shape[1] != experts.H:
+        raise MoeError(2, f"x must be [T, {experts.H}]")
+    T = x.shape[0]
+    if tuple(logits.shape) != (T, experts.E):
+        raise MoeError(2, f"logits must be [{T}, {experts.E}]")
+    for t, name, es in ((indices, "indices", 4), (weights, "weights", logits.element_size())):
+        if t is not None and (_dev_tensor(t, name).numel() != T * top_k or t.element_size() != es):
+            raise MoeError(2, f"{name} must hold T * top_k entries")
+    o = _mx_out(out, T, experts.H, x.dtype, x.device, stream)
+    _on_current_device(x, logits, indices, weights)
+    ws = _scratch(lib.moe_forward_mxfp4_workspace_size(experts.handle, T, top_k, _dt(x)), x.device, workspace, stream)
+    _check(lib.moe_forward_mxfp4(experts.handle, _ptr(x), _dt(x), _ptr(logits), _dt(logits), T, top_k,
+                                 int(bool(renormalize)), _ptr(o), _ptr(indices), _ptr(weights), _ptr(ws), ws.numel(),
+                                 _stream(stream)))
+    return o
+
+
+# ---- gradient norm and clipping
+
+def _grad_table(tensors, out=None):
+    """The moe_grad_tensor array of a list of gradients (and of their destinations)."""
+    dst = tensors if out is None else out
+    if len(dst) != len(tensors):
+        raise MoeError(2, "out must hold one tensor per gradient")
+    table = (GradTensor * max(1, len(tensors)))()
+    cur = torch.cuda.current_device() if tensors and tensors[0].is_cuda else 0
+    for entry, s, d in zip(table, tensors, dst):
+        for t in (s,) if d is s else (s, d):
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError("gradients must be contiguous CUDA tensors")
+            if t.device.index != cur:
+                raise MoeError(7, f"a tensor is on {t.device}, the current device is cuda:{cur}")
+        if d.dtype != s.dtype or d.numel() != s.numel():
+            raise MoeError(2, "out must have the gradients' sizes and dtypes")
+        entry.src, entry.dst, entry.numel, entry.dtype = s.data_ptr(), d.data_ptr(), s.numel(), _dt(s)
+    return table
+
+
+def _grad_norm(lib, table, n: int, device, out, workspace, stream) -> torch.Tensor:
+    norm = out if out is not None else _empty((), torch.float32, device, stream)
+    if norm.dtype != torch.float32 or norm.numel() != 1:
+        raise MoeError(3, "the norm must be one float32")
+    _on_current_device(_dev_tensor(norm, "norm"))
+    ws = _scratch(lib.moe_grad_norm_workspace_size(n), norm.device, workspace, stream)
+    _check(lib.moe_grad_norm(table, n, _ptr(norm), _ptr(ws), ws.numel(), _stream(stream)))
+    return norm
+
+
+def _grad_device(tensors):
+    return tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
+
+
+def moe_grad_norm(tensors, *, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """The L2 norm over all elements of a list of float32, float16 or bfloat16
+    gradients, one float32 on the device (nothing waits for it)."""
+    lib = load_library()
+    tensors = list(tensors)
+    return _grad_norm(lib, _grad_table(tensors), len(tensors), _grad_device(tensors), out, workspace, stream)
+
+
+def moe_grad_clip(tensors, norm: torch.Tensor, max_norm: float, *, out=None, stream=None):
+    """Every gradient times max_norm / norm where norm (one float32 on the
+    device, as moe_grad_norm gives it) is finite and larger than max_norm; in
+    place, or into the list `out`. Returns the clipped list."""
+    lib = load_library()
+    tensors = list(tensors)
+    out = tensors if out is None else list(out)
+    _dev_tensor(norm, "norm")
+    if norm.dtype != torch.float32 or norm.numel() != 1:
+        raise MoeError(3, "the norm must be one float32")
+    _on_current_device(norm)
+    _check(lib.moe_grad_clip(_grad_table(tensors, out), len(tensors), _ptr(norm), float(max_norm), _stream(stream)))
+    return out
+
+
+def moe_clip_grad_norm(tensors, max_norm: float, *, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """moe_grad_norm and moe_grad_clip in turn: returns the norm before the clip."""
+    lib = load_library()
+    tensors = list(tensors)
+    out = tensors if out is None else list(out)
+    table = _grad_table(tensors, out)
+    norm = _grad_norm(lib, table, len(tensors), _grad_device(tensors), None, workspace, stream)
+    _check(lib.moe_grad_clip(table, len(tensors), _ptr(norm), float(max_norm), _stream(stream)))
+    return norm
 
 
 def moe_device_status(clear: bool = True) -> int:

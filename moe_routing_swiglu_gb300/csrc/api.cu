@@ -304,6 +304,28 @@ size_t backward_dh_bytes(const moe_experts* ex, size_t n) {
 
 }  // namespace
 
+namespace moe {
+
+moe_status api_fail(moe_status st, const char* why) noexcept {
+  try {
+    return fail(st, why);
+  } catch (...) {  // no memory for the message: the status still tells
+    return st;
+  }
+}
+
+moe_status api_cuda_fail(cudaError_t err, const char* where, const char* why) noexcept {
+  try {
+    return cuda_fail(err, where, why);
+  } catch (...) {
+    return MOE_ERR_CUDA;
+  }
+}
+
+moe_status api_ok() noexcept { return ok(); }
+
+}  // namespace moe
+
 extern "C" {
 
 const char* moe_status_string(int status) {

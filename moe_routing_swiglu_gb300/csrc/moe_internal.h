@@ -14,6 +14,12 @@
 
 namespace moe {
 
+// The C ABI's error state (api.cu), shared by the files that define entry
+// points: record the message for moe_last_error and return the status.
+moe_status api_fail(moe_status st, const char* why) noexcept;
+moe_status api_cuda_fail(cudaError_t err, const char* where, const char* why = nullptr) noexcept;
+moe_status api_ok() noexcept;
+
 // Launch `kernel` with programmatic stream serialization: its blocks may be
 // scheduled (and run their prologue) while the previous kernel in the stream
 // finishes; the kernel calls grid_dependency_wait() before touching that
@@ -168,6 +174,33 @@ cudaError_t launch_experts_tc_chain(const TcWeights& w, moe_dtype dtype, const v
                                     const TcCache* cache, const uint32_t* offsets, int E, int64_t rows, int64_t H,
                                     int64_t I, void* h, void* y, uint32_t* sched, uint32_t* ready, int num_sms,
                                     cudaStream_t stream, const char** why, const TcCombine* comb = nullptr);
+// ---- MXFP4 (mxfp4.cu, experts_mx.cu)
+// Quantise rows of K elements (K a multiple of 32); inv (optional,
+// [rows * top_k]): row r is written to output rows inv[r * top_k + j].
+cudaError_t launch_mx_quantize(const void* x, moe_dtype dtype, int64_t rows, int64_t K, const uint32_t* inv, int top_k,
+                               void* codes, void* scales, int num_sms, cudaStream_t stream);
+cudaError_t launch_mx_dequantize(const void* codes, const void* scales, int64_t rows, int64_t K, void* out,
+                                 moe_dtype dtype, int num_sms, cudaStream_t stream);
+// Row-major weight scales [E, R, pitch] -> the tensor cores' atoms.
+cudaError_t launch_mx_layout_scales(const void* scales, void* dst, int64_t E, int64_t R, int64_t row_blocks, int64_t K,
+                                    cudaStream_t stream);
+struct MxWeights {
+  CUtensorMap gate, up, down;  // 3-D maps over the codes [E, rows, K / 2], 128 B x 128 x 1 boxes
+  const void* gate_sf;         // scales in atoms
+  const void* up_sf;
+  const void* down_sf;
+};
+int64_t mx_weight_row_blocks(bool gate_up, int64_t R);
+size_t mx_weight_scale_bytes(bool gate_up, int64_t E, int64_t R, int64_t K);
+bool mx_encode_weights(const void* gate, const void* up, const void* down, int64_t E, int64_t H, int64_t I,
+                       MxWeights* out, const char** why);
+// gate_up: codes/scales = x rows (K = H) -> h [rows, I] in out_dtype (out)
+// and / or as MXFP4 (q_codes, q_scales); else h rows (K = I) -> y [rows, H].
+cudaError_t launch_experts_mx(const MxWeights& w, bool gate_up, const void* codes, const void* scales,
+                              const uint32_t* offsets, int E, int64_t rows, int64_t H, int64_t I, moe_dtype out_dtype,
+                              void* out, void* q_codes, void* q_scales, int num_sms, cudaStream_t stream,
+                              const char** why);
+
 cudaError_t read_device_status(uint32_t* code, bool clear);
 // Device address of the status word the bounded waits report into.
 cudaError_t device_status_ptr(uint32_t** p);
@@ -216,6 +249,12 @@ cudaError_t launch_experts_backward(moe_dtype dtype, const TrainBuffers& b, cons
 cudaError_t launch_experts_backward_tc(moe_dtype dtype, const TrainBuffers& b, const uint32_t* offsets, int E,
                                        int64_t rows, int64_t H, int64_t I, uint32_t* sched, int num_sms,
                                        cudaStream_t stream, const char** why);
+// ---- gradient norm and clipping (grad_clip.cu)
+size_t grad_norm_scratch_bytes(int64_t n);
+cudaError_t launch_grad_norm(const moe_grad_tensor* tensors, int64_t n, float* norm, void* scratch, int num_sms,
+                             cudaStream_t stream);
+cudaError_t launch_grad_clip(const moe_grad_tensor* tensors, int64_t n, const float* norm, float max_norm, int num_sms,
+                             cudaStream_t stream);
 cudaError_t launch_bounded_wait_selftest(uint32_t limit_us, cudaStream_t stream);
 
 }  // namespace moe
