@@ -9,6 +9,7 @@ fallback: if the library is missing or fails to load, every call raises.
 from __future__ import annotations
 
 import ctypes
+from array import array
 from collections import namedtuple
 from pathlib import Path
 
@@ -64,7 +65,6 @@ _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_
 _OPT = ctypes.POINTER(GroupRoutingOptions)
 _ROPT = ctypes.POINTER(RouterWeightOptions)
 _FP = ctypes.c_void_p
-_GT = ctypes.POINTER(GradTensor)
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "moe_last_error": (ctypes.c_char_p, []),
@@ -125,8 +125,8 @@ SIGNATURES = {
     "moe_forward_mxfp4": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, ctypes.c_int, _I64, _I32, _I32, _P, _P, _P, _P,
                                          _SZ, _P]),
     "moe_grad_norm_workspace_size": (_SZ, [_I64]),
-    "moe_grad_norm": (ctypes.c_int, [_GT, _I64, _P, _P, _SZ, _P]),
-    "moe_grad_clip": (ctypes.c_int, [_GT, _I64, _P, ctypes.c_float, _P]),
+    "moe_grad_norm": (ctypes.c_int, [_P, _I64, _P, _P, _SZ, _P]),
+    "moe_grad_clip": (ctypes.c_int, [_P, _I64, _P, ctypes.c_float, _P]),
     "moe_device_status": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _I32]),
     "moe_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_uint32, _P]),
 }
@@ -693,38 +693,55 @@ Mxfp4.__doc__ = """An MXFP4 matrix [.., K]: codes uint8 [.., K/2] (element 2i in
 scales uint8 [.., moe_mxfp4_scale_pitch(K)] (E8M0, one per 32 elements)."""
 
 
-def _on_current_device(*tensors):
-    """The library launches on the current device: tensors of another one are refused."""
+def _here(stream, *tensors) -> int:
+    """The raw stream of a call. The library launches on the current device: tensors of another one are refused
+    (host tensors by the callers' own checks)."""
     cur = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and t.device.index != cur:
+        if t is not None and t.get_device() != cur:
             raise MoeError(7, f"a tensor is on {t.device}, the current device is cuda:{cur}")
+    return torch._C._cuda_getCurrentRawStream(cur) if stream is None else stream.cuda_stream
 
 
 def _empty(shape, dtype: torch.dtype, device, stream) -> torch.Tensor:
     """torch.empty on the stream the call runs on: memory that an earlier use on another stream may still touch is
     not handed out, and scratch that the call drops is reused in that stream's order only."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
 def _scratch(nbytes: int, device, workspace, stream) -> torch.Tensor:
     if workspace is not None:
-        return workspace
+        return _dev_tensor(workspace, "workspace").view(torch.uint8)
     return _empty((max(int(nbytes), 1),), torch.uint8, device, stream)
+
+
+def _addr(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
 
 
 def _mx(q, name: str) -> tuple[torch.Tensor, torch.Tensor, int]:
     """(codes, scales, K) of an Mxfp4, checked: contiguous uint8 on the device, shapes that belong together."""
-    codes, scales = _dev_tensor(q.codes, f"{name}.codes"), _dev_tensor(q.scales, f"{name}.scales")
+    codes, scales = q
+    _dev_tensor(codes, name)
+    _dev_tensor(scales, name)
     if codes.dtype != torch.uint8 or scales.dtype != torch.uint8:
         raise MoeError(3, f"{name}: codes and scales must be uint8")
-    if codes.dim() < 1 or scales.dim() < 1:
-        raise MoeError(2, f"{name}: codes and scales need at least one dimension")
-    K = codes.shape[-1] * 2
-    if tuple(scales.shape) != tuple(codes.shape[:-1]) + (moe_mxfp4_scale_pitch(K),):
-        raise MoeError(2, f"{name}: scales {tuple(scales.shape)} do not belong to codes {tuple(codes.shape)}")
+    cs, ss = codes.shape, scales.shape
+    if len(cs) < 1 or len(ss) != len(cs):
+        raise MoeError(2, f"{name}: codes and scales need the same number of dimensions, at least one")
+    K = cs[-1] * 2
+    if ss[-1] != _pitch(K) or ss[:-1] != cs[:-1]:
+        raise MoeError(2, f"{name}: scales {tuple(ss)} do not belong to codes {tuple(cs)}")
     return codes, scales, K
+
+
+def _pitch(K: int) -> int:
+    if K < 32 or K % 32:
+        raise MoeError(2, "K must be a positive multiple of 32")
+    return (K + 127) // 128 * 4
 
 
 def moe_mxfp4_scale_pitch(K: int) -> int:
@@ -744,28 +761,32 @@ def moe_mxfp4_quantize(x: torch.Tensor, *, inv: torch.Tensor | None = None, top_
     (not set, without `out`)."""
     lib = load_library()
     _dev_tensor(x, "x")
-    if x.dim() < 1:
+    shape = x.shape
+    if len(shape) < 1:
         raise MoeError(2, "x needs at least one dimension")
-    K = x.shape[-1]
-    lead = tuple(x.shape[:-1])
-    pitch = moe_mxfp4_scale_pitch(K)
+    K = shape[-1]
+    pitch = _pitch(K)
     rows = x.numel() // K
+    lead = shape[:-1]
     if inv is not None:
         _dev_tensor(inv, "inv")
-        if x.dim() != 2 or inv.numel() != rows * top_k:
+        if len(shape) != 2 or inv.numel() != rows * top_k:
             raise MoeError(2, "inv must hold one entry per slot of x [T, K]")
-        if inv.element_size() != 4:
+        if inv.dtype != torch.int32 and inv.dtype != getattr(torch, "uint32", torch.int32):
             raise MoeError(3, "inv must be uint32 (or its int32 view)")
         lead = (rows * top_k,)
+    raw = _here(stream, x, inv)
     if out is None:
-        out = Mxfp4(_empty(lead + (K // 2,), torch.uint8, x.device, stream),
-                    _empty(lead + (pitch,), torch.uint8, x.device, stream))
-    codes, scales, k_out = _mx(out, "out")
-    if k_out != K or codes.numel() * 2 != (rows * top_k if inv is not None else rows) * K:
-        raise MoeError(2, "out does not have the result's shape")
-    _on_current_device(x, inv, codes, scales)
-    _check(lib.moe_mxfp4_quantize(_ptr(x), _dt(x), rows, K, _ptr(inv), top_k, _ptr(codes), _ptr(scales),
-                                  _stream(stream)))
+        codes = _empty((*lead, K // 2), torch.uint8, x.device, stream)
+        scales = _empty((*lead, pitch), torch.uint8, x.device, stream)
+        out = Mxfp4(codes, scales)
+    else:
+        codes, scales, k_out = _mx(out, "out")
+        if k_out != K or codes.numel() * 2 != (rows * top_k if inv is not None else rows) * K:
+            raise MoeError(2, "out does not have the result's shape")
+        _here(stream, codes, scales)
+    _check(lib.moe_mxfp4_quantize(x.data_ptr(), _dt(x), rows, K, _addr(inv), top_k, codes.data_ptr(),
+                                  scales.data_ptr(), raw))
     return out
 
 
@@ -773,14 +794,16 @@ def moe_mxfp4_dequantize(q: Mxfp4, dtype: torch.dtype = torch.bfloat16, *, out=N
     """The values an MXFP4 matrix stands for, [.., K] in `dtype`."""
     lib = load_library()
     codes, scales, K = _mx(q, "q")
+    raw = _here(stream, codes, scales)
     if out is None:
-        out = _empty(tuple(codes.shape[:-1]) + (K,), dtype, codes.device, stream)
-    _dev_tensor(out, "out")
-    if out.dtype != dtype or out.numel() != codes.numel() * 2:
-        raise MoeError(2, "out does not have the result's shape and dtype")
-    _on_current_device(codes, scales, out)
-    _check(lib.moe_mxfp4_dequantize(_ptr(codes), _ptr(scales), codes.numel() * 2 // K, K, _ptr(out), _dt(out),
-                                    _stream(stream)))
+        out = _empty((*codes.shape[:-1], K), dtype, codes.device, stream)
+    else:
+        _dev_tensor(out, "out")
+        if out.dtype != dtype or out.numel() != codes.numel() * 2:
+            raise MoeError(2, "out does not have the result's shape and dtype")
+        _here(stream, out)
+    _check(lib.moe_mxfp4_dequantize(codes.data_ptr(), scales.data_ptr(), codes.numel() * 2 // K, K, out.data_ptr(),
+                                    _dt(out), raw))
     return out
 
 
@@ -799,7 +822,7 @@ class ExpertsMxfp4:
         if (tuple(gc.shape) != (E, I, H // 2) or tuple(uc.shape) != tuple(gc.shape) or Hu != H or
                 tuple(dc.shape) != (E, H, I // 2)):
             raise MoeError(2, "gate and up must be [E, I, H] and down [E, H, I]")
-        _on_current_device(gc, gs, uc, us, dc, ds)
+        _here(None, gc, gs, uc, us, dc, ds)
         self.E, self.H, self.I = E, H, I
         self.device = gc.device
         self._codes = (gc, uc, dc)
@@ -829,11 +852,10 @@ def _mx_rows(experts: ExpertsMxfp4, q: Mxfp4, name: str, K: int, offsets: torch.
     if codes.dim() != 2 or k != K:
         raise MoeError(2, f"{name} must be [rows, {K}]")
     _dev_tensor(offsets, "offsets")
-    if offsets.element_size() != 4:
+    if offsets.dtype != torch.int32 and offsets.dtype != getattr(torch, "uint32", torch.int32):
         raise MoeError(3, "offsets must be uint32 (or its int32 view)")
     if offsets.numel() != experts.E + 1:
         raise MoeError(2, "offsets must hold E + 1 entries")
-    _on_current_device(codes, scales, offsets)
     return codes, scales, codes.shape[0]
 
 
@@ -843,7 +865,7 @@ def _mx_out(out, rows: int, cols: int, dtype: torch.dtype, device, stream) -> to
     _dev_tensor(out, "out")
     if out.dtype != dtype or tuple(out.shape) != (rows, cols):
         raise MoeError(2, f"out must be [{rows}, {cols}] in {dtype}")
-    _on_current_device(out)
+    _here(stream, out)
     return out
 
 
@@ -854,21 +876,22 @@ def moe_experts_mxfp4_gate_up(experts: ExpertsMxfp4, x: Mxfp4, offsets: torch.Te
     `dtype` and quantised, an Mxfp4 (what moe_mxfp4_quantize gives on h)."""
     lib = load_library()
     codes, scales, rows = _mx_rows(experts, x, "x", experts.H, offsets)
+    raw = _here(stream, codes, scales, offsets)
+    if dtype not in _DTYPE:
+        raise MoeError(3, f"unsupported dtype {dtype}")
     h, hc, hs = None, None, None
     if quantized:
         if out is None:
             out = Mxfp4(_empty((rows, experts.I // 2), torch.uint8, codes.device, stream),
-                        _empty((rows, moe_mxfp4_scale_pitch(experts.I)), torch.uint8, codes.device, stream))
+                        _empty((rows, _pitch(experts.I)), torch.uint8, codes.device, stream))
         hc, hs, k = _mx(out, "out")
         if k != experts.I or hc.dim() != 2 or hc.shape[0] != rows:
             raise MoeError(2, f"out must be [{rows}, {experts.I}]")
-        _on_current_device(hc, hs)
+        _here(stream, hc, hs)
     else:
         out = h = _mx_out(out, rows, experts.I, dtype, codes.device, stream)
-    if dtype not in _DTYPE:
-        raise MoeError(3, f"unsupported dtype {dtype}")
-    _check(lib.moe_experts_mxfp4_gate_up(experts.handle, _ptr(codes), _ptr(scales), _ptr(offsets), rows,
-                                         _DTYPE[dtype], _ptr(h), _ptr(hc), _ptr(hs), _stream(stream)))
+    _check(lib.moe_experts_mxfp4_gate_up(experts.handle, codes.data_ptr(), scales.data_ptr(), offsets.data_ptr(), rows,
+                                         _DTYPE[dtype], _addr(h), _addr(hc), _addr(hs), raw))
     return out
 
 
@@ -877,9 +900,10 @@ def moe_experts_mxfp4_down(experts: ExpertsMxfp4, h: Mxfp4, offsets: torch.Tenso
     """Second stage: y [rows, H] = h W_down^T per expert, from MXFP4 h."""
     lib = load_library()
     codes, scales, rows = _mx_rows(experts, h, "h", experts.I, offsets)
+    raw = _here(stream, codes, scales, offsets)
     y = _mx_out(out, rows, experts.H, dtype, codes.device, stream)
-    _check(lib.moe_experts_mxfp4_down(experts.handle, _ptr(codes), _ptr(scales), _ptr(offsets), rows, _dt(y), _ptr(y),
-                                      _stream(stream)))
+    _check(lib.moe_experts_mxfp4_down(experts.handle, codes.data_ptr(), scales.data_ptr(), offsets.data_ptr(), rows,
+                                      _dt(y), y.data_ptr(), raw))
     return y
 
 
@@ -890,11 +914,13 @@ def moe_experts_mxfp4_forward_dispatched(experts: ExpertsMxfp4, x: Mxfp4, offset
     between them as MXFP4 (rounded to `dtype` first)."""
     lib = load_library()
     codes, scales, rows = _mx_rows(experts, x, "x", experts.H, offsets)
+    raw = _here(stream, codes, scales, offsets, workspace)
     y = _mx_out(out, rows, experts.H, dtype, codes.device, stream)
     need = lib.moe_experts_mxfp4_forward_dispatched_workspace_size(experts.handle, rows)
     ws = _scratch(need, codes.device, workspace, stream)
-    _check(lib.moe_experts_mxfp4_forward_dispatched(experts.handle, _ptr(codes), _ptr(scales), _ptr(offsets), rows,
-                                                    _dt(y), _ptr(y), _ptr(ws), ws.numel(), _stream(stream)))
+    _check(lib.moe_experts_mxfp4_forward_dispatched(experts.handle, codes.data_ptr(), scales.data_ptr(),
+                                                    offsets.data_ptr(), rows, _dt(y), y.data_ptr(), ws.data_ptr(),
+                                                    ws.numel(), raw))
     return y
 
 
@@ -914,48 +940,60 @@ def moe_forward_mxfp4(experts: ExpertsMxfp4, x: torch.Tensor, logits: torch.Tens
     for t, name, es in ((indices, "indices", 4), (weights, "weights", logits.element_size())):
         if t is not None and (_dev_tensor(t, name).numel() != T * top_k or t.element_size() != es):
             raise MoeError(2, f"{name} must hold T * top_k entries")
+    raw = _here(stream, x, logits, indices, weights, workspace)
     o = _mx_out(out, T, experts.H, x.dtype, x.device, stream)
-    _on_current_device(x, logits, indices, weights)
     ws = _scratch(lib.moe_forward_mxfp4_workspace_size(experts.handle, T, top_k, _dt(x)), x.device, workspace, stream)
-    _check(lib.moe_forward_mxfp4(experts.handle, _ptr(x), _dt(x), _ptr(logits), _dt(logits), T, top_k,
-                                 int(bool(renormalize)), _ptr(o), _ptr(indices), _ptr(weights), _ptr(ws), ws.numel(),
-                                 _stream(stream)))
+    _check(lib.moe_forward_mxfp4(experts.handle, x.data_ptr(), _dt(x), logits.data_ptr(), _dt(logits), T, top_k,
+                                 int(bool(renormalize)), o.data_ptr(), _addr(indices), _addr(weights), ws.data_ptr(),
+                                 ws.numel(), raw))
     return o
 
 
 # ---- gradient norm and clipping
 
-def _grad_table(tensors, out=None):
-    """The moe_grad_tensor array of a list of gradients (and of their destinations)."""
-    dst = tensors if out is None else out
-    if len(dst) != len(tensors):
-        raise MoeError(2, "out must hold one tensor per gradient")
-    table = (GradTensor * max(1, len(tensors)))()
-    cur = torch.cuda.current_device() if tensors and tensors[0].is_cuda else 0
-    for entry, s, d in zip(table, tensors, dst):
-        for t in (s,) if d is s else (s, d):
-            if not t.is_cuda or not t.is_contiguous():
-                raise ValueError("gradients must be contiguous CUDA tensors")
-            if t.device.index != cur:
-                raise MoeError(7, f"a tensor is on {t.device}, the current device is cuda:{cur}")
-        if d.dtype != s.dtype or d.numel() != s.numel():
+def _grad_table(tensors, out, cur: int) -> array:
+    """The moe_grad_tensor array of a list of gradients and of their destinations (`out` is the same list to clip in
+    place): rows of four 64-bit words, the dtype code in the low half of the last. Column by column, because a
+    model's list is long and this is the call's host time."""
+    lists = (tensors,) if out is tensors else (tensors, out)
+    for ts in lists:
+        if not all([t.is_contiguous() for t in ts]):
+            raise ValueError("gradients must be contiguous CUDA tensors")
+        if any([t.get_device() != cur for t in ts]):
+            raise MoeError(7, f"a gradient is not on the current device, cuda:{cur}")
+    numel = [t.numel() for t in tensors]
+    dtypes = [t.dtype for t in tensors]
+    src = dst = [t.data_ptr() for t in tensors]
+    if out is not tensors:
+        if len(out) != len(tensors):
+            raise MoeError(2, "out must hold one tensor per gradient")
+        if [t.numel() for t in out] != numel or [t.dtype for t in out] != dtypes:
             raise MoeError(2, "out must have the gradients' sizes and dtypes")
-        entry.src, entry.dst, entry.numel, entry.dtype = s.data_ptr(), d.data_ptr(), s.numel(), _dt(s)
+        dst = [t.data_ptr() for t in out]
+    try:
+        codes = [_DTYPE[d] for d in dtypes]
+    except KeyError as e:
+        raise MoeError(3, f"unsupported dtype {e.args[0]}") from None
+    table = array("q", bytes(32 * max(1, len(src))))
+    n = len(src)
+    for i, column in enumerate((src, dst, numel, codes)):
+        table[i:4 * n:4] = array("q", column)
     return table
 
 
-def _grad_norm(lib, table, n: int, device, out, workspace, stream) -> torch.Tensor:
+def _grad_norm(lib, table, n: int, cur: int, out, workspace, stream, raw) -> torch.Tensor:
+    device = torch.device("cuda", cur)
     norm = out if out is not None else _empty((), torch.float32, device, stream)
-    if norm.dtype != torch.float32 or norm.numel() != 1:
-        raise MoeError(3, "the norm must be one float32")
-    _on_current_device(_dev_tensor(norm, "norm"))
-    ws = _scratch(lib.moe_grad_norm_workspace_size(n), norm.device, workspace, stream)
-    _check(lib.moe_grad_norm(table, n, _ptr(norm), _ptr(ws), ws.numel(), _stream(stream)))
+    ws = _scratch(lib.moe_grad_norm_workspace_size(n), device, workspace, stream)
+    _check(lib.moe_grad_norm(table.buffer_info()[0], n, norm.data_ptr(), ws.data_ptr(), ws.numel(), raw))
     return norm
 
 
-def _grad_device(tensors):
-    return tensors[0].device if tensors else torch.device("cuda", torch.cuda.current_device())
+def _one_float(t: torch.Tensor):
+    _dev_tensor(t, "norm")
+    if t.dtype != torch.float32 or t.numel() != 1:
+        raise MoeError(3, "the norm must be one float32")
+    return t
 
 
 def moe_grad_norm(tensors, *, out=None, workspace=None, stream=None) -> torch.Tensor:
@@ -963,7 +1001,11 @@ def moe_grad_norm(tensors, *, out=None, workspace=None, stream=None) -> torch.Te
     gradients, one float32 on the device (nothing waits for it)."""
     lib = load_library()
     tensors = list(tensors)
-    return _grad_norm(lib, _grad_table(tensors), len(tensors), _grad_device(tensors), out, workspace, stream)
+    if tensors and not tensors[0].is_cuda:
+        raise ValueError("gradients must be contiguous CUDA tensors")
+    raw = _here(stream, out if out is None else _one_float(out), workspace)
+    cur = torch.cuda.current_device()
+    return _grad_norm(lib, _grad_table(tensors, tensors, cur), len(tensors), cur, out, workspace, stream, raw)
 
 
 def moe_grad_clip(tensors, norm: torch.Tensor, max_norm: float, *, out=None, stream=None):
@@ -973,11 +1015,9 @@ def moe_grad_clip(tensors, norm: torch.Tensor, max_norm: float, *, out=None, str
     lib = load_library()
     tensors = list(tensors)
     out = tensors if out is None else list(out)
-    _dev_tensor(norm, "norm")
-    if norm.dtype != torch.float32 or norm.numel() != 1:
-        raise MoeError(3, "the norm must be one float32")
-    _on_current_device(norm)
-    _check(lib.moe_grad_clip(_grad_table(tensors, out), len(tensors), _ptr(norm), float(max_norm), _stream(stream)))
+    raw = _here(stream, _one_float(norm))
+    table = _grad_table(tensors, out, torch.cuda.current_device())
+    _check(lib.moe_grad_clip(table.buffer_info()[0], len(tensors), norm.data_ptr(), float(max_norm), raw))
     return out
 
 
@@ -985,10 +1025,13 @@ def moe_clip_grad_norm(tensors, max_norm: float, *, out=None, workspace=None, st
     """moe_grad_norm and moe_grad_clip in turn: returns the norm before the clip."""
     lib = load_library()
     tensors = list(tensors)
-    out = tensors if out is None else list(out)
-    table = _grad_table(tensors, out)
-    norm = _grad_norm(lib, table, len(tensors), _grad_device(tensors), None, workspace, stream)
-    _check(lib.moe_grad_clip(table, len(tensors), _ptr(norm), float(max_norm), _stream(stream)))
+    if tensors and not tensors[0].is_cuda:
+        raise ValueError("gradients must be contiguous CUDA tensors")
+    raw = _here(stream, workspace)
+    cur = torch.cuda.current_device()
+    table = _grad_table(tensors, tensors if out is None else list(out), cur)
+    norm = _grad_norm(lib, table, len(tensors), cur, None, workspace, stream, raw)
+    _check(lib.moe_grad_clip(table.buffer_info()[0], len(tensors), norm.data_ptr(), float(max_norm), raw))
     return norm
 
 
