@@ -1,6 +1,8 @@
 // MXFP4 quantisation and its inverse (the format and its rounding are in
 // mxfp4.cuh), and the one-time layout of the expert weights' scales for the
 // tensor cores.
+#include <type_traits>
+
 #include "moe_common.cuh"
 #include "moe_internal.h"
 #include "mxfp4.cuh"
@@ -9,36 +11,88 @@ namespace moe {
 namespace {
 
 constexpr int MXQ_THREADS = 256;
-constexpr int MXQ_UNROLL = 4;                           // 8-element units per thread and step
+constexpr int MXQ_UNROLL = 2;                           // 16-element units per thread and step
 constexpr int MXQ_WARP_UNITS = 32 * MXQ_UNROLL;
 
-// Eight consecutive elements as FP32, and the largest |x| bits among them.
-template <typename T> struct Load8;
-template <> struct Load8<float> {
-  uint4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = *reinterpret_cast<const uint4*>(p);
-    b = *reinterpret_cast<const uint4*>(p + 4);
+// 32 bytes with one load or store (both addresses 32-byte aligned).
+__device__ __forceinline__ void ld32(const void* p, uint32_t (&r)[8]) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st32(void* p, const uint32_t (&r)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// The same in two 16-byte halves, for bases that are only 16-byte aligned.
+template <bool WIDE>
+__device__ __forceinline__ void load32(const uint8_t* p, uint32_t (&r)[8]) {
+  if (WIDE) {
+    ld32(p, r);
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4*>(p), b = *reinterpret_cast<const uint4*>(p + 16);
+    r[0] = a.x; r[1] = a.y; r[2] = a.z; r[3] = a.w;
+    r[4] = b.x; r[5] = b.y; r[6] = b.z; r[7] = b.w;
   }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
-    v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+}
+template <bool WIDE>
+__device__ __forceinline__ void store32(uint8_t* p, const uint32_t (&r)[8]) {
+  if (WIDE) {
+    st32(p, r);
+  } else {
+    *reinterpret_cast<uint4*>(p) = make_uint4(r[0], r[1], r[2], r[3]);
+    *reinterpret_cast<uint4*>(p + 16) = make_uint4(r[4], r[5], r[6], r[7]);
+  }
+}
+
+// 16 consecutive elements: raw words, the largest magnitude's FP32 bits
+// (of this thread's 16), and the elements times a power of two.
+template <typename T> struct Unit16 {  // F16, BF16
+  uint32_t w[8];
+  template <bool WIDE> __device__ __forceinline__ void load(const uint8_t* p) { load32<WIDE>(p, w); }
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    // Magnitudes as pairs of 16-bit integers: integer order is the order of
+    // the values, with infinities and NaNs on top.
+    uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+    const uint32_t h = max(m & 0xFFFFu, m >> 16);
+    if (std::is_same<T, __nv_bfloat16>::value) return h << 16;
+    return __float_as_uint(__half2float(__ushort_as_half(static_cast<unsigned short>(h))));
+  }
+  __device__ __forceinline__ void scaled8(int half, float s, float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const T* e = reinterpret_cast<const T*>(&w[half * 4 + i]);
+      v[2 * i] = to_f32(e[0]) * s;
+      v[2 * i + 1] = to_f32(e[1]) * s;
+    }
   }
 };
-template <typename T> struct Load8 {
-  uint4 a;
-  __device__ __forceinline__ void load(const T* p) { a = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    const T* e = reinterpret_cast<const T*>(&a);
+template <> struct Unit16<float> {
+  uint32_t a[8], b[8];
+  template <bool WIDE> __device__ __forceinline__ void load(const uint8_t* p) {
+    load32<WIDE>(p, a);
+    load32<WIDE>(p + 32, b);
+  }
+  __device__ __forceinline__ uint32_t amax_bits() const {
+    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32(e[i]);
+    for (int i = 0; i < 8; ++i) m = max(m, max(a[i] & 0x7FFFFFFFu, b[i] & 0x7FFFFFFFu));
+    return m;
+  }
+  __device__ __forceinline__ void scaled8(int half, float s, float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(half == 0 ? a[i] : b[i]) * s;
   }
 };
 
 struct QuantArgs {
-  const void* x;
+  const uint8_t* x;
   uint32_t rows;
-  uint32_t upr;        // 8-element units per row, K / 8
+  uint32_t upr;        // 16-element units per row, K / 16
   uint32_t upr_magic;  // ceil(2^32 / upr)
   uint32_t units;      // rows * upr
   const uint32_t* inv; // [rows * top_k] output row of each slot, or NULL (row r -> row r)
@@ -49,64 +103,60 @@ struct QuantArgs {
   int pitch;
 };
 
-// One thread quantises 8 elements, four lanes share a block: 16 (or 32)
-// bytes in, 4 bytes of codes out, coalesced over the warp; the block's
-// largest magnitude is exchanged by two shuffles. Row by row the units are
-// contiguous, so a warp takes 128 consecutive units whatever K is. With inv
-// each row's codes go to its top_k dispatched rows: x is read once and no
-// dispatched copy of it in its own type is ever written.
-template <typename T>
+// One thread quantises 16 elements, two lanes share a block: 32 (or 64) bytes
+// in, 8 bytes of codes out, coalesced over the warp; the block's largest
+// magnitude takes one shuffle. Row by row the units are contiguous, so a warp
+// takes 64 consecutive units whatever K is. With inv each row's codes go to
+// its top_k dispatched rows: x is read once and no dispatched copy of it in
+// its own type is ever written.
+template <typename T, bool WIDE>
 __global__ void __launch_bounds__(MXQ_THREADS) mx_quantize_kernel(const QuantArgs a) {
   grid_dependency_wait();
   launch_dependents();
+  constexpr int UNIT_BYTES = 16 * static_cast<int>(sizeof(T));
   const uint32_t lane = threadIdx.x & 31;
   const uint32_t warp = (blockIdx.x * MXQ_THREADS + threadIdx.x) >> 5;
   const uint32_t n_warps = gridDim.x * (MXQ_THREADS / 32);
-  const T* __restrict__ x = static_cast<const T*>(a.x);
   const uint32_t n_seg = (a.units + MXQ_WARP_UNITS - 1) / MXQ_WARP_UNITS;
-  const int64_t code_pitch = static_cast<int64_t>(a.upr) * 4;
+  const int64_t code_pitch = static_cast<int64_t>(a.upr) * 8;
   for (uint32_t seg = warp; seg < n_seg; seg += n_warps) {
     const uint32_t u0 = seg * MXQ_WARP_UNITS;
-    Load8<T> in[MXQ_UNROLL];
+    Unit16<T> in[MXQ_UNROLL];
 #pragma unroll
     for (int i = 0; i < MXQ_UNROLL; ++i) {
+      // units is even: a block's two lanes are both in or both out (those out read unit 0 and store nothing)
       const uint32_t u = u0 + i * 32 + lane;
-      if (u < a.units) in[i].load(x + static_cast<int64_t>(u) * 8);
+      in[i].template load<WIDE>(a.x + static_cast<int64_t>(u < a.units ? u : 0) * UNIT_BYTES);
     }
     const uint32_t row0 = u0 / a.upr;
     const uint32_t rem0 = u0 - row0 * a.upr;
 #pragma unroll
     for (int i = 0; i < MXQ_UNROLL; ++i) {
       const uint32_t off = i * 32 + lane;
-      const bool live = u0 + off < a.units;  // units is a multiple of 4: a block is all in or all out
-      float v[8];
-      uint32_t amax = 0;
-      if (live) {
-        in[i].get(v);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) amax = max(amax, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-      }
+      uint32_t amax = in[i].amax_bits();
       amax = max(amax, __shfl_xor_sync(FULL_MASK, amax, 1));
-      amax = max(amax, __shfl_xor_sync(FULL_MASK, amax, 2));
-      if (!live) continue;
+      if (u0 + off >= a.units) continue;
       const uint32_t byte = mx_scale_byte(amax);
       const float s = mx_inv_scale(byte);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] *= s;
-      const uint32_t codes = byte == 255u ? 0u : mx_pack8(v);
-      const uint32_t local = rem0 + off;                      // < upr + 128
+      uint2 codes;
+      float v[8];
+      in[i].scaled8(0, s, v);
+      codes.x = mx_pack8(v);
+      in[i].scaled8(1, s, v);
+      codes.y = mx_pack8(v);
+      if (byte == 255u) codes = make_uint2(0u, 0u);
+      const uint32_t local = rem0 + off;                      // < upr + 64
       const uint32_t dr = __umulhi(local, a.upr_magic);       // local / upr
       const uint32_t row = row0 + dr;
       const uint32_t unit = local - dr * a.upr;
-      const uint32_t blk = unit >> 2;
-      const bool head = (unit & 3u) == 0;
-      const bool last = unit + 4 >= a.upr;                    // the row's last block also clears the row's pad bytes
+      const uint32_t blk = unit >> 1;
+      const bool head = (unit & 1u) == 0;
       auto store = [&](uint32_t r) {
-        *reinterpret_cast<uint32_t*>(a.codes + static_cast<int64_t>(r) * code_pitch + unit * 4) = codes;
+        *reinterpret_cast<uint2*>(a.codes + static_cast<int64_t>(r) * code_pitch + unit * 8) = codes;
         if (head) {
           uint8_t* sp = a.scales + static_cast<int64_t>(r) * a.pitch;
           sp[blk] = static_cast<uint8_t>(byte);
-          if (last)
+          if (unit + 2 >= a.upr)  // the row's last block also clears the row's pad bytes
             for (int p = static_cast<int>(blk) + 1; p < a.pitch; ++p) sp[p] = 0;
         }
       };
@@ -129,11 +179,11 @@ struct DequantArgs {
   uint32_t upr_magic;
   uint32_t units;
   int pitch;
-  void* out;
+  uint8_t* out;
 };
 
-// One thread: 4 bytes of codes -> 8 values (one 16-byte store, two for FP32).
-template <typename T>
+// One thread: 8 bytes of codes -> 16 values.
+template <typename T, bool WIDE>
 __global__ void __launch_bounds__(MXQ_THREADS) mx_dequantize_kernel(const DequantArgs a) {
   grid_dependency_wait();
   launch_dependents();
@@ -145,7 +195,8 @@ __global__ void __launch_bounds__(MXQ_THREADS) mx_dequantize_kernel(const Dequan
     const uint32_t u0 = seg * MXQ_WARP_UNITS;
     const uint32_t row0 = u0 / a.upr;
     const uint32_t rem0 = u0 - row0 * a.upr;
-    uint32_t c[MXQ_UNROLL], sb[MXQ_UNROLL];
+    uint2 c[MXQ_UNROLL];
+    uint32_t sb[MXQ_UNROLL];
 #pragma unroll
     for (int i = 0; i < MXQ_UNROLL; ++i) {
       const uint32_t off = i * 32 + lane;
@@ -153,28 +204,34 @@ __global__ void __launch_bounds__(MXQ_THREADS) mx_dequantize_kernel(const Dequan
         const uint32_t local = rem0 + off;
         const uint32_t dr = __umulhi(local, a.upr_magic);
         const uint32_t unit = local - dr * a.upr;
-        c[i] = *reinterpret_cast<const uint32_t*>(a.codes + static_cast<int64_t>(u0 + off) * 4);
-        sb[i] = a.scales[static_cast<int64_t>(row0 + dr) * a.pitch + (unit >> 2)];
+        c[i] = *reinterpret_cast<const uint2*>(a.codes + static_cast<int64_t>(u0 + off) * 8);
+        sb[i] = a.scales[static_cast<int64_t>(row0 + dr) * a.pitch + (unit >> 1)];
       }
     }
 #pragma unroll
     for (int i = 0; i < MXQ_UNROLL; ++i) {
       const uint32_t u = u0 + i * 32 + lane;
       if (u >= a.units) continue;
-      uint32_t h[4];
-      mx_unpack8(c[i], h);
       const float s = mx_scale(sb[i]);
-      T o[8];
+      uint8_t* dst = a.out + static_cast<int64_t>(u) * (16 * static_cast<int>(sizeof(T)));
+      uint32_t o[8];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
-        o[2 * j] = from_f32<T>(f.x * s);
-        o[2 * j + 1] = from_f32<T>(f.y * s);
+      for (int half = 0; half < 2; ++half) {
+        uint32_t h[4];
+        mx_unpack8(half == 0 ? c[i].x : c[i].y, h);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[j]));
+          if constexpr (std::is_same<T, float>::value) {
+            o[2 * j] = __float_as_uint(f.x * s);
+            o[2 * j + 1] = __float_as_uint(f.y * s);
+          } else {
+            o[half * 4 + j] = pack2<T>(f.x * s, f.y * s);
+          }
+        }
+        if (std::is_same<T, float>::value) store32<WIDE>(dst + half * 32, o);
       }
-      T* dst = static_cast<T*>(a.out) + static_cast<int64_t>(u) * 8;
-      constexpr int VEC = static_cast<int>(sizeof(T) * 8 / 16);
-#pragma unroll
-      for (int q = 0; q < VEC; ++q) reinterpret_cast<uint4*>(dst)[q] = reinterpret_cast<const uint4*>(o)[q];
+      if (!std::is_same<T, float>::value) store32<WIDE>(dst, o);
     }
   }
 }
@@ -206,7 +263,7 @@ __global__ void mx_layout_scales_kernel(const uint8_t* __restrict__ src, uint32_
 }
 
 // Rows per launch so that the unit count stays below 2^31.
-int64_t rows_per_launch(int64_t K) { return ((int64_t{1} << 31) - MXQ_WARP_UNITS) / (K / 8); }
+int64_t rows_per_launch(int64_t K) { return ((int64_t{1} << 31) - MXQ_WARP_UNITS) / (K / 16); }
 
 int grid_for(uint32_t units, int num_sms) {
   const int64_t want = (static_cast<int64_t>(units) + MXQ_WARP_UNITS * (MXQ_THREADS / 32) - 1) /
@@ -221,13 +278,14 @@ uint32_t magic_for(uint32_t upr) { return static_cast<uint32_t>(((uint64_t{1} <<
 
 cudaError_t launch_mx_quantize(const void* x, moe_dtype dtype, int64_t rows, int64_t K, const uint32_t* inv, int top_k,
                                void* codes, void* scales, int num_sms, cudaStream_t stream) {
-  const uint32_t upr = static_cast<uint32_t>(K / 8);
+  const uint32_t upr = static_cast<uint32_t>(K / 16);
   const int64_t step = rows_per_launch(K);
   const int64_t pitch = mx_scale_pitch(K);
   for (int64_t r0 = 0; r0 < rows; r0 += step) {
     const int64_t n = rows - r0 < step ? rows - r0 : step;
     QuantArgs a{};
     a.x = static_cast<const uint8_t*>(x) + r0 * K * static_cast<int64_t>(dtype_size(dtype));
+    const bool wide = reinterpret_cast<uintptr_t>(a.x) % 32 == 0;
     a.rows = static_cast<uint32_t>(n);
     a.upr = upr;
     a.upr_magic = magic_for(upr);
@@ -239,10 +297,11 @@ cudaError_t launch_mx_quantize(const void* x, moe_dtype dtype, int64_t rows, int
     a.scales = static_cast<uint8_t*>(scales) + (inv != nullptr ? 0 : r0 * pitch);
     a.pitch = static_cast<int>(pitch);
     const dim3 grid(grid_for(a.units, num_sms)), block(MXQ_THREADS);
-    cudaError_t err;
-    if (dtype == MOE_F32) err = launch_dependent(mx_quantize_kernel<float>, grid, block, 0, stream, a);
-    else if (dtype == MOE_F16) err = launch_dependent(mx_quantize_kernel<__half>, grid, block, 0, stream, a);
-    else err = launch_dependent(mx_quantize_kernel<__nv_bfloat16>, grid, block, 0, stream, a);
+    auto kern = dtype == MOE_F32   ? (wide ? mx_quantize_kernel<float, true> : mx_quantize_kernel<float, false>)
+                : dtype == MOE_F16 ? (wide ? mx_quantize_kernel<__half, true> : mx_quantize_kernel<__half, false>)
+                                   : (wide ? mx_quantize_kernel<__nv_bfloat16, true>
+                                           : mx_quantize_kernel<__nv_bfloat16, false>);
+    const cudaError_t err = launch_dependent(kern, grid, block, 0, stream, a);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
@@ -250,7 +309,7 @@ cudaError_t launch_mx_quantize(const void* x, moe_dtype dtype, int64_t rows, int
 
 cudaError_t launch_mx_dequantize(const void* codes, const void* scales, int64_t rows, int64_t K, void* out,
                                  moe_dtype dtype, int num_sms, cudaStream_t stream) {
-  const uint32_t upr = static_cast<uint32_t>(K / 8);
+  const uint32_t upr = static_cast<uint32_t>(K / 16);
   const int64_t step = rows_per_launch(K);
   const int64_t pitch = mx_scale_pitch(K);
   for (int64_t r0 = 0; r0 < rows; r0 += step) {
@@ -263,11 +322,13 @@ cudaError_t launch_mx_dequantize(const void* codes, const void* scales, int64_t 
     a.units = static_cast<uint32_t>(n * upr);
     a.pitch = static_cast<int>(pitch);
     a.out = static_cast<uint8_t*>(out) + r0 * K * static_cast<int64_t>(dtype_size(dtype));
+    const bool wide = reinterpret_cast<uintptr_t>(a.out) % 32 == 0;
     const dim3 grid(grid_for(a.units, num_sms)), block(MXQ_THREADS);
-    cudaError_t err;
-    if (dtype == MOE_F32) err = launch_dependent(mx_dequantize_kernel<float>, grid, block, 0, stream, a);
-    else if (dtype == MOE_F16) err = launch_dependent(mx_dequantize_kernel<__half>, grid, block, 0, stream, a);
-    else err = launch_dependent(mx_dequantize_kernel<__nv_bfloat16>, grid, block, 0, stream, a);
+    auto kern = dtype == MOE_F32   ? (wide ? mx_dequantize_kernel<float, true> : mx_dequantize_kernel<float, false>)
+                : dtype == MOE_F16 ? (wide ? mx_dequantize_kernel<__half, true> : mx_dequantize_kernel<__half, false>)
+                                   : (wide ? mx_dequantize_kernel<__nv_bfloat16, true>
+                                           : mx_dequantize_kernel<__nv_bfloat16, false>);
+    const cudaError_t err = launch_dependent(kern, grid, block, 0, stream, a);
     if (err != cudaSuccess) return err;
   }
   return cudaSuccess;
