@@ -815,10 +815,11 @@ moe_status moe_grad_clip(const moe_grad_tensor* tensors, int64_t n, const float*
  * down launch waiting for its expert's h rows, 0x1A the combine of
  * moe_experts_forward_combine waiting for the last down tile, 0x1B the grid
  * barrier of moe_route_dispatch and moe_route_sigmoid_grouped_dispatch (and
- * of the forward calls' routing), 0x21 - 0x28 the waits of the MXFP4 expert
+ * of the forward calls' routing), 0x21 - 0x2A the waits of the MXFP4 expert
  * products (0x21 producer, 0x22 MMA for a loaded stage, 0x23 MMA for a drained
- * accumulator, 0x24 epilogue, 0x25 / 0x26 teardown drains, 0x27 scale loader,
- * 0x28 MMA for a free scale buffer), 0x100
+ * accumulator, 0x24 epilogue, 0x25 / 0x26 teardown drains, 0x27 - 0x29 scale
+ * warps for a free or loaded ring slot or a free scale buffer, 0x2A MMA for a
+ * stage's scales), 0x100
  * moe_selftest_bounded_wait. Synchronises the current device; *code = 0 when
  * no wait has timed out.
  */

@@ -168,7 +168,7 @@ moe_status moe_mxfp4_dequantize(const void* codes, const void* scales, int64_t r
 
 size_t moe_experts_mxfp4_storage_size(int64_t E, int64_t H, int64_t I) {
   if (E < 1 || E > moe::ROUTE_MAX_E || !k_valid(H) || !k_valid(I)) return 0;
-  return 2 * moe::mx_weight_scale_bytes(true, E, I, H) + moe::mx_weight_scale_bytes(false, E, H, I);
+  return moe::mx_weight_scale_bytes(true, E, I, H) + moe::mx_weight_scale_bytes(false, E, H, I);
 }
 
 moe_status moe_experts_mxfp4_create(const void* gate_codes, const void* gate_scales, const void* up_codes,
@@ -198,22 +198,16 @@ moe_status moe_experts_mxfp4_create(const void* gate_codes, const void* gate_sca
     delete ex;
     return api_cuda_fail(err, "moe_experts_mxfp4_create device query");
   }
-  const char* why = nullptr;
-  if (!moe::mx_encode_weights(gate_codes, up_codes, down_codes, E, H, I, &ex->w, &why)) {
-    delete ex;
-    return api_fail(MOE_ERR_CUDA, why != nullptr ? why : "tensor map encoding failed");
-  }
+  ex->w.gate = gate_codes;
+  ex->w.up = up_codes;
+  ex->w.down = down_codes;
   uint8_t* sf = static_cast<uint8_t*>(storage);
-  const size_t gu = moe::mx_weight_scale_bytes(true, E, I, H);
-  ex->w.gate_sf = sf;
-  ex->w.up_sf = sf + gu;
-  ex->w.down_sf = sf + 2 * gu;
+  uint8_t* sf_down = sf + moe::mx_weight_scale_bytes(true, E, I, H);
+  ex->w.gate_up_sf = sf;
+  ex->w.down_sf = sf_down;
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
-  err = moe::launch_mx_layout_scales(gate_scales, sf, E, I, moe::mx_weight_row_blocks(true, I), H, s);
-  if (err == cudaSuccess)
-    err = moe::launch_mx_layout_scales(up_scales, sf + gu, E, I, moe::mx_weight_row_blocks(true, I), H, s);
-  if (err == cudaSuccess)
-    err = moe::launch_mx_layout_scales(down_scales, sf + 2 * gu, E, H, moe::mx_weight_row_blocks(false, H), I, s);
+  err = moe::launch_mx_layout_scales(gate_scales, up_scales, sf, E, I, H, s);
+  if (err == cudaSuccess) err = moe::launch_mx_layout_scales(down_scales, nullptr, sf_down, E, H, I, s);
   if (err != cudaSuccess) {
     delete ex;
     return api_cuda_fail(err, "moe_experts_mxfp4_create scale layout");

@@ -14,28 +14,34 @@
 // or two tokens costs N = 16, and two MMAs share each token tile (gate and up
 // rows of the same channels, or two blocks of down rows).
 //
-// A stage is 256 elements of K: one 128-byte swizzle atom per row, four
-// MMA steps of 64. Shared memory holds, per stage, two 16 KB weight tiles, the
-// token tile, and the scales in the order tcgen05.cp copies to TMEM: atoms of
-// 512 bytes, row m of 128 at byte (m % 32) * 16 + (m / 32) * 4, four scale
-// bytes (128 elements of K) each. The weights' scales were laid out this way
-// once, at the handle's creation (one 1 KB bulk copy per tile and stage);
-// the tokens' scales are row-major, because a tile may start at any row, and
-// two loader warps place their 32-bit words with cp.async.
+// A stage is 256 elements of K: one 128-byte swizzle atom per row, four MMA
+// steps of 64; shared memory holds STAGES of two 16 KB weight tiles and the
+// token tile. Scales travel apart, in a deeper ring: the MMA reads them from
+// TMEM as atoms of 128 rows x 4 bytes (128 elements of K), row m in lane
+// m % 32, column m / 32, repeated in the four 32-lane quarters. The weights'
+// scales were laid out as such atoms once, at the handle's creation (one 2 KB
+// bulk copy per stage); the tokens' scales are row-major, because a tile may
+// start at any row, and are placed word by word with cp.async.
 //
 // One persistent CTA per SM takes tiles blockIdx, blockIdx + grid, ...
-//   warp 0 lane 0   producer: TMA of weights, tokens and weight scales
-//   warp 1 lane 0   tcgen05.cp of the stage's scales to TMEM, then the MMAs
-//                   (both run in issue order); warp 1 also owns the TMEM
-//   warps 2..9      epilogue, as in experts_tc.cu
-//   warps 10..11    the tokens' scales
-// Scales in TMEM have SLOTS buffers; a buffer is rewritten only after the
-// MMAs that read it have completed (their stage's "empty" barrier).
+//   warp 0 lane 0   producer: TMA of weights and tokens
+//   warp 1 lane 0   MMAs; warp 1 also owns the TMEM
+//   warps 2..9      epilogue: accumulators to registers in fragment order,
+//                   packed in token pairs, transposed by stmatrix into token
+//                   rows, written in 64-byte runs (or quantised)
+//   warps 10..13    scales: global -> shared a few stages ahead, shared ->
+//                   TMEM by tcgen05.st into one of SLOTS buffers, rewritten
+//                   only after the MMAs that read it have completed
+// The scales go to TMEM by stores and not by tcgen05.cp because the copies
+// run on the tensor pipe in turn with the MMAs: eight a stage took 0.2 to
+// 0.3 us beside 0.29 us of MMAs (gate/up of 16384 rows, E=8, H=4096, I=14336:
+// 961 us with copies, 734 us = 5.2 PFLOP/s with stores; the loads alone take
+// 533 us, at the 64 bytes a clock an SM takes in).
 //
 // Token tiles: an expert's rows are split evenly into ceil(rows / TBN) tiles
-// of at most TBN (224: what the 512 TMEM columns hold beside the scales; 32
-// for decode, double buffered). Every wait is bounded (about a second), as in
-// experts_tc.cu.
+// of at most TBN (208: what the 512 TMEM columns hold beside three scale
+// buffers; 32 for decode, double buffered). Every wait is bounded (about a
+// second), as in experts_tc.cu.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -55,45 +61,53 @@ constexpr int ROW_BYTES = BK / 2;      // 128 B: one swizzle atom
 constexpr int A_BYTES = BM * ROW_BYTES;
 constexpr int ATOM = 512;              // scale atom: 128 rows x 4 scale bytes
 constexpr int ATOMS_K = BK / 128;      // atoms per 128 rows and stage
-constexpr int SFA_BYTES = ATOMS_K * ATOM;
+constexpr int SFA_BYTES = 2 * ATOMS_K * ATOM;  // scales of both weight tiles of a stage
 constexpr int NUM_EPI_WARPS = 8;
-constexpr int NUM_LOAD_WARPS = 2;
+constexpr int NUM_LOAD_WARPS = 4;      // each takes every fourth stage
 constexpr int FIRST_LOAD_WARP = 2 + NUM_EPI_WARPS;
 constexpr int NUM_THREADS = 32 * (2 + NUM_EPI_WARPS + NUM_LOAD_WARPS);
 constexpr int XPOSE_BYTES = 2048;      // per-warp transpose buffer: 32 tokens x 32 channels of 16 bits
-constexpr int STAGE_SMEM = 200 * 1024; // shared memory given to pipeline stages
 constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
 
 template <int TBN>
 struct MxCfg {
   static constexpr int GROUPS = (TBN + 127) / 128;           // 128-row groups of the token tile
-  static constexpr int B_BYTES = TBN * ROW_BYTES;
-  static constexpr int SFB_BYTES = GROUPS * ATOMS_K * ATOM;
-  static constexpr int STAGE_BYTES = 2 * A_BYTES + B_BYTES + 2 * SFA_BYTES + SFB_BYTES;
+  static constexpr int STAGE_BYTES = 2 * A_BYTES + TBN * ROW_BYTES;
   static constexpr int OFF_B = 2 * A_BYTES;
-  static constexpr int OFF_SFA = OFF_B + B_BYTES;
-  static constexpr int OFF_SFB = OFF_SFA + 2 * SFA_BYTES;
-  static constexpr int STAGES = STAGE_SMEM / STAGE_BYTES;
+  static constexpr int STAGES = 184 * 1024 / STAGE_BYTES;
+  static constexpr int SFB_BYTES = GROUPS * ATOMS_K * ATOM;
+  static constexpr int SF_BYTES = SFA_BYTES + SFB_BYTES;     // a stage's scales: their own, deeper ring
+  static constexpr int SF_STAGES = 24 * 1024 / SF_BYTES;
+  static constexpr int SF_AHEAD = SF_STAGES - 2;             // stages between a slot's loads and its use
   // TMEM columns: ACC accumulator buffers of (D0, D1), then SLOTS scale
   // buffers of (SFA0, SFA1, SFB), 4 columns per atom.
-  static constexpr int ACC = TBN <= 96 ? 2 : 1;
+  static constexpr int ACC = TBN <= 112 ? 2 : 1;
   static constexpr int SF_COLS = 4 * ATOMS_K * (2 + GROUPS);
   static constexpr int SF_BASE = ACC * 2 * TBN;
   static constexpr int SLOTS_FIT = (512 - SF_BASE) / SF_COLS;
-  static constexpr int SLOTS = SLOTS_FIT < STAGES ? SLOTS_FIT : STAGES;
+  static constexpr int SLOTS = SLOTS_FIT < 4 ? SLOTS_FIT : 4;
   static constexpr int COLS_USED = SF_BASE + SLOTS * SF_COLS;
   static constexpr uint32_t TMEM_COLS = COLS_USED <= 128 ? 128 : COLS_USED <= 256 ? 256 : 512;
-  static constexpr int SMEM_XPOSE = STAGES * STAGE_BYTES;
+  static constexpr int SMEM_SF = STAGES * STAGE_BYTES;
+  static constexpr int SMEM_XPOSE = SMEM_SF + SF_STAGES * SF_BYTES;
   static constexpr int SMEM_BAR = SMEM_XPOSE + NUM_EPI_WARPS * XPOSE_BYTES;
-  static constexpr int NUM_BARS = 2 * STAGES + 2 * ACC + 1;  // full, empty, tfull, tempty, drain
+  // full, empty; sf_full, sf_empty; sf_ready; tfull, tempty; drain
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * SF_STAGES + SLOTS + 2 * ACC + 1;
   static constexpr int SMEM_MISC = SMEM_BAR + 8 * NUM_BARS;  // TMEM address, abort flag
   static constexpr int SMEM_TILES = SMEM_MISC + 16;
   static constexpr int SMEM_BYTES = 1024 + SMEM_TILES + 4 * (ROUTE_MAX_E + 1);
-  static_assert(STAGE_BYTES % 1024 == 0, "stage alignment");
+  static_assert(STAGE_BYTES % 1024 == 0, "swizzle atom alignment");
   static_assert(STAGES >= 3, "pipeline depth");
-  static_assert(SLOTS >= 2, "scale buffers");
+  static_assert(SLOTS >= 2 && SLOTS <= STAGES, "a stage barrier advances only once the scale warps have passed its last phase");
+  static_assert(SF_COLS % 8 == 0, "scale stores of 8 columns");
+  static_assert(SF_AHEAD >= 1 && SF_AHEAD < SF_STAGES, "scale prefetch distance");
+  // A loader warp takes every NUM_LOAD_WARPS-th stage. Its parity wait for
+  // the ring slot of stage n + NUM_LOAD_WARPS is unambiguous only if the slot's
+  // use before the awaited one is known to be over, which its last wait (for
+  // stage n) tells it up to stage n - SF_STAGES.
+  static_assert(NUM_LOAD_WARPS <= SF_STAGES, "loader warps run at most a ring ahead");
   static_assert(COLS_USED <= 512, "TMEM columns");
-  static_assert(TBN % 32 == 0 && TBN <= 256, "token tile");
+  static_assert(TBN % 16 == 0 && TBN <= 256, "token tile");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
 
@@ -105,16 +119,16 @@ constexpr uint32_t ST_EPI_TMEM_FULL = 0x24;
 constexpr uint32_t ST_MMA_DRAIN = 0x25;
 constexpr uint32_t ST_PRODUCER_DRAIN = 0x26;
 constexpr uint32_t ST_LOADER_EMPTY = 0x27;
-constexpr uint32_t ST_MMA_SLOT = 0x28;
+constexpr uint32_t ST_SCALE_SLOT = 0x28;
+constexpr uint32_t ST_SCALE_FULL = 0x29;
+constexpr uint32_t ST_MMA_SF_READY = 0x2A;
 
 struct MxArgs {
   const uint32_t* offsets;   // [E + 1]
-  const uint8_t* sfa0;       // weight scales in atoms (gate, or down)
-  const uint8_t* sfa1;       // up, or down
+  const uint8_t* sfa;        // weight scales in atoms, [E, n_wblocks, K / 128, 2, ATOM]
   const uint8_t* sfb;        // token scales [rows_total, sfb_pitch]
   int sfb_pitch;
   int sf_blocks;             // scale bytes per token row, K / 32
-  int row_blocks;            // 128-row blocks of the weight scales per expert
   int E;
   int n_wblocks;             // weight blocks per expert (I/128, or H/256)
   int K;
@@ -126,6 +140,15 @@ struct MxArgs {
   uint8_t* q_scales;         // [rows_total, q_pitch]
   int q_pitch;
   uint32_t* status;
+};
+
+// Token rows come in boxes of 128, 64, 32 and 16 rows, the binary digits of
+// the tile's N: at most four copies a stage.
+constexpr int NUM_BOXES = 4;
+struct MxMaps {
+  CUtensorMap a0;            // gate, or down (256-row box)
+  CUtensorMap a1;            // up
+  CUtensorMap b[NUM_BOXES];
 };
 
 // Token tiles of an expert with cnt rows: ceil(cnt / TBN), each of bn rows
@@ -214,15 +237,14 @@ __device__ __forceinline__ uint32_t idesc_mxf4(int N, uint32_t sf_byte) {
          (sf_byte << 29);
 }
 
-// One 512-byte scale atom shared -> TMEM: 32 rows of 16 bytes to 32 lanes x 4
-// columns, repeated in all four 32-lane quarters.
-__device__ __forceinline__ void tmem_cp_atom(uint32_t taddr, uint32_t smem_addr) {
-  // Unswizzled descriptor: 8-row x 16-byte core matrices 128 bytes apart
-  // (stride field), version 1.
-  const uint64_t d = static_cast<uint64_t>((smem_addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128u >> 4) << 32) |
-                     (static_cast<uint64_t>(1u) << 46);
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d) : "memory");
+// Eight TMEM columns of this warp's 32 lanes (lane i of the warp writes TMEM
+// lane base + i).
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, uint4 a, uint4 b) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(a.x),
+               "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
 }
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Untiled bulk copy global -> shared, counted on `bar` (16-byte aligned).
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -237,28 +259,91 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst_smem, const void* src, u
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst_smem), "l"(src), "r"(src_bytes) : "memory");
 }
 
-// SiLU(g) = g / (1 + e^-g). 16-bit outputs: two approximate functions
-// (relative error a few 2^-22, far below the output's rounding); FP32: expf
-// and a true division.
+// SiLU(g) = g / (1 + e^-g). 16-bit outputs: the hardware's 2^x and reciprocal
+// (relative error a few 2^-22, below 2^-17 for |g| near 88: far under the
+// output's rounding); FP32: expf and a true division.
 template <typename T>
 __device__ __forceinline__ float mx_silu(float g) {
   if (std::is_same<T, float>::value) return g / (1.0f + expf(-g));
-  return __fdividef(g, 1.0f + __expf(-g));
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-1.4426950408889634f * g));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return g * r;
+}
+
+// 32 columns of 16 TMEM lanes, in the order of a matrix fragment: thread t
+// gets, for each group i of 8 columns, columns 8i + 2 (t % 4) and the next of
+// lane t / 4 (r[4i], r[4i + 1]) and of lane t / 4 + 8 (r[4i + 2], r[4i + 3]).
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit elements from fragments, each transposed:
+// element [row t / 4][2 (t % 4) ..] of matrix q goes to the 16-byte row that
+// lane 8 q + column addresses.
+__device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+               "r"(c), "r"(d)
+               : "memory");
+}
+
+// One token's block of 32 channels, read from shared memory as 16-byte runs
+// (run(q): its address), quantised and written as 16 bytes of codes and one
+// scale byte (with the row's pad bytes after its last block).
+template <typename T, typename Run>
+__device__ __forceinline__ void quantize_token(Run run, uint8_t* codes, uint8_t* scale_row, int64_t blk, int pitch,
+                                               bool last_block) {
+  constexpr int RUNS = 32 * static_cast<int>(sizeof(T)) / 16;
+  constexpr int EPR = 16 / static_cast<int>(sizeof(T));
+  float v[32];
+  uint32_t amax = 0;
+#pragma unroll
+  for (int q = 0; q < RUNS; ++q) {
+    const uint4 raw = *reinterpret_cast<const uint4*>(run(q));
+    const T* e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+    for (int i = 0; i < EPR; ++i) {
+      v[q * EPR + i] = to_f32(e[i]);
+      amax = max(amax, __float_as_uint(v[q * EPR + i]) & 0x7FFFFFFFu);
+    }
+  }
+  const uint32_t byte = mx_scale_byte(amax);
+  const float s = mx_inv_scale(byte);
+  uint32_t w[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float e8[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) e8[i] = v[q * 8 + i] * s;
+    w[q] = byte == 255u ? 0u : mx_pack8(e8);
+  }
+  *reinterpret_cast<uint4*>(codes) = make_uint4(w[0], w[1], w[2], w[3]);
+  scale_row[blk] = static_cast<uint8_t>(byte);
+  if (last_block)
+    for (int p = static_cast<int>(blk) + 1; p < pitch; ++p) scale_row[p] = 0;
 }
 
 template <typename T, bool GATE_UP, int TBN>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
-    experts_mx_kernel(const __grid_constant__ CUtensorMap tm_a0, const __grid_constant__ CUtensorMap tm_a1,
-                      const __grid_constant__ CUtensorMap tm_b128, const __grid_constant__ CUtensorMap tm_b16,
-                      const MxArgs args) {
+    experts_mx_kernel(const __grid_constant__ MxMaps maps, const __grid_constant__ MxArgs args) {
   using C = MxCfg<TBN>;
   constexpr int STAGES = C::STAGES;
   constexpr int ACC = C::ACC;
+  constexpr int SF_STAGES = C::SF_STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::SMEM_BAR);
   uint64_t* empty = full + STAGES;
-  uint64_t* tfull = empty + STAGES;   // [ACC]
+  uint64_t* sf_full = empty + STAGES;
+  uint64_t* sf_empty = sf_full + SF_STAGES;
+  uint64_t* sf_ready = sf_empty + SF_STAGES;  // [SLOTS]
+  uint64_t* tfull = sf_ready + C::SLOTS;      // [ACC]
   uint64_t* tempty = tfull + ACC;     // [ACC]
   uint64_t* drain = tempty + ACC;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::SMEM_MISC);
@@ -270,9 +355,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1 + 32 * NUM_LOAD_WARPS);  // the producer's expect_tx and each loader thread's copies
+      mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
+    for (int s = 0; s < SF_STAGES; ++s) {
+      mbar_init(&sf_full[s], 1 + 32);  // the expect_tx of the weights' atoms, and each lane's copies of the tokens' words
+      mbar_init(&sf_empty[s], NUM_LOAD_WARPS);
+    }
+    for (int s = 0; s < C::SLOTS; ++s) mbar_init(&sf_ready[s], NUM_LOAD_WARPS);
     for (int a = 0; a < ACC; ++a) {
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], NUM_EPI_WARPS);
@@ -281,10 +371,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     *abort_flag = 0;
     fence_mbarrier_init();
     fence_proxy_async_smem();
-    tma_prefetch_desc(&tm_a0);
-    tma_prefetch_desc(&tm_a1);
-    tma_prefetch_desc(&tm_b128);
-    tma_prefetch_desc(&tm_b16);
+    tma_prefetch_desc(&maps.a0);
+    if (GATE_UP) tma_prefetch_desc(&maps.a1);
+    for (int i = 0; i < NUM_BOXES; ++i) tma_prefetch_desc(&maps.b[i]);
   }
   __syncwarp();
   if (warp == 1) {
@@ -301,6 +390,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // The cap keeps a corrupt offsets array from producing an endless tile loop.
   const uint32_t total = min(tile_start[args.E], args.tile_cap);
   const int k_blocks = (args.K + BK - 1) / BK;
+  const int k_words = (args.K + 127) / 128;  // 32-bit scale words of a row
 
   if (warp == 0) {
     // ------------------------------------------------------------ producer
@@ -311,14 +401,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       bool ok = true;
       for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
         const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, args.offsets);
-        const int n128 = tc.n_tok >> 7;
-        const int n16 = (tc.n_tok & 127) >> 4;
-        const uint32_t tx = static_cast<uint32_t>(2 * A_BYTES + 2 * SFA_BYTES + tc.n_tok * ROW_BYTES);
-        const int rb0 = GATE_UP ? tc.w : 2 * tc.w;
-        const int rb1 = GATE_UP ? tc.w : 2 * tc.w + 1;
-        const int64_t sf_expert = static_cast<int64_t>(tc.e) * args.row_blocks;
-        const uint8_t* s0 = args.sfa0 + (sf_expert + rb0) * k_blocks * SFA_BYTES;
-        const uint8_t* s1 = args.sfa1 + (sf_expert + rb1) * k_blocks * SFA_BYTES;
+        const uint32_t tx = static_cast<uint32_t>(2 * A_BYTES + tc.n_tok * ROW_BYTES);
+        const int row = tc.w * (GATE_UP ? BM : 2 * BM);
         for (int kb = 0; kb < k_blocks; ++kb) {
           if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, args.status, ST_PRODUCER_EMPTY,
                                  WAIT_LIMIT_NS)) {
@@ -328,16 +412,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           uint8_t* st = smem + stage * C::STAGE_BYTES;
           const int k0 = kb * ROW_BYTES;
           mbar_arrive_expect_tx(&full[stage], tx);
-          tma_load_3d(st, &tm_a0, &full[stage], k0, rb0 * BM, tc.e);
-          tma_load_3d(st + A_BYTES, &tm_a1, &full[stage], k0, rb1 * BM, tc.e);
-          bulk_load(st + C::OFF_SFA, s0 + static_cast<int64_t>(kb) * SFA_BYTES, SFA_BYTES, &full[stage]);
-          bulk_load(st + C::OFF_SFA + SFA_BYTES, s1 + static_cast<int64_t>(kb) * SFA_BYTES, SFA_BYTES, &full[stage]);
+          tma_load_3d(st, &maps.a0, &full[stage], k0, row, tc.e);  // down: both 128-row blocks in one box
+          if (GATE_UP) tma_load_3d(st + A_BYTES, &maps.a1, &full[stage], k0, row, tc.e);
           uint8_t* b_dst = st + C::OFF_B;
           int r = 0;
-          for (int b = 0; b < n128; ++b, r += 128)
-            tma_load_2d(b_dst + r * ROW_BYTES, &tm_b128, &full[stage], k0, static_cast<int>(tc.row0) + r);
-          for (int b = 0; b < n16; ++b, r += 16)
-            tma_load_2d(b_dst + r * ROW_BYTES, &tm_b16, &full[stage], k0, static_cast<int>(tc.row0) + r);
+#pragma unroll
+          for (int i = 0; i < NUM_BOXES; ++i) {  // 128, 64, 32, 16 rows: the binary digits of n_tok
+            if ((tc.n_tok & (128 >> i)) != 0) {
+              tma_load_2d(b_dst + r * ROW_BYTES, &maps.b[i], &full[stage], k0, static_cast<int>(tc.row0) + r);
+              r += 128 >> i;
+            }
+          }
           ++issued;
           if (++stage == STAGES) {
             stage = 0;
@@ -361,50 +446,32 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     // ------------------------------------------------------------ scales to TMEM, MMAs
     if (lane == 0) {
       uint32_t n = 0;  // stages consumed
-      bool ok = true;
       uint32_t it = 0;
+      bool ok = true;
       for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++it) {
         const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, args.offsets);
         const uint32_t idesc0 = idesc_mxf4(tc.n_tok, 0), idesc2 = idesc_mxf4(tc.n_tok, 2);
-        const int groups = (tc.n_tok + 127) >> 7;
         const uint32_t acc = it % ACC;
         if (!mbar_wait_bounded(&tempty[acc], ((it / ACC) & 1u) ^ 1u, abort_flag, args.status, ST_MMA_TMEM_EMPTY,
                                WAIT_LIMIT_NS)) {
           ok = false;
           break;
         }
-        tc_fence_after();
         const uint32_t d0 = tmem_base + acc * (2 * TBN);
         for (int kb = 0; kb < k_blocks; ++kb, ++n) {
-          const uint32_t stage = n % STAGES;
+          const uint32_t stage = n % STAGES, slot = n % C::SLOTS;
           if (!mbar_wait_bounded(&full[stage], (n / STAGES) & 1u, abort_flag, args.status, ST_MMA_FULL,
+                                 WAIT_LIMIT_NS) ||
+              !mbar_wait_bounded(&sf_ready[slot], (n / C::SLOTS) & 1u, abort_flag, args.status, ST_MMA_SF_READY,
                                  WAIT_LIMIT_NS)) {
             ok = false;
             break;
           }
-          if (C::SLOTS < STAGES && n >= static_cast<uint32_t>(C::SLOTS)) {
-            // The scale buffer's previous readers: the MMAs of stage n - SLOTS.
-            const uint32_t p = n - C::SLOTS;
-            if (!mbar_wait_bounded(&empty[p % STAGES], (p / STAGES) & 1u, abort_flag, args.status, ST_MMA_SLOT,
-                                   WAIT_LIMIT_NS)) {
-              ok = false;
-              break;
-            }
-          }
-          fence_proxy_async_smem();  // the loaders' cp.async (generic proxy) before tcgen05.cp
           tc_fence_after();
-          const uint32_t st = smem_u32(smem + stage * C::STAGE_BYTES);
-          const uint32_t sf = tmem_base + C::SF_BASE + (n % C::SLOTS) * C::SF_COLS;
+          const uint32_t sf = tmem_base + C::SF_BASE + slot * C::SF_COLS;
           const uint32_t sfb = sf + 8 * ATOMS_K;
-#pragma unroll
-          for (int a = 0; a < ATOMS_K; ++a) {
-            tmem_cp_atom(sf + 4 * a, st + C::OFF_SFA + a * ATOM);
-            tmem_cp_atom(sf + 4 * ATOMS_K + 4 * a, st + C::OFF_SFA + SFA_BYTES + a * ATOM);
-            for (int g = 0; g < groups; ++g)
-              tmem_cp_atom(sfb + 4 * (a * C::GROUPS + g), st + C::OFF_SFB + (a * C::GROUPS + g) * ATOM);
-          }
           const int left = args.K - kb * BK;  // MMA steps wholly past K are left out
-          const uint32_t a0 = st, a1 = st + A_BYTES, b = st + C::OFF_B;
+          const uint32_t a0 = smem_u32(smem + stage * C::STAGE_BYTES), a1 = a0 + A_BYTES, b = a0 + C::OFF_B;
 #pragma unroll
           for (int k = 0; k < BK / UMMA_K; ++k) {
             if (k * UMMA_K < left) {
@@ -429,12 +496,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncwarp();
   } else if (warp < FIRST_LOAD_WARP) {
     // ------------------------------------------------------------ epilogue
-    constexpr int TOK = XPOSE_BYTES / (32 * static_cast<int>(sizeof(T)));  // tokens per transpose: 32, or 16 for FP32
     const int ew = warp - 2;
     const int quad = warp & 3;                  // TMEM lanes 32*quad ..
     const int half = ew >> 2;                   // takes 32-token chunks half, half+2, ...
     uint8_t* xp = smem + C::SMEM_XPOSE + ew * XPOSE_BYTES;
-    T* xt = reinterpret_cast<T*>(xp);
+    const uint32_t xp_u32 = smem_u32(xp);
     uint32_t it = 0;
     for (uint32_t tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
       const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, args.offsets);
@@ -445,107 +511,103 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       tc_fence_after();
       const uint32_t t_lane = tmem_base + acc * (2 * TBN) + (static_cast<uint32_t>(quad * 32) << 16);
       const int64_t colA = static_cast<int64_t>(tc.w) * (GATE_UP ? BM : 2 * BM) + quad * 32;
+      // Rows of the tile that exist in the buffers (all of them, for valid offsets).
+      const int live = tc.row0 < args.rows_total
+                           ? static_cast<int>(min(static_cast<uint32_t>(tc.rows), args.rows_total - tc.row0)) : 0;
       for (int c0 = 32 * half; c0 < tc.n_tok; c0 += 64) {
-        uint32_t v0[32], v1[32];
-        tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(c0), v0);
-        tmem_ld_32x32b_x32(t_lane + TBN + static_cast<uint32_t>(c0), v1);
-        tmem_ld_wait();
+        if constexpr (sizeof(T) == 2) {
+          // Fragments of 16 channels x 32 tokens, packed in token pairs and
+          // transposed by stmatrix into token rows of 32 channels (64 bytes,
+          // 16-byte runs swizzled by the token so that the stores and both
+          // kinds of reads below are free of bank conflicts).
+          uint32_t f0[2][16], f1[2][16];
 #pragma unroll
-        for (int blk = 0; blk < (GATE_UP ? 1 : 2); ++blk) {
-          const int64_t col0 = colA + blk * BM;
-          const bool col_ok = col0 < args.n_out;  // n_out is a multiple of 32: the warp's block is in or out
+          for (int h = 0; h < 2; ++h) {
+            tmem_ld_16x256b_x4(t_lane + (static_cast<uint32_t>(16 * h) << 16) + static_cast<uint32_t>(c0), f0[h]);
+            tmem_ld_16x256b_x4(t_lane + (static_cast<uint32_t>(16 * h) << 16) + static_cast<uint32_t>(TBN + c0),
+                               f1[h]);
+          }
+          tmem_ld_wait();
 #pragma unroll
-          for (int t0 = 0; t0 < 32; t0 += TOK) {
-            // Lane = output channel, register = token: write token rows.
+          for (int blk = 0; blk < (GATE_UP ? 1 : 2); ++blk) {
+            const int64_t col0 = colA + blk * BM;
+            const bool col_ok = col0 < args.n_out;  // n_out is a multiple of 32: the warp's block is in or out
 #pragma unroll
-            for (int j = 0; j < TOK; ++j) {
-              float val;
-              if (GATE_UP) val = mx_silu<T>(__uint_as_float(v0[t0 + j])) * __uint_as_float(v1[t0 + j]);
-              else val = __uint_as_float(blk == 0 ? v0[t0 + j] : v1[t0 + j]);
-              xt[j * 32 + lane] = from_f32<T>(val);
+            for (int i = 0; i < 4; ++i) {
+              uint32_t m[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int r = 4 * i + 2 * (q & 1);
+                const float a0 = __uint_as_float(f0[q >> 1][r]), a1 = __uint_as_float(f0[q >> 1][r + 1]);
+                const float b0 = __uint_as_float(f1[q >> 1][r]), b1 = __uint_as_float(f1[q >> 1][r + 1]);
+                if (GATE_UP) m[q] = pack2<T>(mx_silu<T>(a0) * b0, mx_silu<T>(a1) * b1);
+                else m[q] = blk == 0 ? pack2<T>(a0, a1) : pack2<T>(b0, b1);
+              }
+              const int tok = 8 * i + (lane & 7);
+              stmatrix_x4_trans(xp_u32 + static_cast<uint32_t>(tok * 64 + (((lane >> 3) ^ (tok >> 1)) & 3) * 16), m[0],
+                                m[1], m[2], m[3]);
             }
             __syncwarp();
-            if (args.out != nullptr) {
-              constexpr int PARTS = 32 * static_cast<int>(sizeof(T)) / 16;  // 16-byte runs per token row
-              constexpr int TPP = 32 / PARTS;                               // tokens per pass
-              const int part = lane % PARTS;
+            if (args.out != nullptr && col_ok) {
+              const int part = lane & 3;
 #pragma unroll
-              for (int p = 0; p < TOK / TPP; ++p) {
-                const int j = p * TPP + lane / PARTS;
-                const uint4 row = *reinterpret_cast<const uint4*>(xp + (j * PARTS + part) * 16);
-                const int t_in = c0 + t0 + j;
-                if (t_in < tc.rows && tc.row0 + static_cast<uint32_t>(t_in) < args.rows_total && col_ok) {
-                  T* dst = static_cast<T*>(args.out) + (static_cast<int64_t>(tc.row0) + t_in) * args.n_out + col0;
+              for (int p = 0; p < 4; ++p) {
+                const int j = p * 8 + (lane >> 2);
+                if (c0 + j < live) {
+                  const uint4 row = *reinterpret_cast<const uint4*>(xp + j * 64 + ((part ^ (j >> 1)) & 3) * 16);
+                  T* dst = static_cast<T*>(args.out) + (static_cast<int64_t>(tc.row0) + c0 + j) * args.n_out + col0;
                   reinterpret_cast<uint4*>(dst)[part] = row;
                 }
               }
             }
-            if (GATE_UP && args.q_codes != nullptr) {
-              // One lane per token: its 32 channels are one block. The
-              // 16-byte runs are read in a lane-rotated order so that a
-              // quarter-warp's reads fall into different banks.
-              const int j = lane % TOK;
-              float v[32];
-              uint32_t amax = 0;
-              constexpr int RUNS = 32 * static_cast<int>(sizeof(T)) / 16;
-              constexpr int EPR = 16 / static_cast<int>(sizeof(T));
-#pragma unroll
-              for (int q = 0; q < RUNS; ++q) {
-                const int run = sizeof(T) == 2 ? ((q + (j >> 1)) & (RUNS - 1)) : ((q + j) & (RUNS - 1));
-                const uint4 raw = *reinterpret_cast<const uint4*>(xp + (j * RUNS + run) * 16);
-                const T* e = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-                for (int i = 0; i < EPR; ++i) {
-                  v[q * EPR + i] = to_f32(e[i]);
-                  amax = max(amax, __float_as_uint(v[q * EPR + i]) & 0x7FFFFFFFu);
-                }
-              }
-              const uint32_t byte = mx_scale_byte(amax);
-              const float s = mx_inv_scale(byte);
-              uint32_t w[4];
-              // v[8q ..] holds elements 8 ((q + rot) % 4) .. of the token
-              // (FP32: runs of 4, rotated by an even or odd number of them).
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                float e8[8];
-#pragma unroll
-                for (int i = 0; i < 8; ++i) e8[i] = v[q * 8 + i] * s;
-                w[q] = byte == 255u ? 0u : mx_pack8(e8);
-              }
-              uint32_t o[4];
-              if (sizeof(T) == 2) {
-                const int rot = (j >> 1) & 3;
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {  // word d was read at step (d - rot) % 4
-                  const int q = (d - rot) & 3;
-                  o[d] = q == 0 ? w[0] : q == 1 ? w[1] : q == 2 ? w[2] : w[3];
-                }
-              } else {
-                // 16-bit halves: half h (4 elements) was read at step (h - j) % 8.
-#pragma unroll
-                for (int d = 0; d < 4; ++d) {
-                  uint32_t lo = 0, hi = 0;
-#pragma unroll
-                  for (int q = 0; q < 8; ++q) {
-                    const uint32_t hw = (w[q >> 1] >> (16 * (q & 1))) & 0xFFFFu;
-                    if (q == ((2 * d - j) & 7)) lo = hw;
-                    if (q == ((2 * d + 1 - j) & 7)) hi = hw;
-                  }
-                  o[d] = lo | (hi << 16);
-                }
-              }
-              const int t_in = c0 + t0 + j;
-              if (lane < TOK && t_in < tc.rows && tc.row0 + static_cast<uint32_t>(t_in) < args.rows_total && col_ok) {
-                const int64_t r = static_cast<int64_t>(tc.row0) + t_in;
-                *reinterpret_cast<uint4*>(args.q_codes + r * (args.n_out / 2) + col0 / 2) =
-                    make_uint4(o[0], o[1], o[2], o[3]);
-                uint8_t* sp = args.q_scales + r * args.q_pitch;
-                sp[col0 / MX_BLOCK] = static_cast<uint8_t>(byte);
-                if (col0 + MX_BLOCK >= args.n_out)
-                  for (int p = static_cast<int>(col0 / MX_BLOCK) + 1; p < args.q_pitch; ++p) sp[p] = 0;
-              }
+            if (GATE_UP && args.q_codes != nullptr && col_ok && c0 + lane < live) {
+              const int64_t r = static_cast<int64_t>(tc.row0) + c0 + lane;
+              quantize_token<T>([&](int q) { return xp + lane * 64 + ((q ^ (lane >> 1)) & 3) * 16; },
+                                args.q_codes + r * (args.n_out / 2) + col0 / 2, args.q_scales + r * args.q_pitch,
+                                col0 / MX_BLOCK, args.q_pitch, col0 + MX_BLOCK >= args.n_out);
             }
             __syncwarp();
+          }
+        } else {
+          // FP32: lane = output channel, register = token, 16 tokens at a
+          // time through the buffer.
+          uint32_t v0[32], v1[32];
+          tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(c0), v0);
+          tmem_ld_32x32b_x32(t_lane + TBN + static_cast<uint32_t>(c0), v1);
+          tmem_ld_wait();
+          float* xf = reinterpret_cast<float*>(xp);
+#pragma unroll
+          for (int blk = 0; blk < (GATE_UP ? 1 : 2); ++blk) {
+            const int64_t col0 = colA + blk * BM;
+            const bool col_ok = col0 < args.n_out;
+#pragma unroll
+            for (int t0 = 0; t0 < 32; t0 += 16) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const float a = __uint_as_float(v0[t0 + j]), b = __uint_as_float(v1[t0 + j]);
+                xf[j * 32 + lane] = GATE_UP ? mx_silu<T>(a) * b : (blk == 0 ? a : b);
+              }
+              __syncwarp();
+              if (args.out != nullptr && col_ok) {
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                  const int j = p * 4 + (lane >> 3);
+                  if (c0 + t0 + j < live) {
+                    T* dst = static_cast<T*>(args.out) + (static_cast<int64_t>(tc.row0) + c0 + t0 + j) * args.n_out +
+                             col0;
+                    reinterpret_cast<uint4*>(dst)[lane & 7] =
+                        *reinterpret_cast<const uint4*>(xf + j * 32 + (lane & 7) * 4);
+                  }
+                }
+              }
+              if (GATE_UP && args.q_codes != nullptr && col_ok && lane < 16 && c0 + t0 + lane < live) {
+                const int64_t r = static_cast<int64_t>(tc.row0) + c0 + t0 + lane;
+                quantize_token<T>([&](int q) { return xp + lane * 128 + q * 16; },
+                                  args.q_codes + r * (args.n_out / 2) + col0 / 2, args.q_scales + r * args.q_pitch,
+                                  col0 / MX_BLOCK, args.q_pitch, col0 + MX_BLOCK >= args.n_out);
+              }
+              __syncwarp();
+            }
           }
         }
       }
@@ -554,39 +616,105 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (lane == 0) mbar_arrive(&tempty[acc]);
     }
   } else {
-    // ------------------------------------------------------------ the tokens' scales
-    // Word a of token n (its four scale bytes for K elements 256 kb + 128 a
-    // ..) goes to atom (a, n / 128). Bytes past K / 32 and rows past the tile
-    // are filled with 0, never read.
-    const int lt = threadIdx.x - 32 * FIRST_LOAD_WARP;   // 0 .. 63
-    uint32_t n = 0;
-    for (uint32_t tile = blockIdx.x; tile < total; tile += gridDim.x) {
-      const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, args.offsets);
-      bool ok = true;
-      for (int kb = 0; kb < k_blocks; ++kb, ++n) {
-        const uint32_t stage = n % STAGES;
-        ok = mbar_wait_bounded(&empty[stage], ((n / STAGES) & 1u) ^ 1u, abort_flag, args.status, ST_LOADER_EMPTY,
-                               WAIT_LIMIT_NS);
-        if (!__all_sync(FULL_MASK, ok)) {
-          ok = false;
-          break;
+    // ------------------------------------------------------------ scales
+    // Global -> shared, SF_AHEAD stages before use: warp lw fills the ring
+    // slots of stages lw, lw + NUM_LOAD_WARPS, ...: lane 0 with one bulk copy
+    // of the weights' atoms, all lanes with the tokens' words. Word a of token
+    // t (its four scale bytes for K elements 256 kb + 128 a ..) goes to atom
+    // (a, t / 128); bytes past K / 32 and rows past the tile are filled with
+    // 0, never read. Shared -> TMEM: each warp writes its 32 lanes' quarter of
+    // every stage's scale buffer (the MMA wants the atoms' 32 rows repeated
+    // in the four quarters).
+    const uint32_t lw = static_cast<uint32_t>(warp - FIRST_LOAD_WARP);
+    const uint32_t quad_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    // The load side walks the same tiles as the use side, SF_AHEAD stages on.
+    uint32_t ln = 0, ltile = blockIdx.x;  // next stage to load, its tile
+    int lkb = 0;
+    MxTile ltc{};
+    if (ltile < total) ltc = decode_mx_tile<TBN>(ltile, tile_start, args.E, args.n_wblocks, args.offsets);
+    auto load_next = [&]() -> bool {
+      if (ltile >= total) return true;
+      if (ln % NUM_LOAD_WARPS == lw) {
+        const uint32_t ss = ln % SF_STAGES;
+        const bool got = mbar_wait_bounded(&sf_empty[ss], ((ln / SF_STAGES) & 1u) ^ 1u, abort_flag, args.status,
+                                           ST_LOADER_EMPTY, WAIT_LIMIT_NS);
+        if (!__all_sync(FULL_MASK, got)) return false;
+        uint8_t* slot = smem + C::SMEM_SF + ss * C::SF_BYTES;
+        if (lane == 0) {
+          // The last stage may hold fewer atoms than the others (the MMA
+          // steps past K are left out).
+          const uint8_t* sfa =
+              args.sfa + (static_cast<int64_t>(ltc.e) * args.n_wblocks + ltc.w) * k_words * (2 * ATOM);
+          const uint32_t bytes = static_cast<uint32_t>(min(ATOMS_K, k_words - lkb * ATOMS_K)) * (2 * ATOM);
+          mbar_arrive_expect_tx(&sf_full[ss], bytes);
+          bulk_load(slot, sfa + static_cast<int64_t>(lkb) * SFA_BYTES, bytes, &sf_full[ss]);
         }
-        const uint32_t sfb = smem_u32(smem + stage * C::STAGE_BYTES + C::OFF_SFB);
-        for (int i = lt; i < tc.n_tok * ATOMS_K; i += 32 * NUM_LOAD_WARPS) {
+        const uint32_t sfb = smem_u32(slot) + SFA_BYTES;
+#pragma unroll 4
+        for (int i = lane; i < ltc.n_tok * ATOMS_K; i += 32) {
           const int tok = i / ATOMS_K, a = i % ATOMS_K;
           const uint32_t dst = sfb + static_cast<uint32_t>((a * C::GROUPS + (tok >> 7)) * ATOM + (tok & 31) * 16 +
                                                            ((tok >> 5) & 3) * 4);
-          const int byte0 = (kb * ATOMS_K + a) * 4;
+          const int byte0 = (lkb * ATOMS_K + a) * 4;
           int valid = args.sf_blocks - byte0;
           valid = valid < 0 ? 0 : valid > 4 ? 4 : valid;
-          const uint32_t row = tc.row0 + static_cast<uint32_t>(tok);
-          if (tok >= tc.rows || row >= args.rows_total) valid = 0;
+          const uint32_t row = ltc.row0 + static_cast<uint32_t>(tok);
+          if (tok >= ltc.rows || row >= args.rows_total) valid = 0;
           const uint8_t* src = valid > 0 ? args.sfb + static_cast<int64_t>(row) * args.sfb_pitch + byte0 : args.sfb;
           cp_async_4(dst, src, static_cast<uint32_t>(valid));
         }
-        cp_async_mbar_arrive_noinc(&full[stage]);
+        cp_async_mbar_arrive_noinc(&sf_full[ss]);
       }
-      if (!ok) break;
+      ++ln;
+      if (++lkb == k_blocks) {
+        lkb = 0;
+        ltile += gridDim.x;
+        if (ltile < total) ltc = decode_mx_tile<TBN>(ltile, tile_start, args.E, args.n_wblocks, args.offsets);
+      }
+      return true;
+    };
+    bool ok = true;
+    for (int i = 0; ok && i < C::SF_AHEAD; ++i) ok = load_next();
+    uint32_t n = 0;
+    for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      for (int kb = 0; ok && kb < k_blocks; ++kb, ++n) {
+        ok = load_next();
+        if (!ok) break;
+        const uint32_t ss = n % SF_STAGES;
+        ok = mbar_wait_bounded(&sf_full[ss], (n / SF_STAGES) & 1u, abort_flag, args.status, ST_SCALE_FULL,
+                               WAIT_LIMIT_NS);
+        ok = __all_sync(FULL_MASK, ok);
+        if (!ok) break;
+        // Atoms in the order of the buffer's columns: SFA0 and SFA1 by K
+        // atom (they lie interleaved), then SFB.
+        const uint8_t* slot = smem + C::SMEM_SF + ss * C::SF_BYTES + lane * 16;
+        uint4 v[C::SF_COLS / 4];
+#pragma unroll
+        for (int a = 0; a < ATOMS_K; ++a) {
+          v[a] = *reinterpret_cast<const uint4*>(slot + 2 * a * ATOM);
+          v[ATOMS_K + a] = *reinterpret_cast<const uint4*>(slot + (2 * a + 1) * ATOM);
+        }
+#pragma unroll
+        for (int i = 2 * ATOMS_K; i < C::SF_COLS / 4; ++i) v[i] = *reinterpret_cast<const uint4*>(slot + i * ATOM);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sf_empty[ss]);
+        if (n >= static_cast<uint32_t>(C::SLOTS)) {
+          // The buffer's last readers: the MMAs of stage n - SLOTS.
+          const uint32_t p = n - C::SLOTS;
+          ok = mbar_wait_bounded(&empty[p % STAGES], (p / STAGES) & 1u, abort_flag, args.status, ST_SCALE_SLOT,
+                                 WAIT_LIMIT_NS);
+          ok = __all_sync(FULL_MASK, ok);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        const uint32_t sf = tmem_base + C::SF_BASE + (n % C::SLOTS) * C::SF_COLS + quad_lane;
+#pragma unroll
+        for (int i = 0; i < C::SF_COLS / 8; ++i) tmem_st_32x32b_x8(sf + 8 * i, v[2 * i], v[2 * i + 1]);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sf_ready[n % C::SLOTS]);
+      }
     }
     cp_async_wait_all();  // no copy may land after the block has exited
   }
@@ -615,7 +743,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn_mx() {
   return fn;
 }
 
-// [E, rows, row_bytes] codes, box 128 bytes x box_rows x 1.
+// [E, rows, row_bytes] codes, box 128 bytes (one swizzle atom) x box_rows x 1.
 bool encode_codes(CUtensorMap* m, const void* ptr, uint64_t row_bytes, uint64_t rows, uint64_t E, uint32_t box_rows,
                   int rank) {
   auto fn = encode_fn_mx();
@@ -630,8 +758,7 @@ bool encode_codes(CUtensorMap* m, const void* ptr, uint64_t row_bytes, uint64_t 
 }
 
 template <typename T, bool GATE_UP, int TBN>
-cudaError_t launch_mx(const CUtensorMap& a0, const CUtensorMap& a1, const CUtensorMap& b128, const CUtensorMap& b16,
-                      MxArgs args, int64_t rows, int num_sms, cudaStream_t stream) {
+cudaError_t launch_mx(const MxMaps& maps, MxArgs args, int64_t rows, int num_sms, cudaStream_t stream) {
   auto kern = experts_mx_kernel<T, GATE_UP, TBN>;
   constexpr int SMEM_BYTES = MxCfg<TBN>::SMEM_BYTES;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
@@ -640,47 +767,52 @@ cudaError_t launch_mx(const CUtensorMap& a0, const CUtensorMap& a1, const CUtens
   const int64_t cap = (rows / TBN + (rows < args.E ? rows : args.E)) * args.n_wblocks;
   args.tile_cap = static_cast<uint32_t>(cap < 0xFFFFFFFFll ? cap : 0xFFFFFFFFll);
   const int grid = static_cast<int>(cap < num_sms ? cap : num_sms);
-  return launch_dependent(kern, dim3(grid), dim3(NUM_THREADS), SMEM_BYTES, stream, a0, a1, b128, b16, args);
+  return launch_dependent(kern, dim3(grid), dim3(NUM_THREADS), SMEM_BYTES, stream, maps, args);
+}
+
+// What a launch needs beside MxArgs: the operands' pointers for its maps.
+struct MxOperands {
+  bool gate_up;
+  const void* w0;      // gate or down codes [E, N, K / 2]
+  const void* w1;      // up codes
+  const void* tokens;  // [rows, K / 2]
+};
+
+template <typename T, int TBN>
+cudaError_t stage_n(const MxOperands& op, const MxArgs& args, int64_t rows, int num_sms, cudaStream_t stream,
+                    const char** why) {
+  const uint64_t kb = static_cast<uint64_t>(args.K / 2), N = static_cast<uint64_t>(args.n_out);
+  const uint64_t E = static_cast<uint64_t>(args.E);
+  MxMaps maps;
+  bool ok = encode_codes(&maps.a0, op.w0, kb, N, E, op.gate_up ? BM : 2 * BM, 3);
+  maps.a1 = maps.a0;
+  if (op.gate_up) ok = ok && encode_codes(&maps.a1, op.w1, kb, N, E, BM, 3);
+  for (int i = 0; i < NUM_BOXES; ++i)
+    ok = ok && encode_codes(&maps.b[i], op.tokens, kb, static_cast<uint64_t>(rows), 1, 128u >> i, 2);
+  if (!ok) {
+    *why = "cuTensorMapEncodeTiled rejected a tensor map";
+    return cudaErrorInvalidValue;
+  }
+  return op.gate_up ? launch_mx<T, true, TBN>(maps, args, rows, num_sms, stream)
+                    : launch_mx<T, false, TBN>(maps, args, rows, num_sms, stream);
 }
 
 template <typename T>
-cudaError_t stage_t(const MxWeights& w, bool gate_up, const CUtensorMap& b128, const CUtensorMap& b16,
-                    const MxArgs& args, int64_t rows, int num_sms, cudaStream_t stream) {
-  // Decode-sized batches (at most 8 rows per expert on average) take
-  // 32-token tiles: more weight bytes in flight and double-buffered
-  // accumulators; larger ones 224-token tiles, which read each weight tile
-  // for seven times the tokens.
-  const bool small = rows <= 8 * static_cast<int64_t>(args.E);
-  if (gate_up)
-    return small ? launch_mx<T, true, 32>(w.gate, w.up, b128, b16, args, rows, num_sms, stream)
-                 : launch_mx<T, true, 224>(w.gate, w.up, b128, b16, args, rows, num_sms, stream);
-  return small ? launch_mx<T, false, 32>(w.down, w.down, b128, b16, args, rows, num_sms, stream)
-               : launch_mx<T, false, 224>(w.down, w.down, b128, b16, args, rows, num_sms, stream);
+cudaError_t stage_t(const MxOperands& op, const MxArgs& args, int64_t rows, int num_sms, cudaStream_t stream,
+                    const char** why) {
+  if (rows <= 8 * static_cast<int64_t>(args.E)) return stage_n<T, 32>(op, args, rows, num_sms, stream, why);
+  return stage_n<T, 208>(op, args, rows, num_sms, stream, why);
 }
 
 }  // namespace
 
-int64_t mx_weight_row_blocks(bool gate_up, int64_t R) {
-  return gate_up ? (R + BM - 1) / BM : (R + 2 * BM - 1) / (2 * BM) * 2;
-}
+// Weight blocks per expert of a stage: 128 gate and 128 up rows, or 256 down
+// rows; each has two 128-row atoms' worth of scales per K block.
+int64_t mx_weight_blocks(bool gate_up, int64_t R) { return gate_up ? (R + BM - 1) / BM : (R + 2 * BM - 1) / (2 * BM); }
 
 size_t mx_weight_scale_bytes(bool gate_up, int64_t E, int64_t R, int64_t K) {
-  return static_cast<size_t>(E) * static_cast<size_t>(mx_weight_row_blocks(gate_up, R)) *
-         static_cast<size_t>((K + BK - 1) / BK) * SFA_BYTES;
-}
-
-bool mx_encode_weights(const void* gate, const void* up, const void* down, int64_t E, int64_t H, int64_t I,
-                       MxWeights* out, const char** why) {
-  if (encode_fn_mx() == nullptr) {
-    *why = "the CUDA driver does not provide cuTensorMapEncodeTiled";
-    return false;
-  }
-  if (!encode_codes(&out->gate, gate, H / 2, I, E, BM, 3) || !encode_codes(&out->up, up, H / 2, I, E, BM, 3) ||
-      !encode_codes(&out->down, down, I / 2, H, E, BM, 3)) {
-    *why = "cuTensorMapEncodeTiled rejected an expert weight tensor map";
-    return false;
-  }
-  return true;
+  return static_cast<size_t>(E) * static_cast<size_t>(mx_weight_blocks(gate_up, R)) *
+         static_cast<size_t>((K + 127) / 128) * (2 * ATOM);
 }
 
 cudaError_t launch_experts_mx(const MxWeights& w, bool gate_up, const void* codes, const void* scales,
@@ -690,23 +822,16 @@ cudaError_t launch_experts_mx(const MxWeights& w, bool gate_up, const void* code
   if (rows == 0) return cudaSuccess;
   const int64_t K = gate_up ? H : I;
   const int64_t N = gate_up ? I : H;
-  CUtensorMap b128, b16;
-  if (!encode_codes(&b128, codes, K / 2, rows, 1, 128, 2) || !encode_codes(&b16, codes, K / 2, rows, 1, 16, 2)) {
-    *why = "cuTensorMapEncodeTiled rejected the token tensor map";
-    return cudaErrorInvalidValue;
-  }
   MxArgs a{};
   cudaError_t err = device_status_ptr(&a.status);
   if (err != cudaSuccess) return err;
   a.offsets = offsets;
-  a.sfa0 = static_cast<const uint8_t*>(gate_up ? w.gate_sf : w.down_sf);
-  a.sfa1 = static_cast<const uint8_t*>(gate_up ? w.up_sf : w.down_sf);
+  a.sfa = static_cast<const uint8_t*>(gate_up ? w.gate_up_sf : w.down_sf);
   a.sfb = static_cast<const uint8_t*>(scales);
   a.sfb_pitch = static_cast<int>(mx_scale_pitch(K));
   a.sf_blocks = static_cast<int>(K / MX_BLOCK);
-  a.row_blocks = static_cast<int>(mx_weight_row_blocks(gate_up, N));
   a.E = E;
-  a.n_wblocks = static_cast<int>(gate_up ? (N + BM - 1) / BM : (N + 2 * BM - 1) / (2 * BM));
+  a.n_wblocks = static_cast<int>(mx_weight_blocks(gate_up, N));
   a.K = static_cast<int>(K);
   a.n_out = static_cast<int>(N);
   a.rows_total = static_cast<uint32_t>(rows);
@@ -714,9 +839,10 @@ cudaError_t launch_experts_mx(const MxWeights& w, bool gate_up, const void* code
   a.q_codes = static_cast<uint8_t*>(q_codes);
   a.q_scales = static_cast<uint8_t*>(q_scales);
   a.q_pitch = static_cast<int>(mx_scale_pitch(N));
-  if (out_dtype == MOE_F32) return stage_t<float>(w, gate_up, b128, b16, a, rows, num_sms, stream);
-  if (out_dtype == MOE_F16) return stage_t<__half>(w, gate_up, b128, b16, a, rows, num_sms, stream);
-  return stage_t<__nv_bfloat16>(w, gate_up, b128, b16, a, rows, num_sms, stream);
+  const MxOperands op{gate_up, gate_up ? w.gate : w.down, w.up, codes};
+  if (out_dtype == MOE_F32) return stage_t<float>(op, a, rows, num_sms, stream, why);
+  if (out_dtype == MOE_F16) return stage_t<__half>(op, a, rows, num_sms, stream, why);
+  return stage_t<__nv_bfloat16>(op, a, rows, num_sms, stream, why);
 }
 
 }  // namespace moe

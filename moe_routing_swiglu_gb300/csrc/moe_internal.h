@@ -181,19 +181,19 @@ cudaError_t launch_mx_quantize(const void* x, moe_dtype dtype, int64_t rows, int
                                void* codes, void* scales, int num_sms, cudaStream_t stream);
 cudaError_t launch_mx_dequantize(const void* codes, const void* scales, int64_t rows, int64_t K, void* out,
                                  moe_dtype dtype, int num_sms, cudaStream_t stream);
-// Row-major weight scales [E, R, pitch] -> the tensor cores' atoms.
-cudaError_t launch_mx_layout_scales(const void* scales, void* dst, int64_t E, int64_t R, int64_t row_blocks, int64_t K,
+// Row-major weight scales -> the tensor cores' atoms: s0 and s1 are gate and
+// up [E, R, pitch], or s0 is down and s1 NULL.
+cudaError_t launch_mx_layout_scales(const void* s0, const void* s1, void* dst, int64_t E, int64_t R, int64_t K,
                                     cudaStream_t stream);
 struct MxWeights {
-  CUtensorMap gate, up, down;  // 3-D maps over the codes [E, rows, K / 2], 128 B x 128 x 1 boxes
-  const void* gate_sf;         // scales in atoms
-  const void* up_sf;
+  const void* gate;        // codes [E, I, H / 2]
+  const void* up;
+  const void* down;        // codes [E, H, I / 2]
+  const void* gate_up_sf;  // scales in atoms
   const void* down_sf;
 };
-int64_t mx_weight_row_blocks(bool gate_up, int64_t R);
+int64_t mx_weight_blocks(bool gate_up, int64_t R);
 size_t mx_weight_scale_bytes(bool gate_up, int64_t E, int64_t R, int64_t K);
-bool mx_encode_weights(const void* gate, const void* up, const void* down, int64_t E, int64_t H, int64_t I,
-                       MxWeights* out, const char** why);
 // gate_up: codes/scales = x rows (K = H) -> h [rows, I] in out_dtype (out)
 // and / or as MXFP4 (q_codes, q_scales); else h rows (K = I) -> y [rows, H].
 cudaError_t launch_experts_mx(const MxWeights& w, bool gate_up, const void* codes, const void* scales,

@@ -237,23 +237,24 @@ __global__ void __launch_bounds__(MXQ_THREADS) mx_dequantize_kernel(const Dequan
 }
 
 // Row-major scales [E, R, pitch] -> the tensor cores' order: for each expert,
-// 128-row block and 256-element K block two atoms of 512 bytes, atom a
-// holding the four scale bytes of K elements 128 a .. 128 a + 127 of row m at
-// byte (m % 32) * 16 + (m / 32) * 4. Rows and blocks past the matrix get 0.
-__global__ void mx_layout_scales_kernel(const uint8_t* __restrict__ src, uint32_t* __restrict__ dst, int64_t R,
-                                        int64_t row_blocks, int64_t k_blocks, int64_t pitch, int64_t blocks_per_row,
-                                        int64_t n_words) {
+// weight block and 128 K elements two atoms of 512 bytes, of two 128-row tiles
+// (gate and up rows of the same channels, or two halves of 256 down rows). An
+// atom holds the four scale bytes of row m at byte (m % 32) * 16 + (m / 32) * 4.
+// Rows and blocks past the matrix get 0.
+__global__ void mx_layout_scales_kernel(const uint8_t* __restrict__ s0, const uint8_t* __restrict__ s1,
+                                        uint32_t* __restrict__ dst, int64_t R, int64_t w_blocks, int64_t k_words,
+                                        int64_t pitch, int64_t blocks_per_row, int64_t n_words) {
   for (int64_t w = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; w < n_words;
        w += static_cast<int64_t>(gridDim.x) * blockDim.x) {
     const int in = static_cast<int>(w & 127);          // word of the atom
-    const int64_t atom = w >> 7;
-    const int64_t kw = atom % (2 * k_blocks);          // which 128 K elements
-    const int64_t rb = atom / (2 * k_blocks) % row_blocks;
-    const int64_t e = atom / (2 * k_blocks * row_blocks);
-    const int64_t m = rb * 128 + (in & 3) * 32 + (in >> 2);
+    const int half = static_cast<int>((w >> 7) & 1);   // tile of the block
+    const int64_t kw = (w >> 8) % k_words;             // which 128 K elements
+    const int64_t wb = (w >> 8) / k_words % w_blocks;
+    const int64_t e = (w >> 8) / k_words / w_blocks;
+    const int64_t m = (s1 != nullptr ? wb : 2 * wb + half) * 128 + (in & 3) * 32 + (in >> 2);
     uint32_t v = 0;
     if (m < R) {
-      const uint8_t* p = src + (e * R + m) * pitch;
+      const uint8_t* p = (s1 != nullptr && half != 0 ? s1 : s0) + (e * R + m) * pitch;
 #pragma unroll
       for (int b = 0; b < 4; ++b)
         if (kw * 4 + b < blocks_per_row) v |= static_cast<uint32_t>(p[kw * 4 + b]) << (8 * b);
@@ -334,14 +335,15 @@ cudaError_t launch_mx_dequantize(const void* codes, const void* scales, int64_t 
   return cudaSuccess;
 }
 
-cudaError_t launch_mx_layout_scales(const void* scales, void* dst, int64_t E, int64_t R, int64_t row_blocks, int64_t K,
+cudaError_t launch_mx_layout_scales(const void* s0, const void* s1, void* dst, int64_t E, int64_t R, int64_t K,
                                     cudaStream_t stream) {
-  const int64_t k_blocks = (K + 255) / 256;
-  const int64_t n_words = E * row_blocks * k_blocks * 256;
+  const int64_t k_words = (K + 127) / 128;
+  const int64_t w_blocks = mx_weight_blocks(s1 != nullptr, R);
+  const int64_t n_words = E * w_blocks * k_words * 256;
   const int64_t want = (n_words + 255) / 256;
   mx_layout_scales_kernel<<<static_cast<unsigned>(want < 65535 ? want : 65535), 256, 0, stream>>>(
-      static_cast<const uint8_t*>(scales), static_cast<uint32_t*>(dst), R, row_blocks, k_blocks, mx_scale_pitch(K),
-      K / MX_BLOCK, n_words);
+      static_cast<const uint8_t*>(s0), static_cast<const uint8_t*>(s1), static_cast<uint32_t*>(dst), R, w_blocks,
+      k_words, mx_scale_pitch(K), K / MX_BLOCK, n_words);
   return cudaGetLastError();
 }
 

@@ -131,10 +131,10 @@ def test_create_rejects_bad_arguments(lib, kwargs, status):
 
 
 def test_storage_size(lib):
-    # gate and up: 1 row block of 128, 1 K block; down: 2 row blocks; 1 KB each, 4 experts
-    assert lib.moe_experts_mxfp4_storage_size(4, 64, 96) == 4 * (1 + 1 + 2) * 1024
-    # 768 channels are 6 row blocks of 8 K blocks; 2048 down rows 16 row blocks of 3
-    assert lib.moe_experts_mxfp4_storage_size(128, 2048, 768) == 128 * (2 * 6 * 8 + 16 * 3) * 1024
+    # gate and up: 1 row block of 128, 1 word of 128 K elements; down: 2 row blocks; 512 bytes each, 4 experts
+    assert lib.moe_experts_mxfp4_storage_size(4, 64, 96) == 4 * (1 + 1 + 2) * 512
+    # 768 channels are 6 row blocks of 16 words; 2048 down rows 16 row blocks of 6
+    assert lib.moe_experts_mxfp4_storage_size(128, 2048, 768) == 128 * (2 * 6 * 16 + 16 * 6) * 512
     assert lib.moe_experts_mxfp4_storage_size(0, 64, 96) == 0
     assert lib.moe_experts_mxfp4_storage_size(4, 65, 96) == 0
 
