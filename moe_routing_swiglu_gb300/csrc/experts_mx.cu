@@ -77,7 +77,7 @@ struct MxCfg {
   static constexpr int STAGES = 184 * 1024 / STAGE_BYTES;
   static constexpr int SFB_BYTES = GROUPS * ATOMS_K * ATOM;
   static constexpr int SF_BYTES = SFA_BYTES + SFB_BYTES;     // a stage's scales: their own, deeper ring
-  static constexpr int SF_STAGES = 24 * 1024 / SF_BYTES;
+  static constexpr int SF_STAGES = 20 * 1024 / SF_BYTES;
   static constexpr int SF_AHEAD = SF_STAGES - 2;             // stages between a slot's loads and its use
   // TMEM columns: ACC accumulator buffers of (D0, D1), then SLOTS scale
   // buffers of (SFA0, SFA1, SFB), 4 columns per atom.
@@ -94,8 +94,8 @@ struct MxCfg {
   // full, empty; sf_full, sf_empty; sf_ready; tfull, tempty; drain
   static constexpr int NUM_BARS = 2 * STAGES + 2 * SF_STAGES + SLOTS + 2 * ACC + 1;
   static constexpr int SMEM_MISC = SMEM_BAR + 8 * NUM_BARS;  // TMEM address, abort flag
-  static constexpr int SMEM_TILES = SMEM_MISC + 16;
-  static constexpr int SMEM_BYTES = 1024 + SMEM_TILES + 4 * (ROUTE_MAX_E + 1);
+  static constexpr int SMEM_TILES = SMEM_MISC + 16;          // tile prefix, then the row offsets
+  static constexpr int SMEM_BYTES = 1024 + SMEM_TILES + 8 * (ROUTE_MAX_E + 1);
   static_assert(STAGE_BYTES % 1024 == 0, "swizzle atom alignment");
   static_assert(STAGES >= 3, "pipeline depth");
   static_assert(SLOTS >= 2 && SLOTS <= STAGES, "a stage barrier advances only once the scale warps have passed its last phase");
@@ -164,23 +164,41 @@ struct MxTile {
   int n_tok;      // rows rounded up to 16: the MMA's N
 };
 
+// Exclusive prefix of the experts' tiles, tile_start[0..E], and a copy of the
+// offsets, by one warp. Eight experts' counts per lane are loaded before they
+// are used: one trip to memory for 256 experts.
 template <int TBN>
 __device__ __forceinline__ void build_mx_prefix(const uint32_t* __restrict__ offsets, int E, int n_wblocks,
-                                                uint32_t* tile_start) {
+                                                uint32_t* tile_start, uint32_t* offs) {
+  constexpr int BATCH = 8;
   const int lane = threadIdx.x & 31;
   uint32_t carry = 0;
-  for (int base = 0; base < E; base += 32) {
-    const int e = base + lane;
-    const uint32_t cnt = e < E ? offsets[e + 1] - offsets[e] : 0u;
-    const uint32_t tiles = token_tiles<TBN>(cnt) * static_cast<uint32_t>(n_wblocks);
-    uint32_t incl = tiles;
+  for (int base = 0; base < E; base += 32 * BATCH) {
+    uint32_t lo[BATCH], hi[BATCH];
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const uint32_t o = __shfl_up_sync(FULL_MASK, incl, off);
-      if (lane >= off) incl += o;
+    for (int i = 0; i < BATCH; ++i) {
+      const int e = base + 32 * i + lane;
+      lo[i] = e < E ? offsets[e] : 0u;
+      hi[i] = e < E ? offsets[e + 1] : 0u;
     }
-    if (e < E) tile_start[e] = carry + incl - tiles;
-    carry += __shfl_sync(FULL_MASK, incl, 31);
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int e = base + 32 * i + lane;
+      if (base + 32 * i >= E) break;
+      const uint32_t tiles = token_tiles<TBN>(hi[i] - lo[i]) * static_cast<uint32_t>(n_wblocks);
+      uint32_t incl = tiles;
+#pragma unroll
+      for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t o = __shfl_up_sync(FULL_MASK, incl, off);
+        if (lane >= off) incl += o;
+      }
+      if (e < E) {
+        tile_start[e] = carry + incl - tiles;
+        offs[e] = lo[i];
+        if (e == E - 1) offs[E] = hi[i];
+      }
+      carry += __shfl_sync(FULL_MASK, incl, 31);
+    }
   }
   if (lane == 0) tile_start[E] = carry;
 }
@@ -189,7 +207,7 @@ __device__ __forceinline__ void build_mx_prefix(const uint32_t* __restrict__ off
 // weight tile run together and read it from L2. Requires tile < tile_start[E].
 template <int TBN>
 __device__ __forceinline__ MxTile decode_mx_tile(uint32_t tile, const uint32_t* tile_start, int E, int n_wblocks,
-                                                 const uint32_t* __restrict__ offsets) {
+                                                 const uint32_t* offsets) {
   int lo = 0, hi = E;
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -348,7 +366,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint64_t* drain = tempty + ACC;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::SMEM_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::SMEM_MISC + 4);
-  uint32_t* tile_start = reinterpret_cast<uint32_t*>(smem + C::SMEM_TILES);
+  uint32_t* tile_start = reinterpret_cast<uint32_t*>(smem + C::SMEM_TILES);  // [E + 1]
+  uint32_t* offs = tile_start + args.E + 1;                                   // [E + 1]
 
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -382,7 +401,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   // From here on the kernel reads what earlier kernels wrote.
   grid_dependency_wait();
-  if (warp == 0) build_mx_prefix<TBN>(args.offsets, args.E, args.n_wblocks, tile_start);
+  if (warp == 0) build_mx_prefix<TBN>(args.offsets, args.E, args.n_wblocks, tile_start, offs);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -400,7 +419,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t issued = 0;
       bool ok = true;
       for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-        const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, args.offsets);
+        const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, offs);
         const uint32_t tx = static_cast<uint32_t>(2 * A_BYTES + tc.n_tok * ROW_BYTES);
         const int row = tc.w * (GATE_UP ? BM : 2 * BM);
         for (int kb = 0; kb < k_blocks; ++kb) {
@@ -449,7 +468,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t it = 0;
       bool ok = true;
       for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++it) {
-        const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, args.offsets);
+        const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, offs);
         const uint32_t idesc0 = idesc_mxf4(tc.n_tok, 0), idesc2 = idesc_mxf4(tc.n_tok, 2);
         const uint32_t acc = it % ACC;
         if (!mbar_wait_bounded(&tempty[acc], ((it / ACC) & 1u) ^ 1u, abort_flag, args.status, ST_MMA_TMEM_EMPTY,
@@ -503,7 +522,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t xp_u32 = smem_u32(xp);
     uint32_t it = 0;
     for (uint32_t tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
-      const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, args.offsets);
+      const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, offs);
       const uint32_t acc = it % ACC;
       const bool ok = mbar_wait_bounded(&tfull[acc], (it / ACC) & 1u, abort_flag, args.status, ST_EPI_TMEM_FULL,
                                         WAIT_LIMIT_NS);
@@ -631,7 +650,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t ln = 0, ltile = blockIdx.x;  // next stage to load, its tile
     int lkb = 0;
     MxTile ltc{};
-    if (ltile < total) ltc = decode_mx_tile<TBN>(ltile, tile_start, args.E, args.n_wblocks, args.offsets);
+    if (ltile < total) ltc = decode_mx_tile<TBN>(ltile, tile_start, args.E, args.n_wblocks, offs);
     auto load_next = [&]() -> bool {
       if (ltile >= total) return true;
       if (ln % NUM_LOAD_WARPS == lw) {
@@ -669,7 +688,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (++lkb == k_blocks) {
         lkb = 0;
         ltile += gridDim.x;
-        if (ltile < total) ltc = decode_mx_tile<TBN>(ltile, tile_start, args.E, args.n_wblocks, args.offsets);
+        if (ltile < total) ltc = decode_mx_tile<TBN>(ltile, tile_start, args.E, args.n_wblocks, offs);
       }
       return true;
     };
