@@ -108,6 +108,7 @@ struct MxCfg {
   static_assert(NUM_LOAD_WARPS <= SF_STAGES, "loader warps run at most a ring ahead");
   static_assert(COLS_USED <= 512, "TMEM columns");
   static_assert(TBN % 16 == 0 && TBN <= 256, "token tile");
+  static_assert(SMEM_XPOSE % 512 == 0, "the transpose buffers start on the 64-byte swizzle's period");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
 };
 
@@ -149,6 +150,7 @@ struct MxMaps {
   CUtensorMap a0;            // gate, or down (256-row box)
   CUtensorMap a1;            // up
   CUtensorMap b[NUM_BOXES];
+  CUtensorMap out;           // 16-bit outputs: boxes of 32 columns x 32 rows, 64-byte swizzle
 };
 
 // Token tiles of an expert with cnt rows: ceil(cnt / TBN), each of bn rows
@@ -263,6 +265,14 @@ __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, uint4 a, uint4
                : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Tensor store shared -> global of one box of a 2-D map, in the issuing
+// thread's current bulk async-group.
+__device__ __forceinline__ void tma_store_2d(const void* desc, uint32_t smem_src, int c0, int c1) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(desc), "r"(c0),
+               "r"(c1), "r"(smem_src)
+               : "memory");
+}
 
 // Untiled bulk copy global -> shared, counted on `bar` (16-byte aligned).
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -393,6 +403,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tma_prefetch_desc(&maps.a0);
     if (GATE_UP) tma_prefetch_desc(&maps.a1);
     for (int i = 0; i < NUM_BOXES; ++i) tma_prefetch_desc(&maps.b[i]);
+    if (sizeof(T) == 2 && args.out != nullptr) tma_prefetch_desc(&maps.out);
   }
   __syncwarp();
   if (warp == 1) {
@@ -551,33 +562,54 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int blk = 0; blk < (GATE_UP ? 1 : 2); ++blk) {
             const int64_t col0 = colA + blk * BM;
             const bool col_ok = col0 < args.n_out;  // n_out is a multiple of 32: the warp's block is in or out
+            uint32_t m[4][4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              uint32_t m[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 const int r = 4 * i + 2 * (q & 1);
                 const float a0 = __uint_as_float(f0[q >> 1][r]), a1 = __uint_as_float(f0[q >> 1][r + 1]);
                 const float b0 = __uint_as_float(f1[q >> 1][r]), b1 = __uint_as_float(f1[q >> 1][r + 1]);
-                if (GATE_UP) m[q] = pack2<T>(mx_silu<T>(a0) * b0, mx_silu<T>(a1) * b1);
-                else m[q] = blk == 0 ? pack2<T>(a0, a1) : pack2<T>(b0, b1);
+                if (GATE_UP) m[i][q] = pack2<T>(mx_silu<T>(a0) * b0, mx_silu<T>(a1) * b1);
+                else m[i][q] = blk == 0 ? pack2<T>(a0, a1) : pack2<T>(b0, b1);
               }
-              const int tok = 8 * i + (lane & 7);
-              stmatrix_x4_trans(xp_u32 + static_cast<uint32_t>(tok * 64 + (((lane >> 3) ^ (tok >> 1)) & 3) * 16), m[0],
-                                m[1], m[2], m[3]);
             }
+            // The buffer's last bulk store has read it (it had this block's
+            // arithmetic to do so).
+            if (lane == 0) bulk_wait_read_all();
             __syncwarp();
-            if (args.out != nullptr && col_ok) {
-              const int part = lane & 3;
 #pragma unroll
-              for (int p = 0; p < 4; ++p) {
-                const int j = p * 8 + (lane >> 2);
-                if (c0 + j < live) {
-                  const uint4 row = *reinterpret_cast<const uint4*>(xp + j * 64 + ((part ^ (j >> 1)) & 3) * 16);
-                  T* dst = static_cast<T*>(args.out) + (static_cast<int64_t>(tc.row0) + c0 + j) * args.n_out + col0;
-                  reinterpret_cast<uint4*>(dst)[part] = row;
+            for (int i = 0; i < 4; ++i) {
+              const int tok = 8 * i + (lane & 7);
+              stmatrix_x4_trans(xp_u32 + static_cast<uint32_t>(tok * 64 + (((lane >> 3) ^ (tok >> 1)) & 3) * 16),
+                                m[i][0], m[i][1], m[i][2], m[i][3]);
+            }
+            if (args.out != nullptr && col_ok) {
+              if (c0 + 32 <= live) {
+                // All 32 tokens are the tile's: one tensor store (the swizzle
+                // is the 64-byte one).
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                  tma_store_2d(&maps.out, xp_u32, static_cast<int>(col0), static_cast<int>(tc.row0) + c0);
+                  bulk_commit_group();
+                }
+              } else {
+                // The rows after the tile's are another expert's.
+                __syncwarp();
+                const int part = lane & 3;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                  const int j = p * 8 + (lane >> 2);
+                  if (c0 + j < live) {
+                    const uint4 row = *reinterpret_cast<const uint4*>(xp + j * 64 + ((part ^ (j >> 1)) & 3) * 16);
+                    T* dst = static_cast<T*>(args.out) + (static_cast<int64_t>(tc.row0) + c0 + j) * args.n_out + col0;
+                    reinterpret_cast<uint4*>(dst)[part] = row;
+                  }
                 }
               }
+            } else {
+              __syncwarp();
             }
             if (GATE_UP && args.q_codes != nullptr && col_ok && c0 + lane < live) {
               const int64_t r = static_cast<int64_t>(tc.row0) + c0 + lane;
@@ -634,6 +666,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&tempty[acc]);
     }
+    if (lane == 0) bulk_wait_all();  // the stores have left shared memory and are done
   } else {
     // ------------------------------------------------------------ scales
     // Global -> shared, SF_AHEAD stages before use: warp lw fills the ring
@@ -763,6 +796,19 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn_mx() {
 }
 
 // [E, rows, row_bytes] codes, box 128 bytes (one swizzle atom) x box_rows x 1.
+// [rows, n] 16-bit outputs, boxes of 32 x 32 with the 64-byte swizzle.
+bool encode_out(CUtensorMap* m, moe_dtype dtype, void* ptr, uint64_t n, uint64_t rows) {
+  auto fn = encode_fn_mx();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {n, rows};
+  const cuuint64_t strides[1] = {n * 2};
+  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(m, dtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ptr, dims,
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool encode_codes(CUtensorMap* m, const void* ptr, uint64_t row_bytes, uint64_t rows, uint64_t E, uint32_t box_rows,
                   int rank) {
   auto fn = encode_fn_mx();
@@ -808,6 +854,10 @@ cudaError_t stage_n(const MxOperands& op, const MxArgs& args, int64_t rows, int 
   if (op.gate_up) ok = ok && encode_codes(&maps.a1, op.w1, kb, N, E, BM, 3);
   for (int i = 0; i < NUM_BOXES; ++i)
     ok = ok && encode_codes(&maps.b[i], op.tokens, kb, static_cast<uint64_t>(rows), 1, 128u >> i, 2);
+  maps.out = maps.a0;
+  if (sizeof(T) == 2 && args.out != nullptr)
+    ok = ok && encode_out(&maps.out, std::is_same<T, __half>::value ? MOE_F16 : MOE_BF16, args.out, N,
+                          static_cast<uint64_t>(rows));
   if (!ok) {
     *why = "cuTensorMapEncodeTiled rejected a tensor map";
     return cudaErrorInvalidValue;
