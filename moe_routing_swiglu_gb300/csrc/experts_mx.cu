@@ -26,10 +26,10 @@
 // One persistent CTA per SM takes tiles blockIdx, blockIdx + grid, ...
 //   warp 0 lane 0   producer: TMA of weights and tokens
 //   warp 1 lane 0   MMAs; warp 1 also owns the TMEM
-//   warps 2..9      epilogue: accumulators to registers in fragment order,
+//   warps 2..17     epilogue: accumulators to registers in fragment order,
 //                   packed in token pairs, transposed by stmatrix into token
 //                   rows, written in 64-byte runs (or quantised)
-//   warps 10..13    scales: global -> shared a few stages ahead, shared ->
+//   warps 18..21    scales: global -> shared a few stages ahead, shared ->
 //                   TMEM by tcgen05.st into one of SLOTS buffers, rewritten
 //                   only after the MMAs that read it have completed
 // The scales go to TMEM by stores and not by tcgen05.cp because the copies
@@ -62,11 +62,14 @@ constexpr int A_BYTES = BM * ROW_BYTES;
 constexpr int ATOM = 512;              // scale atom: 128 rows x 4 scale bytes
 constexpr int ATOMS_K = BK / 128;      // atoms per 128 rows and stage
 constexpr int SFA_BYTES = 2 * ATOMS_K * ATOM;  // scales of both weight tiles of a stage
-constexpr int NUM_EPI_WARPS = 8;
-constexpr int NUM_LOAD_WARPS = 4;      // each takes every fourth stage
-constexpr int FIRST_LOAD_WARP = 2 + NUM_EPI_WARPS;
-constexpr int NUM_THREADS = 32 * (2 + NUM_EPI_WARPS + NUM_LOAD_WARPS);
-constexpr int XPOSE_BYTES = 2048;      // per-warp transpose buffer: 32 tokens x 32 channels of 16 bits
+constexpr int NUM_EPI_WARPS = 12;     // three per 32 TMEM lanes
+constexpr int SCALE_SETS = 2;          // sets of four warps that write the scale buffers, a stage each in turn
+constexpr int NUM_LOAD_WARPS = 2;      // warps that load scales, a stage each in turn
+constexpr int FIRST_SCALE_WARP = 2 + NUM_EPI_WARPS;
+constexpr int FIRST_LOAD_WARP = FIRST_SCALE_WARP + 4 * SCALE_SETS;
+constexpr int NUM_THREADS = 32 * (FIRST_LOAD_WARP + NUM_LOAD_WARPS);
+constexpr int EPI_TOKENS = 16;         // tokens an epilogue warp takes at a time
+constexpr int XPOSE_BYTES = 1024;      // its transpose buffer: 16 tokens x 32 channels of 16 bits
 constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
 
 template <int TBN>
@@ -77,8 +80,7 @@ struct MxCfg {
   static constexpr int STAGES = 184 * 1024 / STAGE_BYTES;
   static constexpr int SFB_BYTES = GROUPS * ATOMS_K * ATOM;
   static constexpr int SF_BYTES = SFA_BYTES + SFB_BYTES;     // a stage's scales: their own, deeper ring
-  static constexpr int SF_STAGES = 20 * 1024 / SF_BYTES;
-  static constexpr int SF_AHEAD = SF_STAGES - 2;             // stages between a slot's loads and its use
+  static constexpr int SF_STAGES = 6;
   // TMEM columns: ACC accumulator buffers of (D0, D1), then SLOTS scale
   // buffers of (SFA0, SFA1, SFB), 4 columns per atom.
   static constexpr int ACC = TBN <= 112 ? 2 : 1;
@@ -100,12 +102,12 @@ struct MxCfg {
   static_assert(STAGES >= 3, "pipeline depth");
   static_assert(SLOTS >= 2 && SLOTS <= STAGES, "a stage barrier advances only once the scale warps have passed its last phase");
   static_assert(SF_COLS % 8 == 0, "scale stores of 8 columns");
-  static_assert(SF_AHEAD >= 1 && SF_AHEAD < SF_STAGES, "scale prefetch distance");
-  // A loader warp takes every NUM_LOAD_WARPS-th stage. Its parity wait for
-  // the ring slot of stage n + NUM_LOAD_WARPS is unambiguous only if the slot's
-  // use before the awaited one is known to be over, which its last wait (for
-  // stage n) tells it up to stage n - SF_STAGES.
-  static_assert(NUM_LOAD_WARPS <= SF_STAGES, "loader warps run at most a ring ahead");
+  // Scale and loader warps take every SCALE_SETS-th (NUM_LOAD_WARPS-th)
+  // stage. A wait by parity is unambiguous only if the use before the awaited
+  // one of the same barrier is known to be over: for the ring's barriers that
+  // is a stage of the same warps when the ring's length is a multiple of the
+  // step; for a stage barrier it is one before the stage last waited for.
+  static_assert(SF_STAGES % SCALE_SETS == 0 && SF_STAGES % NUM_LOAD_WARPS == 0 && SCALE_SETS <= STAGES, "parity waits");
   static_assert(COLS_USED <= 512, "TMEM columns");
   static_assert(TBN % 16 == 0 && TBN <= 256, "token tile");
   static_assert(SMEM_XPOSE % 512 == 0, "the transpose buffers start on the 64-byte swizzle's period");
@@ -150,7 +152,7 @@ struct MxMaps {
   CUtensorMap a0;            // gate, or down (256-row box)
   CUtensorMap a1;            // up
   CUtensorMap b[NUM_BOXES];
-  CUtensorMap out;           // 16-bit outputs: boxes of 32 columns x 32 rows, 64-byte swizzle
+  CUtensorMap out;           // 16-bit outputs: boxes of 32 columns x 16 rows, 64-byte swizzle
 };
 
 // Token tiles of an expert with cnt rows: ceil(cnt / TBN), each of bn rows
@@ -299,12 +301,20 @@ __device__ __forceinline__ float mx_silu(float g) {
   return g * r;
 }
 
-// 32 columns of 16 TMEM lanes, in the order of a matrix fragment: thread t
+// 16 columns of 16 TMEM lanes, in the order of a matrix fragment: thread t
 // gets, for each group i of 8 columns, columns 8i + 2 (t % 4) and the next of
 // lane t / 4 (r[4i], r[4i + 1]) and of lane t / 4 + 8 (r[4i + 2], r[4i + 3]).
-__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_ld_16x256b_x2(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+}
+
+// 16 columns of this warp's 32 TMEM lanes (one lane a thread).
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
@@ -321,19 +331,24 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
                : "memory");
 }
 
-// One token's block of 32 channels, read from shared memory as 16-byte runs
-// (run(q): its address), quantised and written as 16 bytes of codes and one
-// scale byte (with the row's pad bytes after its last block).
+// A warp's tokens x 32 channels in shared memory, one block of 32 per token,
+// quantised: LPT lanes share a token, each with two 16-byte runs (run(tok, q):
+// the address of the token's run q). Row r0 + tok of the codes and scales gets
+// block `blk`; `live` tokens are written (the last block of a row also clears
+// the row's pad bytes).
 template <typename T, typename Run>
-__device__ __forceinline__ void quantize_token(Run run, uint8_t* codes, uint8_t* scale_row, int64_t blk, int pitch,
-                                               bool last_block) {
-  constexpr int RUNS = 32 * static_cast<int>(sizeof(T)) / 16;
-  constexpr int EPR = 16 / static_cast<int>(sizeof(T));
-  float v[32];
+__device__ __forceinline__ void quantize_tokens(Run run, uint8_t* codes, uint8_t* scales, int64_t r0, int64_t blk,
+                                                int64_t code_pitch, int pitch, int live, bool last_block) {
+  constexpr int LPT = static_cast<int>(sizeof(T));        // 2, or 4 for FP32
+  constexpr int EPL = 32 / LPT;                           // elements per lane
+  constexpr int EPR = 16 / static_cast<int>(sizeof(T));   // elements per run
+  const int lane = threadIdx.x & 31;
+  const int tok = lane / LPT, part = lane % LPT;
+  float v[EPL];
   uint32_t amax = 0;
 #pragma unroll
-  for (int q = 0; q < RUNS; ++q) {
-    const uint4 raw = *reinterpret_cast<const uint4*>(run(q));
+  for (int q = 0; q < 2; ++q) {
+    const uint4 raw = *reinterpret_cast<const uint4*>(run(tok, 2 * part + q));
     const T* e = reinterpret_cast<const T*>(&raw);
 #pragma unroll
     for (int i = 0; i < EPR; ++i) {
@@ -341,20 +356,28 @@ __device__ __forceinline__ void quantize_token(Run run, uint8_t* codes, uint8_t*
       amax = max(amax, __float_as_uint(v[q * EPR + i]) & 0x7FFFFFFFu);
     }
   }
+#pragma unroll
+  for (int off = 1; off < LPT; off <<= 1) amax = max(amax, __shfl_xor_sync(FULL_MASK, amax, off));
   const uint32_t byte = mx_scale_byte(amax);
   const float s = mx_inv_scale(byte);
-  uint32_t w[4];
+  uint32_t w[EPL / 8];
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
+  for (int q = 0; q < EPL / 8; ++q) {
     float e8[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) e8[i] = v[q * 8 + i] * s;
     w[q] = byte == 255u ? 0u : mx_pack8(e8);
   }
-  *reinterpret_cast<uint4*>(codes) = make_uint4(w[0], w[1], w[2], w[3]);
-  scale_row[blk] = static_cast<uint8_t>(byte);
-  if (last_block)
-    for (int p = static_cast<int>(blk) + 1; p < pitch; ++p) scale_row[p] = 0;
+  if (tok >= live) return;
+  uint8_t* c = codes + (r0 + tok) * code_pitch + blk * 16 + part * (EPL / 2);
+  if constexpr (EPL == 16) *reinterpret_cast<uint2*>(c) = make_uint2(w[0], w[1]);
+  else *reinterpret_cast<uint32_t*>(c) = w[0];
+  if (part == 0) {
+    uint8_t* sp = scales + (r0 + tok) * pitch;
+    sp[blk] = static_cast<uint8_t>(byte);
+    if (last_block)
+      for (int p = static_cast<int>(blk) + 1; p < pitch; ++p) sp[p] = 0;
+  }
 }
 
 template <typename T, bool GATE_UP, int TBN>
@@ -389,9 +412,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     for (int s = 0; s < SF_STAGES; ++s) {
       mbar_init(&sf_full[s], 1 + 32);  // the expect_tx of the weights' atoms, and each lane's copies of the tokens' words
-      mbar_init(&sf_empty[s], NUM_LOAD_WARPS);
+      mbar_init(&sf_empty[s], 4);
     }
-    for (int s = 0; s < C::SLOTS; ++s) mbar_init(&sf_ready[s], NUM_LOAD_WARPS);
+    for (int s = 0; s < C::SLOTS; ++s) mbar_init(&sf_ready[s], 4);
     for (int a = 0; a < ACC; ++a) {
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], NUM_EPI_WARPS);
@@ -524,11 +547,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_wait_bounded(drain, 0, nullptr, args.status, ST_MMA_DRAIN, WAIT_LIMIT_NS);
     }
     __syncwarp();
-  } else if (warp < FIRST_LOAD_WARP) {
+  } else if (warp < FIRST_SCALE_WARP) {
     // ------------------------------------------------------------ epilogue
     const int ew = warp - 2;
     const int quad = warp & 3;                  // TMEM lanes 32*quad ..
-    const int half = ew >> 2;                   // takes 32-token chunks half, half+2, ...
+    const int group = ew >> 2;                  // takes 16-token chunks group, group + 4, ...
     uint8_t* xp = smem + C::SMEM_XPOSE + ew * XPOSE_BYTES;
     const uint32_t xp_u32 = smem_u32(xp);
     uint32_t it = 0;
@@ -544,27 +567,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // Rows of the tile that exist in the buffers (all of them, for valid offsets).
       const int live = tc.row0 < args.rows_total
                            ? static_cast<int>(min(static_cast<uint32_t>(tc.rows), args.rows_total - tc.row0)) : 0;
-      for (int c0 = 32 * half; c0 < tc.n_tok; c0 += 64) {
+      for (int c0 = EPI_TOKENS * group; c0 < tc.n_tok; c0 += EPI_TOKENS * (NUM_EPI_WARPS / 4)) {
+        const int64_t row = static_cast<int64_t>(tc.row0) + c0;
         if constexpr (sizeof(T) == 2) {
-          // Fragments of 16 channels x 32 tokens, packed in token pairs and
+          // Fragments of 16 channels x 16 tokens, packed in token pairs and
           // transposed by stmatrix into token rows of 32 channels (64 bytes,
-          // 16-byte runs swizzled by the token so that the stores and both
-          // kinds of reads below are free of bank conflicts).
-          uint32_t f0[2][16], f1[2][16];
+          // 16-byte runs in the 64-byte swizzle: the stores and both kinds of
+          // reads below are free of bank conflicts).
+          uint32_t f0[2][8], f1[2][8];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            tmem_ld_16x256b_x4(t_lane + (static_cast<uint32_t>(16 * h) << 16) + static_cast<uint32_t>(c0), f0[h]);
-            tmem_ld_16x256b_x4(t_lane + (static_cast<uint32_t>(16 * h) << 16) + static_cast<uint32_t>(TBN + c0),
-                               f1[h]);
+            const uint32_t at = t_lane + (static_cast<uint32_t>(16 * h) << 16) + static_cast<uint32_t>(c0);
+            tmem_ld_16x256b_x2(at, f0[h]);
+            tmem_ld_16x256b_x2(at + TBN, f1[h]);
           }
           tmem_ld_wait();
 #pragma unroll
           for (int blk = 0; blk < (GATE_UP ? 1 : 2); ++blk) {
             const int64_t col0 = colA + blk * BM;
             const bool col_ok = col0 < args.n_out;  // n_out is a multiple of 32: the warp's block is in or out
-            uint32_t m[4][4];
+            uint32_t m[2][4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
                 const int r = 4 * i + 2 * (q & 1);
@@ -579,52 +603,44 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (lane == 0) bulk_wait_read_all();
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 2; ++i) {
               const int tok = 8 * i + (lane & 7);
               stmatrix_x4_trans(xp_u32 + static_cast<uint32_t>(tok * 64 + (((lane >> 3) ^ (tok >> 1)) & 3) * 16),
                                 m[i][0], m[i][1], m[i][2], m[i][3]);
             }
-            if (args.out != nullptr && col_ok) {
-              if (c0 + 32 <= live) {
-                // All 32 tokens are the tile's: one tensor store (the swizzle
-                // is the 64-byte one).
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                  tma_store_2d(&maps.out, xp_u32, static_cast<int>(col0), static_cast<int>(tc.row0) + c0);
-                  bulk_commit_group();
-                }
-              } else {
-                // The rows after the tile's are another expert's.
-                __syncwarp();
-                const int part = lane & 3;
-#pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                  const int j = p * 8 + (lane >> 2);
-                  if (c0 + j < live) {
-                    const uint4 row = *reinterpret_cast<const uint4*>(xp + j * 64 + ((part ^ (j >> 1)) & 3) * 16);
-                    T* dst = static_cast<T*>(args.out) + (static_cast<int64_t>(tc.row0) + c0 + j) * args.n_out + col0;
-                    reinterpret_cast<uint4*>(dst)[part] = row;
-                  }
-                }
+            const bool full_chunk = args.out != nullptr && c0 + EPI_TOKENS <= live;
+            if (full_chunk) fence_proxy_async_smem();
+            __syncwarp();
+            if (!col_ok) continue;
+            if (full_chunk) {
+              // Every token is the tile's: one tensor store.
+              if (lane == 0) {
+                tma_store_2d(&maps.out, xp_u32, static_cast<int>(col0), static_cast<int>(row));
+                bulk_commit_group();
               }
-            } else {
-              __syncwarp();
+            } else if (args.out != nullptr) {
+              // The rows after the tile's are another expert's.
+              const int part = lane & 3;
+#pragma unroll
+              for (int p = 0; p < 2; ++p) {
+                const int j = p * 8 + (lane >> 2);
+                if (c0 + j < live)
+                  reinterpret_cast<uint4*>(static_cast<T*>(args.out) + (row + j) * args.n_out + col0)[part] =
+                      *reinterpret_cast<const uint4*>(xp + j * 64 + ((part ^ (j >> 1)) & 3) * 16);
+              }
             }
-            if (GATE_UP && args.q_codes != nullptr && col_ok && c0 + lane < live) {
-              const int64_t r = static_cast<int64_t>(tc.row0) + c0 + lane;
-              quantize_token<T>([&](int q) { return xp + lane * 64 + ((q ^ (lane >> 1)) & 3) * 16; },
-                                args.q_codes + r * (args.n_out / 2) + col0 / 2, args.q_scales + r * args.q_pitch,
-                                col0 / MX_BLOCK, args.q_pitch, col0 + MX_BLOCK >= args.n_out);
-            }
+            if (GATE_UP && args.q_codes != nullptr)
+              quantize_tokens<T>([&](int tok, int q) { return xp + tok * 64 + ((q ^ (tok >> 1)) & 3) * 16; },
+                                 args.q_codes, args.q_scales, row, col0 / MX_BLOCK, args.n_out / 2, args.q_pitch,
+                                 live - c0, col0 + MX_BLOCK >= args.n_out);
             __syncwarp();
           }
         } else {
-          // FP32: lane = output channel, register = token, 16 tokens at a
-          // time through the buffer.
-          uint32_t v0[32], v1[32];
-          tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(c0), v0);
-          tmem_ld_32x32b_x32(t_lane + TBN + static_cast<uint32_t>(c0), v1);
+          // FP32: lane = output channel, register = token, 8 tokens at a time
+          // through the buffer.
+          uint32_t v0[16], v1[16];
+          tmem_ld_32x32b_x16(t_lane + static_cast<uint32_t>(c0), v0);
+          tmem_ld_32x32b_x16(t_lane + TBN + static_cast<uint32_t>(c0), v1);
           tmem_ld_wait();
           float* xf = reinterpret_cast<float*>(xp);
 #pragma unroll
@@ -632,31 +648,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             const int64_t col0 = colA + blk * BM;
             const bool col_ok = col0 < args.n_out;
 #pragma unroll
-            for (int t0 = 0; t0 < 32; t0 += 16) {
+            for (int t0 = 0; t0 < EPI_TOKENS; t0 += 8) {
 #pragma unroll
-              for (int j = 0; j < 16; ++j) {
+              for (int j = 0; j < 8; ++j) {
                 const float a = __uint_as_float(v0[t0 + j]), b = __uint_as_float(v1[t0 + j]);
                 xf[j * 32 + lane] = GATE_UP ? mx_silu<T>(a) * b : (blk == 0 ? a : b);
               }
               __syncwarp();
               if (args.out != nullptr && col_ok) {
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
+                for (int p = 0; p < 2; ++p) {
                   const int j = p * 4 + (lane >> 3);
-                  if (c0 + t0 + j < live) {
-                    T* dst = static_cast<T*>(args.out) + (static_cast<int64_t>(tc.row0) + c0 + t0 + j) * args.n_out +
-                             col0;
-                    reinterpret_cast<uint4*>(dst)[lane & 7] =
+                  if (c0 + t0 + j < live)
+                    reinterpret_cast<uint4*>(static_cast<T*>(args.out) + (row + t0 + j) * args.n_out + col0)[lane & 7] =
                         *reinterpret_cast<const uint4*>(xf + j * 32 + (lane & 7) * 4);
-                  }
                 }
               }
-              if (GATE_UP && args.q_codes != nullptr && col_ok && lane < 16 && c0 + t0 + lane < live) {
-                const int64_t r = static_cast<int64_t>(tc.row0) + c0 + t0 + lane;
-                quantize_token<T>([&](int q) { return xp + lane * 128 + q * 16; },
-                                  args.q_codes + r * (args.n_out / 2) + col0 / 2, args.q_scales + r * args.q_pitch,
-                                  col0 / MX_BLOCK, args.q_pitch, col0 + MX_BLOCK >= args.n_out);
-              }
+              if (GATE_UP && args.q_codes != nullptr && col_ok)
+                quantize_tokens<T>([&](int tok, int q) { return xp + tok * 128 + q * 16; }, args.q_codes,
+                                   args.q_scales, row + t0, col0 / MX_BLOCK, args.n_out / 2, args.q_pitch,
+                                   live - c0 - t0, col0 + MX_BLOCK >= args.n_out);
               __syncwarp();
             }
           }
@@ -667,71 +678,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (lane == 0) mbar_arrive(&tempty[acc]);
     }
     if (lane == 0) bulk_wait_all();  // the stores have left shared memory and are done
-  } else {
-    // ------------------------------------------------------------ scales
-    // Global -> shared, SF_AHEAD stages before use: warp lw fills the ring
-    // slots of stages lw, lw + NUM_LOAD_WARPS, ...: lane 0 with one bulk copy
-    // of the weights' atoms, all lanes with the tokens' words. Word a of token
-    // t (its four scale bytes for K elements 256 kb + 128 a ..) goes to atom
-    // (a, t / 128); bytes past K / 32 and rows past the tile are filled with
-    // 0, never read. Shared -> TMEM: each warp writes its 32 lanes' quarter of
-    // every stage's scale buffer (the MMA wants the atoms' 32 rows repeated
-    // in the four quarters).
-    const uint32_t lw = static_cast<uint32_t>(warp - FIRST_LOAD_WARP);
+  } else if (warp < FIRST_LOAD_WARP) {
+    // ------------------------------------------------------------ scales, shared -> TMEM
+    // Set s writes the scale buffers of stages s, s + SCALE_SETS, ...; each of
+    // its four warps its 32 lanes' quarter (the MMA wants the atoms' 32 rows
+    // repeated in the four quarters). One set alone, a stage after another,
+    // took 0.42 us a stage.
+    const uint32_t set = static_cast<uint32_t>(warp - FIRST_SCALE_WARP) / 4;
     const uint32_t quad_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    // The load side walks the same tiles as the use side, SF_AHEAD stages on.
-    uint32_t ln = 0, ltile = blockIdx.x;  // next stage to load, its tile
-    int lkb = 0;
-    MxTile ltc{};
-    if (ltile < total) ltc = decode_mx_tile<TBN>(ltile, tile_start, args.E, args.n_wblocks, offs);
-    auto load_next = [&]() -> bool {
-      if (ltile >= total) return true;
-      if (ln % NUM_LOAD_WARPS == lw) {
-        const uint32_t ss = ln % SF_STAGES;
-        const bool got = mbar_wait_bounded(&sf_empty[ss], ((ln / SF_STAGES) & 1u) ^ 1u, abort_flag, args.status,
-                                           ST_LOADER_EMPTY, WAIT_LIMIT_NS);
-        if (!__all_sync(FULL_MASK, got)) return false;
-        uint8_t* slot = smem + C::SMEM_SF + ss * C::SF_BYTES;
-        if (lane == 0) {
-          // The last stage may hold fewer atoms than the others (the MMA
-          // steps past K are left out).
-          const uint8_t* sfa =
-              args.sfa + (static_cast<int64_t>(ltc.e) * args.n_wblocks + ltc.w) * k_words * (2 * ATOM);
-          const uint32_t bytes = static_cast<uint32_t>(min(ATOMS_K, k_words - lkb * ATOMS_K)) * (2 * ATOM);
-          mbar_arrive_expect_tx(&sf_full[ss], bytes);
-          bulk_load(slot, sfa + static_cast<int64_t>(lkb) * SFA_BYTES, bytes, &sf_full[ss]);
-        }
-        const uint32_t sfb = smem_u32(slot) + SFA_BYTES;
-#pragma unroll 4
-        for (int i = lane; i < ltc.n_tok * ATOMS_K; i += 32) {
-          const int tok = i / ATOMS_K, a = i % ATOMS_K;
-          const uint32_t dst = sfb + static_cast<uint32_t>((a * C::GROUPS + (tok >> 7)) * ATOM + (tok & 31) * 16 +
-                                                           ((tok >> 5) & 3) * 4);
-          const int byte0 = (lkb * ATOMS_K + a) * 4;
-          int valid = args.sf_blocks - byte0;
-          valid = valid < 0 ? 0 : valid > 4 ? 4 : valid;
-          const uint32_t row = ltc.row0 + static_cast<uint32_t>(tok);
-          if (tok >= ltc.rows || row >= args.rows_total) valid = 0;
-          const uint8_t* src = valid > 0 ? args.sfb + static_cast<int64_t>(row) * args.sfb_pitch + byte0 : args.sfb;
-          cp_async_4(dst, src, static_cast<uint32_t>(valid));
-        }
-        cp_async_mbar_arrive_noinc(&sf_full[ss]);
-      }
-      ++ln;
-      if (++lkb == k_blocks) {
-        lkb = 0;
-        ltile += gridDim.x;
-        if (ltile < total) ltc = decode_mx_tile<TBN>(ltile, tile_start, args.E, args.n_wblocks, offs);
-      }
-      return true;
-    };
-    bool ok = true;
-    for (int i = 0; ok && i < C::SF_AHEAD; ++i) ok = load_next();
     uint32_t n = 0;
+    bool ok = true;
     for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-      for (int kb = 0; ok && kb < k_blocks; ++kb, ++n) {
-        ok = load_next();
-        if (!ok) break;
+      for (int kb = 0; kb < k_blocks; ++kb, ++n) {
+        if (n % SCALE_SETS != set) continue;
         const uint32_t ss = n % SF_STAGES;
         ok = mbar_wait_bounded(&sf_full[ss], (n / SF_STAGES) & 1u, abort_flag, args.status, ST_SCALE_FULL,
                                WAIT_LIMIT_NS);
@@ -739,15 +698,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (!ok) break;
         // Atoms in the order of the buffer's columns: SFA0 and SFA1 by K
         // atom (they lie interleaved), then SFB.
-        const uint8_t* slot = smem + C::SMEM_SF + ss * C::SF_BYTES + lane * 16;
+        const uint8_t* src = smem + C::SMEM_SF + ss * C::SF_BYTES + lane * 16;
         uint4 v[C::SF_COLS / 4];
 #pragma unroll
         for (int a = 0; a < ATOMS_K; ++a) {
-          v[a] = *reinterpret_cast<const uint4*>(slot + 2 * a * ATOM);
-          v[ATOMS_K + a] = *reinterpret_cast<const uint4*>(slot + (2 * a + 1) * ATOM);
+          v[a] = *reinterpret_cast<const uint4*>(src + 2 * a * ATOM);
+          v[ATOMS_K + a] = *reinterpret_cast<const uint4*>(src + (2 * a + 1) * ATOM);
         }
 #pragma unroll
-        for (int i = 2 * ATOMS_K; i < C::SF_COLS / 4; ++i) v[i] = *reinterpret_cast<const uint4*>(slot + i * ATOM);
+        for (int i = 2 * ATOMS_K; i < C::SF_COLS / 4; ++i) v[i] = *reinterpret_cast<const uint4*>(src + i * ATOM);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sf_empty[ss]);
         if (n >= static_cast<uint32_t>(C::SLOTS)) {
@@ -766,6 +725,51 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&sf_ready[n % C::SLOTS]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ scales, global -> shared
+    // Loader warp lw fills the ring slots of stages lw, lw + NUM_LOAD_WARPS,
+    // ...: lane 0 with one bulk copy of the weights' atoms, all lanes with the
+    // tokens' words. Word a of token t (its four scale bytes for K elements
+    // 256 kb + 128 a ..) goes to atom (a, t / 128); bytes past K / 32 and rows
+    // past the tile are filled with 0, never read.
+    const uint32_t lw = static_cast<uint32_t>(warp - FIRST_LOAD_WARP);
+    uint32_t n = 0;
+    bool ok = true;
+    for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
+      const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, offs);
+      const uint8_t* sfa = args.sfa + (static_cast<int64_t>(tc.e) * args.n_wblocks + tc.w) * k_words * (2 * ATOM);
+      for (int kb = 0; kb < k_blocks; ++kb, ++n) {
+        if (n % NUM_LOAD_WARPS != lw) continue;
+        const uint32_t ss = n % SF_STAGES;
+        ok = mbar_wait_bounded(&sf_empty[ss], ((n / SF_STAGES) & 1u) ^ 1u, abort_flag, args.status, ST_LOADER_EMPTY,
+                               WAIT_LIMIT_NS);
+        ok = __all_sync(FULL_MASK, ok);
+        if (!ok) break;
+        uint8_t* slot = smem + C::SMEM_SF + ss * C::SF_BYTES;
+        if (lane == 0) {
+          // The last stage may hold fewer atoms than the others (the MMA
+          // steps past K are left out).
+          const uint32_t bytes = static_cast<uint32_t>(min(ATOMS_K, k_words - kb * ATOMS_K)) * (2 * ATOM);
+          mbar_arrive_expect_tx(&sf_full[ss], bytes);
+          bulk_load(slot, sfa + static_cast<int64_t>(kb) * SFA_BYTES, bytes, &sf_full[ss]);
+        }
+        const uint32_t sfb = smem_u32(slot) + SFA_BYTES;
+#pragma unroll 4
+        for (int i = lane; i < tc.n_tok * ATOMS_K; i += 32) {
+          const int tok = i / ATOMS_K, a = i % ATOMS_K;
+          const uint32_t dst = sfb + static_cast<uint32_t>((a * C::GROUPS + (tok >> 7)) * ATOM + (tok & 31) * 16 +
+                                                           ((tok >> 5) & 3) * 4);
+          const int byte0 = (kb * ATOMS_K + a) * 4;
+          int valid = args.sf_blocks - byte0;
+          valid = valid < 0 ? 0 : valid > 4 ? 4 : valid;
+          const uint32_t row = tc.row0 + static_cast<uint32_t>(tok);
+          if (tok >= tc.rows || row >= args.rows_total) valid = 0;
+          const uint8_t* src = valid > 0 ? args.sfb + static_cast<int64_t>(row) * args.sfb_pitch + byte0 : args.sfb;
+          cp_async_4(dst, src, static_cast<uint32_t>(valid));
+        }
+        cp_async_mbar_arrive_noinc(&sf_full[ss]);
       }
     }
     cp_async_wait_all();  // no copy may land after the block has exited
@@ -796,13 +800,13 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn_mx() {
 }
 
 // [E, rows, row_bytes] codes, box 128 bytes (one swizzle atom) x box_rows x 1.
-// [rows, n] 16-bit outputs, boxes of 32 x 32 with the 64-byte swizzle.
+// [rows, n] 16-bit outputs, boxes of 32 columns x EPI_TOKENS rows with the 64-byte swizzle.
 bool encode_out(CUtensorMap* m, moe_dtype dtype, void* ptr, uint64_t n, uint64_t rows) {
   auto fn = encode_fn_mx();
   if (fn == nullptr) return false;
   const cuuint64_t dims[2] = {n, rows};
   const cuuint64_t strides[1] = {n * 2};
-  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t box[2] = {32, EPI_TOKENS};
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, dtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ptr, dims,
             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
