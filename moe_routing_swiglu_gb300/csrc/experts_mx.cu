@@ -28,15 +28,21 @@
 //   warp 1 lane 0   MMAs; warp 1 also owns the TMEM
 //   warps 2..17     epilogue: accumulators to registers in fragment order,
 //                   packed in token pairs, transposed by stmatrix into token
-//                   rows, written in 64-byte runs (or quantised)
-//   warps 18..21    scales: global -> shared a few stages ahead, shared ->
-//                   TMEM by tcgen05.st into one of SLOTS buffers, rewritten
-//                   only after the MMAs that read it have completed
+//                   rows, which leave by bulk tensor stores (or quantised)
+//   warps 18..21    scales, shared -> TMEM by tcgen05.st into one of SLOTS
+//                   buffers, rewritten only after the MMAs that read it
+//   warp 22         scales, global -> shared
 // The scales go to TMEM by stores and not by tcgen05.cp because the copies
 // run on the tensor pipe in turn with the MMAs: eight a stage took 0.2 to
-// 0.3 us beside 0.29 us of MMAs (gate/up of 16384 rows, E=8, H=4096, I=14336:
-// 961 us with copies, 734 us = 5.2 PFLOP/s with stores; the loads alone take
-// 533 us, at the 64 bytes a clock an SM takes in).
+// 0.3 us beside 0.5 us of MMAs.
+//
+// What bounds it (gate/up of 16384 rows, E=8, H=4096, I=14336, 672 us =
+// 5.7 PFLOP/s): an MMA takes 128 clocks whatever its N (the time of its 128-row
+// operand), 8 a stage, 467 us in all; 537 us without the epilogue, which only
+// the loads of the next tile's first stages overlap: two accumulators would
+// need 832 TMEM columns. Tried and slower: N <= 112 with two accumulators
+// (twice the MMAs, 1013 us), one weight tile per MMA with two accumulators (half
+// the work a stage for the same 0.25 us of waits, 979 us).
 //
 // Token tiles: an expert's rows are split evenly into ceil(rows / TBN) tiles
 // of at most TBN (208: what the 512 TMEM columns hold beside three scale
@@ -62,12 +68,10 @@ constexpr int A_BYTES = BM * ROW_BYTES;
 constexpr int ATOM = 512;              // scale atom: 128 rows x 4 scale bytes
 constexpr int ATOMS_K = BK / 128;      // atoms per 128 rows and stage
 constexpr int SFA_BYTES = 2 * ATOMS_K * ATOM;  // scales of both weight tiles of a stage
-constexpr int NUM_EPI_WARPS = 12;     // three per 32 TMEM lanes
-constexpr int SCALE_SETS = 2;          // sets of four warps that write the scale buffers, a stage each in turn
-constexpr int NUM_LOAD_WARPS = 2;      // warps that load scales, a stage each in turn
-constexpr int FIRST_SCALE_WARP = 2 + NUM_EPI_WARPS;
-constexpr int FIRST_LOAD_WARP = FIRST_SCALE_WARP + 4 * SCALE_SETS;
-constexpr int NUM_THREADS = 32 * (FIRST_LOAD_WARP + NUM_LOAD_WARPS);
+constexpr int NUM_EPI_WARPS = 16;     // four per 32 TMEM lanes
+constexpr int FIRST_SCALE_WARP = 2 + NUM_EPI_WARPS;  // four warps, one per 32 TMEM lanes
+constexpr int LOAD_WARP = FIRST_SCALE_WARP + 4;
+constexpr int NUM_THREADS = 32 * (LOAD_WARP + 1);
 constexpr int EPI_TOKENS = 16;         // tokens an epilogue warp takes at a time
 constexpr int XPOSE_BYTES = 1024;      // its transpose buffer: 16 tokens x 32 channels of 16 bits
 constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
@@ -100,14 +104,12 @@ struct MxCfg {
   static constexpr int SMEM_BYTES = 1024 + SMEM_TILES + 8 * (ROUTE_MAX_E + 1);
   static_assert(STAGE_BYTES % 1024 == 0, "swizzle atom alignment");
   static_assert(STAGES >= 3, "pipeline depth");
-  static_assert(SLOTS >= 2 && SLOTS <= STAGES, "a stage barrier advances only once the scale warps have passed its last phase");
+  // Every role walks the stages one by one, so each of its waits by parity
+  // follows on the one before; and a stage's barrier cannot advance twice
+  // before the scale warps have looked at it, because its next MMAs need scales
+  // that they write after.
+  static_assert(SLOTS >= 2 && SLOTS <= STAGES, "scale buffers");
   static_assert(SF_COLS % 8 == 0, "scale stores of 8 columns");
-  // Scale and loader warps take every SCALE_SETS-th (NUM_LOAD_WARPS-th)
-  // stage. A wait by parity is unambiguous only if the use before the awaited
-  // one of the same barrier is known to be over: for the ring's barriers that
-  // is a stage of the same warps when the ring's length is a multiple of the
-  // step; for a stage barrier it is one before the stage last waited for.
-  static_assert(SF_STAGES % SCALE_SETS == 0 && SF_STAGES % NUM_LOAD_WARPS == 0 && SCALE_SETS <= STAGES, "parity waits");
   static_assert(COLS_USED <= 512, "TMEM columns");
   static_assert(TBN % 16 == 0 && TBN <= 256, "token tile");
   static_assert(SMEM_XPOSE % 512 == 0, "the transpose buffers start on the 64-byte swizzle's period");
@@ -678,19 +680,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (lane == 0) mbar_arrive(&tempty[acc]);
     }
     if (lane == 0) bulk_wait_all();  // the stores have left shared memory and are done
-  } else if (warp < FIRST_LOAD_WARP) {
+  } else if (warp < LOAD_WARP) {
     // ------------------------------------------------------------ scales, shared -> TMEM
-    // Set s writes the scale buffers of stages s, s + SCALE_SETS, ...; each of
-    // its four warps its 32 lanes' quarter (the MMA wants the atoms' 32 rows
-    // repeated in the four quarters). One set alone, a stage after another,
-    // took 0.42 us a stage.
-    const uint32_t set = static_cast<uint32_t>(warp - FIRST_SCALE_WARP) / 4;
+    // Each warp writes its 32 lanes' quarter of every stage's scale buffer (the
+    // MMA wants the atoms' 32 rows repeated in the four quarters).
     const uint32_t quad_lane = static_cast<uint32_t>((warp & 3) * 32) << 16;
     uint32_t n = 0;
     bool ok = true;
     for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
       for (int kb = 0; kb < k_blocks; ++kb, ++n) {
-        if (n % SCALE_SETS != set) continue;
         const uint32_t ss = n % SF_STAGES;
         ok = mbar_wait_bounded(&sf_full[ss], (n / SF_STAGES) & 1u, abort_flag, args.status, ST_SCALE_FULL,
                                WAIT_LIMIT_NS);
@@ -707,8 +705,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
 #pragma unroll
         for (int i = 2 * ATOMS_K; i < C::SF_COLS / 4; ++i) v[i] = *reinterpret_cast<const uint4*>(src + i * ATOM);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sf_empty[ss]);
         if (n >= static_cast<uint32_t>(C::SLOTS)) {
           // The buffer's last readers: the MMAs of stage n - SLOTS.
           const uint32_t p = n - C::SLOTS;
@@ -724,24 +720,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sf_ready[n % C::SLOTS]);
+        if (lane == 0) {
+          mbar_arrive(&sf_ready[n % C::SLOTS]);
+          // Only now is the ring slot free: the stores have used the loads'
+          // results. Released right after the loads were issued, a slot could
+          // be overwritten under them.
+          mbar_arrive(&sf_empty[ss]);
+        }
       }
     }
   } else {
     // ------------------------------------------------------------ scales, global -> shared
-    // Loader warp lw fills the ring slots of stages lw, lw + NUM_LOAD_WARPS,
-    // ...: lane 0 with one bulk copy of the weights' atoms, all lanes with the
-    // tokens' words. Word a of token t (its four scale bytes for K elements
-    // 256 kb + 128 a ..) goes to atom (a, t / 128); bytes past K / 32 and rows
-    // past the tile are filled with 0, never read.
-    const uint32_t lw = static_cast<uint32_t>(warp - FIRST_LOAD_WARP);
+    // Lane 0 takes a stage's weight atoms with one bulk copy, all lanes the
+    // tokens' words: word a of token t (its four scale bytes for K elements
+    // 256 kb + 128 a ..) goes to atom (a, t / 128). Bytes past K / 32 and rows
+    // past the tile are filled with 0, never read. (One warp keeps up: two or
+    // four measured the same or slower, each a further poller of barriers.)
     uint32_t n = 0;
     bool ok = true;
     for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
       const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, offs);
       const uint8_t* sfa = args.sfa + (static_cast<int64_t>(tc.e) * args.n_wblocks + tc.w) * k_words * (2 * ATOM);
+      // This lane's tokens lane, lane + 32, ...: their rows, or NULL past the tile's.
+      constexpr int TPL = (TBN + 31) / 32;
+      const uint8_t* rows[TPL];
+#pragma unroll
+      for (int i = 0; i < TPL; ++i) {
+        const int tok = lane + 32 * i;
+        const uint32_t row = tc.row0 + static_cast<uint32_t>(tok);
+        const bool in = tok < tc.rows && row < args.rows_total;
+        rows[i] = in ? args.sfb + static_cast<int64_t>(row) * args.sfb_pitch : nullptr;
+      }
       for (int kb = 0; kb < k_blocks; ++kb, ++n) {
-        if (n % NUM_LOAD_WARPS != lw) continue;
         const uint32_t ss = n % SF_STAGES;
         ok = mbar_wait_bounded(&sf_empty[ss], ((n / SF_STAGES) & 1u) ^ 1u, abort_flag, args.status, ST_LOADER_EMPTY,
                                WAIT_LIMIT_NS);
@@ -755,19 +765,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           mbar_arrive_expect_tx(&sf_full[ss], bytes);
           bulk_load(slot, sfa + static_cast<int64_t>(kb) * SFA_BYTES, bytes, &sf_full[ss]);
         }
-        const uint32_t sfb = smem_u32(slot) + SFA_BYTES;
-#pragma unroll 4
-        for (int i = lane; i < tc.n_tok * ATOMS_K; i += 32) {
-          const int tok = i / ATOMS_K, a = i % ATOMS_K;
-          const uint32_t dst = sfb + static_cast<uint32_t>((a * C::GROUPS + (tok >> 7)) * ATOM + (tok & 31) * 16 +
-                                                           ((tok >> 5) & 3) * 4);
-          const int byte0 = (kb * ATOMS_K + a) * 4;
-          int valid = args.sf_blocks - byte0;
-          valid = valid < 0 ? 0 : valid > 4 ? 4 : valid;
-          const uint32_t row = tc.row0 + static_cast<uint32_t>(tok);
-          if (tok >= tc.rows || row >= args.rows_total) valid = 0;
-          const uint8_t* src = valid > 0 ? args.sfb + static_cast<int64_t>(row) * args.sfb_pitch + byte0 : args.sfb;
-          cp_async_4(dst, src, static_cast<uint32_t>(valid));
+        const uint32_t dst = smem_u32(slot) + SFA_BYTES + static_cast<uint32_t>(lane * 16);
+#pragma unroll
+        for (int i = 0; i < TPL; ++i) {
+          if (32 * i >= tc.n_tok) break;
+#pragma unroll
+          for (int a = 0; a < ATOMS_K; ++a) {
+            const int byte0 = (kb * ATOMS_K + a) * 4;
+            const int valid = rows[i] != nullptr ? max(0, min(4, args.sf_blocks - byte0)) : 0;
+            cp_async_4(dst + static_cast<uint32_t>((a * C::GROUPS + i / 4) * ATOM + (i % 4) * 4),
+                       valid > 0 ? rows[i] + byte0 : args.sfb, static_cast<uint32_t>(valid));
+          }
         }
         cp_async_mbar_arrive_noinc(&sf_full[ss]);
       }

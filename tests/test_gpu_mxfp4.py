@@ -228,6 +228,59 @@ def test_gate_up_matches_the_oracle(cuda_lib, shape, dtype):
     assert torch.equal(hq.codes, q.codes)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("op", ["gate_up", "down"])
+@pytest.mark.parametrize("E,H,I,counts", [
+    (8, 512, 2048, [700, 300, 900, 1, 0, 450, 1000, 208]),
+    (48, 1024, 736, [200 + 3 * i for i in range(48)]),
+    (128, 1536, 768, [i % 4 for i in range(128)])])
+def test_many_tiles_on_every_sm(cuda_lib, op, dtype, E, H, I, counts):
+    """Far more tiles than SMs, so that every ring, accumulator and scale buffer is used over and over: against FP64
+    products on the GPU, and the same bits on every one of twelve runs."""
+    moe = cuda_lib
+    g = torch.Generator(device=DEV).manual_seed(E)
+    K, N = (H, I) if op == "gate_up" else (I, H)
+
+    def mx(*lead, K):
+        return moe.Mxfp4(torch.randint(0, 256, lead + (K // 2,), dtype=torch.uint8, device=DEV, generator=g),
+                         torch.randint(122, 126, lead + (mxfp4.scale_pitch(K),), dtype=torch.uint8, device=DEV,
+                                       generator=g))
+
+    w = [mx(E, I, K=H), mx(E, I, K=H), mx(E, H, K=I)]
+    ex = moe.ExpertsMxfp4(*w)
+    offs = np.concatenate(([0], np.cumsum(counts)))
+    a = mx(int(offs[-1]), K=K)
+    call = moe.moe_experts_mxfp4_gate_up if op == "gate_up" else moe.moe_experts_mxfp4_down
+    o32 = torch.from_numpy(offs).to(torch.int32).to(DEV)
+    got = call(ex, a, o32, dtype=dtype)
+    for _ in range(11):
+        assert torch.equal(got, call(ex, a, o32, dtype=dtype))
+    if op == "gate_up":
+        hq = call(ex, a, o32, dtype=dtype, quantized=True)
+        q = moe.moe_mxfp4_quantize(got)
+        assert torch.equal(hq.codes, q.codes) and torch.equal(hq.scales, q.scales)
+    f = lambda q: moe.moe_mxfp4_dequantize(q, torch.float32).double()
+    av = f(a)
+    for e in range(E):
+        r = slice(int(offs[e]), int(offs[e + 1]))
+        m = [f(moe.Mxfp4(t.codes[e], t.scales[e])) for t in w]
+        if op == "down":
+            ref = av[r] @ m[2].T
+            err = ACC * K * (av[r].abs() @ m[2].abs().T)
+        else:
+            gv, uv = av[r] @ m[0].T, av[r] @ m[1].T
+            eg, eu = (ACC * K * (av[r].abs() @ t.abs().T) for t in m[:2])
+            s = torch.sigmoid(gv)
+            ref = gv * s * uv
+            err = 1.1 * eg * uv.abs() + ((gv * s).abs() + 1.1 * eg) * eu + 2.0 ** -20 * ref.abs()
+        tol = err + HALF_ULP[dtype] * (ref.abs() + err) + TINY[dtype]
+        diff = (got[r].double() - ref).abs()
+        if dtype == torch.float16:   # beyond FP16's largest value: infinity
+            diff = torch.where(ref.abs() < 65000, diff, 0.0)
+        assert bool((diff <= tol).all()), (e, float((diff / tol).max()))
+    assert moe.moe_device_status() == 0
+
+
 def test_forward_dispatched_is_the_two_stages(cuda_lib):
     moe = cuda_lib
     c = Case(5, 416, 544, [70, 0, 3, 230, 16], seed=3)
