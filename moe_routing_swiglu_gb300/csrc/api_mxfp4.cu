@@ -24,6 +24,8 @@ struct moe_experts_mxfp4 {
 namespace {
 
 constexpr int64_t MX_MAX_K = 262144;
+// Dispatched rows of the products: tensor-map coordinates are signed 32-bit.
+constexpr int64_t MX_MAX_ROWS = (int64_t{1} << 31) - 1024;
 
 bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 bool k_valid(int64_t K) { return K >= 32 && K <= MX_MAX_K && K % 32 == 0; }
@@ -58,7 +60,7 @@ moe_status check_stage(const moe_experts_mxfp4* ex, const void* codes, const voi
                        int64_t rows, int dtype) {
   if (ex == nullptr || offsets == nullptr) return api_fail(MOE_ERR_NULL, "experts and offsets must be non-NULL");
   if (!dtype_valid(dtype)) return api_fail(MOE_ERR_DTYPE, "output dtype must be MOE_F32, MOE_F16 or MOE_BF16");
-  if (!rows_valid(rows)) return api_fail(MOE_ERR_SHAPE, "rows must be in 0 .. 2^32-2");
+  if (rows < 0 || rows > MX_MAX_ROWS) return api_fail(MOE_ERR_SHAPE, "rows must be in 0 .. 2^31 - 1024");
   if (rows > 0) {
     const moe_status st = check_mx(codes, scales, "input codes and scales must be non-NULL", MX_ALIGN);
     if (st != MOE_OK) return st;
@@ -247,7 +249,7 @@ moe_status moe_experts_mxfp4_down(const moe_experts_mxfp4* ex, const void* h_cod
 }
 
 size_t moe_experts_mxfp4_forward_dispatched_workspace_size(const moe_experts_mxfp4* ex, int64_t rows) {
-  if (ex == nullptr || !rows_valid(rows)) return 0;
+  if (ex == nullptr || rows < 0 || rows > MX_MAX_ROWS) return 0;
   return hidden_layout(ex, rows).total;
 }
 
@@ -272,7 +274,7 @@ moe_status moe_experts_mxfp4_forward_dispatched(const moe_experts_mxfp4* ex, con
 }
 
 size_t moe_forward_mxfp4_workspace_size(const moe_experts_mxfp4* ex, int64_t T, int32_t top_k, moe_dtype dtype) {
-  if (ex == nullptr || !slots_fit(T, top_k) || !dtype_valid(dtype)) return 0;
+  if (ex == nullptr || T < 0 || top_k < 1 || T > MX_MAX_ROWS / top_k || !dtype_valid(dtype)) return 0;
   return forward_mx_layout(ex, T, top_k, dtype).total;
 }
 
@@ -284,7 +286,7 @@ moe_status moe_forward_mxfp4(const moe_experts_mxfp4* ex, const void* x, moe_dty
   if (!dtype_valid(dtype) || !dtype_valid(logits_dtype))
     return api_fail(MOE_ERR_DTYPE, "dtypes must be MOE_F32, MOE_F16 or MOE_BF16");
   if (top_k < 1 || top_k > ex->E) return api_fail(MOE_ERR_TOP_K, "top_k must satisfy 1 <= top_k <= E");
-  if (!slots_fit(T, top_k)) return api_fail(MOE_ERR_SHAPE, "T must be >= 0 and T*top_k < 2^32-1");
+  if (T < 0 || T > MX_MAX_ROWS / top_k) return api_fail(MOE_ERR_SHAPE, "T must be >= 0 and T*top_k <= 2^31 - 1024");
   if (T > 0 && (x == nullptr || logits == nullptr || out == nullptr))
     return api_fail(MOE_ERR_NULL, "x, logits and out must be non-NULL");
   if (!aligned(x, 16) || !aligned(out, 16)) return api_fail(MOE_ERR_ALIGNMENT, "x and out must be 16-byte aligned");

@@ -117,16 +117,16 @@ struct MxCfg {
 };
 
 // Status codes recorded by a wait that timed out.
-constexpr uint32_t ST_PRODUCER_EMPTY = 0x21;
-constexpr uint32_t ST_MMA_FULL = 0x22;
-constexpr uint32_t ST_MMA_TMEM_EMPTY = 0x23;
-constexpr uint32_t ST_EPI_TMEM_FULL = 0x24;
-constexpr uint32_t ST_MMA_DRAIN = 0x25;
-constexpr uint32_t ST_PRODUCER_DRAIN = 0x26;
-constexpr uint32_t ST_LOADER_EMPTY = 0x27;
-constexpr uint32_t ST_SCALE_SLOT = 0x28;
-constexpr uint32_t ST_SCALE_FULL = 0x29;
-constexpr uint32_t ST_MMA_SF_READY = 0x2A;
+constexpr uint32_t ST_PRODUCER_EMPTY = 0x31;
+constexpr uint32_t ST_MMA_FULL = 0x32;
+constexpr uint32_t ST_MMA_TMEM_EMPTY = 0x33;
+constexpr uint32_t ST_EPI_TMEM_FULL = 0x34;
+constexpr uint32_t ST_MMA_DRAIN = 0x35;
+constexpr uint32_t ST_PRODUCER_DRAIN = 0x36;
+constexpr uint32_t ST_LOADER_EMPTY = 0x37;
+constexpr uint32_t ST_SCALE_SLOT = 0x38;
+constexpr uint32_t ST_SCALE_FULL = 0x39;
+constexpr uint32_t ST_MMA_SF_READY = 0x3A;
 
 struct MxArgs {
   const uint32_t* offsets;   // [E + 1]
@@ -172,10 +172,11 @@ struct MxTile {
 
 // Exclusive prefix of the experts' tiles, tile_start[0..E], and a copy of the
 // offsets, by one warp. Eight experts' counts per lane are loaded before they
-// are used: one trip to memory for 256 experts.
+// are used: one trip to memory for 256 experts. Offsets past
+// the buffers' rows count as the end of the buffers.
 template <int TBN>
-__device__ __forceinline__ void build_mx_prefix(const uint32_t* __restrict__ offsets, int E, int n_wblocks,
-                                                uint32_t* tile_start, uint32_t* offs) {
+__device__ __forceinline__ void build_mx_prefix(const uint32_t* __restrict__ offsets, int E, uint32_t rows_total,
+                                                int n_wblocks, uint32_t* tile_start, uint32_t* offs) {
   constexpr int BATCH = 8;
   const int lane = threadIdx.x & 31;
   uint32_t carry = 0;
@@ -184,8 +185,8 @@ __device__ __forceinline__ void build_mx_prefix(const uint32_t* __restrict__ off
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
       const int e = base + 32 * i + lane;
-      lo[i] = e < E ? offsets[e] : 0u;
-      hi[i] = e < E ? offsets[e + 1] : 0u;
+      lo[i] = e < E ? min(offsets[e], rows_total) : 0u;
+      hi[i] = e < E ? max(min(offsets[e + 1], rows_total), lo[i]) : 0u;
     }
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
@@ -413,7 +414,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(&empty[s], 1);
     }
     for (int s = 0; s < SF_STAGES; ++s) {
-      mbar_init(&sf_full[s], 1 + 32);  // the expect_tx of the weights' atoms, and each lane's copies of the tokens' words
+      mbar_init(&sf_full[s], 1 + 32);  // the weights' expect_tx, and each lane's copies of the tokens' words
       mbar_init(&sf_empty[s], 4);
     }
     for (int s = 0; s < C::SLOTS; ++s) mbar_init(&sf_ready[s], 4);
@@ -437,7 +438,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   }
   // From here on the kernel reads what earlier kernels wrote.
   grid_dependency_wait();
-  if (warp == 0) build_mx_prefix<TBN>(args.offsets, args.E, args.n_wblocks, tile_start, offs);
+  if (warp == 0)
+    build_mx_prefix<TBN>(args.offsets, args.E, args.rows_total, args.n_wblocks, tile_start, offs);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -817,8 +819,8 @@ bool encode_out(CUtensorMap* m, moe_dtype dtype, void* ptr, uint64_t n, uint64_t
   const cuuint32_t box[2] = {32, EPI_TOKENS};
   const cuuint32_t estr[2] = {1, 1};
   return fn(m, dtype == MOE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, ptr, dims,
-            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 bool encode_codes(CUtensorMap* m, const void* ptr, uint64_t row_bytes, uint64_t rows, uint64_t E, uint32_t box_rows,

@@ -182,7 +182,8 @@ __device__ __forceinline__ bool add_unit(const uint4 (&raw)[GC_GROUP], Sum& acc)
   float s[GC_GROUP];
 #pragma unroll
   for (int g = 0; g < GC_GROUP; ++g)
-    s[g] = word_squares<T>(raw[g].w, word_squares<T>(raw[g].z, word_squares<T>(raw[g].y, word_squares<T>(raw[g].x, 0.0f))));
+    s[g] = word_squares<T>(raw[g].w, word_squares<T>(raw[g].z,
+                           word_squares<T>(raw[g].y, word_squares<T>(raw[g].x, 0.0f))));
   const float sum = (s[0] + s[1]) + (s[2] + s[3]);
   // Two-sum: t + err is exactly hi + sum.
   const float t = acc.hi + sum;
@@ -385,7 +386,8 @@ __global__ void __launch_bounds__(GC_THREADS, GC_BLOCKS_PER_SM)
 // Units of a tensor: by its 16-byte vectors, at least one.
 int64_t units_of(const moe_grad_tensor& t) {
   const int64_t bytes = t.numel * static_cast<int64_t>(dtype_size(static_cast<moe_dtype>(t.dtype)));
-  const int64_t head = std::min<int64_t>((16 - static_cast<int64_t>(reinterpret_cast<uintptr_t>(t.src) % 16)) % 16, bytes);
+  const int64_t mis = static_cast<int64_t>(reinterpret_cast<uintptr_t>(t.src) % 16);
+  const int64_t head = std::min<int64_t>((16 - mis) % 16, bytes);
   const int64_t vecs = (bytes - head) / 16;
   return std::max<int64_t>(1, (vecs + GC_UNIT_VECS - 1) / GC_UNIT_VECS);
 }

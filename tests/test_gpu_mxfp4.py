@@ -41,7 +41,8 @@ def special_rows(dtype):
     grid = torch.tensor([0, .25, .5, .75, 1, 1.25, 1.5, 1.75, 2, 2.5, 3, 3.5, 4, 5, 6, 7], dtype=torch.float64)
     both = torch.cat((grid, -grid))
     rows = [torch.zeros(32), -torch.zeros(32), both, both * 2.0 ** -10, both * 3.0, torch.full((32,), big),
-            torch.full((32,), tiny), both * tiny * 8, torch.linspace(-7.999, 7.999, 32), torch.linspace(-1, 1, 32) * big]
+            torch.full((32,), tiny), both * tiny * 8, torch.linspace(-7.999, 7.999, 32),
+            torch.linspace(-1, 1, 32) * big]
     x = torch.stack([r.double() for r in rows])
     for bad in (float("inf"), -float("inf"), float("nan")):
         r = torch.linspace(-3, 3, 32).double()
@@ -331,6 +332,81 @@ def test_pad_bytes_of_scales_are_not_read(cuda_lib):
         p[1][:, nb:] = 255
     ex2, _ = c.on(moe)
     assert torch.equal(ref, moe.moe_experts_mxfp4_forward_dispatched(ex2, c.mx(moe, c.x), offs))
+
+
+def test_offsets_that_leave_the_buffers(cuda_lib):
+    """offsets[E] past the rows of the buffers: the rows that exist are right, nothing else is touched."""
+    moe = cuda_lib
+    c = Case(3, 96, 160, [20, 1, 40], seed=8)
+    ex, offs = c.on(moe)
+    x = c.mx(moe, c.x)
+    ref = moe.moe_experts_mxfp4_gate_up(ex, x, offs)
+    far = offs.clone()
+    far[3] += 300
+    guard = torch.full((c.rows + 400, c.I), 7.0, dtype=torch.bfloat16, device=DEV)
+    moe.moe_experts_mxfp4_gate_up(ex, x, far, out=guard[:c.rows])
+    assert torch.equal(guard[:c.rows], ref) and (guard[c.rows:] == 7.0).all()
+
+
+def test_both_outputs_of_the_first_stage_at_once(cuda_lib):
+    """The C ABI gives h and its quantisation in one call."""
+    import ctypes
+    moe = cuda_lib
+    lib = moe.load_library()
+    c = Case(3, 160, 288, [230, 1, 40], seed=9)
+    ex, offs = c.on(moe)
+    x = c.mx(moe, c.x)
+    for dtype, code in ((torch.float32, 0), (torch.float16, 1), (torch.bfloat16, 2)):
+        h = torch.empty(c.rows, c.I, dtype=dtype, device=DEV)
+        q = moe.Mxfp4(torch.empty(c.rows, c.I // 2, dtype=torch.uint8, device=DEV),
+                      torch.empty(c.rows, mxfp4.scale_pitch(c.I), dtype=torch.uint8, device=DEV))
+        args = [ctypes.c_void_p(t.data_ptr()) for t in (x.codes, x.scales, offs)]
+        st = lib.moe_experts_mxfp4_gate_up(ex.handle, *args, c.rows, code, h.data_ptr(), q.codes.data_ptr(),
+                                           q.scales.data_ptr(), torch.cuda.current_stream().cuda_stream)
+        assert st == 0
+        assert torch.equal(h, moe.moe_experts_mxfp4_gate_up(ex, x, offs, dtype=dtype))
+        ref = moe.moe_mxfp4_quantize(h)
+        assert torch.equal(q.codes, ref.codes) and torch.equal(q.scales, ref.scales)
+        # refusals that need a handle: one of the pair missing, no output, misaligned, too many rows
+        hp = h.data_ptr()
+        for rows, hh, qc, qs, want in ((c.rows, hp, q.codes.data_ptr(), None, 1), (c.rows, None, None, None, 1),
+                                       (c.rows, hp + 2, None, None, 5), (1 << 31, hp, None, None, 2),
+                                       (-1, hp, None, None, 2)):
+            assert lib.moe_experts_mxfp4_gate_up(ex.handle, *args, rows, code, hh, qc, qs, None) == want
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_buffers_on_16_byte_boundaries(cuda_lib, dtype):
+    """Bases that are 16- but not 32-byte aligned (the wide loads and stores do not apply), and odd outputs."""
+    moe = cuda_lib
+    es = torch.finfo(dtype).bits // 8
+    x = activations(7, 224, dtype, 4)
+    buf = torch.empty(7 * 224 + 32, dtype=dtype, device=DEV)
+    v = buf[16 // es:16 // es + 7 * 224].view(7, 224)
+    assert v.data_ptr() % 32 == 16
+    v.copy_(x)
+    codes, scales = mxfp4.quantize(f64(x))
+    q = moe.moe_mxfp4_quantize(v)
+    assert np.array_equal(u8(q.codes), codes) and np.array_equal(u8(q.scales), scales)
+    back = torch.empty(7 * 224 + 32, dtype=dtype, device=DEV)
+    o = back[16 // es:16 // es + 7 * 224].view(7, 224)
+    assert torch.equal(moe.moe_mxfp4_dequantize(q, dtype, out=o), moe.moe_mxfp4_dequantize(q, dtype))
+    c = Case(2, 64, 96, [5, 30], seed=3)
+    ex, offs = c.on(moe)
+    out = torch.empty(35 * 96 + 32, dtype=dtype, device=DEV)
+    o = out[16 // es:16 // es + 35 * 96].view(35, 96)
+    h = moe.moe_experts_mxfp4_gate_up(ex, c.mx(moe, c.x), offs, dtype=dtype)
+    assert torch.equal(moe.moe_experts_mxfp4_gate_up(ex, c.mx(moe, c.x), offs, dtype=dtype, out=o), h)
+
+
+def test_the_largest_expert_count(cuda_lib):
+    moe = cuda_lib
+    counts = [(7 * e) % 3 for e in range(1024)]
+    c = Case(1024, 32, 32, counts, seed=10)
+    ex, offs = c.on(moe)
+    y = moe.moe_experts_mxfp4_down(ex, c.mx(moe, c.h), offs, dtype=torch.float32)
+    hv, w = mxfp4.values(*c.h), c.values()[2]
+    check(y, mxfp4.down(hv, w, c.offsets), ACC * c.I * mxfp4.down(np.abs(hv), np.abs(w), c.offsets), torch.float32, "y")
 
 
 # ------------------------------------------------------------------ the chain

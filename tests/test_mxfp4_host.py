@@ -84,7 +84,8 @@ def _quantize(lib, x=A, dtype=2, rows=4, K=64, inv=None, top_k=1, codes=A, scale
 
 
 @pytest.mark.parametrize("kwargs,status", [
-    (dict(dtype=3), 3), (dict(dtype=-1), 3), (dict(K=0), 2), (dict(K=48), 2), (dict(K=262144 + 32), 2), (dict(K=-32), 2),
+    (dict(dtype=3), 3), (dict(dtype=-1), 3), (dict(K=0), 2), (dict(K=48), 2), (dict(K=262144 + 32), 2),
+    (dict(K=-32), 2),
     (dict(top_k=2), 4), (dict(top_k=0), 4), (dict(inv=A, top_k=0), 4), (dict(rows=-1), 2),
     (dict(rows=1 << 31, inv=A, top_k=2), 2), (dict(rows=(1 << 32) - 1), 2),
     (dict(x=None), 1), (dict(codes=None), 1), (dict(scales=None), 1),
