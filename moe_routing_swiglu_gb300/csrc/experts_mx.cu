@@ -571,13 +571,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       // Rows of the tile that exist in the buffers (all of them, for valid offsets).
       const int live = tc.row0 < args.rows_total
                            ? static_cast<int>(min(static_cast<uint32_t>(tc.rows), args.rows_total - tc.row0)) : 0;
-      for (int c0 = EPI_TOKENS * group; c0 < tc.n_tok; c0 += EPI_TOKENS * (NUM_EPI_WARPS / 4)) {
-        const int64_t row = static_cast<int64_t>(tc.row0) + c0;
-        if constexpr (sizeof(T) == 2) {
-          // Fragments of 16 channels x 16 tokens, packed in token pairs and
-          // transposed by stmatrix into token rows of 32 channels (64 bytes,
-          // 16-byte runs in the 64-byte swizzle: the stores and both kinds of
-          // reads below are free of bank conflicts).
+      constexpr int GROUPS = NUM_EPI_WARPS / 4;
+      // The accumulators may be overwritten once every warp has read its part.
+      auto release = [&]() {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[acc]);
+      };
+      if constexpr (sizeof(T) == 2) {
+        // A chunk is read as fragments of 16 channels x 16 tokens and packed,
+        // token pairs in a word; it leaves through the warp's buffer, transposed
+        // by stmatrix into token rows of 32 channels (64 bytes, 16-byte runs in
+        // the 64-byte swizzle: the stores and both kinds of reads below are free
+        // of bank conflicts). The last HOLD chunks are all read before any of
+        // them is stored: the next tile's MMAs start after the reads, and the
+        // transposes and stores overlap them (gate/up of 16384 rows: 672 -> 639
+        // us; down has twice the words a chunk, and holding all four spills).
+        constexpr int CHUNKS = (TBN / EPI_TOKENS + GROUPS - 1) / GROUPS;
+        constexpr int BLKS = GATE_UP ? 1 : 2;
+        constexpr int HOLD = GATE_UP || CHUNKS < 2 ? CHUNKS : 2;
+        auto read_chunk = [&](int c0, uint32_t (&m)[BLKS][2][4]) {
           uint32_t f0[2][8], f1[2][8];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -587,35 +600,38 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
           tmem_ld_wait();
 #pragma unroll
-          for (int blk = 0; blk < (GATE_UP ? 1 : 2); ++blk) {
-            const int64_t col0 = colA + blk * BM;
-            const bool col_ok = col0 < args.n_out;  // n_out is a multiple of 32: the warp's block is in or out
-            uint32_t m[2][4];
+          for (int i = 0; i < 2; ++i) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int r = 4 * i + 2 * (q & 1);
-                const float a0 = __uint_as_float(f0[q >> 1][r]), a1 = __uint_as_float(f0[q >> 1][r + 1]);
-                const float b0 = __uint_as_float(f1[q >> 1][r]), b1 = __uint_as_float(f1[q >> 1][r + 1]);
-                if (GATE_UP) m[i][q] = pack2<T>(mx_silu<T>(a0) * b0, mx_silu<T>(a1) * b1);
-                else m[i][q] = blk == 0 ? pack2<T>(a0, a1) : pack2<T>(b0, b1);
+            for (int q = 0; q < 4; ++q) {
+              const int r = 4 * i + 2 * (q & 1);
+              const float a0 = __uint_as_float(f0[q >> 1][r]), a1 = __uint_as_float(f0[q >> 1][r + 1]);
+              const float b0 = __uint_as_float(f1[q >> 1][r]), b1 = __uint_as_float(f1[q >> 1][r + 1]);
+              if constexpr (GATE_UP) {
+                m[0][i][q] = pack2<T>(mx_silu<T>(a0) * b0, mx_silu<T>(a1) * b1);
+              } else {
+                m[0][i][q] = pack2<T>(a0, a1);
+                m[BLKS - 1][i][q] = pack2<T>(b0, b1);
               }
             }
-            // The buffer's last bulk store has read it (it had this block's
-            // arithmetic to do so).
-            if (lane == 0) bulk_wait_read_all();
+          }
+        };
+        auto store_chunk = [&](int c0, const uint32_t (&m)[BLKS][2][4]) {
+          const int64_t row = static_cast<int64_t>(tc.row0) + c0;
+#pragma unroll
+          for (int blk = 0; blk < BLKS; ++blk) {
+            const int64_t col0 = colA + blk * BM;
+            if (col0 >= args.n_out) continue;  // n_out is a multiple of 32: the warp's block is in or out
+            if (lane == 0) bulk_wait_read_all();  // the buffer's last bulk store has read it
             __syncwarp();
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int tok = 8 * i + (lane & 7);
               stmatrix_x4_trans(xp_u32 + static_cast<uint32_t>(tok * 64 + (((lane >> 3) ^ (tok >> 1)) & 3) * 16),
-                                m[i][0], m[i][1], m[i][2], m[i][3]);
+                                m[blk][i][0], m[blk][i][1], m[blk][i][2], m[blk][i][3]);
             }
             const bool full_chunk = args.out != nullptr && c0 + EPI_TOKENS <= live;
             if (full_chunk) fence_proxy_async_smem();
             __syncwarp();
-            if (!col_ok) continue;
             if (full_chunk) {
               // Every token is the tile's: one tensor store.
               if (lane == 0) {
@@ -639,7 +655,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                                  live - c0, col0 + MX_BLOCK >= args.n_out);
             __syncwarp();
           }
-        } else {
+        };
+        auto chunk_at = [&](int c) { return EPI_TOKENS * (group + GROUPS * c); };
+        const int mine = (tc.n_tok / EPI_TOKENS - group + GROUPS - 1) / GROUPS;  // this warp's chunks
+        const int first_held = mine > HOLD ? mine - HOLD : 0;
+#pragma unroll 1
+        for (int c = 0; c < first_held; ++c) {
+          uint32_t m[BLKS][2][4];
+          read_chunk(chunk_at(c), m);
+          store_chunk(chunk_at(c), m);
+        }
+        uint32_t held[HOLD][BLKS][2][4];
+#pragma unroll
+        for (int c = 0; c < HOLD; ++c)
+          if (first_held + c < mine) read_chunk(chunk_at(first_held + c), held[c]);
+        release();
+#pragma unroll
+        for (int c = 0; c < HOLD; ++c)
+          if (first_held + c < mine) store_chunk(chunk_at(first_held + c), held[c]);
+      } else {
+        for (int c0 = EPI_TOKENS * group; c0 < tc.n_tok; c0 += EPI_TOKENS * GROUPS) {
+          const int64_t row = static_cast<int64_t>(tc.row0) + c0;
           // FP32: lane = output channel, register = token, 8 tokens at a time
           // through the buffer.
           uint32_t v0[16], v1[16];
@@ -676,10 +712,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             }
           }
         }
+        release();
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[acc]);
     }
     if (lane == 0) bulk_wait_all();  // the stores have left shared memory and are done
   } else if (warp < LOAD_WARP) {
