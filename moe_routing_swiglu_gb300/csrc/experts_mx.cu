@@ -36,18 +36,25 @@
 // run on the tensor pipe in turn with the MMAs: eight a stage took 0.2 to
 // 0.3 us beside 0.5 us of MMAs.
 //
-// What bounds it (gate/up of 16384 rows, E=8, H=4096, I=14336, 672 us =
-// 5.7 PFLOP/s): an MMA takes 128 clocks whatever its N (the time of its 128-row
-// operand), 8 a stage, 467 us in all; 537 us without the epilogue, which only
-// the loads of the next tile's first stages overlap: two accumulators would
-// need 832 TMEM columns. Tried and slower: N <= 112 with two accumulators
-// (twice the MMAs, 1013 us), one weight tile per MMA with two accumulators (half
-// the work a stage for the same 0.25 us of waits, 979 us).
+// What bounds it (gate/up of 16384 rows, E=8, H=4096, I=14336, 645 us =
+// 6.0 PFLOP/s): an MMA takes 128 clocks whatever its N (the time of its 128-row
+// operand), 8 a stage, 467 us in all; the pipeline without the epilogue takes
+// 537 us, and the epilogue's reads of the accumulators are overlapped by
+// nothing but the loads of the next tile's first stages: two accumulators
+// would need 832 TMEM columns. Tried and slower: N <= 112 with two accumulators
+// (twice the MMAs; 1061 us when N <= 208 took 712), one weight tile per MMA with
+// two accumulators (half the work a stage for the same 0.25 us of waits; 979 us
+// when two took 680).
 //
-// Token tiles: an expert's rows are split evenly into ceil(rows / TBN) tiles
-// of at most TBN (208: what the 512 TMEM columns hold beside three scale
-// buffers; 32 for decode, double buffered). Every wait is bounded (about a
-// second), as in experts_tc.cu.
+// Token tiles: an expert's rows are split evenly into ceil(rows / 208) tiles of
+// at most 208 tokens, what the 512 TMEM columns hold beside three scale
+// buffers. Decode batches take the same tiles: 32-token ones with more stages
+// and two accumulators measured within 6 % of them, either way, at 1 to 24
+// rows per expert (gate/up in us, 32 / 208 tokens: 30.6 / 30.6 at one row and
+// 41.7 / 42.9 at 24 for E=128, H=2048, I=768; 81.6 / 79.6 at 24 for E=8,
+// H=4096, I=14336, whose down products they ran in 44.0 / 46.3), and behind
+// from 32 rows on (45.1 / 42.5, 96.6 / 79.8). Every wait is bounded (about
+// a second), as in experts_tc.cu.
 #include <cudaTypedefs.h>
 
 #include <mutex>
@@ -74,9 +81,9 @@ constexpr int LOAD_WARP = FIRST_SCALE_WARP + 4;
 constexpr int NUM_THREADS = 32 * (LOAD_WARP + 1);
 constexpr int EPI_TOKENS = 16;         // tokens an epilogue warp takes at a time
 constexpr int XPOSE_BYTES = 1024;      // its transpose buffer: 16 tokens x 32 channels of 16 bits
+constexpr int TBN = 208;               // most tokens of a tile: the MMA's N
 constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
 
-template <int TBN>
 struct MxCfg {
   static constexpr int GROUPS = (TBN + 127) / 128;           // 128-row groups of the token tile
   static constexpr int STAGE_BYTES = 2 * A_BYTES + TBN * ROW_BYTES;
@@ -85,20 +92,17 @@ struct MxCfg {
   static constexpr int SFB_BYTES = GROUPS * ATOMS_K * ATOM;
   static constexpr int SF_BYTES = SFA_BYTES + SFB_BYTES;     // a stage's scales: their own, deeper ring
   static constexpr int SF_STAGES = 6;
-  // TMEM columns: ACC accumulator buffers of (D0, D1), then SLOTS scale
-  // buffers of (SFA0, SFA1, SFB), 4 columns per atom.
-  static constexpr int ACC = TBN <= 112 ? 2 : 1;
+  // TMEM columns: the accumulators D0 and D1, then SLOTS scale buffers of
+  // (SFA0, SFA1, SFB), 4 columns per atom.
+  static constexpr uint32_t TMEM_COLS = 512;
   static constexpr int SF_COLS = 4 * ATOMS_K * (2 + GROUPS);
-  static constexpr int SF_BASE = ACC * 2 * TBN;
-  static constexpr int SLOTS_FIT = (512 - SF_BASE) / SF_COLS;
-  static constexpr int SLOTS = SLOTS_FIT < 4 ? SLOTS_FIT : 4;
-  static constexpr int COLS_USED = SF_BASE + SLOTS * SF_COLS;
-  static constexpr uint32_t TMEM_COLS = COLS_USED <= 128 ? 128 : COLS_USED <= 256 ? 256 : 512;
+  static constexpr int SF_BASE = 2 * TBN;
+  static constexpr int SLOTS = (static_cast<int>(TMEM_COLS) - SF_BASE) / SF_COLS;
   static constexpr int SMEM_SF = STAGES * STAGE_BYTES;
   static constexpr int SMEM_XPOSE = SMEM_SF + SF_STAGES * SF_BYTES;
   static constexpr int SMEM_BAR = SMEM_XPOSE + NUM_EPI_WARPS * XPOSE_BYTES;
   // full, empty; sf_full, sf_empty; sf_ready; tfull, tempty; drain
-  static constexpr int NUM_BARS = 2 * STAGES + 2 * SF_STAGES + SLOTS + 2 * ACC + 1;
+  static constexpr int NUM_BARS = 2 * STAGES + 2 * SF_STAGES + SLOTS + 3;
   static constexpr int SMEM_MISC = SMEM_BAR + 8 * NUM_BARS;  // TMEM address, abort flag
   static constexpr int SMEM_TILES = SMEM_MISC + 16;          // tile prefix, then the row offsets
   static constexpr int SMEM_BYTES = 1024 + SMEM_TILES + 8 * (ROUTE_MAX_E + 1);
@@ -110,7 +114,6 @@ struct MxCfg {
   // that they write after.
   static_assert(SLOTS >= 2 && SLOTS <= STAGES, "scale buffers");
   static_assert(SF_COLS % 8 == 0, "scale stores of 8 columns");
-  static_assert(COLS_USED <= 512, "TMEM columns");
   static_assert(TBN % 16 == 0 && TBN <= 256, "token tile");
   static_assert(SMEM_XPOSE % 512 == 0, "the transpose buffers start on the 64-byte swizzle's period");
   static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
@@ -159,7 +162,6 @@ struct MxMaps {
 
 // Token tiles of an expert with cnt rows: ceil(cnt / TBN), each of bn rows
 // (a multiple of 16) but the last.
-template <int TBN>
 __device__ __forceinline__ uint32_t token_tiles(uint32_t cnt) { return (cnt + TBN - 1) / TBN; }
 
 struct MxTile {
@@ -174,7 +176,6 @@ struct MxTile {
 // offsets, by one warp. Eight experts' counts per lane are loaded before they
 // are used: one trip to memory for 256 experts. Offsets past
 // the buffers' rows count as the end of the buffers.
-template <int TBN>
 __device__ __forceinline__ void build_mx_prefix(const uint32_t* __restrict__ offsets, int E, uint32_t rows_total,
                                                 int n_wblocks, uint32_t* tile_start, uint32_t* offs) {
   constexpr int BATCH = 8;
@@ -192,7 +193,7 @@ __device__ __forceinline__ void build_mx_prefix(const uint32_t* __restrict__ off
     for (int i = 0; i < BATCH; ++i) {
       const int e = base + 32 * i + lane;
       if (base + 32 * i >= E) break;
-      const uint32_t tiles = token_tiles<TBN>(hi[i] - lo[i]) * static_cast<uint32_t>(n_wblocks);
+      const uint32_t tiles = token_tiles(hi[i] - lo[i]) * static_cast<uint32_t>(n_wblocks);
       uint32_t incl = tiles;
 #pragma unroll
       for (int off = 1; off < 32; off <<= 1) {
@@ -212,7 +213,6 @@ __device__ __forceinline__ void build_mx_prefix(const uint32_t* __restrict__ off
 
 // Tile -> coordinates; token tiles vary fastest so that the CTAs sharing a
 // weight tile run together and read it from L2. Requires tile < tile_start[E].
-template <int TBN>
 __device__ __forceinline__ MxTile decode_mx_tile(uint32_t tile, const uint32_t* tile_start, int E, int n_wblocks,
                                                  const uint32_t* offsets) {
   int lo = 0, hi = E;
@@ -226,7 +226,7 @@ __device__ __forceinline__ MxTile decode_mx_tile(uint32_t tile, const uint32_t* 
   const uint32_t cnt = offsets[lo + 1] - o0;
   // The bounds (nt >= 1, bn <= TBN, w < n_wblocks) hold by themselves for
   // valid offsets; for corrupt ones they keep every access in range.
-  const uint32_t nt = max(token_tiles<TBN>(cnt), 1u);
+  const uint32_t nt = max(token_tiles(cnt), 1u);
   const uint32_t bn = min(((cnt + nt - 1) / nt + 15) & ~15u, static_cast<uint32_t>(TBN));
   const uint32_t local = tile - tile_start[lo];
   const uint32_t w = local / nt;
@@ -383,12 +383,11 @@ __device__ __forceinline__ void quantize_tokens(Run run, uint8_t* codes, uint8_t
   }
 }
 
-template <typename T, bool GATE_UP, int TBN>
+template <typename T, bool GATE_UP>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     experts_mx_kernel(const __grid_constant__ MxMaps maps, const __grid_constant__ MxArgs args) {
-  using C = MxCfg<TBN>;
+  using C = MxCfg;
   constexpr int STAGES = C::STAGES;
-  constexpr int ACC = C::ACC;
   constexpr int SF_STAGES = C::SF_STAGES;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -397,9 +396,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint64_t* sf_full = empty + STAGES;
   uint64_t* sf_empty = sf_full + SF_STAGES;
   uint64_t* sf_ready = sf_empty + SF_STAGES;  // [SLOTS]
-  uint64_t* tfull = sf_ready + C::SLOTS;      // [ACC]
-  uint64_t* tempty = tfull + ACC;     // [ACC]
-  uint64_t* drain = tempty + ACC;
+  uint64_t* tfull = sf_ready + C::SLOTS;
+  uint64_t* tempty = tfull + 1;
+  uint64_t* drain = tempty + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::SMEM_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::SMEM_MISC + 4);
   uint32_t* tile_start = reinterpret_cast<uint32_t*>(smem + C::SMEM_TILES);  // [E + 1]
@@ -418,10 +417,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       mbar_init(&sf_empty[s], 4);
     }
     for (int s = 0; s < C::SLOTS; ++s) mbar_init(&sf_ready[s], 4);
-    for (int a = 0; a < ACC; ++a) {
-      mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], NUM_EPI_WARPS);
-    }
+    mbar_init(tfull, 1);
+    mbar_init(tempty, NUM_EPI_WARPS);
     mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbarrier_init();
@@ -439,7 +436,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   // From here on the kernel reads what earlier kernels wrote.
   grid_dependency_wait();
   if (warp == 0)
-    build_mx_prefix<TBN>(args.offsets, args.E, args.rows_total, args.n_wblocks, tile_start, offs);
+    build_mx_prefix(args.offsets, args.E, args.rows_total, args.n_wblocks, tile_start, offs);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -457,7 +454,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t issued = 0;
       bool ok = true;
       for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-        const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, offs);
+        const MxTile tc = decode_mx_tile(tile, tile_start, args.E, args.n_wblocks, offs);
         const uint32_t tx = static_cast<uint32_t>(2 * A_BYTES + tc.n_tok * ROW_BYTES);
         const int row = tc.w * (GATE_UP ? BM : 2 * BM);
         for (int kb = 0; kb < k_blocks; ++kb) {
@@ -506,15 +503,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       uint32_t it = 0;
       bool ok = true;
       for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x, ++it) {
-        const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, offs);
+        const MxTile tc = decode_mx_tile(tile, tile_start, args.E, args.n_wblocks, offs);
         const uint32_t idesc0 = idesc_mxf4(tc.n_tok, 0), idesc2 = idesc_mxf4(tc.n_tok, 2);
-        const uint32_t acc = it % ACC;
-        if (!mbar_wait_bounded(&tempty[acc], ((it / ACC) & 1u) ^ 1u, abort_flag, args.status, ST_MMA_TMEM_EMPTY,
+        if (!mbar_wait_bounded(tempty, (it & 1u) ^ 1u, abort_flag, args.status, ST_MMA_TMEM_EMPTY,
                                WAIT_LIMIT_NS)) {
           ok = false;
           break;
         }
-        const uint32_t d0 = tmem_base + acc * (2 * TBN);
         for (int kb = 0; kb < k_blocks; ++kb, ++n) {
           const uint32_t stage = n % STAGES, slot = n % C::SLOTS;
           if (!mbar_wait_bounded(&full[stage], (n / STAGES) & 1u, abort_flag, args.status, ST_MMA_FULL,
@@ -536,15 +531,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               const uint32_t id = (k & 1) != 0 ? idesc2 : idesc0;
               const uint64_t bd = sdesc_kmajor_sw128(b + k * (UMMA_K / 2));
               const uint32_t sb = sfb + 4 * (k >> 1) * C::GROUPS;
-              umma_mxf4(d0, sdesc_kmajor_sw128(a0 + k * (UMMA_K / 2)), bd, id, sf + 4 * (k >> 1), sb, accum);
-              umma_mxf4(d0 + TBN, sdesc_kmajor_sw128(a1 + k * (UMMA_K / 2)), bd, id,
+              umma_mxf4(tmem_base, sdesc_kmajor_sw128(a0 + k * (UMMA_K / 2)), bd, id, sf + 4 * (k >> 1), sb, accum);
+              umma_mxf4(tmem_base + TBN, sdesc_kmajor_sw128(a1 + k * (UMMA_K / 2)), bd, id,
                         sf + 4 * ATOMS_K + 4 * (k >> 1), sb, accum);
             }
           }
           umma_commit(&empty[stage]);
         }
         if (!ok) break;
-        umma_commit(&tfull[acc]);
+        umma_commit(tfull);
       }
       // Every copy and MMA issued above completes before TMEM is released.
       umma_commit(drain);
@@ -560,13 +555,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t xp_u32 = smem_u32(xp);
     uint32_t it = 0;
     for (uint32_t tile = blockIdx.x; tile < total; tile += gridDim.x, ++it) {
-      const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, offs);
-      const uint32_t acc = it % ACC;
-      const bool ok = mbar_wait_bounded(&tfull[acc], (it / ACC) & 1u, abort_flag, args.status, ST_EPI_TMEM_FULL,
+      const MxTile tc = decode_mx_tile(tile, tile_start, args.E, args.n_wblocks, offs);
+      const bool ok = mbar_wait_bounded(tfull, it & 1u, abort_flag, args.status, ST_EPI_TMEM_FULL,
                                         WAIT_LIMIT_NS);
       if (!__all_sync(FULL_MASK, ok)) break;  // tcgen05.ld is warp-collective: the whole warp goes on or stops
       tc_fence_after();
-      const uint32_t t_lane = tmem_base + acc * (2 * TBN) + (static_cast<uint32_t>(quad * 32) << 16);
+      const uint32_t t_lane = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
       const int64_t colA = static_cast<int64_t>(tc.w) * (GATE_UP ? BM : 2 * BM) + quad * 32;
       // Rows of the tile that exist in the buffers (all of them, for valid offsets).
       const int live = tc.row0 < args.rows_total
@@ -576,7 +570,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       auto release = [&]() {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&tempty[acc]);
+        if (lane == 0) mbar_arrive(tempty);
       };
       if constexpr (sizeof(T) == 2) {
         // A chunk is read as fragments of 16 channels x 16 tokens and packed,
@@ -589,7 +583,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         // us; down has twice the words a chunk, and holding all four spills).
         constexpr int CHUNKS = (TBN / EPI_TOKENS + GROUPS - 1) / GROUPS;
         constexpr int BLKS = GATE_UP ? 1 : 2;
-        constexpr int HOLD = GATE_UP || CHUNKS < 2 ? CHUNKS : 2;
+        constexpr int HOLD = GATE_UP ? CHUNKS : 2;
         auto read_chunk = [&](int c0, uint32_t (&m)[BLKS][2][4]) {
           uint32_t f0[2][8], f1[2][8];
 #pragma unroll
@@ -775,7 +769,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     uint32_t n = 0;
     bool ok = true;
     for (uint32_t tile = blockIdx.x; ok && tile < total; tile += gridDim.x) {
-      const MxTile tc = decode_mx_tile<TBN>(tile, tile_start, args.E, args.n_wblocks, offs);
+      const MxTile tc = decode_mx_tile(tile, tile_start, args.E, args.n_wblocks, offs);
       const uint8_t* sfa = args.sfa + (static_cast<int64_t>(tc.e) * args.n_wblocks + tc.w) * k_words * (2 * ATOM);
       // This lane's tokens lane, lane + 32, ...: their rows, or NULL past the tile's.
       constexpr int TPL = (TBN + 31) / 32;
@@ -870,10 +864,10 @@ bool encode_codes(CUtensorMap* m, const void* ptr, uint64_t row_bytes, uint64_t 
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, bool GATE_UP, int TBN>
+template <typename T, bool GATE_UP>
 cudaError_t launch_mx(const MxMaps& maps, MxArgs args, int64_t rows, int num_sms, cudaStream_t stream) {
-  auto kern = experts_mx_kernel<T, GATE_UP, TBN>;
-  constexpr int SMEM_BYTES = MxCfg<TBN>::SMEM_BYTES;
+  auto kern = experts_mx_kernel<T, GATE_UP>;
+  constexpr int SMEM_BYTES = MxCfg::SMEM_BYTES;
   cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (err != cudaSuccess) return err;
   // At most ceil(rows_e / TBN) token tiles per expert.
@@ -891,8 +885,8 @@ struct MxOperands {
   const void* tokens;  // [rows, K / 2]
 };
 
-template <typename T, int TBN>
-cudaError_t stage_n(const MxOperands& op, const MxArgs& args, int64_t rows, int num_sms, cudaStream_t stream,
+template <typename T>
+cudaError_t stage_t(const MxOperands& op, const MxArgs& args, int64_t rows, int num_sms, cudaStream_t stream,
                     const char** why) {
   const uint64_t kb = static_cast<uint64_t>(args.K / 2), N = static_cast<uint64_t>(args.n_out);
   const uint64_t E = static_cast<uint64_t>(args.E);
@@ -910,15 +904,8 @@ cudaError_t stage_n(const MxOperands& op, const MxArgs& args, int64_t rows, int 
     *why = "cuTensorMapEncodeTiled rejected a tensor map";
     return cudaErrorInvalidValue;
   }
-  return op.gate_up ? launch_mx<T, true, TBN>(maps, args, rows, num_sms, stream)
-                    : launch_mx<T, false, TBN>(maps, args, rows, num_sms, stream);
-}
-
-template <typename T>
-cudaError_t stage_t(const MxOperands& op, const MxArgs& args, int64_t rows, int num_sms, cudaStream_t stream,
-                    const char** why) {
-  if (rows <= 8 * static_cast<int64_t>(args.E)) return stage_n<T, 32>(op, args, rows, num_sms, stream, why);
-  return stage_n<T, 208>(op, args, rows, num_sms, stream, why);
+  return op.gate_up ? launch_mx<T, true>(maps, args, rows, num_sms, stream)
+                    : launch_mx<T, false>(maps, args, rows, num_sms, stream);
 }
 
 }  // namespace

@@ -17,8 +17,8 @@
 // loads in FP32 and carries the units' sums as a compensated pair of FP32 (the
 // rounding error of each addition is kept in the second word; one FP64
 // addition per unit kept the FP64 units busy for a third of the time: BF16
-// norm of 300 MB 65 us). FP32 squares overflow above 1.8e19 and lose bits
-// below 1e-19, so a unit's sum above 2^80 or below 2^-60 that is not of zeros
+// norm of 300 MB 65 us, now 48 us = 6.2 TB/s, its clip 96 us = 6.3 TB/s).
+// FP32 squares overflow above 1.8e19 and lose bits below 1e-19, so a unit's sum above 2^80 or below 2^-60 that is not of zeros
 // alone is read and added again in FP64. Threads and blocks are
 // added in FP64. Every sum has a fixed order: block b's units, its threads by
 // a fixed tree, the blocks by one last block; the result does not depend on
