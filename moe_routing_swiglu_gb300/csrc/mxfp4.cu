@@ -186,8 +186,8 @@ struct DequantArgs {
 };
 
 // One thread: 8 bytes of codes -> 16 values. Bound by HBM writes: 16384 x 4096
-// to BF16 31 us in repeated calls (170 MB; 36.6 with a unit's two 16-byte halves stored in turn),
-// 98304 x 2048 to BF16 89 us (5.7 TB/s).
+// to BF16 31 us in repeated calls (170 MB; 36.6 with a unit's two 16-byte
+// halves stored in turn), 98304 x 2048 to BF16 89 us (5.7 TB/s).
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(MXQ_THREADS) mx_dequantize_kernel(const DequantArgs a) {
   grid_dependency_wait();
