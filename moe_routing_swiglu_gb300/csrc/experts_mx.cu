@@ -37,9 +37,9 @@
 // 0.3 us beside 0.5 us of MMAs.
 //
 // What bounds it (gate/up of 16384 rows, E=8, H=4096, I=14336, 645 us =
-// 6.0 PFLOP/s): an MMA takes 128 clocks whatever its N (the time of its 128-row
-// operand), 8 a stage, 467 us in all; the pipeline without the epilogue takes
-// 537 us, and the epilogue's reads of the accumulators are overlapped by
+// 6.0 PFLOP/s): an MMA takes about 128 clocks at N = 112 as at N = 208 (from a
+// stage's time without loads and epilogue), 8 a stage, 467 us in all; the
+// pipeline without the epilogue takes 537 us, and the epilogue's reads of the accumulators are overlapped by
 // nothing but the loads of the next tile's first stages: two accumulators
 // would need 832 TMEM columns. Tried and slower: N <= 112 with two accumulators
 // (twice the MMAs; 1061 us when N <= 208 took 712), one weight tile per MMA with
