@@ -819,11 +819,12 @@ moe_status moe_grad_clip(const moe_grad_tensor* tensors, int64_t n, const float*
  * down launch waiting for its expert's h rows, 0x1A the combine of
  * moe_experts_forward_combine waiting for the last down tile, 0x1B the grid
  * barrier of moe_route_dispatch and moe_route_sigmoid_grouped_dispatch (and
- * of the forward calls' routing), 0x31 - 0x3A the waits of the MXFP4 expert
+ * of the forward calls' routing), 0x31 - 0x3B the waits of the MXFP4 expert
  * products (0x31 producer, 0x32 MMA for a loaded stage, 0x33 MMA for a drained
  * accumulator, 0x34 epilogue, 0x35 / 0x36 teardown drains, 0x37 scale loader
  * for a free ring slot, 0x38 scale warps for a free scale buffer, 0x39 for a
- * loaded ring slot, 0x3A MMA for a stage's scales), 0x100
+ * loaded ring slot, 0x3A MMA for a stage's scales, 0x3B a teardown drain of
+ * the scale loader), 0x100
  * moe_selftest_bounded_wait. Synchronises the current device; *code = 0 when
  * no wait has timed out.
  */

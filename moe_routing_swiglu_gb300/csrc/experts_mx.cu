@@ -63,6 +63,7 @@
 #include "moe_common.cuh"
 #include "moe_internal.h"
 #include "mxfp4.cuh"
+#include "ring_drain.h"
 
 namespace moe {
 namespace {
@@ -103,7 +104,7 @@ struct MxCfg {
   static constexpr int SMEM_BAR = SMEM_XPOSE + NUM_EPI_WARPS * XPOSE_BYTES;
   // full, empty; sf_full, sf_empty; sf_ready; tfull, tempty; drain
   static constexpr int NUM_BARS = 2 * STAGES + 2 * SF_STAGES + SLOTS + 3;
-  static constexpr int SMEM_MISC = SMEM_BAR + 8 * NUM_BARS;  // TMEM address, abort flag
+  static constexpr int SMEM_MISC = SMEM_BAR + 8 * NUM_BARS;  // TMEM address, abort flag, stages issued by the two loaders
   static constexpr int SMEM_TILES = SMEM_MISC + 16;          // tile prefix, then the row offsets
   static constexpr int SMEM_BYTES = 1024 + SMEM_TILES + 8 * (ROUTE_MAX_E + 1);
   static_assert(STAGE_BYTES % 1024 == 0, "swizzle atom alignment");
@@ -130,6 +131,7 @@ constexpr uint32_t ST_LOADER_EMPTY = 0x37;
 constexpr uint32_t ST_SCALE_SLOT = 0x38;
 constexpr uint32_t ST_SCALE_FULL = 0x39;
 constexpr uint32_t ST_MMA_SF_READY = 0x3A;
+constexpr uint32_t ST_LOADER_DRAIN = 0x3B;
 
 struct MxArgs {
   const uint32_t* offsets;   // [E + 1]
@@ -401,6 +403,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint64_t* drain = tempty + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::SMEM_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::SMEM_MISC + 4);
+  uint32_t* issued_stages = reinterpret_cast<uint32_t*>(smem + C::SMEM_MISC + 8);  // producer's, scale loader's
   uint32_t* tile_start = reinterpret_cast<uint32_t*>(smem + C::SMEM_TILES);  // [E + 1]
   uint32_t* offs = tile_start + args.E + 1;                                   // [E + 1]
 
@@ -485,15 +488,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
       }
       launch_dependents();  // this CTA issues no more loads
-      if (!ok) {
-        // Let the copies already in flight land before the block can exit.
-        const uint32_t n_back = issued < STAGES ? issued : STAGES;
-        for (uint32_t i = 1; i <= n_back; ++i) {
-          const uint32_t n = issued - i;
-          mbar_wait_bounded(&full[n % STAGES], (n / STAGES) & 1u, nullptr, args.status, ST_PRODUCER_DRAIN,
-                            WAIT_LIMIT_NS);
-        }
-      }
+      issued_stages[0] = issued;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -810,11 +805,27 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         cp_async_mbar_arrive_noinc(&sf_full[ss]);
       }
     }
-    cp_async_wait_all();  // no copy may land after the block has exited
+    cp_async_wait_all();  // this lane's copies of token scales; the bulk copies of weight scales are waited for below
+    if (lane == 0) issued_stages[1] = n;
   }
 
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag != 0) {
+    // A role gave up: the copies that nobody waited for land before the block
+    // exits (they would write shared memory, and signal barriers, that are the
+    // next block's). Every lane of the scale loader has arrived on each stage
+    // that its lane 0 armed: it leaves its loop before arming, as one warp.
+    if (threadIdx.x == 0)
+      drain_ring(issued_stages[0], STAGES, [&](uint32_t slot, uint32_t parity) {
+        mbar_wait_bounded(&full[slot], parity, nullptr, args.status, ST_PRODUCER_DRAIN, WAIT_LIMIT_NS);
+      });
+    if (threadIdx.x == 32 * LOAD_WARP)
+      drain_ring(issued_stages[1], SF_STAGES, [&](uint32_t slot, uint32_t parity) {
+        mbar_wait_bounded(&sf_full[slot], parity, nullptr, args.status, ST_LOADER_DRAIN, WAIT_LIMIT_NS);
+      });
+    __syncwarp();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM_COLS);
