@@ -33,6 +33,7 @@
 
 #include "moe_common.cuh"
 #include "moe_internal.h"
+#include "ring_drain.h"
 
 namespace moe {
 namespace {
@@ -96,7 +97,7 @@ struct BwdCfg {
   static constexpr int SMEM_BAR = SMEM_XPOSE + NUM_EPI_WARPS * XPOSE_WARP;
   static constexpr int NUM_BARS = 2 * STAGES + 2 * RING + 5;
   static constexpr int SMEM_RING = SMEM_BAR + 8 * NUM_BARS;
-  static constexpr int SMEM_MISC = SMEM_RING + 4 * RING;
+  static constexpr int SMEM_MISC = SMEM_RING + 4 * RING;               // TMEM address, abort flag, stages issued
   static constexpr int SMEM_TILES = SMEM_MISC + 16;
   static constexpr int SMEM_BYTES = 1024 + SMEM_TILES + (DGRAD ? 4 * (ROUTE_MAX_E + 1) : 0);
   static_assert(STAGE_BYTES % 1024 == 0, "stage alignment");
@@ -151,6 +152,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   volatile uint32_t* ring = reinterpret_cast<volatile uint32_t*>(smem + C::SMEM_RING);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::SMEM_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::SMEM_MISC + 4);
+  uint32_t* issued_stages = reinterpret_cast<uint32_t*>(smem + C::SMEM_MISC + 8);
   uint32_t* tile_start = reinterpret_cast<uint32_t*>(smem + C::SMEM_TILES);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
@@ -305,14 +307,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         if (!ok) break;
       }
-      if (!ok) {
-        const uint32_t n_back = issued < STAGES ? issued : STAGES;
-        for (uint32_t i = 1; i <= n_back; ++i) {
-          const uint32_t n = issued - i;
-          mbar_wait_bounded(&full[n % STAGES], (n / STAGES) & 1u, nullptr, args.status, ST_PRODUCER_DRAIN,
-                            WAIT_LIMIT_NS);
-        }
-      }
+      *issued_stages = issued;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -580,6 +575,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag != 0) {
+    // A role gave up: the copies that nobody waited for land before the block exits.
+    if (threadIdx.x == 0)
+      drain_ring(*issued_stages, STAGES, [&](uint32_t slot, uint32_t parity) {
+        mbar_wait_bounded(&full[slot], parity, nullptr, args.status, ST_PRODUCER_DRAIN, WAIT_LIMIT_NS);
+      });
+    __syncwarp();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);

@@ -69,6 +69,7 @@
 
 #include "moe_common.cuh"
 #include "moe_internal.h"
+#include "ring_drain.h"
 
 namespace moe {
 
@@ -116,7 +117,7 @@ struct TcCfg {
   // full[S], empty[S], tile_full[R], tile_empty[R], tfull[2], tempty[2], drain
   static constexpr int NUM_BARS = 2 * STAGES + 2 * RING + 5;
   static constexpr int SMEM_RING = SMEM_BAR + 8 * NUM_BARS;
-  static constexpr int SMEM_MISC = SMEM_RING + 4 * RING;          // TMEM address, abort flag, combine flag
+  static constexpr int SMEM_MISC = SMEM_RING + 4 * RING;          // TMEM address, abort flag, combine flag, stages issued
   static constexpr int SMEM_BAD = SMEM_MISC + 16;                  // [RING][BAD_WORDS]
   static constexpr int SMEM_TILES = SMEM_BAD + 4 * RING * BAD_WORDS;
   static constexpr int SMEM_BYTES = 1024 + SMEM_TILES + 4 * (ROUTE_MAX_E + 1);
@@ -326,6 +327,7 @@ __global__ void __launch_bounds__(num_threads<LOAD>(), 1)
   volatile uint32_t* ring = reinterpret_cast<volatile uint32_t*>(smem + C::SMEM_RING);
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + C::SMEM_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::SMEM_MISC + 4);
+  uint32_t* issued_stages = reinterpret_cast<uint32_t*>(smem + C::SMEM_MISC + 12);
   volatile uint32_t* tile_bad = reinterpret_cast<volatile uint32_t*>(smem + C::SMEM_BAD);
   uint32_t* tile_start = reinterpret_cast<uint32_t*>(smem + C::SMEM_TILES);
   uint32_t* tile_start2 = reinterpret_cast<uint32_t*>(smem + C::SMEM_TILES2);  // CHAIN: down tiles
@@ -526,15 +528,7 @@ __global__ void __launch_bounds__(num_threads<LOAD>(), 1)
       }
       if (!ok) break;
     }
-    if (!ok && lane == 0) {
-      // Let the copies already in flight land before the block can exit.
-      const uint32_t n_back = issued < STAGES ? issued : STAGES;
-      for (uint32_t i = 1; i <= n_back; ++i) {
-        const uint32_t n = issued - i;
-        mbar_wait_bounded(&full[n % STAGES], (n / STAGES) & 1u, nullptr, args.status, ST_PRODUCER_DRAIN,
-                          WAIT_LIMIT_NS);
-      }
-    }
+    if (lane == 0) *issued_stages = issued;
     __syncwarp();
   } else if (warp == 0) {
     // ------------------------------------------------------------ scheduler + TMA producer
@@ -611,15 +605,7 @@ __global__ void __launch_bounds__(num_threads<LOAD>(), 1)
         }
         if (!ok) break;
       }
-      if (!ok) {
-        // Let the copies already in flight land before the block can exit.
-        const uint32_t n_back = issued < STAGES ? issued : STAGES;
-        for (uint32_t i = 1; i <= n_back; ++i) {
-          const uint32_t n = issued - i;
-          mbar_wait_bounded(&full[n % STAGES], (n / STAGES) & 1u, nullptr, args.status,
-                            ST_PRODUCER_DRAIN, WAIT_LIMIT_NS);
-        }
-      }
+      *issued_stages = issued;
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -935,6 +921,16 @@ __global__ void __launch_bounds__(num_threads<LOAD>(), 1)
 
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag != 0) {
+    // A role gave up: the copies that nobody waited for land before the block
+    // exits. (A token loader that stopped short of a stage leaves its barrier
+    // one arrival short: that wait runs to its limit, long after the copy.)
+    if (threadIdx.x == 0)
+      drain_ring(*issued_stages, STAGES, [&](uint32_t slot, uint32_t parity) {
+        mbar_wait_bounded(&full[slot], parity, nullptr, args.status, ST_PRODUCER_DRAIN, WAIT_LIMIT_NS);
+      });
+    __syncwarp();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem_base, TMEM_COLS);

@@ -70,7 +70,7 @@ def test_every_copy_in_flight_is_waited_for(tmp_path):
 
 
 # file: the "full" barriers of the rings that bulk copies of the file's kernel fill
-RINGS = {"experts_mx.cu": {"full", "sf_full"}}
+RINGS = {"experts_mx.cu": {"full", "sf_full"}, "experts_tc.cu": {"full"}, "experts_bwd_tc.cu": {"full"}}
 
 
 @pytest.mark.parametrize("name", sorted(RINGS))
