@@ -811,7 +811,10 @@ class ExpertsMxfp4:
     """SwiGLU experts in MXFP4: a handle over gate/up [E, I, H] and down
     [E, H, I] (Mxfp4 tensors; the codes are kept alive here, the scales are
     laid out once for the tensor cores). Waits for its set-up, so that the
-    handle can be used on any stream; not to be made during a graph capture."""
+    handle can be used on any stream, and may be dropped while a call's work
+    is still queued: its memory is handed out again only after the streams that
+    used it. A captured graph is not such a stream: the handle has to outlive
+    its replays. Not to be made during a graph capture."""
 
     def __init__(self, gate: Mxfp4, up: Mxfp4, down: Mxfp4):
         lib = load_library()
@@ -826,6 +829,7 @@ class ExpertsMxfp4:
         self.E, self.H, self.I = E, H, I
         self.device = gc.device
         self._codes = (gc, uc, dc)
+        self._streams = set()   # the raw streams that the allocator knows as users of the codes and scales
         self._storage = torch.empty(max(1, lib.moe_experts_mxfp4_storage_size(E, H, I)), dtype=torch.uint8,
                                     device=gc.device)
         handle = ctypes.c_void_p()
@@ -839,6 +843,15 @@ class ExpertsMxfp4:
     def from_float(cls, gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor) -> "ExpertsMxfp4":
         """Quantise float gate/up [E, I, H] and down [E, H, I]."""
         return cls(*(moe_mxfp4_quantize(t) for t in (gate, up, down)))
+
+    def _used_on(self, raw: int, stream) -> None:
+        """Tells the allocator, once per stream, that a call reads the codes and scales on it: a handle that is
+        dropped with work queued there keeps its blocks until that work is done."""
+        if raw not in self._streams:
+            s = torch.cuda.current_stream() if stream is None else stream
+            for t in (*self._codes, self._storage):
+                t.record_stream(s)
+            self._streams.add(raw)
 
     def __del__(self):
         if getattr(self, "handle", None) and _lib is not None:
@@ -877,6 +890,7 @@ def moe_experts_mxfp4_gate_up(experts: ExpertsMxfp4, x: Mxfp4, offsets: torch.Te
     lib = load_library()
     codes, scales, rows = _mx_rows(experts, x, "x", experts.H, offsets)
     raw = _here(stream, codes, scales, offsets)
+    experts._used_on(raw, stream)
     if dtype not in _DTYPE:
         raise MoeError(3, f"unsupported dtype {dtype}")
     h, hc, hs = None, None, None
@@ -901,6 +915,7 @@ def moe_experts_mxfp4_down(experts: ExpertsMxfp4, h: Mxfp4, offsets: torch.Tenso
     lib = load_library()
     codes, scales, rows = _mx_rows(experts, h, "h", experts.I, offsets)
     raw = _here(stream, codes, scales, offsets)
+    experts._used_on(raw, stream)
     y = _mx_out(out, rows, experts.H, dtype, codes.device, stream)
     _check(lib.moe_experts_mxfp4_down(experts.handle, codes.data_ptr(), scales.data_ptr(), offsets.data_ptr(), rows,
                                       _dt(y), y.data_ptr(), raw))
@@ -915,6 +930,7 @@ def moe_experts_mxfp4_forward_dispatched(experts: ExpertsMxfp4, x: Mxfp4, offset
     lib = load_library()
     codes, scales, rows = _mx_rows(experts, x, "x", experts.H, offsets)
     raw = _here(stream, codes, scales, offsets, workspace)
+    experts._used_on(raw, stream)
     y = _mx_out(out, rows, experts.H, dtype, codes.device, stream)
     need = lib.moe_experts_mxfp4_forward_dispatched_workspace_size(experts.handle, rows)
     ws = _scratch(need, codes.device, workspace, stream)
@@ -941,6 +957,7 @@ def moe_forward_mxfp4(experts: ExpertsMxfp4, x: torch.Tensor, logits: torch.Tens
         if t is not None and (_dev_tensor(t, name).numel() != T * top_k or t.element_size() != es):
             raise MoeError(2, f"{name} must hold T * top_k entries")
     raw = _here(stream, x, logits, indices, weights, workspace)
+    experts._used_on(raw, stream)
     o = _mx_out(out, T, experts.H, x.dtype, x.device, stream)
     ws = _scratch(lib.moe_forward_mxfp4_workspace_size(experts.handle, T, top_k, _dt(x)), x.device, workspace, stream)
     _check(lib.moe_forward_mxfp4(experts.handle, x.data_ptr(), _dt(x), logits.data_ptr(), _dt(logits), T, top_k,
