@@ -944,7 +944,9 @@ def moe_forward_mxfp4(experts: ExpertsMxfp4, x: torch.Tensor, logits: torch.Tens
                       out=None, indices=None, weights=None, workspace=None, stream=None) -> torch.Tensor:
     """The whole local chain on MXFP4 experts: x [T, H] (float32, float16 or
     bfloat16) is routed, quantised into dispatched order, run through the
-    experts' 4-bit products and combined to out [T, H] in x's dtype."""
+    experts' 4-bit products and combined to out [T, H] in x's dtype. indices
+    and weights, where given, receive the routing: T * top_k entries, uint32
+    (or its int32 view) and the logits' dtype."""
     lib = load_library()
     _dev_tensor(x, "x")
     _dev_tensor(logits, "logits")
@@ -953,9 +955,13 @@ def moe_forward_mxfp4(experts: ExpertsMxfp4, x: torch.Tensor, logits: torch.Tens
     T = x.shape[0]
     if tuple(logits.shape) != (T, experts.E):
         raise MoeError(2, f"logits must be [{T}, {experts.E}]")
-    for t, name, es in ((indices, "indices", 4), (weights, "weights", logits.element_size())):
-        if t is not None and (_dev_tensor(t, name).numel() != T * top_k or t.element_size() != es):
+    for t, name in ((indices, "indices"), (weights, "weights")):
+        if t is not None and _dev_tensor(t, name).numel() != T * top_k:
             raise MoeError(2, f"{name} must hold T * top_k entries")
+    if indices is not None and indices.dtype not in (torch.int32, getattr(torch, "uint32", torch.int32)):
+        raise MoeError(3, "indices must be uint32 (or its int32 view)")
+    if weights is not None and weights.dtype != logits.dtype:
+        raise MoeError(3, f"weights must be in the logits' dtype, {logits.dtype}")
     raw = _here(stream, x, logits, indices, weights, workspace)
     experts._used_on(raw, stream)
     o = _mx_out(out, T, experts.H, x.dtype, x.device, stream)

@@ -1,4 +1,5 @@
-"""GPU checks of the MXFP4 experts at the ends of their ranges: handles dropped while their work is queued."""
+"""GPU checks of the MXFP4 experts at the ends of their ranges: handles dropped while their work is queued, and buffers
+of another type."""
 import pytest
 import torch
 
@@ -38,3 +39,20 @@ def test_a_handle_dropped_while_its_work_is_queued(cuda_lib, how):
     torch.cuda.synchronize()
     assert moe.moe_device_status() == 0
     assert torch.equal(out, ref) and len(junk) == 8
+
+
+def test_forward_refuses_buffers_of_another_type(cuda_lib):
+    """The routing weights come in the logits' type and the indices as 32-bit integers: a buffer of the same size but
+    another type would be read as something else."""
+    moe = cuda_lib
+    ex, _ = _layer(moe, 3, 64, 96, torch.bfloat16, 1)
+    x = torch.zeros(8, 64, dtype=torch.bfloat16, device=DEV)
+    lg = torch.zeros(8, 3, dtype=torch.bfloat16, device=DEV)
+    e = lambda dtype: torch.empty(8, 2, dtype=dtype, device=DEV)
+    for kw in (dict(weights=e(torch.float16)), dict(weights=e(torch.int16)), dict(indices=e(torch.float32)),
+               dict(weights=e(torch.bfloat16), indices=e(torch.float32))):
+        with pytest.raises(moe.MoeError):
+            moe.moe_forward_mxfp4(ex, x, lg, 2, True, **kw)
+    w, i = e(torch.bfloat16), e(torch.int32)
+    moe.moe_forward_mxfp4(ex, x, lg, 2, True, weights=w, indices=i)
+    assert torch.equal(w, torch.full_like(w, 0.5)) and i.tolist() == [[0, 1]] * 8
