@@ -711,8 +711,9 @@ void moe_experts_mxfp4_destroy(moe_experts_mxfp4* experts);
  *   dtype         MOE_F32, MOE_F16 or MOE_BF16.
  *
  * No workspace. A row with a NaN block gives NaN outputs for its token only.
- * 16-bit h: SiLU by the hardware's exponential and reciprocal (relative error
- * a few 2^-22, 2^-17 for |g| near 88), far below the rounding to the type.
+ * SiLU's relative error: below 2^-20 for FP32 h, 2^-20 + |g| 2^-23 for 16-bit
+ * h (the hardware's exponential), and 2^-142 more; a SiLU below 2^-126, where
+ * g < -92, may count as 0.
  */
 moe_status moe_experts_mxfp4_gate_up(const moe_experts_mxfp4* experts, const void* x_codes, const void* x_scales,
                                      const uint32_t* offsets, int64_t rows, moe_dtype dtype, void* h, void* h_codes,
