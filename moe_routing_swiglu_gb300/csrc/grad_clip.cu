@@ -299,7 +299,9 @@ __device__ __forceinline__ uint4 scale_vec(uint4 r, float f) {
   return make_uint4(scale_word<T>(r.x, f), scale_word<T>(r.y, f), scale_word<T>(r.z, f), scale_word<T>(r.w, f));
 }
 
-// Writes this thread's vectors of unit u (local: within its tensor), scaled.
+// Writes this thread's vectors of unit u (local: within its tensor), scaled; a
+// factor of 1 copies the words (a product and a conversion would make one NaN
+// of them all).
 // dst on src's 16-byte phase takes 16-byte stores, on another one the vector's
 // elements one by one.
 template <typename T>
@@ -314,7 +316,7 @@ __device__ __forceinline__ void store_unit(const GradEntry& e, uint32_t local, i
   for (int g = 0; g < GC_GROUP; ++g) {
     const int v = static_cast<int>(threadIdx.x) + g * GC_THREADS;
     if (v >= vecs) continue;
-    const uint4 o = scale_vec<T>(raw[g], f);
+    const uint4 o = f == 1.0f ? raw[g] : scale_vec<T>(raw[g], f);
     if (aligned) {
       reinterpret_cast<uint4*>(d)[v] = o;
     } else {
@@ -332,8 +334,10 @@ __device__ __forceinline__ void store_unit(const GradEntry& e, uint32_t local, i
   }
   if (last || local == 0) {
     const int64_t odd = odd_element(e, local, last);
-    if (odd >= 0)
-      static_cast<T*>(e.dst)[odd] = from_f32<T>(to_f32(static_cast<const T*>(e.src)[odd]) * f);
+    if (odd >= 0) {
+      const T v = static_cast<const T*>(e.src)[odd];
+      static_cast<T*>(e.dst)[odd] = f == 1.0f ? v : from_f32<T>(to_f32(v) * f);
+    }
   }
 }
 

@@ -1,0 +1,45 @@
+"""GPU checks of the gradient clip's bits where its factor is 1."""
+import pytest
+import torch
+
+from tests.test_gpu_grad_clip import DEV, DTYPES, grads
+
+pytestmark = pytest.mark.gpu
+BITS = {torch.float32: torch.int32, torch.float16: torch.int16, torch.bfloat16: torch.int16}
+INF_BITS = {torch.float32: 0x7F800000, torch.float16: 0x7C00, torch.bfloat16: 0x7F80}
+SIGN = {torch.float32: -1 << 31, torch.float16: -1 << 15, torch.bfloat16: -1 << 15}
+
+
+def with_nans(n, dtype, seed):
+    """Random gradients with infinities, zeros and NaNs of both signs and many payloads in the head (before a 16-byte
+    boundary), the vectors and the tail."""
+    t = grads([(n, dtype)], seed)[0]
+    b = t.view(BITS[dtype])
+    at = torch.cat((torch.arange(0, n, 13), torch.arange(max(0, n - 9), n))).to(DEV)
+    payload = (torch.arange(len(at), device=DEV) * 37 % (1 << 6)).to(BITS[dtype])   # 0: an infinity
+    b[at] = payload + INF_BITS[dtype]
+    b[at[::2]] |= SIGN[dtype]
+    b[at[1::7]] = SIGN[dtype]                                                      # -0
+    return t
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("a,b", [(0, 0), (1, 1), (3, 3), (0, 1), (5, 2)])
+def test_a_factor_of_one_copies_every_bit(cuda_lib, dtype, a, b):
+    """With a norm that is not finite (and with one that is not larger than max_norm) dst gets src's bits, NaN signs
+    and payloads among them, at equal and at different alignments."""
+    moe = cuda_lib
+    n = 70001
+    src = with_nans(n + 8, dtype, a)
+    dst = torch.full((n + 8,), 9.0, dtype=dtype, device=DEV)
+    s, d = src[a:a + n], dst[b:b + n]
+    norm = moe.moe_grad_norm([s])
+    assert not torch.isfinite(norm)
+    for v in (norm, torch.tensor(float("inf"), device=DEV), torch.tensor(0.5, device=DEV)):
+        d.fill_(9.0)
+        moe.moe_grad_clip([s], v, 0.5, out=[d])
+        assert torch.equal(d.view(BITS[dtype]), s.view(BITS[dtype]))
+        assert (dst[:b] == 9.0).all() and (dst[b + n:] == 9.0).all()
+    keep = src.clone()
+    moe.moe_grad_clip([s], norm, 0.5)
+    assert torch.equal(src.view(BITS[dtype]), keep.view(BITS[dtype]))
