@@ -801,8 +801,8 @@ moe_status moe_grad_norm(const moe_grad_tensor* tensors, int64_t n, float* norm,
  *              they are: the caller sees it in *norm and skips the step.
  *   max_norm   finite and >= 0.
  *
- * dst ranges must not overlap one another or another entry's src, and a dst
- * that is not its own src must not overlap it (MOE_ERR_SHAPE).
+ * dst ranges must not overlap one another, another entry's src or norm, and a
+ * dst that is not its own src must not overlap it (MOE_ERR_SHAPE).
  */
 moe_status moe_grad_clip(const moe_grad_tensor* tensors, int64_t n, const float* norm, float max_norm, void* stream);
 

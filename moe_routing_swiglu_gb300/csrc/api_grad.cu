@@ -29,12 +29,14 @@ moe_status check_tensors(const moe_grad_tensor* t, int64_t n, bool with_dst) {
   return MOE_OK;
 }
 
-// No written range overlaps any other range (an in-place entry is one range).
-moe_status check_overlap(const moe_grad_tensor* t, int64_t n) {
+// No written range overlaps any other range (an in-place entry is one range),
+// nor the norm, which blocks still read while others write.
+moe_status check_overlap(const moe_grad_tensor* t, int64_t n, const float* norm) {
   struct Range {
     uintptr_t lo, hi;
     bool written;
   };
+  const uintptr_t norm_lo = reinterpret_cast<uintptr_t>(norm), norm_hi = norm_lo + sizeof(float);
   try {
     std::vector<Range> r;
     r.reserve(static_cast<size_t>(2 * n));
@@ -43,6 +45,7 @@ moe_status check_overlap(const moe_grad_tensor* t, int64_t n) {
       const uintptr_t bytes =
           static_cast<uintptr_t>(t[i].numel) * moe::dtype_size(static_cast<moe_dtype>(t[i].dtype));
       const uintptr_t d = reinterpret_cast<uintptr_t>(t[i].dst), s = reinterpret_cast<uintptr_t>(t[i].src);
+      if (norm_lo < d + bytes && d < norm_hi) return api_fail(MOE_ERR_SHAPE, "norm lies in a dst");
       r.push_back({d, d + bytes, true});
       if (s != d) r.push_back({s, s + bytes, false});
     }
@@ -99,7 +102,7 @@ moe_status moe_grad_clip(const moe_grad_tensor* tensors, int64_t n, const float*
     return api_fail(MOE_ERR_SHAPE, "max_norm must be finite and >= 0");
   if (norm == nullptr) return api_fail(MOE_ERR_NULL, "norm must be non-NULL");
   if (reinterpret_cast<uintptr_t>(norm) % 4 != 0) return api_fail(MOE_ERR_ALIGNMENT, "norm must be 4-byte aligned");
-  st = check_overlap(tensors, n);
+  st = check_overlap(tensors, n, norm);
   if (st != MOE_OK) return st;
   int sms = 0;
   st = device_sms(&sms);
