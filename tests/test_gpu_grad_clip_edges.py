@@ -1,8 +1,9 @@
-"""GPU checks of the gradient clip's bits where its factor is 1."""
+"""GPU checks of the gradient clip's bits and of the norm's small magnitudes (tolerances of tests/test_gpu_grad_clip.py:
+the sums' rounding does not depend on the size of the gradients)."""
 import pytest
 import torch
 
-from tests.test_gpu_grad_clip import DEV, DTYPES, grads
+from tests.test_gpu_grad_clip import DEV, DTYPES, check_norm, grads
 
 pytestmark = pytest.mark.gpu
 BITS = {torch.float32: torch.int32, torch.float16: torch.int16, torch.bfloat16: torch.int16}
@@ -43,3 +44,22 @@ def test_a_factor_of_one_copies_every_bit(cuda_lib, dtype, a, b):
     keep = src.clone()
     moe.moe_grad_clip([s], norm, 0.5)
     assert torch.equal(src.view(BITS[dtype]), keep.view(BITS[dtype]))
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("scale", [2.0 ** -30, 1e-10, 1e-12, 1e-14, 2.0 ** -50, 2.0 ** -52, 1e-17])
+def test_norm_of_small_gradients(cuda_lib, dtype, scale):
+    """Across the magnitudes at which a thread's sum of squares passes 2^-60 and 2^-100, with units of both kinds in
+    one sum, and zeros of both signs."""
+    ts = grads([(300_000, dtype), (5, dtype), (70_001, dtype)], 9, scale)
+    ts[0][:30_000] = 0
+    ts[0][30_000:60_000] = -0.0
+    ts[2][:20_000] *= 2.0 ** 12
+    check_norm(cuda_lib.moe_grad_norm(ts), ts)
+    tiny = [t * 2.0 ** -40 for t in ts]
+    check_norm(cuda_lib.moe_grad_norm(tiny + ts), tiny + ts)
+
+
+def test_negative_zeros(cuda_lib):
+    for dtype in DTYPES:
+        assert float(cuda_lib.moe_grad_norm([torch.full((50_001,), -0.0, dtype=dtype, device=DEV)])) == 0.0
