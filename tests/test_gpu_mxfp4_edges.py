@@ -1,5 +1,6 @@
 """GPU checks of the MXFP4 experts at the ends of their ranges: gates whose exponential leaves FP32, handles dropped
-while their work is queued, and buffers of another type.
+while their work is queued, buffers of another type, buffers past 2^31 elements, and the grouped sigmoid routing in
+front of the 4-bit stages.
 
 Tolerance of SiLU for gates that are exact in FP32 (a sum of a few multiples of 1/4), relative to it. 16-bit outputs: the
 exponent |g| log2(e) + 8 carries two roundings (|g| 2^-23 of the power), the hardware's exponential and reciprocal are
@@ -10,8 +11,9 @@ import numpy as np
 import pytest
 import torch
 
-from oracle import mxfp4
-from tests.test_gpu_mxfp4 import DEV, DTYPES, _layer, activations, check
+from oracle import moe_oracle, mxfp4
+from tests.parity import f64
+from tests.test_gpu_mxfp4 import ACC, DEV, DTYPES, _layer, activations, check, u8
 
 pytestmark = pytest.mark.gpu
 
@@ -148,3 +150,90 @@ def test_forward_refuses_buffers_of_another_type(cuda_lib):
     w, i = e(torch.bfloat16), e(torch.int32)
     moe.moe_forward_mxfp4(ex, x, lg, 2, True, weights=w, indices=i)
     assert torch.equal(w, torch.full_like(w, 0.5)) and i.tolist() == [[0, 1]] * 8
+
+
+# ------------------------------------------------------------------ sizes
+
+def test_buffers_past_2_to_the_31_elements(cuda_lib):
+    """Quantise, dequantise and the down product whose last rows lie past 2^31 elements (and past 2^32 bytes)."""
+    moe = cuda_lib
+    K, rows = 8192, (1 << 31) // 8192 + 37
+    tail = torch.randn(64, K, generator=torch.Generator().manual_seed(3)).to(torch.bfloat16)
+    x = torch.ones(rows, K, dtype=torch.bfloat16, device=DEV)
+    x[-64:] = tail.to(DEV)
+    q = moe.moe_mxfp4_quantize(x)
+    codes, scales = mxfp4.quantize(f64(tail))
+    assert np.array_equal(u8(q.codes[-64:]), codes) and np.array_equal(u8(q.scales[-64:]), scales)
+    assert bool((q.codes[:-64] == 0x66).all()) and bool((q.scales[:-64] == 125).all())   # 1 = 4 * 2^-2
+    v = moe.moe_mxfp4_dequantize(q, out=x)
+    assert np.array_equal(f64(v[-64:]), mxfp4.values(codes, scales)) and bool((v[:-64] == 1.0).all())
+    # y [rows, 8192] from 32 elements of K: two experts, the second with the last 50 rows
+    w = mxfp4.quantize(np.random.default_rng(4).standard_normal((2 * K, 32)))
+    mx = lambda p, *lead: moe.Mxfp4(*(torch.from_numpy(a).to(DEV).view(*lead, a.shape[-1]) for a in p))
+    gate = mxfp4.quantize(np.ones((64, K)))
+    ex = moe.ExpertsMxfp4(mx(gate, 2, 32), mx(gate, 2, 32), mx(w, 2, K))
+    h = moe.Mxfp4(q.codes[:, -16:].contiguous(), torch.zeros(rows, 4, dtype=torch.uint8, device=DEV))
+    h.scales[:, 0] = q.scales[:, -1]
+    hv = mxfp4.values(*(u8(t[-60:]) for t in h))
+    del q
+    offs = torch.tensor([0, rows - 50, rows], dtype=torch.int32, device=DEV)
+    y = moe.moe_experts_mxfp4_down(ex, h, offs, out=x)
+    wv = mxfp4.values(*w).reshape(2, K, 32)
+    ref = mxfp4.down(hv, wv, np.array([0, 10, 60]))
+    check(y[-60:], ref, ACC * 32 * mxfp4.down(np.abs(hv), np.abs(wv), np.array([0, 10, 60])), torch.bfloat16, "y")
+    assert moe.moe_device_status() == 0
+    # the rows of ones, all alike
+    assert torch.equal(y[:-64], y[:1].expand(rows - 64, K))
+
+
+@pytest.mark.parametrize("quantized", [False, True])
+def test_a_first_stage_past_2_to_the_31_elements(cuda_lib, quantized):
+    """h [rows, I] with rows * I above 2^31, in BF16 and as codes (one byte for two): every row is the one row that a
+    small call gives, two experts share the rows."""
+    moe = cuda_lib
+    H, I, n, split = 64, 16384, (1 << 31) // 16384 + 301, 90_000
+    rng = np.random.default_rng(6)
+    mx = lambda p, *lead: moe.Mxfp4(*(torch.from_numpy(a).to(DEV).view(*lead, a.shape[-1]) for a in p))
+    gate, up = (mx(mxfp4.quantize(rng.standard_normal((2 * I, H)) * H ** -0.5), 2, I) for _ in range(2))
+    ex = moe.ExpertsMxfp4(gate, up, mx(mxfp4.quantize(np.ones((2 * H, I))), 2, H))
+    one = moe.moe_mxfp4_quantize(torch.from_numpy(rng.standard_normal((1, H))).to(torch.bfloat16).to(DEV))
+    rep = lambda r: moe.Mxfp4(*(t.expand(r, t.shape[1]).contiguous() for t in one))
+    offs = lambda *o: torch.tensor(o, dtype=torch.int32, device=DEV)
+    call = lambda x, o: moe.moe_experts_mxfp4_gate_up(ex, x, o, quantized=quantized)
+    few, many = call(rep(2), offs(0, 1, 2)), call(rep(n), offs(0, split, n))
+    for f, m in zip(*((few, many) if quantized else ((few,), (many,)))):
+        assert torch.equal(m[:split], f[:1].expand(split, f.shape[1]))
+        assert torch.equal(m[split:], f[1:].expand(n - split, f.shape[1]))
+        assert not torch.equal(f[0], f[1])
+    assert moe.moe_device_status() == 0
+
+
+# ------------------------------------------------------------------ the other routing
+
+def test_grouped_sigmoid_routing_in_front_of_the_4_bit_stages(cuda_lib):
+    """The split calls together: grouped routing with its dispatch, quantise, both products, combine."""
+    moe = cuda_lib
+    T, E, k, H, I = 200, 16, 4, 512, 384
+    ex, w = _layer(moe, E, H, I, torch.bfloat16, 21)
+    x = activations(T, H, torch.bfloat16, 22)
+    g = torch.Generator().manual_seed(23)
+    logits, bias = torch.randn(T, E, generator=g), torch.randn(E, generator=g) * 0.1
+    opt = moe.GroupRoutingOptions(k, 4, 2, group_top_two=True, renormalize=True, scale=2.5)
+    idx, wt, disp = moe.moe_route_sigmoid_grouped_dispatch(logits.to(DEV), bias.to(DEV), opt)
+    xq = moe.moe_mxfp4_quantize(x.to(DEV), inv=disp.inv, top_k=k)
+    hq = moe.moe_experts_mxfp4_gate_up(ex, xq, disp.offsets, quantized=True)
+    y = moe.moe_experts_mxfp4_forward_dispatched(ex, xq, disp.offsets)
+    out = moe.moe_combine(y, disp.inv, wt)
+    assert torch.equal(y, moe.moe_experts_mxfp4_down(ex, hq, disp.offsets))
+    dp = moe_oracle.dispatch(idx.cpu().numpy().view(np.uint32), E)
+    codes, scales = mxfp4.quantize(f64(x))
+    src = dp.row_src.astype(np.int64) // k
+    assert np.array_equal(u8(xq.codes), codes[src]) and np.array_equal(u8(xq.scales), scales[src])
+    offs = dp.offsets.astype(np.int64)
+    wv = [mxfp4.values(*mxfp4.quantize(f64(t).reshape(-1, t.shape[-1]))).reshape(t.shape) for t in w]
+    hv = mxfp4.values(u8(hq.codes), u8(hq.scales))
+    check(y, mxfp4.down(hv, wv[2], offs), ACC * I * mxfp4.down(np.abs(hv), np.abs(wv[2]), offs), torch.bfloat16, "y")
+    rows = dp.inv.astype(np.int64).reshape(T, k)
+    yv, wf = f64(y), f64(wt)
+    check(out, np.einsum("tj,tjh->th", wf, yv[rows]),
+          k * ACC * np.einsum("tj,tjh->th", np.abs(wf), np.abs(yv[rows])), torch.bfloat16, "out")
