@@ -629,7 +629,9 @@ moe_status moe_dispatch_backward(const void* dinput, moe_dtype dtype, const uint
  *   scales   [rows, moe_mxfp4_scale_pitch(K)] bytes: byte b < K / 32 of a row
  *            is the scale 2^(byte - 127) of its elements 32b .. 32b + 31, 255
  *            is NaN. The pitch is K / 32 rounded up to 4; the bytes past K / 32
- *            are written as 0 and never read. 4-byte aligned.
+ *            are written as 0 and never read. 4-byte aligned. (Scales made
+ *            elsewhere with K / 32 bytes a row have to be copied to this
+ *            pitch where K / 32 is not a multiple of 4.)
  * ---------------------------------------------------------------------- */
 
 /* 4 * ceil(K / 128), or 0 where K is not a positive multiple of 32. */
@@ -746,7 +748,8 @@ moe_status moe_experts_mxfp4_forward_dispatched(const moe_experts_mxfp4* experts
  *
  *   x, out        device, [T, H] in `dtype` (MOE_F32, MOE_F16, MOE_BF16),
  *                 16-byte aligned; h is rounded to `dtype` before it is
- *                 quantised.
+ *                 quantised (in MOE_F16 an h beyond 65504 is an infinity, as
+ *                 in moe_forward, and its block of 32 channels NaN).
  *   logits, logits_dtype, T, top_k, renormalize, indices_opt, weights_opt
  *                 as in moe_forward.
  *   workspace     device, moe_forward_mxfp4_workspace_size(experts, T, top_k,
@@ -779,9 +782,12 @@ typedef struct {
  * moe_grad_norm - the L2 norm over all elements of n tensors.
  *
  *   tensors    host, n entries, read during the call only (n >= 0).
- *   norm       device, one float out: sqrt of the sum of squares (FP64 sums;
- *              the same bits on every run). 0 without elements; NaN or
- *              infinity where the gradients hold one.
+ *   norm       device, one float out: sqrt of the sum of squares (a thread's
+ *              16 or 32 squares in FP32, its running sum as a compensated FP32
+ *              pair, or in FP64 where FP32 does not hold the squares; threads
+ *              and blocks in FP64; the same bits on every run). 0 without
+ *              elements; NaN or infinity where the gradients hold one,
+ *              infinity also where the norm exceeds FP32.
  *   workspace  device, moe_grad_norm_workspace_size(n) bytes, 256-byte
  *              aligned; contents need not be initialised. Calls that may
  *              overlap need separate workspaces.

@@ -690,7 +690,8 @@ def moe_dispatch_backward(dinput: torch.Tensor, inv: torch.Tensor, T: int, top_k
 
 Mxfp4 = namedtuple("Mxfp4", "codes scales")
 Mxfp4.__doc__ = """An MXFP4 matrix [.., K]: codes uint8 [.., K/2] (element 2i in the low half of byte i) and
-scales uint8 [.., moe_mxfp4_scale_pitch(K)] (E8M0, one per 32 elements)."""
+scales uint8 [.., moe_mxfp4_scale_pitch(K)] (E8M0, one per 32 elements; rows of K / 32 bytes from elsewhere are padded
+to the pitch, with any bytes)."""
 
 
 def _here(stream, *tensors) -> int:

@@ -10,9 +10,10 @@
 // (32 channels of a token are one block), or both.
 //
 // Operand roles as in experts_tc.cu: the MMA's M side (128 TMEM lanes) holds
-// weight rows, its N side the expert's tokens, so a decode expert with one
-// or two tokens costs N = 16, and two MMAs share each token tile (gate and up
-// rows of the same channels, or two blocks of down rows).
+// weight rows, its N side the expert's tokens (16 at least: what an MMA of
+// N = 16 takes was not measured apart, decode is bound by the weights' bytes),
+// and two MMAs share each token tile (gate and up rows of the same channels,
+// or two blocks of down rows).
 //
 // A stage is 256 elements of K: one 128-byte swizzle atom per row, four MMA
 // steps of 64; shared memory holds STAGES of two 16 KB weight tiles and the
@@ -23,7 +24,11 @@
 // bulk copy per stage); the tokens' scales are row-major, because a tile may
 // start at any row, and are placed word by word with cp.async.
 //
-// One persistent CTA per SM takes tiles blockIdx, blockIdx + grid, ...
+// One persistent CTA per SM takes tiles blockIdx, blockIdx + grid, ... (the
+// five roles find their tiles alone: no counter to clear before the launch and
+// no ring of claimed tiles between them; the price is a last round as long as
+// its longest tile, which counts where there are few rounds: 504 tiles in the
+// decode step of 84 touched experts at I=768. Claiming was not tried here).
 //   warp 0 lane 0   producer: TMA of weights and tokens
 //   warp 1 lane 0   MMAs; warp 1 also owns the TMEM
 //   warps 2..17     epilogue: accumulators to registers in fragment order,
@@ -36,15 +41,18 @@
 // run on the tensor pipe in turn with the MMAs: eight a stage took 0.2 to
 // 0.3 us beside 0.5 us of MMAs.
 //
-// What bounds it (gate/up of 16384 rows, E=8, H=4096, I=14336, 645 us =
-// 6.0 PFLOP/s): an MMA takes about 128 clocks at N = 112 as at N = 208 (from a
-// stage's time without loads and epilogue), 8 a stage, 467 us in all; the
-// pipeline without the epilogue takes 537 us, and the epilogue's reads of the accumulators are overlapped by
-// nothing but the loads of the next tile's first stages: two accumulators
-// would need 832 TMEM columns. Tried and slower: N <= 112 with two accumulators
-// (twice the MMAs; 1061 us when N <= 208 took 712), one weight tile per MMA with
-// two accumulators (half the work a stage for the same 0.25 us of waits; 979 us
-// when two took 680).
+// What bounds it (gate/up of 16384 rows, E=8, H=4096, I=14336: 640-650 us in
+// repeated calls on the same operands, 5.9-6.0 PFLOP/s; 685-700 us when every
+// call gets new ones): an MMA takes about 128 clocks at N = 112 as at N = 208
+// (from a stage's time without loads and epilogue), 8 a stage, 467 us in all;
+// the loads bring 63.5 KB a stage into each SM, 48 bytes a clock and SM on
+// average (profile of 4096 rows: 1.32 GB from L2 in 105 us), and take nearly as
+// long; the pipeline without the epilogue takes 537 us, and the epilogue's
+// reads of the accumulators are overlapped by nothing but the loads of the next
+// tile's first stages: two accumulators would need 832 TMEM columns. Tried and
+// slower: N <= 112 with two accumulators (twice the MMAs; 1061 us when N <= 208
+// took 712), one weight tile per MMA with two accumulators (half the work a
+// stage for the same 0.25 us of waits; 979 us when two took 680).
 //
 // Token tiles: an expert's rows are split evenly into ceil(rows / 208) tiles of
 // at most 208 tokens, what the 512 TMEM columns hold beside three scale
@@ -354,7 +362,10 @@ __device__ __forceinline__ void stmatrix_x4_trans(uint32_t addr, uint32_t a, uin
 
 // A warp's tokens x 32 channels in shared memory, one block of 32 per token,
 // quantised: LPT lanes share a token, each with two 16-byte runs (run(tok, q):
-// the address of the token's run q). Row r0 + tok of the codes and scales gets
+// the address of the token's run q). The values come rounded to T, also where h
+// itself is not stored: a call that fuses the quantisation gives the bytes that
+// h and moe_mxfp4_quantize give (an F16 h beyond 65504 is an infinity in both,
+// and its block NaN). Row r0 + tok of the codes and scales gets
 // block `blk`; `live` tokens are written (the last block of a row also clears
 // the row's pad bytes).
 template <typename T, typename Run>
@@ -508,7 +519,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------------ scales to TMEM, MMAs
+    // ------------------------------------------------------------ MMAs
     if (lane == 0) {
       uint32_t n = 0;  // stages consumed
       uint32_t it = 0;
@@ -682,7 +693,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         for (int c0 = EPI_TOKENS * group; c0 < tc.n_tok; c0 += EPI_TOKENS * GROUPS) {
           const int64_t row = static_cast<int64_t>(tc.row0) + c0;
           // FP32: lane = output channel, register = token, 8 tokens at a time
-          // through the buffer.
+          // through the buffer, stored lane by lane. The accumulators are
+          // released after the last store (held, they would be twice the words
+          // of the 16-bit outputs), so the stores overlap no MMA either:
+          // gate/up of 16384 rows 758 us against 646 in BF16, the down product
+          // of 32768 rows, E=128, H=2048, I=768 74 against 54.
           uint32_t v0[16], v1[16];
           tmem_ld_32x32b_x16(t_lane + static_cast<uint32_t>(c0), v0);
           tmem_ld_32x32b_x16(t_lane + TBN + static_cast<uint32_t>(c0), v1);
@@ -864,7 +879,6 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn_mx() {
   return fn;
 }
 
-// [E, rows, row_bytes] codes, box 128 bytes (one swizzle atom) x box_rows x 1.
 // [rows, n] 16-bit outputs, boxes of 32 columns x EPI_TOKENS rows with the 64-byte swizzle.
 bool encode_out(CUtensorMap* m, moe_dtype dtype, void* ptr, uint64_t n, uint64_t rows) {
   auto fn = encode_fn_mx();
@@ -878,6 +892,7 @@ bool encode_out(CUtensorMap* m, moe_dtype dtype, void* ptr, uint64_t n, uint64_t
             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [E, rows, row_bytes] codes, box 128 bytes (one swizzle atom) x box_rows x 1.
 bool encode_codes(CUtensorMap* m, const void* ptr, uint64_t row_bytes, uint64_t rows, uint64_t E, uint32_t box_rows,
                   int rank) {
   auto fn = encode_fn_mx();

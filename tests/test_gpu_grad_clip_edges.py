@@ -1,5 +1,9 @@
-"""GPU checks of the gradient clip's bits and of the norm's small magnitudes (tolerances of tests/test_gpu_grad_clip.py:
-the sums' rounding does not depend on the size of the gradients)."""
+"""GPU checks of the gradient clip's bits and of the norm's small magnitudes.
+
+Tolerance of tests/test_gpu_grad_clip.py, from a thread's 16 or 32 squares in FP32. A thread carries its units' sums as a
+pair of FP32 whose additions are compensated: each rounding error goes to the second word, whose own rounding is 2^-48 of
+the sum, so that n units are off by n 2^-48; where FP32 does not hold the squares, and above threads, sums are FP64. Both
+are far below the 2^-24 that the bound counts, and neither depends on the size of the gradients."""
 import pytest
 import torch
 
