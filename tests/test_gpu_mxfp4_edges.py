@@ -1,6 +1,6 @@
 """GPU checks of the MXFP4 experts at the ends of their ranges: gates whose exponential leaves FP32, handles dropped
-while their work is queued, buffers of another type, buffers past 2^31 elements, and the grouped sigmoid routing in
-front of the 4-bit stages.
+while their work is queued, buffers of another type, buffers past 2^31 elements, the longest rows, every expert chosen,
+and the grouped sigmoid routing in front of the 4-bit stages.
 
 Tolerance of SiLU for gates that are exact in FP32 (a sum of a few multiples of 1/4), relative to it. 16-bit outputs: the
 exponent |g| log2(e) + 8 carries two roundings (|g| 2^-23 of the power), the hardware's exponential and reciprocal are
@@ -205,6 +205,50 @@ def test_a_first_stage_past_2_to_the_31_elements(cuda_lib, quantized):
         assert torch.equal(m[:split], f[:1].expand(split, f.shape[1]))
         assert torch.equal(m[split:], f[1:].expand(n - split, f.shape[1]))
         assert not torch.equal(f[0], f[1])
+    assert moe.moe_device_status() == 0
+
+
+@pytest.mark.parametrize("H,I", [(262144, 32), (32, 262144)])
+def test_the_longest_rows(cuda_lib, H, I):
+    """K = 262144 in either stage (1024 stages a tile, rows of 128 KB of codes) and as many output columns."""
+    moe = cuda_lib
+    rows, g = 5, torch.Generator().manual_seed(7)
+    x = torch.randn(rows, H, generator=g).to(torch.bfloat16)
+    w = [(torch.randn(1, n, K, generator=g) * K ** -0.5).to(torch.bfloat16) for n, K in ((I, H), (I, H), (H, I))]
+    ex = moe.ExpertsMxfp4.from_float(*(t.to(DEV) for t in w))
+    offs = torch.tensor([0, rows], dtype=torch.int32, device=DEV)
+    q = moe.moe_mxfp4_quantize(x.to(DEV))
+    codes, scales = mxfp4.quantize(f64(x))
+    assert np.array_equal(u8(q.codes), codes) and np.array_equal(u8(q.scales), scales)
+    hq = moe.moe_experts_mxfp4_gate_up(ex, q, offs, dtype=torch.float32, quantized=True)
+    h = moe.moe_experts_mxfp4_gate_up(ex, q, offs, dtype=torch.float32)
+    qh = moe.moe_mxfp4_quantize(h)
+    assert torch.equal(hq.codes, qh.codes) and torch.equal(hq.scales, qh.scales)
+    y = moe.moe_experts_mxfp4_down(ex, hq, offs, dtype=torch.float32)
+    wv = [mxfp4.values(*mxfp4.quantize(f64(t)[0]))[None] for t in w]
+    xv, hv, o = mxfp4.values(codes, scales), mxfp4.values(u8(hq.codes), u8(hq.scales)), np.array([0, rows])
+    href, gv, uv = mxfp4.gate_up(xv, wv[0], wv[1], o)
+    _, ag, au = mxfp4.gate_up(np.abs(xv), np.abs(wv[0]), np.abs(wv[1]), o)
+    eg, eu = ACC * H * ag, ACC * H * au
+    silu = np.abs(gv / (1.0 + np.exp(-gv)))
+    check(h, href, 1.1 * eg * np.abs(uv) + (silu + 1.1 * eg) * eu + 2.0 ** -20 * np.abs(href), torch.float32, "h")
+    check(y, mxfp4.down(hv, wv[2], o), ACC * I * mxfp4.down(np.abs(hv), np.abs(wv[2]), o), torch.float32, "y")
+
+
+@pytest.mark.parametrize("E,k", [(128, 128), (1024, 1024)])
+def test_forward_with_every_expert_chosen(cuda_lib, E, k):
+    """top_k = E: the whole forward gives the bits of its split calls."""
+    moe = cuda_lib
+    T, H, I = 7, 64, 32
+    ex, _ = _layer(moe, E, H, I, torch.bfloat16, 31)
+    x = activations(T, H, torch.bfloat16, 32).to(DEV)
+    lg = torch.randn(T, E, generator=torch.Generator().manual_seed(33)).to(DEV)
+    out = moe.moe_forward_mxfp4(ex, x, lg, k, True)
+    idx, wt = moe.moe_route(lg, k, True)
+    disp = moe.moe_dispatch(idx, E)
+    xq = moe.moe_mxfp4_quantize(x, inv=disp.inv, top_k=k)
+    y = moe.moe_experts_mxfp4_forward_dispatched(ex, xq, disp.offsets)
+    assert torch.equal(out, moe.moe_combine(y, disp.inv, wt)) and bool(torch.isfinite(out).all())
     assert moe.moe_device_status() == 0
 
 
