@@ -812,6 +812,107 @@ moe_status moe_grad_norm(const moe_grad_tensor* tensors, int64_t n, float* norm,
  */
 moe_status moe_grad_clip(const moe_grad_tensor* tensors, int64_t n, const float* norm, float max_norm, void* stream);
 
+/* ------------------------------------------------------------------------
+ * The norms around a block of a residual stream: before the layer (its input),
+ * after it (its output, gated and scaled, back into the stream) and the next
+ * block's, forward and backward. Not on the pages, which stop at the layer.
+ *
+ *   norm(v; w) = v * w / sqrt(mean(v^2) + eps)      over the H columns of a row
+ *
+ * Rows are [T, H] in `dtype`, H <= 32768, aligned to their element size (16-byte
+ * aligned rows, H a multiple of 8, take the wide loads). Weight vectors are
+ * MOE_F32 or of the rows' dtype. Arithmetic and sums are FP32, each output is
+ * rounded once; a row whose sum of squares passes FP32's range is normed to
+ * zeros. An output may be the same [T, H] tensor as an input; any other overlap
+ * with an output is MOE_ERR_SHAPE. Gradients of weights and channel gates are
+ * FP32; every sum has a fixed order (the same bits on every run).
+ * ---------------------------------------------------------------------- */
+
+/*
+ * moe_block_norm - y = norm(x; weight).
+ *   x, y      device, [T, H] in `dtype` (T = 0 enqueues nothing).
+ *   weight    device, [H] in `weight_dtype`.
+ *   eps       finite, > 0.
+ */
+moe_status moe_block_norm(const void* x, moe_dtype dtype, const void* weight, moe_dtype weight_dtype, float eps,
+                          int64_t T, int64_t H, void* y, void* stream);
+
+/*
+ * moe_block_norm_backward - from dy: dx = (dy's gradient of x) + dresidual, and
+ * dweight[h] = sum over rows of dy * x / sqrt(mean(x^2) + eps).
+ *   dresidual   device, [T, H]: the gradient that reaches x past the block, or
+ *               NULL for none.
+ *   dx          device, [T, H] out in `dtype`.
+ *   dweight     device, [H] float out (zeros for T = 0).
+ *   workspace   device, moe_block_norm_backward_workspace_size(T, H) bytes,
+ *               256-byte aligned; contents need not be initialised.
+ */
+size_t moe_block_norm_backward_workspace_size(int64_t T, int64_t H);
+moe_status moe_block_norm_backward(const void* dy, const void* x, moe_dtype dtype, const void* weight,
+                                   moe_dtype weight_dtype, const void* dresidual, float eps, int64_t T, int64_t H,
+                                   void* dx, float* dweight, void* workspace, size_t workspace_bytes, void* stream);
+
+/* What a join's gate is shared by. */
+typedef enum {
+  MOE_GATE_NONE = 0,
+  MOE_GATE_CHANNEL = 1,  /* [H], in vec_dtype      */
+  MOE_GATE_TOKEN = 2,    /* [T], in vec_dtype      */
+  MOE_GATE_ELEMENT = 3   /* [T, H], in the rows' dtype */
+} moe_gate_kind;
+
+typedef struct {
+  const void* norm_weight;  /* device, [H], or NULL: the branch is not normed   */
+  const void* next_weight;  /* device, [H], or NULL: no norm of the joined rows */
+  const void* gate;         /* device, by gate_kind                             */
+  int32_t gate_kind;        /* moe_gate_kind                                    */
+  int32_t vec_dtype;        /* of norm_weight, next_weight, channel and token gates: MOE_F32 or the rows' dtype */
+  float residual_scale;     /* finite */
+  float branch_scale;       /* finite */
+  float eps;                /* of both norms; finite, > 0 */
+} moe_block_join_params;
+
+/*
+ * moe_block_join - the block's output back into the residual stream, and the
+ * next block's norm:
+ *   out    = residual_scale * residual + branch_scale * gate * norm(branch; norm_weight)
+ *   normed = norm(out; next_weight), of out as stored
+ *   branch, residual, out   device, [T, H] in `dtype`.
+ *   params    host, read during the call only.
+ *   normed    device, [T, H] out, exactly when next_weight is given.
+ */
+moe_status moe_block_join(const void* branch, const void* residual, moe_dtype dtype, const moe_block_join_params* params,
+                          int64_t T, int64_t H, void* out, void* normed, void* stream);
+
+/*
+ * moe_combine_join - moe_combine and moe_block_join in one launch: the branch
+ * is sum over slots j, in order, of weights[t, j] * y_dispatched[inv[t * top_k
+ * + j]] in FP32 (not rounded to `dtype` in between, as moe_combine's result
+ * is). A token with an inv entry >= T * top_k gets NaN rows.
+ *   y_dispatched, inv, weights, weights_dtype, top_k   as moe_combine.
+ */
+moe_status moe_combine_join(const void* y_dispatched, moe_dtype dtype, const uint32_t* inv, const void* weights,
+                            moe_dtype weights_dtype, const void* residual, const moe_block_join_params* params,
+                            int64_t T, int32_t top_k, int64_t H, void* out, void* normed, void* stream);
+
+/*
+ * moe_block_join_backward - from dout (the gradient that reaches out past the
+ * next norm; NULL for none, with next_weight only) and dnormed:
+ *   dbranch, dresidual   device, [T, H] out in `dtype`.
+ *   dnorm_weight, dnext_weight   device, [H] float out, exactly when their
+ *             weights are given.
+ *   dgate     device, out, exactly when there is a gate: [H] or [T] float, or
+ *             [T, H] in `dtype`.
+ *   branch    the forward's (moe_combine's result for a combined branch).
+ *   joined    the forward's out; it and dnormed are read with next_weight only.
+ *   workspace moe_block_join_backward_workspace_size(T, H) bytes, 256-byte
+ *             aligned.
+ */
+size_t moe_block_join_backward_workspace_size(int64_t T, int64_t H);
+moe_status moe_block_join_backward(const void* dout, const void* dnormed, const void* branch, const void* joined,
+                                   moe_dtype dtype, const moe_block_join_params* params, int64_t T, int64_t H,
+                                   void* dbranch, void* dresidual, float* dnorm_weight, void* dgate,
+                                   float* dnext_weight, void* workspace, size_t workspace_bytes, void* stream);
+
 /*
  * moe_device_status - read (and clear, if `clear` is nonzero) the device
  * status word. The expert GEMM kernels bound every pipeline wait (about one

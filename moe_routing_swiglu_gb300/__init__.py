@@ -55,6 +55,13 @@ class GradTensor(ctypes.Structure):
                 ("dtype", ctypes.c_int32)]
 
 
+class BlockJoinParams(ctypes.Structure):
+    """moe_block_join_params: the weights, gate and scales of a join."""
+    _fields_ = [("norm_weight", ctypes.c_void_p), ("next_weight", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("gate_kind", ctypes.c_int32), ("vec_dtype", ctypes.c_int32), ("residual_scale", ctypes.c_float),
+                ("branch_scale", ctypes.c_float), ("eps", ctypes.c_float)]
+
+
 _INDEX = {torch.int32: 1, torch.int64: 2}
 if hasattr(torch, "uint32"):
     _INDEX[torch.uint32] = 0
@@ -64,6 +71,7 @@ if hasattr(torch, "uint32"):
 _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _OPT = ctypes.POINTER(GroupRoutingOptions)
 _ROPT = ctypes.POINTER(RouterWeightOptions)
+_JOIN = ctypes.POINTER(BlockJoinParams)
 _FP = ctypes.c_void_p
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -127,6 +135,16 @@ SIGNATURES = {
     "moe_grad_norm_workspace_size": (_SZ, [_I64]),
     "moe_grad_norm": (ctypes.c_int, [_P, _I64, _P, _P, _SZ, _P]),
     "moe_grad_clip": (ctypes.c_int, [_P, _I64, _P, ctypes.c_float, _P]),
+    "moe_block_norm": (ctypes.c_int, [_P, ctypes.c_int, _P, ctypes.c_int, ctypes.c_float, _I64, _I64, _P, _P]),
+    "moe_block_norm_backward_workspace_size": (_SZ, [_I64, _I64]),
+    "moe_block_norm_backward": (ctypes.c_int, [_P, _P, ctypes.c_int, _P, ctypes.c_int, _P, ctypes.c_float, _I64, _I64,
+                                               _P, _P, _P, _SZ, _P]),
+    "moe_block_join": (ctypes.c_int, [_P, _P, ctypes.c_int, _JOIN, _I64, _I64, _P, _P, _P]),
+    "moe_combine_join": (ctypes.c_int, [_P, ctypes.c_int, _P, _P, ctypes.c_int, _P, _JOIN, _I64, _I32, _I64, _P, _P,
+                                        _P]),
+    "moe_block_join_backward_workspace_size": (_SZ, [_I64, _I64]),
+    "moe_block_join_backward": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, _JOIN, _I64, _I64, _P, _P, _P, _P, _P, _P,
+                                               _SZ, _P]),
     "moe_device_status": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _I32]),
     "moe_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_uint32, _P]),
 }
@@ -1057,6 +1075,181 @@ def moe_clip_grad_norm(tensors, max_norm: float, *, out=None, workspace=None, st
     norm = _grad_norm(lib, table, len(tensors), cur, None, workspace, stream, raw)
     _check(lib.moe_grad_clip(table.buffer_info()[0], len(tensors), norm.data_ptr(), float(max_norm), raw))
     return norm
+
+
+# ---- norms before and after a block
+
+BlockNormGrads = namedtuple("BlockNormGrads", "dx dweight")
+BlockJoinGrads = namedtuple("BlockJoinGrads", "dbranch dresidual dnorm_weight dgate dnext_weight")
+_GATE_NONE, _GATE_CHANNEL, _GATE_TOKEN, _GATE_ELEMENT = range(4)
+
+
+def _rows_of(x: torch.Tensor, name: str) -> tuple[int, int]:
+    """(T, H) of rows [.., H]."""
+    _dev_tensor(x, name)
+    shape = x.shape
+    if len(shape) < 1 or shape[-1] < 1:
+        raise MoeError(2, f"{name} must be [.., H]")
+    return x.numel() // shape[-1], shape[-1]
+
+
+def _like(t, x: torch.Tensor, name: str, stream) -> torch.Tensor:
+    """A row tensor of the call: `t` checked against x, or a new one."""
+    if t is None:
+        return _empty(x.shape, x.dtype, x.device, stream)
+    _dev_tensor(t, name)
+    if t.dtype != x.dtype or t.shape != x.shape:
+        raise MoeError(2, f"{name} must be {tuple(x.shape)} in {x.dtype}")
+    return t
+
+
+def _vector(t: torch.Tensor, name: str, x: torch.Tensor) -> torch.Tensor:
+    _dev_tensor(t, name)
+    if t.shape != x.shape[-1:]:
+        raise MoeError(2, f"{name} must hold one value per column")
+    return t
+
+
+def _join_params(x, norm_weight, gate, next_weight, residual_scale, branch_scale, eps) -> BlockJoinParams:
+    """The params of a join of rows like x, its tensors checked against them."""
+    kind, vectors = _GATE_NONE, []
+    if norm_weight is not None:
+        vectors.append(_vector(norm_weight, "norm_weight", x).dtype)
+    if next_weight is not None:
+        vectors.append(_vector(next_weight, "next_weight", x).dtype)
+    if gate is not None:
+        _dev_tensor(gate, "gate")
+        if gate.shape == x.shape[-1:]:
+            kind = _GATE_CHANNEL
+        elif gate.shape == x.shape and (x.shape[-1] != 1 or gate.dtype == x.dtype):
+            kind = _GATE_ELEMENT
+            if gate.dtype != x.dtype:
+                raise MoeError(3, "a gate for every element must have the rows' dtype")
+        elif gate.shape == (*x.shape[:-1], 1):
+            kind = _GATE_TOKEN
+        else:
+            raise MoeError(2, f"gate must be [H], [.., 1] or [.., H] for rows {tuple(x.shape)}")
+        if kind != _GATE_ELEMENT:
+            vectors.append(gate.dtype)
+    for d in vectors:
+        if d != vectors[0] or (d != torch.float32 and d != x.dtype):
+            raise MoeError(3, "norm_weight, next_weight and a channel or token gate share one dtype: float32 or the rows'")
+    return BlockJoinParams(_addr(norm_weight), _addr(next_weight), _addr(gate), kind,
+                           _DTYPE[vectors[0]] if vectors else MOE_F32, residual_scale, branch_scale, eps)
+
+
+def moe_block_norm(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, out=None, stream=None) -> torch.Tensor:
+    """norm(x) * weight over the last dimension of x [.., H], norm(v) = v /
+    sqrt(mean(v^2) + eps); weight [H] is float32 or of x's dtype. out may be x."""
+    lib = load_library()
+    T, H = _rows_of(x, "x")
+    _vector(weight, "weight", x)
+    raw = _here(stream, x, weight, out)
+    y = _like(out, x, "out", stream)
+    _check(lib.moe_block_norm(x.data_ptr(), _dt(x), weight.data_ptr(), _dt(weight), eps, T, H, y.data_ptr(), raw))
+    return y
+
+
+def moe_block_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6,
+                            dresidual: torch.Tensor | None = None, dx=None, workspace=None,
+                            stream=None) -> BlockNormGrads:
+    """The gradients of moe_block_norm: dx in x's dtype, with dresidual (the
+    gradient that reaches x past the block) added, and dweight [H] float32."""
+    lib = load_library()
+    T, H = _rows_of(x, "x")
+    _vector(weight, "weight", x)
+    _like(dy, x, "dy", stream)
+    if dresidual is not None:
+        _like(dresidual, x, "dresidual", stream)
+    raw = _here(stream, x, dy, weight, dresidual, dx, workspace)
+    dx = _like(dx, x, "dx", stream)
+    dw = _empty((H,), torch.float32, x.device, stream)
+    ws = _scratch(lib.moe_block_norm_backward_workspace_size(T, H), x.device, workspace, stream)
+    _check(lib.moe_block_norm_backward(dy.data_ptr(), x.data_ptr(), _dt(x), weight.data_ptr(), _dt(weight),
+                                       _addr(dresidual), eps, T, H, dx.data_ptr(), dw.data_ptr(), ws.data_ptr(),
+                                       ws.numel(), raw))
+    return BlockNormGrads(dx, dw)
+
+
+def moe_block_join(branch: torch.Tensor, residual: torch.Tensor, *, norm_weight=None, gate=None, next_weight=None,
+                   residual_scale: float = 1.0, branch_scale: float = 1.0, eps: float = 1e-6, out=None, normed=None,
+                   stream=None):
+    """A block's output back into the residual stream, and the next block's
+    norm: out = residual_scale * residual + branch_scale * gate * norm(branch) *
+    norm_weight and normed = norm(out) * next_weight. Without norm_weight the
+    branch is not normed, without next_weight normed is None. gate: [H] (one
+    per channel), [.., 1] (per token) or [.., H]. Returns (out, normed); out
+    and normed may be given, out also as the residual itself."""
+    lib = load_library()
+    T, H = _rows_of(residual, "residual")
+    _like(branch, residual, "branch", stream)
+    p = _join_params(residual, norm_weight, gate, next_weight, residual_scale, branch_scale, eps)
+    raw = _here(stream, residual, branch, norm_weight, gate, next_weight, out, normed)
+    o = _like(out, residual, "out", stream)
+    y = _like(normed, residual, "normed", stream) if next_weight is not None or normed is not None else None
+    _check(lib.moe_block_join(branch.data_ptr(), residual.data_ptr(), _dt(residual), p, T, H, o.data_ptr(), _addr(y),
+                              raw))
+    return o, y
+
+
+def moe_combine_join(y_dispatched: torch.Tensor, inv: torch.Tensor, weights: torch.Tensor, residual: torch.Tensor, *,
+                     norm_weight=None, gate=None, next_weight=None, residual_scale: float = 1.0,
+                     branch_scale: float = 1.0, eps: float = 1e-6, out=None, normed=None, stream=None):
+    """moe_combine and moe_block_join in one launch: the branch is the
+    routing-weighted sum of a token's expert rows, in FP32. y_dispatched
+    [T * top_k, H], inv and weights [T, top_k] as in moe_combine; residual
+    [T, H]. Returns (out, normed)."""
+    lib = load_library()
+    T, H = _rows_of(residual, "residual")
+    for t, name in ((y_dispatched, "y_dispatched"), (inv, "inv"), (weights, "weights")):
+        _dev_tensor(t, name)
+    if residual.dim() != 2 or weights.dim() != 2 or weights.shape[0] != T:
+        raise MoeError(2, "residual must be [T, H] and weights [T, top_k]")
+    k = weights.shape[1]
+    if inv.numel() != T * k or tuple(y_dispatched.shape) != (T * k, H):
+        raise MoeError(2, "inv must hold T * top_k entries and y_dispatched [T * top_k, H]")
+    if y_dispatched.dtype != residual.dtype:
+        raise MoeError(3, "y_dispatched and residual must have one dtype")
+    if inv.dtype not in (torch.int32, getattr(torch, "uint32", torch.int32)):
+        raise MoeError(3, "inv must be uint32 (or its int32 view)")
+    p = _join_params(residual, norm_weight, gate, next_weight, residual_scale, branch_scale, eps)
+    raw = _here(stream, residual, y_dispatched, inv, weights, norm_weight, gate, next_weight, out, normed)
+    o = _like(out, residual, "out", stream)
+    y = _like(normed, residual, "normed", stream) if next_weight is not None or normed is not None else None
+    _check(lib.moe_combine_join(y_dispatched.data_ptr(), _dt(residual), inv.data_ptr(), weights.data_ptr(),
+                                _dt(weights), residual.data_ptr(), p, T, k, H, o.data_ptr(), _addr(y), raw))
+    return o, y
+
+
+def moe_block_join_backward(dout: torch.Tensor | None, branch: torch.Tensor, *, dnormed=None, joined=None,
+                            norm_weight=None, gate=None, next_weight=None, residual_scale: float = 1.0,
+                            branch_scale: float = 1.0, eps: float = 1e-6, dbranch=None, dresidual=None,
+                            workspace=None, stream=None) -> BlockJoinGrads:
+    """The gradients of moe_block_join, from dout (None: nothing reaches out
+    past the next norm) and, with next_weight, dnormed; `joined` is the
+    forward's out. dbranch and dresidual are in the rows' dtype, weight
+    gradients float32, dgate of the gate's shape (float32, or the rows' dtype
+    for a gate of every element); None for what the join does not have."""
+    lib = load_library()
+    T, H = _rows_of(branch, "branch")
+    for t, name in ((dout, "dout"), (dnormed, "dnormed"), (joined, "joined")):
+        if t is not None:
+            _like(t, branch, name, stream)
+    p = _join_params(branch, norm_weight, gate, next_weight, residual_scale, branch_scale, eps)
+    raw = _here(stream, branch, dout, dnormed, joined, norm_weight, gate, next_weight, dbranch, dresidual, workspace)
+    dev = branch.device
+    df = _like(dbranch, branch, "dbranch", stream)
+    dx = _like(dresidual, branch, "dresidual", stream)
+    dw = _empty((H,), torch.float32, dev, stream) if norm_weight is not None else None
+    dw2 = _empty((H,), torch.float32, dev, stream) if next_weight is not None else None
+    dgate = None
+    if gate is not None:
+        dgate = _empty(gate.shape, gate.dtype if p.gate_kind == _GATE_ELEMENT else torch.float32, dev, stream)
+    ws = _scratch(lib.moe_block_join_backward_workspace_size(T, H), dev, workspace, stream)
+    _check(lib.moe_block_join_backward(_addr(dout), _addr(dnormed), branch.data_ptr(), _addr(joined), _dt(branch), p, T,
+                                       H, df.data_ptr(), dx.data_ptr(), _addr(dw), _addr(dgate), _addr(dw2),
+                                       ws.data_ptr(), ws.numel(), raw))
+    return BlockJoinGrads(df, dx, dw, dgate, dw2)
 
 
 def moe_device_status(clear: bool = True) -> int:

@@ -255,6 +255,52 @@ cudaError_t launch_grad_norm(const moe_grad_tensor* tensors, int64_t n, float* n
                              cudaStream_t stream);
 cudaError_t launch_grad_clip(const moe_grad_tensor* tensors, int64_t n, const float* norm, float max_norm, int num_sms,
                              cudaStream_t stream);
+// ---- norms before and after a block (block_norm.cu)
+constexpr int64_t BLOCK_NORM_MAX_H = 32768;
+constexpr int64_t JOIN_BACKWARD_BLOCKS = 304;   // blocks whose column sums the workspace holds
+struct JoinArgs {
+  const void* f;             // branch rows [T, H], or expert rows [rows, H]
+  const void* x;             // [T, H]
+  void* out;                 // [T, H]
+  void* y;                   // [T, H]
+  const void* norm_weight;   // [H] or NULL
+  const void* next_weight;   // [H] or NULL
+  const void* gate;
+  const uint32_t* inv;       // combine only: [T * top_k]
+  const void* weights;       // [T, top_k]
+  int64_t T;
+  int H;
+  int gate_kind;
+  int vec_f32;               // the vectors are FP32 (else of the rows' type)
+  int weights_dtype;
+  int top_k;
+  uint32_t rows;
+  float alpha, beta, eps;
+};
+// branch: 0 y = norm(x), 1 rows of f, 2 the combine of expert rows
+cudaError_t launch_join(moe_dtype dtype, const JoinArgs& a, int branch, int num_sms, cudaStream_t stream);
+struct JoinBackwardArgs {
+  const void* dout;          // [T, H] or NULL
+  const void* dnormed;       // [T, H], with next_weight
+  const void* f;             // [T, H] or NULL (the norm alone)
+  const void* joined;        // [T, H], with next_weight
+  const void* norm_weight;
+  const void* next_weight;
+  const void* gate;
+  void* dbranch;
+  void* dresidual;
+  void* dgate;               // [H] or [T] FP32, or [T, H]
+  float* partial;            // [units, arrays, H]
+  int64_t T;
+  int H;
+  int gate_kind;
+  int vec_f32;
+  int arrays;                // column sums asked for: dw1, a channel gate's, dw2
+  float alpha, beta, eps;
+};
+int64_t join_backward_units(int64_t T, int64_t H);
+cudaError_t launch_join_backward(moe_dtype dtype, const JoinBackwardArgs& a, float* dnorm_weight, float* dnext_weight,
+                                 cudaStream_t stream);
 cudaError_t launch_bounded_wait_selftest(uint32_t limit_us, cudaStream_t stream);
 
 }  // namespace moe
