@@ -913,6 +913,71 @@ moe_status moe_block_join_backward(const void* dout, const void* dnormed, const 
                                    void* dbranch, void* dresidual, float* dnorm_weight, void* dgate,
                                    float* dnext_weight, void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------------------
+ * Orthogonalised updates: what a training step runs between the gradients
+ * (moe_experts_backward's dgate, dup, ddown, clipped) and the weights. Added
+ * beside the pages' training calls.
+ *
+ * Newton-Schulz steps on each matrix G of a batch [E, rows, cols]:
+ *   X = G / (|G|_F + eps), then `steps` times, with A = X X^T,
+ *   X <- 3.4445 X + (-4.7750 A + 2.0315 A A) X
+ * (five steps take the singular values that are not much below the largest
+ * into about [0.7, 1.2] and keep the singular vectors). Products run on the
+ * tensor cores with FP16 pairs as operands (22 bits) and FP32 accumulators;
+ * the result X is off by less than 2^-12 of its largest singular value. A
+ * matrix with a NaN or an infinity becomes NaN as a whole, the others of the
+ * batch are not touched by it; a matrix of zeros stays zero.
+ *
+ *   E           0 .. 65535 matrices, dense, one behind the other.
+ *   rows, cols  0 .. 65536, either may be the longer (no element: nothing is
+ *               enqueued).
+ *   steps       1 .. 100.
+ *   eps         finite, > 0.
+ *   workspace   device, moe_orthogonalize_workspace_size(E, rows, cols) bytes,
+ *               256-byte aligned, of both calls below: about 8 bytes per
+ *               element and 12 min(rows, cols)^2 per matrix. Contents need not
+ *               be initialised. Calls that may overlap need separate ones.
+ * Tensors are aligned to their element size. The same bits on every run.
+ * ---------------------------------------------------------------------- */
+size_t moe_orthogonalize_workspace_size(int64_t E, int64_t rows, int64_t cols);
+
+/*
+ * moe_orthogonalize - out = the orthogonalised matrices.
+ *   matrices   device, [E, rows, cols] in `dtype`.
+ *   out        device, the same shape in out_dtype, MOE_F16 or MOE_BF16 (the
+ *              steps' accuracy is that of 16-bit results, so FP32 is not
+ *              offered); may be the matrices' own memory.
+ */
+moe_status moe_orthogonalize(const void* matrices, moe_dtype dtype, int64_t E, int64_t rows, int64_t cols,
+                             int32_t steps, float eps, void* out, moe_dtype out_dtype, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+typedef struct {
+  float lr;               /* finite */
+  float momentum_decay;   /* in [0, 1) */
+  float weight_decay;     /* finite */
+  float update_scale;     /* finite; commonly sqrt(max(1, rows / cols)) */
+  float eps;
+  int32_t steps;
+  int32_t nesterov;       /* nonzero: orthogonalise grad + momentum_decay * momentum, else the momentum */
+} moe_muon_params;
+
+/*
+ * moe_muon_step - one optimizer step on a batch of weight matrices:
+ *   momentum <- momentum_decay * momentum + grad
+ *   O = the orthogonalised (nesterov ? grad + momentum_decay * momentum : momentum)
+ *   weight <- (1 - lr * weight_decay) * weight - lr * update_scale * O
+ * in FP32 (O is not rounded in between), weight rounded to its dtype once.
+ *   weight     device, [E, rows, cols] in weight_dtype, updated in place.
+ *   grad       device, in grad_dtype.
+ *   momentum   device, float, updated in place (zeros before the first step).
+ *   params     host, read during the call only.
+ * The tensors and the workspace must not overlap.
+ */
+moe_status moe_muon_step(void* weight, moe_dtype weight_dtype, const void* grad, moe_dtype grad_dtype, float* momentum,
+                         int64_t E, int64_t rows, int64_t cols, const moe_muon_params* params, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 /*
  * moe_device_status - read (and clear, if `clear` is nonzero) the device
  * status word. The expert GEMM kernels bound every pipeline wait (about one
@@ -932,7 +997,9 @@ moe_status moe_block_join_backward(const void* dout, const void* dnormed, const 
  * accumulator, 0x34 epilogue, 0x35 / 0x36 teardown drains, 0x37 scale loader
  * for a free ring slot, 0x38 scale warps for a free scale buffer, 0x39 for a
  * loaded ring slot, 0x3A MMA for a stage's scales, 0x3B a teardown drain of
- * the scale loader), 0x100
+ * the scale loader), 0x41 - 0x46 the waits of the Newton-Schulz products (0x41
+ * producer, 0x42 MMA for a loaded stage, 0x43 MMA for a drained accumulator,
+ * 0x44 epilogue, 0x45 / 0x46 teardown drains), 0x100
  * moe_selftest_bounded_wait. Synchronises the current device; *code = 0 when
  * no wait has timed out.
  */

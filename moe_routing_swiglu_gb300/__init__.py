@@ -62,6 +62,13 @@ class BlockJoinParams(ctypes.Structure):
                 ("branch_scale", ctypes.c_float), ("eps", ctypes.c_float)]
 
 
+class MuonParams(ctypes.Structure):
+    """moe_muon_params: the rates and options of an optimizer step."""
+    _fields_ = [("lr", ctypes.c_float), ("momentum_decay", ctypes.c_float), ("weight_decay", ctypes.c_float),
+                ("update_scale", ctypes.c_float), ("eps", ctypes.c_float), ("steps", ctypes.c_int32),
+                ("nesterov", ctypes.c_int32)]
+
+
 _INDEX = {torch.int32: 1, torch.int64: 2}
 if hasattr(torch, "uint32"):
     _INDEX[torch.uint32] = 0
@@ -72,6 +79,7 @@ _P, _I32, _I64, _SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_
 _OPT = ctypes.POINTER(GroupRoutingOptions)
 _ROPT = ctypes.POINTER(RouterWeightOptions)
 _JOIN = ctypes.POINTER(BlockJoinParams)
+_MUON = ctypes.POINTER(MuonParams)
 _FP = ctypes.c_void_p
 SIGNATURES = {
     "moe_status_string": (ctypes.c_char_p, [ctypes.c_int]),
@@ -145,6 +153,10 @@ SIGNATURES = {
     "moe_block_join_backward_workspace_size": (_SZ, [_I64, _I64]),
     "moe_block_join_backward": (ctypes.c_int, [_P, _P, _P, _P, ctypes.c_int, _JOIN, _I64, _I64, _P, _P, _P, _P, _P, _P,
                                                _SZ, _P]),
+    "moe_orthogonalize_workspace_size": (_SZ, [_I64, _I64, _I64]),
+    "moe_orthogonalize": (ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _I64, _I32, ctypes.c_float, _P, ctypes.c_int, _P,
+                                         _SZ, _P]),
+    "moe_muon_step": (ctypes.c_int, [_P, ctypes.c_int, _P, ctypes.c_int, _P, _I64, _I64, _I64, _MUON, _P, _SZ, _P]),
     "moe_device_status": (ctypes.c_int, [ctypes.POINTER(ctypes.c_uint32), _I32]),
     "moe_selftest_bounded_wait": (ctypes.c_int, [ctypes.c_uint32, _P]),
 }
@@ -1250,6 +1262,66 @@ def moe_block_join_backward(dout: torch.Tensor | None, branch: torch.Tensor, *, 
                                        H, df.data_ptr(), dx.data_ptr(), _addr(dw), _addr(dgate), _addr(dw2),
                                        ws.data_ptr(), ws.numel(), raw))
     return BlockJoinGrads(df, dx, dw, dgate, dw2)
+
+
+# ---- orthogonalised updates
+
+def _matrices(t: torch.Tensor, name: str) -> tuple[int, int, int]:
+    """(E, rows, cols) of a batch of matrices [.., rows, cols]."""
+    _dev_tensor(t, name)
+    if t.dim() < 2:
+        raise MoeError(2, f"{name} must be [.., rows, cols]")
+    rows, cols = t.shape[-2:]
+    return t.shape[:-2].numel(), rows, cols
+
+
+def moe_orthogonalize(matrices: torch.Tensor, *, dtype: torch.dtype = torch.bfloat16, steps: int = 5,
+                      eps: float = 1e-7, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Newton-Schulz steps on each matrix of a batch [.., rows, cols] (float32,
+    float16 or bfloat16): X = G / (|G| + eps), then `steps` times X <- 3.4445 X
+    + (-4.7750 A + 2.0315 A A) X with A = X X^T. The result is in `dtype`,
+    bfloat16 or float16 (out's, where out is given)."""
+    lib = load_library()
+    E, rows, cols = _matrices(matrices, "matrices")
+    raw = _here(stream, matrices, out, workspace)
+    if out is None:
+        if dtype not in _DTYPE:
+            raise MoeError(3, f"unsupported dtype {dtype}")
+        out = _empty(matrices.shape, dtype, matrices.device, stream)
+    else:
+        _dev_tensor(out, "out")
+        if out.shape != matrices.shape:
+            raise MoeError(2, "out must have the matrices' shape")
+    ws = _scratch(lib.moe_orthogonalize_workspace_size(E, rows, cols), matrices.device, workspace, stream)
+    _check(lib.moe_orthogonalize(matrices.data_ptr(), _dt(matrices), E, rows, cols, steps, eps, out.data_ptr(),
+                                 _dt(out), ws.data_ptr(), ws.numel(), raw))
+    return out
+
+
+def moe_muon_step(weight: torch.Tensor, grad: torch.Tensor, momentum: torch.Tensor, *, lr: float,
+                  momentum_decay: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0,
+                  update_scale: float | None = None, steps: int = 5, eps: float = 1e-7, workspace=None,
+                  stream=None) -> torch.Tensor:
+    """One optimizer step on a batch of weight matrices [.., rows, cols], in
+    place: momentum (float32) <- momentum_decay * momentum + grad, weight <-
+    (1 - lr * weight_decay) * weight - lr * update_scale * O, O the
+    orthogonalised momentum (nesterov: grad + momentum_decay * momentum).
+    update_scale defaults to sqrt(max(1, rows / cols)). Returns the weight."""
+    lib = load_library()
+    E, rows, cols = _matrices(weight, "weight")
+    for t, name in ((grad, "grad"), (momentum, "momentum")):
+        if _dev_tensor(t, name).shape != weight.shape:
+            raise MoeError(2, f"{name} must have the weight's shape")
+    if momentum.dtype != torch.float32:
+        raise MoeError(3, "momentum must be float32")
+    if update_scale is None:
+        update_scale = max(1.0, rows / max(1, cols)) ** 0.5
+    raw = _here(stream, weight, grad, momentum, workspace)
+    p = MuonParams(lr, momentum_decay, weight_decay, update_scale, eps, steps, int(bool(nesterov)))
+    ws = _scratch(lib.moe_orthogonalize_workspace_size(E, rows, cols), weight.device, workspace, stream)
+    _check(lib.moe_muon_step(weight.data_ptr(), _dt(weight), grad.data_ptr(), _dt(grad), momentum.data_ptr(), E, rows,
+                             cols, p, ws.data_ptr(), ws.numel(), raw))
+    return weight
 
 
 def moe_device_status(clear: bool = True) -> int:

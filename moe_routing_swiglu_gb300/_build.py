@@ -21,7 +21,8 @@ LIB = PKG / "libmoe_gb300.so"
 
 SOURCES = ["api.cu", "route.cu", "route_dispatch.cu", "route_grouped.cu", "dispatch.cu", "combine.cu", "experts_simt.cu", "experts_tc.cu",
            "train_router.cu", "train_experts.cu", "experts_bwd_tc.cu", "mxfp4.cu", "experts_mx.cu", "grad_clip.cu",
-           "api_mxfp4.cu", "api_grad.cu", "block_norm.cu", "api_block.cu"]
+           "api_mxfp4.cu", "api_grad.cu", "block_norm.cu", "api_block.cu",
+           "newton_schulz.cu", "api_muon.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
           "-I", str(INCLUDE), "-I", str(CSRC)]

@@ -301,6 +301,25 @@ struct JoinBackwardArgs {
 int64_t join_backward_units(int64_t T, int64_t H);
 cudaError_t launch_join_backward(moe_dtype dtype, const JoinBackwardArgs& a, float* dnorm_weight, float* dnext_weight,
                                  cudaStream_t stream);
+// ---- orthogonalised updates (newton_schulz.cu)
+struct NewtonSchulz {
+  const void* grad;       // [E, rows, cols]
+  moe_dtype grad_dtype;
+  float* momentum;        // [E, rows, cols] or NULL: grad itself is orthogonalised
+  float momentum_decay;
+  int nesterov;
+  int64_t E, rows, cols;
+  int steps;
+  float eps;
+  void* result;           // [E, rows, cols]: the orthogonalised matrix, or
+  moe_dtype result_dtype; // (update) result = keep * result - rate * matrix
+  int update;
+  float keep, rate;
+};
+size_t newton_schulz_scratch_bytes(int64_t E, int64_t rows, int64_t cols);
+int64_t newton_schulz_tiles(int64_t E, int64_t rows, int64_t cols);   // an upper bound of any product's tiles
+cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, int num_sms, cudaStream_t stream,
+                                 const char** why);
 cudaError_t launch_bounded_wait_selftest(uint32_t limit_us, cudaStream_t stream);
 
 }  // namespace moe
