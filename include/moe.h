@@ -935,8 +935,8 @@ moe_status moe_block_join_backward(const void* dout, const void* dnormed, const 
  *   eps         finite, > 0.
  *   workspace   device, moe_orthogonalize_workspace_size(E, rows, cols) bytes,
  *               256-byte aligned, of both calls below: about 8 bytes per
- *               element and 12 min(rows, cols)^2 per matrix. Contents need not
- *               be initialised. Calls that may overlap need separate ones.
+ *               element, 12 min(rows, cols)^2 per matrix, and up to 34 MB for
+ *               batches of few matrices. Contents need not be initialised. Calls that may overlap need separate ones.
  * Tensors are aligned to their element size. The same bits on every run.
  * ---------------------------------------------------------------------- */
 size_t moe_orthogonalize_workspace_size(int64_t E, int64_t rows, int64_t cols);

@@ -42,12 +42,8 @@ bool misaligned(const void* p, int dtype) {
 }
 
 moe_status launch(const moe::NewtonSchulz& o, void* ws, void* stream, const char* where) {
-  int dev = 0, sms = 0;
-  cudaError_t err = cudaGetDevice(&dev);
-  if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (err != cudaSuccess) return api_cuda_fail(err, "device query");
   const char* why = nullptr;
-  err = moe::launch_newton_schulz(o, ws, sms, static_cast<cudaStream_t>(stream), &why);
+  const cudaError_t err = moe::launch_newton_schulz(o, ws, static_cast<cudaStream_t>(stream), &why);
   if (err != cudaSuccess) return api_cuda_fail(err, where, why);
   return api_ok();
 }

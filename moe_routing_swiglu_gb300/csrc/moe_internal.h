@@ -318,8 +318,7 @@ struct NewtonSchulz {
 };
 size_t newton_schulz_scratch_bytes(int64_t E, int64_t rows, int64_t cols);
 int64_t newton_schulz_tiles(int64_t E, int64_t rows, int64_t cols);   // an upper bound of any product's tiles
-cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, int num_sms, cudaStream_t stream,
-                                 const char** why);
+cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStream_t stream, const char** why);
 cudaError_t launch_bounded_wait_selftest(uint32_t limit_us, cudaStream_t stream);
 
 }  // namespace moe

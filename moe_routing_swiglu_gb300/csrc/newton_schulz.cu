@@ -23,15 +23,19 @@
 // 2^13 (C, B) they stay under FP16's 65504, and lo of an entry as small as
 // 2^-14 is still a normal FP16.
 //
-// Structure: one persistent CTA per SM, tiles of 128 x 256 with K in blocks of
-// 64; warp 0 issues the TMA copies, warp 1 the MMAs, warps 2..9 drain TMEM,
-// whose two 256-column accumulators let one tile's epilogue run under the next
-// one's MMAs. Operands along their rows (K contiguous) are K-major tiles, X as
+// Structure: a persistent pair of CTAs on two SMs (cta_group::2) per tile of
+// 256 x 256, K in blocks of 64. Each CTA brings 128 rows of P and half of Q's
+// columns, hi and lo, 64 KB a k-block for 1536 cycles of MMAs; one CTA alone
+// with 128 x 256 tiles needs 96 KB, all that an SM takes in from L2 in that
+// time. Warp 0 issues the TMA copies, warp 1 of the first CTA the MMAs, warps
+// 2..9 drain TMEM, whose two 256-column accumulators let one tile's epilogue
+// run under the next one's MMAs. Operands along their rows (K contiguous) are K-major tiles, X as
 // a right-hand side and X^T X read X as it is stored, MN-major. Waits are
 // bounded; one that runs out records a code and the CTA winds down.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
+#include <atomic>
 #include <mutex>
 #include <type_traits>
 
@@ -54,14 +58,17 @@ constexpr float APPLY_TO_RESULT = pow2(-B_EXP - X_EXP);
 // ---------------------------------------------------------------- norm, momentum, first X
 
 constexpr int PRE_THREADS = 256;
+constexpr int PRE_GROUP = 4;         // groups of 8 elements that a thread loads together
 constexpr int MAX_CHUNKS = 256;      // partial sums per matrix
-constexpr int64_t MIN_CHUNK = 16384; // elements
+constexpr int64_t MIN_CHUNK = PRE_THREADS * PRE_GROUP * 8;
+constexpr int64_t PRE_BLOCKS = 1216; // blocks that a batch is cut into, at least, where its size allows it: 8 per SM
 
-__host__ __device__ inline int64_t chunk_elems(int64_t n) {
-  const int64_t c = (n + MAX_CHUNKS - 1) / MAX_CHUNKS;
-  return (c < MIN_CHUNK ? MIN_CHUNK : c + 7) / 8 * 8;
+// Elements of a matrix that one block adds the squares of.
+inline int64_t chunk_elems(int64_t E, int64_t n) {
+  const int64_t least = (n + MAX_CHUNKS - 1) / MAX_CHUNKS, fair = E * n / PRE_BLOCKS;
+  return (std::max(std::max(least, fair), MIN_CHUNK) + MIN_CHUNK - 1) / MIN_CHUNK * MIN_CHUNK;
 }
-inline int64_t chunk_count(int64_t n) { return (n + chunk_elems(n) - 1) / chunk_elems(n); }
+inline int64_t chunk_count(int64_t E, int64_t n) { return (n + chunk_elems(E, n) - 1) / chunk_elems(E, n); }
 
 template <typename T>
 struct alignas(16) Eight {
@@ -139,38 +146,50 @@ __global__ void __launch_bounds__(PRE_THREADS) squares_kernel(const PreArgs a) {
   const int64_t base = blockIdx.y * a.n;
   const int64_t lo = blockIdx.x * a.chunk, hi = min(lo + a.chunk, a.n);
   double total = 0.0;
-  // Rounds of a few elements in FP32, the rounds in FP64.
-  constexpr int G = 4;
-  for (int64_t i0 = lo; i0 < hi; i0 += PRE_THREADS * 8 * G) {
-    Squares s{0.0f, 0.0f, 0.0f};
+  // A round's 32 squares in FP32, the rounds in FP64.
+  for (int64_t i0 = lo; i0 < hi; i0 += PRE_THREADS * 8 * PRE_GROUP) {
+    float g[PRE_GROUP][8], m[PRE_GROUP][8];
+    auto at = [&](int k) { return i0 + (k * PRE_THREADS + static_cast<int64_t>(threadIdx.x)) * 8; };
+    auto left = [&](int k) { return static_cast<int>(max(min(hi - at(k), int64_t{8}), int64_t{0})); };
 #pragma unroll
-    for (int k = 0; k < G; ++k) {
-      const int64_t i = i0 + (k * PRE_THREADS + static_cast<int64_t>(threadIdx.x)) * 8;
-      if (i >= hi) continue;
-      const int n = static_cast<int>(min(hi - i, int64_t{8}));
-      const bool vec = a.vec && n == 8;
-      float g[8];
-      load8<T>(static_cast<const T*>(a.g) + base + i, n, vec, g);
-      if (a.m != nullptr) {
-        float m[8];
-        float* p = a.m + base + i;
-        load8<float>(p, n, vec, m);
+    for (int k = 0; k < PRE_GROUP; ++k) {
+      load8<T>(static_cast<const T*>(a.g) + base + at(k), left(k), a.vec && left(k) == 8, g[k]);
+      if (a.m != nullptr) load8<float>(a.m + base + at(k), left(k), a.vec && left(k) == 8, m[k]);
+    }
+    if (a.m != nullptr) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m[j] = fmaf(a.mu, m[j], g[j]);
-        if (vec) {
-          reinterpret_cast<float4*>(p)[0] = make_float4(m[0], m[1], m[2], m[3]);
-          reinterpret_cast<float4*>(p)[1] = make_float4(m[4], m[5], m[6], m[7]);
+      for (int k = 0; k < PRE_GROUP; ++k) {
+        float* p = a.m + base + at(k);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) m[k][j] = fmaf(a.mu, m[k][j], g[k][j]);
+        if (a.vec && left(k) == 8) {
+          reinterpret_cast<float4*>(p)[0] = make_float4(m[k][0], m[k][1], m[k][2], m[k][3]);
+          reinterpret_cast<float4*>(p)[1] = make_float4(m[k][4], m[k][5], m[k][6], m[k][7]);
         } else {
-          for (int j = 0; j < n; ++j) p[j] = m[j];
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < left(k)) p[j] = m[k][j];
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = update_of(a, g[j], m[j]);
+        for (int j = 0; j < 8; ++j) g[k][j] = j < left(k) ? update_of(a, g[k][j], m[k][j]) : 0.0f;
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j < n) s.add(g[j]);
     }
-    total += s.total();
+    float fast = 0.0f;
+#pragma unroll
+    for (int k = 0; k < PRE_GROUP; ++k)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) fast = fmaf(g[k][j], g[k][j], fast);
+    // 32 squares that each lose at most 2^-150 do not show in a sum of 2^-60.
+    if (fast >= 0x1p-60f && fast <= 0x1p100f) {
+      total += fast;
+    } else {
+      Squares s{0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int k = 0; k < PRE_GROUP; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s.add(g[k][j]);
+      total += s.total();
+    }
   }
   total = block_sum(total, sm);
   if (threadIdx.x == 0) a.partial[static_cast<int64_t>(blockIdx.y) * a.chunks + blockIdx.x] = total;
@@ -192,49 +211,67 @@ __global__ void __launch_bounds__(PRE_THREADS) first_x_kernel(const PreArgs a) {
   static_assert(MAX_CHUNKS <= PRE_THREADS, "one partial sum a thread");
   sum = block_sum(sum, sm);
   // 2^14 / (norm + eps) as two FP32 factors, both far from FP32's ends. A
-  // matrix with a NaN or an infinity becomes NaN as a whole.
-  const double scale = isfinite(sum) ? 0x1p14 / (sqrt(sum) + a.eps) : nan("");
-  int ex = 0;
-  const double frac = frexp(scale, &ex);
-  const float s1 = static_cast<float>(ldexp(frac, ex - ex / 2)), s2 = static_cast<float>(ldexp(1.0, ex / 2));
-  const int64_t per_row = a.pitch / 8, groups = per_row * a.r;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * PRE_THREADS + threadIdx.x; i < groups;
-       i += static_cast<int64_t>(gridDim.x) * PRE_THREADS) {
-    const int64_t row = i / per_row, col = (i - row * per_row) * 8;
-    const int n = static_cast<int>(min(a.c - col, int64_t{8}));
-    const int64_t at = e * a.n + row * a.c + col;
-    const bool vec = a.vec && a.c % 8 == 0;
-    float g[8];
-    load8<T>(static_cast<const T*>(a.g) + at, n, vec, g);
-    if (a.m != nullptr) {
-      float m[8];
-      load8<float>(a.m + at, n, vec, m);
+  // matrix with a NaN or an infinity becomes NaN as a whole. By one thread:
+  // FP64 is slow here.
+  __shared__ float factors[2];
+  if (threadIdx.x == 0) {
+    const double scale = isfinite(sum) ? 0x1p14 / (sqrt(sum) + a.eps) : nan("");
+    int ex = 0;
+    const double frac = frexp(scale, &ex);
+    factors[0] = static_cast<float>(ldexp(frac, ex - ex / 2));
+    factors[1] = static_cast<float>(ldexp(1.0, ex / 2));
+  }
+  __syncthreads();
+  const float s1 = factors[0], s2 = factors[1];
+  const uint32_t per_row = static_cast<uint32_t>(a.pitch / 8), groups = per_row * a.r;
+  const bool vec = a.vec && a.c % 8 == 0;
+  const uint32_t step = gridDim.x * PRE_THREADS;
+  for (uint32_t i0 = blockIdx.x * PRE_THREADS + threadIdx.x; i0 < groups; i0 += PRE_GROUP * step) {
+    float g[PRE_GROUP][8], m[PRE_GROUP][8];
+    int64_t to[PRE_GROUP];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = update_of(a, g[j], m[j]);
+    for (int k = 0; k < PRE_GROUP; ++k) {
+      const uint32_t i = i0 + k * step;
+      to[k] = -1;
+      if (i >= groups) continue;
+      const uint32_t row = i / per_row, col = (i - row * per_row) * 8;
+      to[k] = (e * a.r + row) * a.pitch + col;
+      const int64_t at = e * a.n + static_cast<int64_t>(row) * a.c + col;
+      const int n = min(a.c - static_cast<int>(col), 8);
+      load8<T>(static_cast<const T*>(a.g) + at, n, vec, g[k]);
+      if (a.m != nullptr) load8<float>(a.m + at, n, vec, m[k]);
     }
-    Eight<__half> h, l;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) split_half(g[j] * s1 * s2, &h.e[j], &l.e[j]);
-    const int64_t to = (e * a.r + row) * a.pitch + col;
-    *reinterpret_cast<uint4*>(a.hi + to) = *reinterpret_cast<const uint4*>(&h);
-    *reinterpret_cast<uint4*>(a.lo + to) = *reinterpret_cast<const uint4*>(&l);
+    for (int k = 0; k < PRE_GROUP; ++k) {
+      if (to[k] < 0) continue;
+      Eight<__half> h, l;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float u = a.m != nullptr ? update_of(a, g[k][j], m[k][j]) : g[k][j];
+        split_half(u * s1 * s2, &h.e[j], &l.e[j]);
+      }
+      *reinterpret_cast<uint4*>(a.hi + to[k]) = *reinterpret_cast<const uint4*>(&h);
+      *reinterpret_cast<uint4*>(a.lo + to[k]) = *reinterpret_cast<const uint4*>(&l);
+    }
   }
 }
 
 // ---------------------------------------------------------------- the products
 
-enum NsMode { GRAM = 0, POLY = 1, APPLY = 2, FINAL = 3 };
+enum NsMode { GRAM = 0, POLY = 1, APPLY = 2, FINAL = 3, GRAM_PART = 4 };
 
-constexpr int BM = 128, BN = 256, BK = 64, UMMA_K = 16;
+constexpr int TILE = 256, BM = 128, BK = 64, UMMA_K = 16;
 constexpr int BOX = 64 * 128;                        // 64 x 64 elements, or 64 rows of 128 bytes
-constexpr int P_BYTES = BM * BK * 2, Q_BYTES = BN * BK * 2;
-constexpr int STAGE_BYTES = 2 * (P_BYTES + Q_BYTES); // hi and lo of both operands
-constexpr int STAGES = 2;
+constexpr int OP_BYTES = BM * BK * 2;                // a block's half of an operand: 128 rows, or columns
+constexpr int STAGE_BYTES = 4 * OP_BYTES;            // hi and lo of both operands
+constexpr int STAGES = 3;
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int NUM_EPI_WARPS = 8;
 constexpr int NUM_THREADS = 32 * (2 + NUM_EPI_WARPS);
 constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
-constexpr int SMEM_BAR = STAGES * STAGE_BYTES;
+constexpr int STAGING_BYTES = 32 * 32 * 4;           // per epilogue warp: 32 x 32 FP32, or FP16 hi and lo
+constexpr int SMEM_STAGING = STAGES * STAGE_BYTES;
+constexpr int SMEM_BAR = SMEM_STAGING + NUM_EPI_WARPS * STAGING_BYTES;
 constexpr int NUM_BARS = 2 * STAGES + 5;
 constexpr int SMEM_MISC = SMEM_BAR + 8 * NUM_BARS;   // TMEM address, abort flag, stages issued
 constexpr int SMEM_BYTES = 1024 + SMEM_MISC + 16;
@@ -247,126 +284,229 @@ constexpr uint32_t ST_EPI_TMEM_FULL = 0x44;
 constexpr uint32_t ST_MMA_DRAIN = 0x45;
 constexpr uint32_t ST_PRODUCER_DRAIN = 0x46;
 
+// A block pair's instructions (cta_group::2): block 0 of the pair issues one
+// MMA for both, each block holding 128 rows of P, half of Q's columns and 128
+// rows of the accumulator.
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of `p` in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_u32(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void peer_arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void peer_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t peer_load(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+// Into this block's shared memory, counted on a barrier of either block.
+__device__ __forceinline__ void pair_load_3d(void* dst, const void* desc, uint32_t bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(desc), "r"(bar), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+__device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst)), "r"(cols)
+               : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_tmem_dealloc(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+__device__ __forceinline__ void pair_umma_f16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// Arrives on the barrier at this place in both blocks once the MMAs issued so
+// far are complete.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
 // D [E, m, n] = P [E, m, k] Q [E, k, n], both FP16 pairs.
 struct NsArgs {
   int m, n, k;
   int m_blocks, n_blocks;
+  int k_split;          // k-blocks of a part (GRAM_PART), else all
   uint32_t tiles, tiles_per_matrix;
-  __half* out_hi;       // GRAM A, POLY B, APPLY X': [E, m, pitch]
-  __half* out_lo;
-  __half* out2_hi;      // GRAM C
-  __half* out2_lo;
-  int64_t pitch;
+  int64_t pitch;        // GRAM_PART
+  float* parts;         // [parts, E, m, pitch]
+  int64_t part_elems;   // E * m * pitch
   void* result;         // FINAL: [E, m, n] in result_dtype
   int result_dtype;
-  int result_vec;       // rows and pointer 16-byte aligned
   int update;           // FINAL: result = keep * result - rate * X' (weights), else X'
   float keep, rate;
   uint32_t* status;
 };
 
-// Tile -> (matrix, row block, column block). Symmetric products have the
-// tiles whose 256 columns reach the diagonal or lie right of it.
+// Tile -> (matrix, row block, column block, first k-block and their number).
+// Symmetric products have the tiles on and above the diagonal; a product in
+// parts has all tiles of one part before the next part's.
 struct NsTile {
-  int e, mb, nb;
+  int e, mb, nb, kb0, kbs, part;
 };
-template <bool TRI>
+template <int MODE>
 __device__ __forceinline__ NsTile ns_tile(uint32_t tile, const NsArgs& a) {
   NsTile t;
-  t.e = static_cast<int>(tile / a.tiles_per_matrix);
-  int i = static_cast<int>(tile % a.tiles_per_matrix);
-  if (TRI) {
+  const int k_blocks = (a.k + BK - 1) / BK;
+  t.kb0 = 0;
+  t.kbs = k_blocks;
+  t.part = 0;
+  uint32_t matrix = tile / a.tiles_per_matrix;
+  int i = static_cast<int>(tile - matrix * a.tiles_per_matrix);
+  if (MODE == GRAM || MODE == POLY) {
     t.mb = 0;
-    while (i >= a.n_blocks - t.mb / 2) {
-      i -= a.n_blocks - t.mb / 2;
+    while (i >= a.n_blocks - t.mb) {
+      i -= a.n_blocks - t.mb;
       ++t.mb;
     }
-    t.nb = t.mb / 2 + i;
+    t.nb = t.mb + i;
   } else {
     t.mb = i % a.m_blocks;
     t.nb = i / a.m_blocks;
   }
+  if (MODE == GRAM_PART) {
+    const uint32_t matrices = static_cast<uint32_t>(a.part_elems / (a.m * a.pitch));
+    t.part = static_cast<int>(matrix / matrices);
+    matrix -= t.part * matrices;
+    t.kb0 = t.part * a.k_split;
+    t.kbs = min(a.k_split, k_blocks - t.kb0);
+  }
+  t.e = static_cast<int>(matrix);
   return t;
 }
 
-// 32 columns of a row as FP16 pairs, at [row][col ..]; columns up to the pitch
-// are written (those past n are zeros).
-__device__ __forceinline__ void store_pairs(__half* hi, __half* lo, int64_t row_off, int64_t pitch, int col,
-                                            const float (&v)[32]) {
+// A warp's 32 x 32 block (lane: row, v: its columns) as FP16 pairs into its
+// staging tiles, 32 rows of 64 bytes each with the 64-byte swizzle (16-byte
+// chunk q of row r at chunk q ^ (r / 2 % 4)), and from there to (row, col) of
+// both planes by tensor stores, which clip what is past the matrix. MIRROR: the
+// transposed block, at (col, row). Both ways of writing the tiles are free of
+// bank conflicts.
+template <bool MIRROR>
+__device__ __forceinline__ void store_pairs(uint32_t tile, const CUtensorMap* hi, const CUtensorMap* lo, int row, int col,
+                                            int e, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) bulk_wait_read_all();   // the last stores have read the tiles
+  __syncwarp();
+  if (MIRROR) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (col + q * 8 < pitch) {
-      Eight<__half> h, l;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) split_half(v[q * 8 + j], &h.e[j], &l.e[j]);
-      *reinterpret_cast<uint4*>(hi + row_off + col + q * 8) = *reinterpret_cast<const uint4*>(&h);
-      *reinterpret_cast<uint4*>(lo + row_off + col + q * 8) = *reinterpret_cast<const uint4*>(&l);
-    }
-  }
-}
-
-// The same block mirrored: the 32 lanes' row numbers are the columns.
-__device__ __forceinline__ void store_pairs_mirrored(__half* hi, __half* lo, int64_t matrix_off, int64_t pitch, int row,
-                                                     int col, int n, const float (&v)[32]) {
-  for (int j = 0; j < 32; ++j) {
-    if (col + j < n && row < n) {
+    for (int j = 0; j < 32; ++j) {
       __half h, l;
       split_half(v[j], &h, &l);
-      const int64_t at = matrix_off + (col + j) * pitch + row;
-      hi[at] = h;
-      lo[at] = l;
-    }
-  }
-}
-
-template <typename T>
-__device__ __forceinline__ void store_result(const NsArgs& a, int64_t at, int cols, const float (&v)[32]) {
-  T* p = static_cast<T*>(a.result) + at;
-  if (a.result_vec && cols >= 32) {
-    constexpr int N = 16 / sizeof(T);
-#pragma unroll
-    for (int q = 0; q < 32 / N; ++q) {
-      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-      T* e = reinterpret_cast<T*>(&raw);
-      if (a.update) raw = reinterpret_cast<const uint4*>(p)[q];
-#pragma unroll
-      for (int j = 0; j < N; ++j)
-        e[j] = from_f32<T>(a.update ? fmaf(a.keep, to_f32(e[j]), -a.rate * v[q * N + j]) : v[q * N + j]);
-      reinterpret_cast<uint4*>(p)[q] = raw;
+      const uint32_t at = tile + j * 64 + (((lane >> 3) ^ ((j >> 1) & 3)) << 4) + (lane & 7) * 2;
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(__half_as_ushort(h)) : "memory");
+      asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + 2048), "h"(__half_as_ushort(l)) : "memory");
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-      if (j < cols) p[j] = from_f32<T>(a.update ? fmaf(a.keep, to_f32(p[j]), -a.rate * v[j]) : v[j]);
+    for (int q = 0; q < 4; ++q) {
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = v[q * 8 + 2 * j], y = v[q * 8 + 2 * j + 1];
+        const __half2 p = __floats2half2_rn(x, y);
+        const float2 f = __half22float2(p);
+        h[j] = *reinterpret_cast<const uint32_t*>(&p);
+        l[j] = pack2<__half>(x - f.x, y - f.y);
+      }
+      const uint32_t at = tile + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
+      st_shared_v4(at, h[0], h[1], h[2], h[3]);
+      st_shared_v4(at + 2048, l[0], l[1], l[2], l[3]);
+    }
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_3d(hi, tile, MIRROR ? row : col, MIRROR ? col : row, e);
+    tma_store_3d(lo, tile + 2048, MIRROR ? row : col, MIRROR ? col : row, e);
+    bulk_commit_group();
+  }
+}
+
+// A warp's block of the last product through its staging tile (FP32, 32 rows of
+// 128 bytes, 16-byte chunk q of row r at chunk q ^ (r % 8)), so that a warp
+// reads and writes 32 neighbouring elements of a row.
+template <typename T>
+__device__ __forceinline__ void store_result(const NsArgs& a, float* tile, int row, int col, int e, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 8; ++q)
+    *reinterpret_cast<float4*>(tile + lane * 32 + ((q ^ (lane & 7)) << 2)) =
+        make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+  __syncwarp();
+  const bool in = col + lane < a.n;
+  T* p = static_cast<T*>(a.result) + (static_cast<int64_t>(e) * a.m + row) * a.n + col + lane;
+  constexpr int G = 8;    // rows whose weights are loaded together
+#pragma unroll
+  for (int r0 = 0; r0 < 32; r0 += G) {
+    T old[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+      if (a.update && in && row + r0 + i < a.m) old[i] = p[static_cast<int64_t>(r0 + i) * a.n];
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const int r = r0 + i;
+      const float x = tile[r * 32 + ((((lane >> 2) ^ (r & 7)) << 2) | (lane & 3))];
+      if (in && row + r < a.m)
+        p[static_cast<int64_t>(r) * a.n] = from_f32<T>(a.update ? fmaf(a.keep, to_f32(old[i]), -a.rate * x) : x);
+    }
   }
 }
 
 template <int MODE, bool P_MN, bool Q_MN>
-__global__ void __launch_bounds__(NUM_THREADS, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     ns_kernel(const __grid_constant__ CUtensorMap p_hi, const __grid_constant__ CUtensorMap p_lo,
-              const __grid_constant__ CUtensorMap q_hi, const __grid_constant__ CUtensorMap q_lo, const NsArgs args) {
-  constexpr bool TRI = MODE == GRAM || MODE == POLY;
+              const __grid_constant__ CUtensorMap q_hi, const __grid_constant__ CUtensorMap q_lo,
+              const __grid_constant__ CUtensorMap o_hi, const __grid_constant__ CUtensorMap o_lo,
+              const __grid_constant__ CUtensorMap o2_hi, const __grid_constant__ CUtensorMap o2_lo, const NsArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SMEM_BAR);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SMEM_BAR);   // block 0's are used
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;   // [2]
-  uint64_t* tempty = tfull + 2;       // [2]
+  uint64_t* tempty = tfull + 2;       // [2], block 0's are used
   uint64_t* drain = tempty + 2;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + SMEM_MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SMEM_MISC + 4);
   uint32_t* issued_stages = reinterpret_cast<uint32_t*>(smem + SMEM_MISC + 8);
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);          // each block arms its own copies
       mbar_init(&empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], NUM_EPI_WARPS);
+      mbar_init(&tempty[a], 2 * NUM_EPI_WARPS);
     }
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -379,17 +519,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     tma_prefetch_desc(&q_lo);
   }
   __syncwarp();
-  if (warp == 1) {
-    tmem_alloc(tmem_holder, TMEM_COLS);
-    tmem_relinquish();
-  }
+  if (warp == 1) pair_tmem_alloc(tmem_holder, TMEM_COLS);
   tc_fence_before();
   __syncthreads();
+  cluster_sync();   // both blocks' barriers are there before either one's copies and arrivals
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  const int k_blocks = (args.k + BK - 1) / BK;
   grid_dependency_wait();
   launch_dependents();
+
+  // Columns of a tile, of which each block brings half.
+  auto n_of = [&](const NsTile& t) { return min(TILE, (args.n - t.nb * TILE + 31) & ~31); };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -397,25 +537,28 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       int stage = 0;
       uint32_t phase = 0, issued = 0;
       bool ok = true;
-      for (uint32_t tile = blockIdx.x; ok && tile < args.tiles; tile += gridDim.x) {
-        const NsTile t = ns_tile<TRI>(tile, args);
-        for (int kb = 0; kb < k_blocks; ++kb) {
+      for (uint32_t tile = pair; ok && tile < args.tiles; tile += pairs) {
+        const NsTile t = ns_tile<MODE>(tile, args);
+        const int m0 = t.mb * TILE + static_cast<int>(rank) * BM;
+        const int n0 = t.nb * TILE + static_cast<int>(rank) * (n_of(t) / 2);
+        for (int kb = t.kb0; kb < t.kb0 + t.kbs; ++kb) {
           ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, args.status, ST_PRODUCER_EMPTY, WAIT_LIMIT_NS);
           if (!ok) break;
           uint8_t* st = smem + stage * STAGE_BYTES;
-          mbar_arrive_expect_tx(&full[stage], STAGE_BYTES);
+          const uint32_t bar = peer_u32(&full[stage], 0);
+          peer_arrive_expect_tx(bar, STAGE_BYTES);
           const int k0 = kb * BK;
-          auto load = [&](uint8_t* dst, const CUtensorMap* map, bool mn_major, int rows, int at) {
+          auto load = [&](uint8_t* dst, const CUtensorMap* map, bool mn_major, int at) {
             if (!mn_major) {
-              tma_load_3d(dst, map, &full[stage], k0, at, t.e);
+              pair_load_3d(dst, map, bar, k0, at, t.e);
             } else {
-              for (int q = 0; q < rows / 64; ++q) tma_load_3d(dst + q * BOX, map, &full[stage], at + 64 * q, k0, t.e);
+              for (int q = 0; q < BM / 64; ++q) pair_load_3d(dst + q * BOX, map, bar, at + 64 * q, k0, t.e);
             }
           };
-          load(st, &p_hi, P_MN, BM, t.mb * BM);
-          load(st + 2 * P_BYTES, &q_hi, Q_MN, BN, t.nb * BN);
-          load(st + P_BYTES, &p_lo, P_MN, BM, t.mb * BM);
-          load(st + 2 * P_BYTES + Q_BYTES, &q_lo, Q_MN, BN, t.nb * BN);
+          load(st, &p_hi, P_MN, m0);
+          load(st + 2 * OP_BYTES, &q_hi, Q_MN, n0);
+          load(st + OP_BYTES, &p_lo, P_MN, m0);
+          load(st + 3 * OP_BYTES, &q_lo, Q_MN, n0);
           ++issued;
           if (++stage == STAGES) {
             stage = 0;
@@ -427,134 +570,183 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
+    // ------------------------------------------------------------ MMA issuer (block 0, for both)
     if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      uint32_t it = 0;
-      for (uint32_t tile = blockIdx.x; ok && tile < args.tiles; tile += gridDim.x, ++it) {
-        const NsTile t = ns_tile<TRI>(tile, args);
-        const int n_len = min(BN, (args.n - t.nb * BN + 15) & ~15);
-        const uint32_t idesc = idesc_f16_major(false, BM, n_len, P_MN, Q_MN);
-        const uint32_t acc = it & 1u;
-        ok = mbar_wait_bounded(&tempty[acc], ((it >> 1) & 1u) ^ 1u, abort_flag, args.status, ST_MMA_TMEM_EMPTY,
-                               WAIT_LIMIT_NS);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t d = tmem_base + acc * BN;
-        for (int kb = 0; kb < k_blocks; ++kb) {
-          ok = mbar_wait_bounded(&full[stage], phase, abort_flag, args.status, ST_MMA_FULL, WAIT_LIMIT_NS);
+      if (rank == 0) {
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        uint32_t it = 0;
+        for (uint32_t tile = pair; ok && tile < args.tiles; tile += pairs, ++it) {
+          const NsTile t = ns_tile<MODE>(tile, args);
+          const uint32_t idesc = idesc_f16_major(false, TILE, n_of(t), P_MN, Q_MN);
+          const uint32_t acc = it & 1u;
+          ok = mbar_wait_bounded(&tempty[acc], ((it >> 1) & 1u) ^ 1u, abort_flag, args.status, ST_MMA_TMEM_EMPTY,
+                                 WAIT_LIMIT_NS);
           if (!ok) break;
           tc_fence_after();
-          const uint32_t ph = smem_u32(smem + stage * STAGE_BYTES), pl = ph + P_BYTES;
-          const uint32_t qh = ph + 2 * P_BYTES, ql = qh + Q_BYTES;
-          const int n_sub = min(BK / UMMA_K, (args.k - kb * BK + UMMA_K - 1) / UMMA_K);
-          for (int k = 0; k < n_sub; ++k) {
-            auto pd = [&](uint32_t at) {
-              return P_MN ? sdesc_mnmajor_sw128(at + k * 2048, BOX, 1024) : sdesc_kmajor_sw128(at + k * UMMA_K * 2);
-            };
-            auto qd = [&](uint32_t at) {
-              return Q_MN ? sdesc_mnmajor_sw128(at + k * 2048, BOX, 1024) : sdesc_kmajor_sw128(at + k * UMMA_K * 2);
-            };
-            umma_f16(d, pd(pl), qd(qh), idesc, (kb > 0 || k > 0) ? 1u : 0u);
-            umma_f16(d, pd(ph), qd(ql), idesc, 1u);
-            umma_f16(d, pd(ph), qd(qh), idesc, 1u);
+          const uint32_t d = tmem_base + acc * TILE;
+          for (int kb = t.kb0; kb < t.kb0 + t.kbs; ++kb) {
+            ok = mbar_wait_bounded(&full[stage], phase, abort_flag, args.status, ST_MMA_FULL, WAIT_LIMIT_NS);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t ph = smem_u32(smem + stage * STAGE_BYTES), pl = ph + OP_BYTES;
+            const uint32_t qh = ph + 2 * OP_BYTES, ql = qh + OP_BYTES;
+            const int n_sub = min(BK / UMMA_K, (args.k - kb * BK + UMMA_K - 1) / UMMA_K);
+            for (int k = 0; k < n_sub; ++k) {
+              auto pd = [&](uint32_t at) {
+                return P_MN ? sdesc_mnmajor_sw128(at + k * 2048, BOX, 1024) : sdesc_kmajor_sw128(at + k * UMMA_K * 2);
+              };
+              auto qd = [&](uint32_t at) {
+                return Q_MN ? sdesc_mnmajor_sw128(at + k * 2048, BOX, 1024) : sdesc_kmajor_sw128(at + k * UMMA_K * 2);
+              };
+              pair_umma_f16(d, pd(pl), qd(qh), idesc, (kb > t.kb0 || k > 0) ? 1u : 0u);
+              pair_umma_f16(d, pd(ph), qd(ql), idesc, 1u);
+              pair_umma_f16(d, pd(ph), qd(qh), idesc, 1u);
+            }
+            pair_commit(&empty[stage]);
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
           }
-          umma_commit(&empty[stage]);
-          if (++stage == STAGES) {
-            stage = 0;
-            phase ^= 1u;
-          }
+          if (!ok) break;
+          pair_commit(&tfull[acc]);
         }
-        if (!ok) break;
-        umma_commit(&tfull[acc]);
+        pair_commit(drain);
       }
-      umma_commit(drain);
-      mbar_wait_bounded(drain, 0, nullptr, args.status, ST_MMA_DRAIN, WAIT_LIMIT_NS);
     }
     __syncwarp();
   } else {
     // ------------------------------------------------------------ epilogue
     const int quad = warp & 3;
     const int half = (warp - 2) >> 2;
+    uint8_t* staging = smem + SMEM_STAGING + (warp - 2) * STAGING_BYTES;
+    const uint32_t tile_at = smem_u32(staging);
     uint32_t it = 0;
-    for (uint32_t tile = blockIdx.x; tile < args.tiles; tile += gridDim.x, ++it) {
-      const NsTile t = ns_tile<TRI>(tile, args);
+    for (uint32_t tile = pair; tile < args.tiles; tile += pairs, ++it) {
+      const NsTile t = ns_tile<MODE>(tile, args);
       const uint32_t acc = it & 1u;
       const bool ok = mbar_wait_bounded(&tfull[acc], (it >> 1) & 1u, abort_flag, args.status, ST_EPI_TMEM_FULL,
                                         WAIT_LIMIT_NS);
       if (!__all_sync(FULL_MASK, ok)) break;
       tc_fence_after();
-      const uint32_t t_lane = tmem_base + acc * BN + (static_cast<uint32_t>(quad * 32) << 16);
-      const int row = t.mb * BM + quad * 32 + lane;
-      const int64_t matrix_off = static_cast<int64_t>(t.e) * args.m * args.pitch;
-      const int64_t row_off = matrix_off + static_cast<int64_t>(row) * args.pitch;
-      for (int c0 = 32 * half; c0 < BN; c0 += 64) {
-        const int col = t.nb * BN + c0;
-        if (col >= args.n) break;
+      const uint32_t t_lane = tmem_base + acc * TILE + (static_cast<uint32_t>(quad * 32) << 16);
+      const int row = t.mb * TILE + static_cast<int>(rank) * BM + quad * 32;   // of lane 0
+      for (int c0 = 32 * half; c0 < TILE; c0 += 64) {
+        const int col = t.nb * TILE + c0;
+        if (col >= args.n || row >= args.m) break;
         uint32_t raw[32];
         tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(c0), raw);
         tmem_ld_wait();
         float v[32];
         if (MODE == GRAM || MODE == POLY) {
-          // The mirrored block's own tile is computed only if its columns reach the diagonal.
-          const bool mirror = col / BM > t.mb / 2 * 2 + 1;
+          const bool mirror = t.nb != t.mb;
+          const int diag = row + lane - col;
           if (MODE == GRAM) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) * GRAM_TO_A;
-            if (row < args.m) store_pairs(args.out_hi, args.out_lo, row_off, args.pitch, col, v);
-            if (mirror) store_pairs_mirrored(args.out_hi, args.out_lo, matrix_off, args.pitch, row, col, args.n, v);
+            store_pairs<false>(tile_at, &o_hi, &o_lo, row, col, t.e, v);
+            if (mirror) store_pairs<true>(tile_at, &o_hi, &o_lo, row, col, t.e, v);
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              v[j] = fmaf(__uint_as_float(raw[j]), GRAM_TO_C,
-                          row == col + j ? C_DIAG : 0.0f);
-            if (row < args.m) store_pairs(args.out2_hi, args.out2_lo, row_off, args.pitch, col, v);
-            if (mirror) store_pairs_mirrored(args.out2_hi, args.out2_lo, matrix_off, args.pitch, row, col, args.n, v);
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(__uint_as_float(raw[j]), GRAM_TO_C, diag == j ? C_DIAG : 0.0f);
+            store_pairs<false>(tile_at, &o2_hi, &o2_lo, row, col, t.e, v);
+            if (mirror) store_pairs<true>(tile_at, &o2_hi, &o2_lo, row, col, t.e, v);
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              v[j] = fmaf(__uint_as_float(raw[j]), POLY_TO_B,
-                          row == col + j ? B_DIAG : 0.0f);
-            if (row < args.m) store_pairs(args.out_hi, args.out_lo, row_off, args.pitch, col, v);
-            if (mirror) store_pairs_mirrored(args.out_hi, args.out_lo, matrix_off, args.pitch, row, col, args.n, v);
+            for (int j = 0; j < 32; ++j) v[j] = fmaf(__uint_as_float(raw[j]), POLY_TO_B, diag == j ? B_DIAG : 0.0f);
+            store_pairs<false>(tile_at, &o_hi, &o_lo, row, col, t.e, v);
+            if (mirror) store_pairs<true>(tile_at, &o_hi, &o_lo, row, col, t.e, v);
+          }
+        } else if (MODE == GRAM_PART) {
+          if (row + lane < args.m) {
+            float* p = args.parts + t.part * args.part_elems + (static_cast<int64_t>(t.e) * args.m + row + lane) * args.pitch +
+                       col;
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+              if (col + q * 4 < args.pitch)
+                reinterpret_cast<uint4*>(p)[q] = make_uint4(raw[4 * q], raw[4 * q + 1], raw[4 * q + 2], raw[4 * q + 3]);
           }
         } else if (MODE == APPLY) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) * APPLY_TO_X;
-          if (row < args.m) store_pairs(args.out_hi, args.out_lo, row_off, args.pitch, col, v);
+          store_pairs<false>(tile_at, &o_hi, &o_lo, row, col, t.e, v);
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) * APPLY_TO_RESULT;
-          if (row < args.m) {
-            const int64_t at = (static_cast<int64_t>(t.e) * args.m + row) * args.n + col;
-            const int cols = args.n - col;
-            if (args.result_dtype == MOE_F32) store_result<float>(args, at, cols, v);
-            else if (args.result_dtype == MOE_F16) store_result<__half>(args, at, cols, v);
-            else store_result<__nv_bfloat16>(args, at, cols, v);
-          }
+          float* stage = reinterpret_cast<float*>(staging);
+          if (args.result_dtype == MOE_F32) store_result<float>(args, stage, row, col, t.e, v);
+          else if (args.result_dtype == MOE_F16) store_result<__half>(args, stage, row, col, t.e, v);
+          else store_result<__nv_bfloat16>(args, stage, row, col, t.e, v);
         }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&tempty[acc]);
+      if (lane == 0) peer_arrive(peer_u32(&tempty[acc], 0));
     }
+    // The tensor stores read shared memory and write the matrices: both end before the block does.
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
   }
 
   tc_fence_before();
   __syncthreads();
-  if (*abort_flag != 0) {
-    // A role gave up: the copies that nobody waited for land before the block exits.
-    if (threadIdx.x == 0)
-      drain_ring(*issued_stages, STAGES, [&](uint32_t slot, uint32_t parity) {
+  // Every MMA has read its operands, and every commit has arrived, before either block leaves.
+  if (threadIdx.x == 0) mbar_wait_bounded(drain, 0, nullptr, args.status, ST_MMA_DRAIN, WAIT_LIMIT_NS);
+  __syncwarp();
+  cluster_sync();
+  if (*abort_flag != 0 || peer_load(peer_u32(const_cast<int*>(abort_flag), rank ^ 1u)) != 0) {
+    // A role gave up: the copies that nobody waited for land before the blocks
+    // exit. A stage that one block alone has issued is armed here for the other.
+    if (threadIdx.x == 0 && rank == 0) {
+      const uint32_t mine = *issued_stages, other = peer_load(peer_u32(issued_stages, 1));
+      for (uint32_t n = min(mine, other); n < max(mine, other); ++n) mbar_arrive(&full[n % STAGES]);
+      drain_ring(max(mine, other), STAGES, [&](uint32_t slot, uint32_t parity) {
         mbar_wait_bounded(&full[slot], parity, nullptr, args.status, ST_PRODUCER_DRAIN, WAIT_LIMIT_NS);
       });
-    __syncwarp();
+    }
+    __syncthreads();
   }
+  cluster_sync();   // nothing is left that reads or signals the other block's shared memory
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem_base, TMEM_COLS);
+    pair_tmem_dealloc(tmem_base, TMEM_COLS);
   }
+}
+
+// A and C from the parts of GRAM_PART, added in order.
+struct JoinPartsArgs {
+  const float* parts;
+  int64_t part_elems, pitch;
+  int count, s;
+  __half *a_hi, *a_lo, *c_hi, *c_lo;
+};
+__global__ void __launch_bounds__(PRE_THREADS) join_parts_kernel(const JoinPartsArgs a) {
+  grid_dependency_wait();
+  launch_dependents();
+  const int64_t at = (static_cast<int64_t>(blockIdx.x) * PRE_THREADS + threadIdx.x) * 4;
+  if (at >= a.part_elems) return;
+  float4 v = *reinterpret_cast<const float4*>(a.parts + at);
+  for (int p = 1; p < a.count; ++p) {
+    const float4 w = *reinterpret_cast<const float4*>(a.parts + p * a.part_elems + at);
+    v.x += w.x;
+    v.y += w.y;
+    v.z += w.z;
+    v.w += w.w;
+  }
+  const int64_t row_at = at / a.pitch;
+  const int row = static_cast<int>(row_at % a.s), col = static_cast<int>(at - row_at * a.pitch);
+  const float x[4] = {v.x, v.y, v.z, v.w};
+  struct alignas(8) Four { __half e[4]; } ah, al, ch, cl;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    split_half(x[j] * GRAM_TO_A, &ah.e[j], &al.e[j]);
+    split_half(fmaf(x[j], GRAM_TO_C, row == col + j ? C_DIAG : 0.0f), &ch.e[j], &cl.e[j]);
+  }
+  *reinterpret_cast<Four*>(a.a_hi + at) = ah;
+  *reinterpret_cast<Four*>(a.a_lo + at) = al;
+  *reinterpret_cast<Four*>(a.c_hi + at) = ch;
+  *reinterpret_cast<Four*>(a.c_lo + at) = cl;
 }
 
 // ---------------------------------------------------------------- host side
@@ -572,18 +764,19 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// FP16 [E][rows][cols] with rows `pitch` elements apart, as boxes of 64
-// columns x box_rows rows.
-bool enc(CUtensorMap* m, const __half* p, int64_t E, int64_t rows, int64_t cols, int64_t pitch, uint32_t box_rows) {
+// FP16 [E][rows][cols] with rows `pitch` elements apart, as boxes of box_cols
+// columns (64: 128-byte swizzle, 32: 64-byte swizzle) x box_rows rows.
+bool enc(CUtensorMap* m, const __half* p, int64_t E, int64_t rows, int64_t cols, int64_t pitch, uint32_t box_rows,
+         uint32_t box_cols = 64) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(E)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch) * 2, static_cast<cuuint64_t>(rows * pitch) * 2};
-  const cuuint32_t box[3] = {64, box_rows, 1};
+  const cuuint32_t box[3] = {box_cols, box_rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(p), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // A pair [E, rows, pitch] of the workspace.
@@ -593,8 +786,10 @@ struct Pair {
   int64_t rows, cols, pitch;
 };
 
+constexpr int64_t MAX_PART_TILES = 128;   // tiles times parts of a split product
+
 struct Layout {
-  size_t partial, x0, x1, a, c, b, total;
+  size_t partial, x0, x1, a, c, b, parts, total;
   int64_t x_pitch, s_pitch;
 };
 Layout layout(int64_t E, int64_t r, int64_t c) {
@@ -610,41 +805,84 @@ Layout layout(int64_t E, int64_t r, int64_t c) {
     at += bytes;
     return p;
   };
-  l.partial = take(align_up(static_cast<size_t>(E * chunk_count(r * c)) * sizeof(double), 256));
+  l.partial = take(align_up(static_cast<size_t>(E * chunk_count(E, r * c)) * sizeof(double), 256));
   l.x0 = take(2 * x);
   l.x1 = take(2 * x);
   l.a = take(2 * g);
   l.c = take(2 * g);
   l.b = take(2 * g);
+  // The parts of a split product: none where its tiles alone fill the machine.
+  const int64_t blocks = (s + TILE - 1) / TILE, tiles = E * blocks * blocks;
+  l.parts = take(tiles <= MAX_PART_TILES / 2 ? align_up(static_cast<size_t>(MAX_PART_TILES / tiles * E * s * l.s_pitch) * 4, 256) : 0);
   l.total = at;
   return l;
 }
 
 template <int MODE, bool P_MN, bool Q_MN>
-cudaError_t launch_product(int64_t E, const Pair& p, const Pair& q, NsArgs args, int num_sms, cudaStream_t s,
-                           const char** why) {
-  CUtensorMap m[4];
+cudaError_t launch_product(int64_t E, const Pair& p, const Pair& q, const Pair* out, const Pair* out2, NsArgs args,
+                           int num_pairs, cudaStream_t s, const char** why, int parts = 1) {
+  CUtensorMap m[8];
   if (!enc(&m[0], p.hi, E, p.rows, p.cols, p.pitch, P_MN ? 64 : BM) ||
       !enc(&m[1], p.lo, E, p.rows, p.cols, p.pitch, P_MN ? 64 : BM) ||
-      !enc(&m[2], q.hi, E, q.rows, q.cols, q.pitch, Q_MN ? 64 : BN) ||
-      !enc(&m[3], q.lo, E, q.rows, q.cols, q.pitch, Q_MN ? 64 : BN)) {
+      !enc(&m[2], q.hi, E, q.rows, q.cols, q.pitch, Q_MN ? 64 : BM) ||
+      !enc(&m[3], q.lo, E, q.rows, q.cols, q.pitch, Q_MN ? 64 : BM)) {
     *why = "cuTensorMapEncodeTiled rejected an operand";
     return cudaErrorInvalidValue;
   }
-  args.m_blocks = (args.m + BM - 1) / BM;
-  args.n_blocks = (args.n + BN - 1) / BN;
-  int64_t per = 0;
-  if (MODE == GRAM || MODE == POLY)
-    for (int mb = 0; mb < args.m_blocks; ++mb) per += args.n_blocks - mb / 2;
-  else
-    per = static_cast<int64_t>(args.m_blocks) * args.n_blocks;
+  for (int i = 0; i < 4; ++i) {
+    const Pair* o = i < 2 ? out : out2;
+    if (o == nullptr) {
+      m[4 + i] = m[0];   // not used
+    } else if (!enc(&m[4 + i], i % 2 == 0 ? o->hi : o->lo, E, o->rows, o->cols, o->pitch, 32, 32)) {
+      *why = "cuTensorMapEncodeTiled rejected a result";
+      return cudaErrorInvalidValue;
+    }
+  }
+  args.m_blocks = (args.m + TILE - 1) / TILE;
+  args.n_blocks = (args.n + TILE - 1) / TILE;
+  const int64_t per = MODE == GRAM || MODE == POLY ? static_cast<int64_t>(args.n_blocks) * (args.n_blocks + 1) / 2
+                                                   : static_cast<int64_t>(args.m_blocks) * args.n_blocks;
   args.tiles_per_matrix = static_cast<uint32_t>(per);
-  args.tiles = static_cast<uint32_t>(E * per);
+  args.tiles = static_cast<uint32_t>(E * per * parts);
   auto kern = ns_kernel<MODE, P_MN, Q_MN>;
   const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (err != cudaSuccess) return err;
-  const int grid = static_cast<int>(std::min<int64_t>(args.tiles, num_sms));
-  return launch_dependent(kern, dim3(grid), dim3(NUM_THREADS), SMEM_BYTES, s, m[0], m[1], m[2], m[3], args);
+  const int64_t pairs = std::min<int64_t>(args.tiles, num_pairs);
+  return launch_dependent(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(NUM_THREADS), SMEM_BYTES, s, m[0], m[1],
+                          m[2], m[3], m[4], m[5], m[6], m[7], args);
+}
+
+// A matrix's X X^T in parts of K, where whole tiles would leave most block
+// pairs idle: the number of parts (1: not split). With few tiles a pair is
+// bound by the 64 KB that each of its k-blocks brings into one SM: one 128 x
+// 2048 matrix took 33 us in one tile.
+int gram_parts(int64_t E, int64_t s, int64_t l, int num_pairs) {
+  const int64_t blocks = (s + TILE - 1) / TILE, tiles = E * blocks * blocks, k_blocks = (l + BK - 1) / BK;
+  const int64_t parts = std::min<int64_t>(std::min<int64_t>(num_pairs, MAX_PART_TILES) / tiles, k_blocks / 2);
+  return parts < 2 ? 1 : static_cast<int>(parts);
+}
+
+// Block pairs that the current device runs at once: SMs left single in a
+// cluster of SMs take none, and a pair too many would run after all the others.
+cudaError_t resident_pairs(int* pairs) {
+  constexpr int MAX_DEVICES = 64;
+  static std::atomic<int> known[MAX_DEVICES];
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < MAX_DEVICES && (*pairs = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  auto kern = ns_kernel<POLY, false, false>;
+  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+  if (err != cudaSuccess) return err;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2);
+  cfg.blockDim = dim3(NUM_THREADS);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  err = cudaOccupancyMaxActiveClusters(pairs, kern, &cfg);
+  if (err != cudaSuccess) return err;
+  if (*pairs < 1) return cudaErrorLaunchOutOfResources;
+  if (dev < MAX_DEVICES) known[dev].store(*pairs, std::memory_order_relaxed);
+  return cudaSuccess;
 }
 
 template <typename T>
@@ -653,7 +891,10 @@ cudaError_t launch_pre(const PreArgs& a, int64_t E, cudaStream_t s) {
                                      s, a);
   if (err != cudaSuccess) return err;
   const int64_t groups = a.pitch / 8 * a.r;
-  const int64_t blocks = std::min<int64_t>((groups + PRE_THREADS - 1) / PRE_THREADS, 2 * MAX_CHUNKS);
+  // Several rounds a block where there is work for all SMs: its start (the norm's sum in FP64) costs as much as one.
+  const int64_t rounds = std::max<int64_t>(1, std::min<int64_t>(4, E * groups / (PRE_BLOCKS * PRE_THREADS * PRE_GROUP)));
+  const int64_t per_block = rounds * PRE_GROUP * PRE_THREADS;
+  const int64_t blocks = (groups + per_block - 1) / per_block;
   return launch_dependent(first_x_kernel<T>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(E)),
                           dim3(PRE_THREADS), 0, s, a);
 }
@@ -667,12 +908,14 @@ int64_t newton_schulz_tiles(int64_t E, int64_t r, int64_t c) {
   return E * ((most + BM - 1) / BM) * ((most + BM - 1) / BM);
 }
 
-cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, int num_sms, cudaStream_t stream,
-                                 const char** why) {
+cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStream_t stream, const char** why) {
   const int64_t E = o.E, r = o.rows, c = o.cols, s = std::min(r, c);
   if (E == 0 || r == 0 || c == 0) return cudaSuccess;
   uint32_t* status = nullptr;
   cudaError_t err = device_status_ptr(&status);
+  if (err != cudaSuccess) return err;
+  int pairs = 0;
+  err = resident_pairs(&pairs);
   if (err != cudaSuccess) return err;
   const Layout l = layout(E, r, c);
   uint8_t* base = static_cast<uint8_t*>(scratch);
@@ -695,11 +938,11 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, int num_s
   pre.hi = x.hi;
   pre.lo = x.lo;
   pre.n = r * c;
-  pre.chunk = chunk_elems(pre.n);
+  pre.chunk = chunk_elems(E, pre.n);
   pre.pitch = l.x_pitch;
   pre.r = static_cast<int>(r);
   pre.c = static_cast<int>(c);
-  pre.chunks = static_cast<int>(chunk_count(pre.n));
+  pre.chunks = static_cast<int>(chunk_count(E, pre.n));
   pre.nesterov = o.nesterov;
   pre.vec = pre.n % 8 == 0 && reinterpret_cast<uintptr_t>(o.grad) % 16 == 0 &&
             reinterpret_cast<uintptr_t>(o.momentum) % 16 == 0;
@@ -711,6 +954,11 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, int num_s
   if (err != cudaSuccess) return err;
 
   const bool tall = r > c;
+  // Every part has k-blocks: the last ones may take fewer.
+  int parts = gram_parts(E, s, std::max(r, c), pairs);
+  const int k_blocks = static_cast<int>((std::max(r, c) + BK - 1) / BK);
+  const int split = (k_blocks + parts - 1) / parts;
+  parts = (k_blocks + split - 1) / split;
   NsArgs sq{};
   sq.status = status;
   sq.m = sq.n = static_cast<int>(s);
@@ -718,40 +966,41 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, int num_s
   for (int step = 0; step < o.steps; ++step) {
     NsArgs g = sq;
     g.k = static_cast<int>(tall ? r : c);
-    g.out_hi = a.hi;
-    g.out_lo = a.lo;
-    g.out2_hi = cc.hi;
-    g.out2_lo = cc.lo;
-    err = tall ? launch_product<GRAM, true, true>(E, x, x, g, num_sms, stream, why)
-               : launch_product<GRAM, false, false>(E, x, x, g, num_sms, stream, why);
+    if (parts == 1) {
+      err = tall ? launch_product<GRAM, true, true>(E, x, x, &a, &cc, g, pairs, stream, why)
+                 : launch_product<GRAM, false, false>(E, x, x, &a, &cc, g, pairs, stream, why);
+    } else {
+      g.parts = reinterpret_cast<float*>(base + l.parts);
+      g.part_elems = E * s * l.s_pitch;
+      g.k_split = split;
+      err = tall ? launch_product<GRAM_PART, true, true>(E, x, x, nullptr, nullptr, g, pairs, stream, why, parts)
+                 : launch_product<GRAM_PART, false, false>(E, x, x, nullptr, nullptr, g, pairs, stream, why, parts);
+      if (err != cudaSuccess) return err;
+      const JoinPartsArgs j{g.parts, g.part_elems, l.s_pitch, parts, static_cast<int>(s), a.hi, a.lo, cc.hi, cc.lo};
+      const int64_t blocks = (g.part_elems / 4 + PRE_THREADS - 1) / PRE_THREADS;
+      err = launch_dependent(join_parts_kernel, dim3(static_cast<unsigned>(blocks)), dim3(PRE_THREADS), 0, stream, j);
+    }
     if (err != cudaSuccess) return err;
     NsArgs p = sq;
     p.k = static_cast<int>(s);
-    p.out_hi = b.hi;
-    p.out_lo = b.lo;
-    err = launch_product<POLY, false, false>(E, a, cc, p, num_sms, stream, why);
+    err = launch_product<POLY, false, false>(E, a, cc, &b, nullptr, p, pairs, stream, why);
     if (err != cudaSuccess) return err;
     NsArgs f{};
     f.status = status;
     f.m = static_cast<int>(r);
     f.n = static_cast<int>(c);
     f.k = static_cast<int>(s);
-    f.pitch = l.x_pitch;
-    f.out_hi = next.hi;
-    f.out_lo = next.lo;
     if (step + 1 < o.steps) {
-      err = tall ? launch_product<APPLY, false, false>(E, x, b, f, num_sms, stream, why)
-                 : launch_product<APPLY, false, true>(E, b, x, f, num_sms, stream, why);
+      err = tall ? launch_product<APPLY, false, false>(E, x, b, &next, nullptr, f, pairs, stream, why)
+                 : launch_product<APPLY, false, true>(E, b, x, &next, nullptr, f, pairs, stream, why);
     } else {
       f.result = o.result;
       f.result_dtype = o.result_dtype;
-      f.result_vec = (c * static_cast<int64_t>(dtype_size(o.result_dtype))) % 16 == 0 &&
-                     reinterpret_cast<uintptr_t>(o.result) % 16 == 0;
       f.update = o.update;
       f.keep = o.keep;
       f.rate = o.rate;
-      err = tall ? launch_product<FINAL, false, false>(E, x, b, f, num_sms, stream, why)
-                 : launch_product<FINAL, false, true>(E, b, x, f, num_sms, stream, why);
+      err = tall ? launch_product<FINAL, false, false>(E, x, b, nullptr, nullptr, f, pairs, stream, why)
+                 : launch_product<FINAL, false, true>(E, b, x, nullptr, nullptr, f, pairs, stream, why);
     }
     if (err != cudaSuccess) return err;
     std::swap(x, next);
