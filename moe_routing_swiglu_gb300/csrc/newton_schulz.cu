@@ -3,12 +3,13 @@
 // For each matrix G [r, c] of a batch (s = min(r, c), the short side):
 //   X = G / (|G|_F + eps), then per step, with A = X X^T (X^T X where r > c)
 //   and a, b, c = 3.4445, -4.7750, 2.0315:
-//   X <- B X (X B),  B = a I + b A + c A A = a I + A (b I + c A)
+//   X <- B X (X B),  B = a I + b A + c A A
 // which moves every singular value of X from (0, 1] towards the interval
 // [0.7, 1.21] and keeps its singular vectors. Three grouped products a step:
-//   GRAM   A and C = b I + c A   (symmetric: the tiles on and above the
-//          diagonal are computed, each also stored mirrored)
-//   POLY   B = A C + a I         (symmetric too)
+//   GRAM   A           (symmetric: the tiles on and above the diagonal are
+//          computed, each also stored mirrored)
+//   POLY   B = a I + b A + c A A, the first two terms in the epilogue
+//          (symmetric too)
 //   APPLY  X' = B X, or X B; in the last step its epilogue writes the result
 //          (16-bit, or the weights' update) instead of X'
 //
@@ -19,8 +20,8 @@
 // v - hi, and a product is hi hi + hi lo + lo hi: 22 bits, for three MMAs.
 // FP16 rather than BF16 pairs (16 bits) because every value here is bounded:
 // |X| <= 1.21 (its largest singular value: the quintic maps [0, 1.21] into
-// itself), |A| <= 1.47, |C| <= 4.78, |B| <= 3.45. Stored times 2^14 (X, A) or
-// 2^13 (C, B) they stay under FP16's 65504, and lo of an entry as small as
+// itself), |A| <= 1.47, |B| <= 3.45. Stored times 2^14 (X, A) or 2^13 (B) they
+// stay under FP16's 65504, and lo of an entry as small as
 // 2^-14 is still a normal FP16.
 //
 // Structure: a persistent pair of CTAs on two SMs (cta_group::2) per tile of
@@ -48,12 +49,11 @@ namespace {
 
 constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
 constexpr float pow2(int e) { return e == 0 ? 1.0f : e > 0 ? 2.0f * pow2(e - 1) : 0.5f * pow2(e + 1); }
-constexpr int X_EXP = 14, A_EXP = 14, C_EXP = 13, B_EXP = 13;   // stored = value * 2^EXP
-// Accumulators to stored values, and what is added on the diagonal.
-constexpr float GRAM_TO_A = pow2(A_EXP - 2 * X_EXP), GRAM_TO_C = NS_C * pow2(C_EXP - 2 * X_EXP);
-constexpr float C_DIAG = NS_B * pow2(C_EXP), B_DIAG = NS_A * pow2(B_EXP);
-constexpr float POLY_TO_B = pow2(B_EXP - A_EXP - C_EXP), APPLY_TO_X = pow2(-B_EXP);
-constexpr float APPLY_TO_RESULT = pow2(-B_EXP - X_EXP);
+constexpr int X_EXP = 14, A_EXP = 14, B_EXP = 13;   // stored = value * 2^EXP
+// Accumulators (and POLY's A) to stored values, and what is added on the diagonal.
+constexpr float GRAM_TO_A = pow2(A_EXP - 2 * X_EXP);
+constexpr float POLY_TO_B = NS_C * pow2(B_EXP - 2 * A_EXP), A_TO_B = NS_B * pow2(B_EXP - A_EXP), B_DIAG = NS_A * pow2(B_EXP);
+constexpr float APPLY_TO_X = pow2(-B_EXP), APPLY_TO_RESULT = pow2(-B_EXP - X_EXP);
 
 // ---------------------------------------------------------------- norm, momentum, first X
 
@@ -75,18 +75,16 @@ struct alignas(16) Eight {
   T e[8];
 };
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, bool vec, float (&v)[8]) {
-  if (vec) {
-    Eight<T> x;
-    const uint4* s = reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void load8(const T* p, Eight<T>& x) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(x) / 16); ++i) reinterpret_cast<uint4*>(&x)[i] = s[i];
+  for (int i = 0; i < static_cast<int>(sizeof(x) / 16); ++i)
+    reinterpret_cast<uint4*>(&x)[i] = reinterpret_cast<const uint4*>(p)[i];
+}
+// The first n of 8 elements one by one, zeros for the others.
+template <typename T>
+__device__ __forceinline__ void load_some(const T* p, int n, Eight<T>& x) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f32(x.e[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
-  }
+  for (int i = 0; i < 8; ++i) x.e[i] = i < n ? p[i] : from_f32<T>(0.0f);
 }
 
 // Sums of squares that FP32 cannot hold: values above 2^40 and below 2^-40 are
@@ -108,17 +106,6 @@ struct Squares {
   __device__ double total() const { return mid + big * 0x1p180 + small * 0x1p-180; }
 };
 
-__device__ __forceinline__ double block_sum(double v, double* sm) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(FULL_MASK, v, off);
-  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = (threadIdx.x & 31) < PRE_THREADS / 32 ? sm[threadIdx.x & 31] : 0.0;
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(FULL_MASK, v, off);
-  return v;
-}
-
 struct PreArgs {
   const void* g;       // [E, r, c]
   float* m;            // momentum [E, r, c] or NULL
@@ -128,8 +115,7 @@ struct PreArgs {
   int64_t n, chunk;    // elements of a matrix, of a chunk
   int64_t pitch;
   int r, c, chunks, nesterov, vec;
-  float mu;
-  double eps;
+  float mu, eps;
 };
 
 // u of the momentum step: what is orthogonalised.
@@ -137,121 +123,191 @@ __device__ __forceinline__ float update_of(const PreArgs& a, float g, float m) {
   return a.nesterov ? fmaf(a.mu, m, g) : m;
 }
 
+template <typename V>
+__device__ __forceinline__ V warp_sum(V v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(FULL_MASK, v, off);
+  return v;
+}
+
 // partial[e][chunk]: the sum of squares of the chunk's u; updates the momentum.
-template <typename T>
+// A thread's squares are added in FP32 (a norm is off by fewer than 2^-19 of it
+// for any number of them that a chunk has): rounds whose sum FP32 does not hold
+// are added in FP64, of which the SMs have little.
+template <typename T, bool MOMENTUM>
 __global__ void __launch_bounds__(PRE_THREADS) squares_kernel(const PreArgs a) {
   __shared__ double sm[PRE_THREADS / 32];
   grid_dependency_wait();
   launch_dependents();
-  const int64_t base = blockIdx.y * a.n;
+  const T* gp = static_cast<const T*>(a.g) + blockIdx.y * a.n;
+  float* mp = MOMENTUM ? a.m + blockIdx.y * a.n : nullptr;
   const int64_t lo = blockIdx.x * a.chunk, hi = min(lo + a.chunk, a.n);
-  double total = 0.0;
-  // A round's 32 squares in FP32, the rounds in FP64.
-  for (int64_t i0 = lo; i0 < hi; i0 += PRE_THREADS * 8 * PRE_GROUP) {
-    float g[PRE_GROUP][8], m[PRE_GROUP][8];
-    auto at = [&](int k) { return i0 + (k * PRE_THREADS + static_cast<int64_t>(threadIdx.x)) * 8; };
-    auto left = [&](int k) { return static_cast<int>(max(min(hi - at(k), int64_t{8}), int64_t{0})); };
-#pragma unroll
-    for (int k = 0; k < PRE_GROUP; ++k) {
-      load8<T>(static_cast<const T*>(a.g) + base + at(k), left(k), a.vec && left(k) == 8, g[k]);
-      if (a.m != nullptr) load8<float>(a.m + base + at(k), left(k), a.vec && left(k) == 8, m[k]);
-    }
-    if (a.m != nullptr) {
+  constexpr int ROUND = PRE_THREADS * 8 * PRE_GROUP;
+  float near = 0.0f;
+  double far = 0.0;
+  for (int64_t i0 = lo; i0 < hi; i0 += ROUND) {
+    const int64_t at = i0 + static_cast<int64_t>(threadIdx.x) * 8;
+    const bool whole = a.vec && i0 + ROUND <= hi;
+    Eight<T> g[PRE_GROUP];
+    Eight<float> m[PRE_GROUP];
+    int n[PRE_GROUP];
+    if (whole) {
 #pragma unroll
       for (int k = 0; k < PRE_GROUP; ++k) {
-        float* p = a.m + base + at(k);
+        load8<T>(gp + at + k * PRE_THREADS * 8, g[k]);
+        if (MOMENTUM) load8<float>(mp + at + k * PRE_THREADS * 8, m[k]);
+      }
+    } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) m[k][j] = fmaf(a.mu, m[k][j], g[k][j]);
-        if (a.vec && left(k) == 8) {
-          reinterpret_cast<float4*>(p)[0] = make_float4(m[k][0], m[k][1], m[k][2], m[k][3]);
-          reinterpret_cast<float4*>(p)[1] = make_float4(m[k][4], m[k][5], m[k][6], m[k][7]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < left(k)) p[j] = m[k][j];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[k][j] = j < left(k) ? update_of(a, g[k][j], m[k][j]) : 0.0f;
+      for (int k = 0; k < PRE_GROUP; ++k) {
+        const int64_t i = at + k * PRE_THREADS * 8;
+        n[k] = static_cast<int>(max(min(hi - i, int64_t{8}), int64_t{0}));
+        load_some<T>(gp + i, n[k], g[k]);
+        if (MOMENTUM) load_some<float>(mp + i, n[k], m[k]);
       }
     }
-    float fast = 0.0f;
+    float sum = 0.0f;
+    Eight<float> u[PRE_GROUP];
 #pragma unroll
     for (int k = 0; k < PRE_GROUP; ++k)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) fast = fmaf(g[k][j], g[k][j], fast);
-    // 32 squares that each lose at most 2^-150 do not show in a sum of 2^-60.
-    if (fast >= 0x1p-60f && fast <= 0x1p100f) {
-      total += fast;
+      for (int j = 0; j < 8; ++j) {
+        u[k].e[j] = to_f32(g[k].e[j]);
+        if (MOMENTUM) {
+          m[k].e[j] = fmaf(a.mu, m[k].e[j], u[k].e[j]);
+          u[k].e[j] = update_of(a, u[k].e[j], m[k].e[j]);
+        }
+        sum = fmaf(u[k].e[j], u[k].e[j], sum);
+      }
+    if (MOMENTUM) {
+#pragma unroll
+      for (int k = 0; k < PRE_GROUP; ++k) {
+        float* p = mp + at + k * PRE_THREADS * 8;
+        if (whole) {
+          reinterpret_cast<uint4*>(p)[0] = reinterpret_cast<const uint4*>(&m[k])[0];
+          reinterpret_cast<uint4*>(p)[1] = reinterpret_cast<const uint4*>(&m[k])[1];
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < n[k]) p[j] = m[k].e[j];
+        }
+      }
+    }
+    // 32 squares that each lose at most 2^-150 do not show in a sum of 2^-60; 2^80 leaves room for the other rounds.
+    if (sum >= 0x1p-60f && sum <= 0x1p80f) {
+      near += sum;
     } else {
       Squares s{0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < PRE_GROUP; ++k)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s.add(g[k][j]);
-      total += s.total();
+        for (int j = 0; j < 8; ++j) s.add(u[k].e[j]);
+      far += s.total();
     }
   }
-  total = block_sum(total, sm);
-  if (threadIdx.x == 0) a.partial[static_cast<int64_t>(blockIdx.y) * a.chunks + blockIdx.x] = total;
+  near = warp_sum(near);
+  if (__any_sync(FULL_MASK, far != 0.0)) far = warp_sum(far);   // NaN != 0 too
+  if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = near + far;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double total = 0.0;
+    for (int w = 0; w < PRE_THREADS / 32; ++w) total += sm[w];
+    a.partial[static_cast<int64_t>(blockIdx.y) * a.chunks + blockIdx.x] = total;
+  }
 }
 
 __device__ __forceinline__ void split_half(float v, __half* hi, __half* lo) {
   *hi = __float2half_rn(v);
   *lo = __float2half_rn(v - __half2float(*hi));
 }
+__device__ __forceinline__ void split_half2(float x, float y, uint32_t* hi, uint32_t* lo) {
+  const __half2 p = __floats2half2_rn(x, y);
+  const float2 f = __half22float2(p);
+  *hi = *reinterpret_cast<const uint32_t*>(&p);
+  *lo = pack2<__half>(x - f.x, y - f.y);
+}
+
+__device__ __forceinline__ float power2(int e) { return __int_as_float((e + 127) << 23); }   // -126 .. 127
+
+// 2^14 / (sqrt(sum) + eps) as two FP32 factors, both far from FP32's ends: with
+// sum = m 4^k and eps = f 2^j over the larger power p of k and j, 2^(14 - p) /
+// (sqrt(m) 2^(k - p) + f 2^(j - p)). NaN where the sum is not finite: a matrix
+// with a NaN or an infinity becomes NaN as a whole.
+__device__ __forceinline__ float2 scale_of(double sum, float eps) {
+  if (!(sum <= 0x1p1000)) return make_float2(__int_as_float(0x7FC00000), 1.0f);
+  int j, k = -600;
+  const float f = frexpf(eps, &j);
+  float root = 0.0f;
+  if (sum > 0x1p-1000) {
+    const int ex = ((__double2hiint(sum) >> 20) & 0x7FF) - 1022;   // sum = m 2^ex, m in [1/2, 1)
+    k = (ex + (ex & 1)) / 2;
+    root = sqrtf(static_cast<float>(sum * __hiloint2double((1023 - 2 * k) << 20, 0)));
+  }
+  const int p = max(j, k);
+  const float t = (k - p > -100 ? root * power2(k - p) : 0.0f) + (j - p > -100 ? f * power2(j - p) : 0.0f);
+  const int e = 14 - p, h = e / 2;
+  return make_float2(power2(e - h) / t, power2(h));
+}
 
 // X = u / (norm + eps), as FP16 pairs.
-template <typename T>
+template <typename T, bool MOMENTUM>
 __global__ void __launch_bounds__(PRE_THREADS) first_x_kernel(const PreArgs a) {
-  __shared__ double sm[PRE_THREADS / 32];
+  __shared__ float2 factors;
   grid_dependency_wait();
   launch_dependents();
   const int64_t e = blockIdx.y;
-  double sum = static_cast<int>(threadIdx.x) < a.chunks ? a.partial[e * a.chunks + threadIdx.x] : 0.0;
-  static_assert(MAX_CHUNKS <= PRE_THREADS, "one partial sum a thread");
-  sum = block_sum(sum, sm);
-  // 2^14 / (norm + eps) as two FP32 factors, both far from FP32's ends. A
-  // matrix with a NaN or an infinity becomes NaN as a whole. By one thread:
-  // FP64 is slow here.
-  __shared__ float factors[2];
-  if (threadIdx.x == 0) {
-    const double scale = isfinite(sum) ? 0x1p14 / (sqrt(sum) + a.eps) : nan("");
-    int ex = 0;
-    const double frac = frexp(scale, &ex);
-    factors[0] = static_cast<float>(ldexp(frac, ex - ex / 2));
-    factors[1] = static_cast<float>(ldexp(1.0, ex / 2));
+  if (threadIdx.x < 32) {
+    double sum = 0.0;
+    for (int i = threadIdx.x; i < a.chunks; i += 32) sum += a.partial[e * a.chunks + i];
+    sum = warp_sum(sum);
+    if (threadIdx.x == 0) factors = scale_of(sum, a.eps);
   }
   __syncthreads();
-  const float s1 = factors[0], s2 = factors[1];
+  const float s1 = factors.x, s2 = factors.y;
+  const T* gp = static_cast<const T*>(a.g) + e * a.n;
+  const float* mp = MOMENTUM ? a.m + e * a.n : nullptr;
+  __half* hi = a.hi + e * a.r * a.pitch;
+  __half* lo = a.lo + e * a.r * a.pitch;
   const uint32_t per_row = static_cast<uint32_t>(a.pitch / 8), groups = per_row * a.r;
-  const bool vec = a.vec && a.c % 8 == 0;
+  const bool flat = a.vec && a.c % 8 == 0;   // rows without padding: group i is elements 8 i ..
   const uint32_t step = gridDim.x * PRE_THREADS;
   for (uint32_t i0 = blockIdx.x * PRE_THREADS + threadIdx.x; i0 < groups; i0 += PRE_GROUP * step) {
-    float g[PRE_GROUP][8], m[PRE_GROUP][8];
-    int64_t to[PRE_GROUP];
+    Eight<T> g[PRE_GROUP];
+    Eight<float> m[PRE_GROUP];
+    if (flat && i0 + (PRE_GROUP - 1) * step < groups) {
 #pragma unroll
-    for (int k = 0; k < PRE_GROUP; ++k) {
-      const uint32_t i = i0 + k * step;
-      to[k] = -1;
-      if (i >= groups) continue;
-      const uint32_t row = i / per_row, col = (i - row * per_row) * 8;
-      to[k] = (e * a.r + row) * a.pitch + col;
-      const int64_t at = e * a.n + static_cast<int64_t>(row) * a.c + col;
-      const int n = min(a.c - static_cast<int>(col), 8);
-      load8<T>(static_cast<const T*>(a.g) + at, n, vec, g[k]);
-      if (a.m != nullptr) load8<float>(a.m + at, n, vec, m[k]);
+      for (int k = 0; k < PRE_GROUP; ++k) {
+        const int64_t at = static_cast<int64_t>(i0 + k * step) * 8;
+        load8<T>(gp + at, g[k]);
+        if (MOMENTUM) load8<float>(mp + at, m[k]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < PRE_GROUP; ++k) {
+        const uint32_t i = i0 + k * step;
+        if (i >= groups) continue;
+        const uint32_t row = i / per_row, col = (i - row * per_row) * 8;
+        const int64_t at = static_cast<int64_t>(row) * a.c + col;
+        load_some<T>(gp + at, min(a.c - static_cast<int>(col), 8), g[k]);
+        if (MOMENTUM) load_some<float>(mp + at, min(a.c - static_cast<int>(col), 8), m[k]);
+      }
     }
 #pragma unroll
     for (int k = 0; k < PRE_GROUP; ++k) {
-      if (to[k] < 0) continue;
-      Eight<__half> h, l;
+      const uint32_t i = i0 + k * step;
+      if (i >= groups) continue;
+      float u[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float u = a.m != nullptr ? update_of(a, g[k][j], m[k][j]) : g[k][j];
-        split_half(u * s1 * s2, &h.e[j], &l.e[j]);
+        u[j] = to_f32(g[k].e[j]);
+        if (MOMENTUM) u[j] = update_of(a, u[j], m[k].e[j]);
+        u[j] = u[j] * s1 * s2;
       }
-      *reinterpret_cast<uint4*>(a.hi + to[k]) = *reinterpret_cast<const uint4*>(&h);
-      *reinterpret_cast<uint4*>(a.lo + to[k]) = *reinterpret_cast<const uint4*>(&l);
+      uint32_t h[4], l[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) split_half2(u[2 * j], u[2 * j + 1], &h[j], &l[j]);
+      reinterpret_cast<uint4*>(hi)[i] = make_uint4(h[0], h[1], h[2], h[3]);
+      reinterpret_cast<uint4*>(lo)[i] = make_uint4(l[0], l[1], l[2], l[3]);
     }
   }
 }
@@ -347,12 +403,28 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
       : "memory");
 }
 
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+// FP16 pairs [E, rows, pitch] of the workspace; what lies between cols and the
+// pitch (fewer than 8) is written, and never read.
+struct Pair {
+  __half* hi;
+  __half* lo;
+  int64_t rows, cols, pitch;
+};
+
 // D [E, m, n] = P [E, m, k] Q [E, k, n], both FP16 pairs.
 struct NsArgs {
   int m, n, k;
   int m_blocks, n_blocks;
   int k_split;          // k-blocks of a part (GRAM_PART), else all
   uint32_t tiles, tiles_per_matrix;
+  Pair out;             // GRAM A, POLY B, APPLY X'
+  Pair a;               // POLY: A
   int64_t pitch;        // GRAM_PART
   float* parts;         // [parts, E, m, pitch]
   int64_t part_elems;   // E * m * pitch
@@ -365,7 +437,11 @@ struct NsArgs {
 
 // Tile -> (matrix, row block, column block, first k-block and their number).
 // Symmetric products have the tiles on and above the diagonal; a product in
-// parts has all tiles of one part before the next part's.
+// parts has all tiles of one part before the next part's. Row blocks go in
+// bands of BAND, in a band column by column, so that the tiles that run at once
+// share both operands in L2 (2 x 14336 x 4096 with X's 56 row blocks in one
+// column after the other read X from HBM 12 times a product).
+constexpr int BAND = 8;
 struct NsTile {
   int e, mb, nb, kb0, kbs, part;
 };
@@ -378,16 +454,32 @@ __device__ __forceinline__ NsTile ns_tile(uint32_t tile, const NsArgs& a) {
   t.part = 0;
   uint32_t matrix = tile / a.tiles_per_matrix;
   int i = static_cast<int>(tile - matrix * a.tiles_per_matrix);
+  int mb0 = 0;   // the band's first row block
   if (MODE == GRAM || MODE == POLY) {
-    t.mb = 0;
-    while (i >= a.n_blocks - t.mb) {
-      i -= a.n_blocks - t.mb;
-      ++t.mb;
+    int rows = min(BAND, a.m_blocks);
+    for (;;) {
+      const int in_band = rows * (rows + 1) / 2 + rows * (a.n_blocks - mb0 - rows);
+      if (i < in_band) break;
+      i -= in_band;
+      mb0 += rows;
+      rows = min(BAND, a.m_blocks - mb0);
     }
-    t.nb = t.mb + i;
+    const int corner = rows * (rows + 1) / 2;   // the band's triangle at the diagonal, column by column
+    if (i < corner) {
+      int col = 0;
+      while (i > col) i -= ++col;
+      t.mb = mb0 + i;
+      t.nb = mb0 + col;
+    } else {
+      t.mb = mb0 + (i - corner) % rows;
+      t.nb = mb0 + rows + (i - corner) / rows;
+    }
   } else {
-    t.mb = i % a.m_blocks;
-    t.nb = i / a.m_blocks;
+    mb0 = i / (BAND * a.n_blocks) * BAND;
+    i -= mb0 * a.n_blocks;
+    const int rows = min(BAND, a.m_blocks - mb0);
+    t.mb = mb0 + i % rows;
+    t.nb = i / rows;
   }
   if (MODE == GRAM_PART) {
     const uint32_t matrices = static_cast<uint32_t>(a.part_elems / (a.m * a.pitch));
@@ -401,17 +493,13 @@ __device__ __forceinline__ NsTile ns_tile(uint32_t tile, const NsArgs& a) {
 }
 
 // A warp's 32 x 32 block (lane: row, v: its columns) as FP16 pairs into its
-// staging tiles, 32 rows of 64 bytes each with the 64-byte swizzle (16-byte
-// chunk q of row r at chunk q ^ (r / 2 % 4)), and from there to (row, col) of
-// both planes by tensor stores, which clip what is past the matrix. MIRROR: the
-// transposed block, at (col, row). Both ways of writing the tiles are free of
-// bank conflicts.
+// staging tiles, 32 rows of 64 bytes each (16-byte chunk q of row r at chunk
+// q ^ (r / 2 % 4): no bank conflicts either way), and from there to (row, col)
+// of both planes, four lanes a row. MIRROR: the transposed block, at (col, row).
 template <bool MIRROR>
-__device__ __forceinline__ void store_pairs(uint32_t tile, const CUtensorMap* hi, const CUtensorMap* lo, int row, int col,
-                                            int e, const float (&v)[32]) {
+__device__ __forceinline__ void store_pairs(uint32_t tile, const Pair& out, int e, int row, int col, const float (&v)[32]) {
   const int lane = threadIdx.x & 31;
-  if (lane == 0) bulk_wait_read_all();   // the last stores have read the tiles
-  __syncwarp();
+  __syncwarp();   // the last block has left the tiles
   if (MIRROR) {
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
@@ -426,24 +514,67 @@ __device__ __forceinline__ void store_pairs(uint32_t tile, const CUtensorMap* hi
     for (int q = 0; q < 4; ++q) {
       uint32_t h[4], l[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float x = v[q * 8 + 2 * j], y = v[q * 8 + 2 * j + 1];
-        const __half2 p = __floats2half2_rn(x, y);
-        const float2 f = __half22float2(p);
-        h[j] = *reinterpret_cast<const uint32_t*>(&p);
-        l[j] = pack2<__half>(x - f.x, y - f.y);
-      }
+      for (int j = 0; j < 4; ++j) split_half2(v[q * 8 + 2 * j], v[q * 8 + 2 * j + 1], &h[j], &l[j]);
       const uint32_t at = tile + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
       st_shared_v4(at, h[0], h[1], h[2], h[3]);
       st_shared_v4(at + 2048, l[0], l[1], l[2], l[3]);
     }
   }
-  fence_proxy_async_smem();
   __syncwarp();
-  if (lane == 0) {
-    tma_store_3d(hi, tile, MIRROR ? row : col, MIRROR ? col : row, e);
-    tma_store_3d(lo, tile + 2048, MIRROR ? row : col, MIRROR ? col : row, e);
-    bulk_commit_group();
+  const int r0 = MIRROR ? col : row, c0 = (MIRROR ? row : col) + (lane & 3) * 8;
+  if (c0 >= out.pitch) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    const uint32_t at = tile + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4);
+    if (r0 + r < out.rows) {
+      const int64_t to = (static_cast<int64_t>(e) * out.rows + r0 + r) * out.pitch + c0;
+      *reinterpret_cast<uint4*>(out.hi + to) = ld_shared_v4(at);
+      *reinterpret_cast<uint4*>(out.lo + to) = ld_shared_v4(at + 2048);
+    }
+  }
+}
+
+// The 32 x 32 block of `in` at (row, col): in two parts, so that the loads run
+// while the accumulator is read. Past the matrix: anything.
+__device__ __forceinline__ void load_pairs(const Pair& in, int e, int row, int col, uint4 (&hi)[4], uint4 (&lo)[4]) {
+  const int lane = threadIdx.x & 31, c = col + (lane & 3) * 8;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = row + i * 8 + (lane >> 2);
+    hi[i] = lo[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < in.rows && c < in.pitch) {
+      const int64_t at = (static_cast<int64_t>(e) * in.rows + r) * in.pitch + c;
+      hi[i] = *reinterpret_cast<const uint4*>(in.hi + at);
+      lo[i] = *reinterpret_cast<const uint4*>(in.lo + at);
+    }
+  }
+}
+// v = raw * scale + (this lane's row of the loaded block) * block_scale
+__device__ __forceinline__ void add_pairs(uint32_t tile, const uint4 (&hi)[4], const uint4 (&lo)[4], float block_scale,
+                                          const uint32_t (&raw)[32], float scale, float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + (lane >> 2);
+    const uint32_t at = tile + r * 64 + (((lane & 3) ^ ((r >> 1) & 3)) << 4);
+    st_shared_v4(at, hi[i].x, hi[i].y, hi[i].z, hi[i].w);
+    st_shared_v4(at + 2048, lo[i].x, lo[i].y, lo[i].z, lo[i].w);
+  }
+  __syncwarp();
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t at = tile + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4);
+    const uint4 h = ld_shared_v4(at), l = ld_shared_v4(at + 2048);
+    const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&hw[j]));
+      const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&lw[j]));
+      v[q * 8 + 2 * j] = fmaf(__uint_as_float(raw[q * 8 + 2 * j]), scale, (x.x + y.x) * block_scale);
+      v[q * 8 + 2 * j + 1] = fmaf(__uint_as_float(raw[q * 8 + 2 * j + 1]), scale, (x.y + y.y) * block_scale);
+    }
   }
 }
 
@@ -482,8 +613,7 @@ template <int MODE, bool P_MN, bool Q_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     ns_kernel(const __grid_constant__ CUtensorMap p_hi, const __grid_constant__ CUtensorMap p_lo,
               const __grid_constant__ CUtensorMap q_hi, const __grid_constant__ CUtensorMap q_lo,
-              const __grid_constant__ CUtensorMap o_hi, const __grid_constant__ CUtensorMap o_lo,
-              const __grid_constant__ CUtensorMap o2_hi, const __grid_constant__ CUtensorMap o2_lo, const NsArgs args) {
+              const __grid_constant__ NsArgs args) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   uint64_t* full = reinterpret_cast<uint64_t*>(smem + SMEM_BAR);   // block 0's are used
@@ -530,6 +660,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 
   // Columns of a tile, of which each block brings half.
   auto n_of = [&](const NsTile& t) { return min(TILE, (args.n - t.nb * TILE + 31) & ~31); };
+  // A whole tile on the diagonal of M M^T: both operands are the same rows.
+  auto same_operand = [&](const NsTile& t) {
+    return (MODE == GRAM || MODE == POLY || MODE == GRAM_PART) && t.mb == t.nb && n_of(t) == TILE;
+  };
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -541,12 +675,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         const NsTile t = ns_tile<MODE>(tile, args);
         const int m0 = t.mb * TILE + static_cast<int>(rank) * BM;
         const int n0 = t.nb * TILE + static_cast<int>(rank) * (n_of(t) / 2);
+        const bool same = same_operand(t);
         for (int kb = t.kb0; kb < t.kb0 + t.kbs; ++kb) {
           ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, args.status, ST_PRODUCER_EMPTY, WAIT_LIMIT_NS);
           if (!ok) break;
           uint8_t* st = smem + stage * STAGE_BYTES;
           const uint32_t bar = peer_u32(&full[stage], 0);
-          peer_arrive_expect_tx(bar, STAGE_BYTES);
+          peer_arrive_expect_tx(bar, same ? STAGE_BYTES / 2 : STAGE_BYTES);
           const int k0 = kb * BK;
           auto load = [&](uint8_t* dst, const CUtensorMap* map, bool mn_major, int at) {
             if (!mn_major) {
@@ -556,9 +691,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             }
           };
           load(st, &p_hi, P_MN, m0);
-          load(st + 2 * OP_BYTES, &q_hi, Q_MN, n0);
+          if (!same) load(st + 2 * OP_BYTES, &q_hi, Q_MN, n0);
           load(st + OP_BYTES, &p_lo, P_MN, m0);
-          load(st + 3 * OP_BYTES, &q_lo, Q_MN, n0);
+          if (!same) load(st + 3 * OP_BYTES, &q_lo, Q_MN, n0);
           ++issued;
           if (++stage == STAGES) {
             stage = 0;
@@ -591,7 +726,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
             if (!ok) break;
             tc_fence_after();
             const uint32_t ph = smem_u32(smem + stage * STAGE_BYTES), pl = ph + OP_BYTES;
-            const uint32_t qh = ph + 2 * OP_BYTES, ql = qh + OP_BYTES;
+            const uint32_t qh = same_operand(t) ? ph : ph + 2 * OP_BYTES, ql = qh + OP_BYTES;
             const int n_sub = min(BK / UMMA_K, (args.k - kb * BK + UMMA_K - 1) / UMMA_K);
             for (int k = 0; k < n_sub; ++k) {
               auto pd = [&](uint32_t at) {
@@ -636,28 +771,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       for (int c0 = 32 * half; c0 < TILE; c0 += 64) {
         const int col = t.nb * TILE + c0;
         if (col >= args.n || row >= args.m) break;
+        uint4 a_hi[4], a_lo[4];
+        if (MODE == POLY) load_pairs(args.a, t.e, row, col, a_hi, a_lo);
         uint32_t raw[32];
         tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(c0), raw);
         tmem_ld_wait();
         float v[32];
         if (MODE == GRAM || MODE == POLY) {
-          const bool mirror = t.nb != t.mb;
-          const int diag = row + lane - col;
           if (MODE == GRAM) {
 #pragma unroll
             for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) * GRAM_TO_A;
-            store_pairs<false>(tile_at, &o_hi, &o_lo, row, col, t.e, v);
-            if (mirror) store_pairs<true>(tile_at, &o_hi, &o_lo, row, col, t.e, v);
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = fmaf(__uint_as_float(raw[j]), GRAM_TO_C, diag == j ? C_DIAG : 0.0f);
-            store_pairs<false>(tile_at, &o2_hi, &o2_lo, row, col, t.e, v);
-            if (mirror) store_pairs<true>(tile_at, &o2_hi, &o2_lo, row, col, t.e, v);
           } else {
+            add_pairs(tile_at, a_hi, a_lo, A_TO_B, raw, POLY_TO_B, v);
+            const int diag = row + lane - col;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = fmaf(__uint_as_float(raw[j]), POLY_TO_B, diag == j ? B_DIAG : 0.0f);
-            store_pairs<false>(tile_at, &o_hi, &o_lo, row, col, t.e, v);
-            if (mirror) store_pairs<true>(tile_at, &o_hi, &o_lo, row, col, t.e, v);
+            for (int j = 0; j < 32; ++j) v[j] += diag == j ? B_DIAG : 0.0f;
           }
+          store_pairs<false>(tile_at, args.out, t.e, row, col, v);
+          if (t.nb != t.mb) store_pairs<true>(tile_at, args.out, t.e, row, col, v);
         } else if (MODE == GRAM_PART) {
           if (row + lane < args.m) {
             float* p = args.parts + t.part * args.part_elems + (static_cast<int64_t>(t.e) * args.m + row + lane) * args.pitch +
@@ -670,7 +801,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         } else if (MODE == APPLY) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) * APPLY_TO_X;
-          store_pairs<false>(tile_at, &o_hi, &o_lo, row, col, t.e, v);
+          store_pairs<false>(tile_at, args.out, t.e, row, col, v);
         } else {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) * APPLY_TO_RESULT;
@@ -684,9 +815,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
       __syncwarp();
       if (lane == 0) peer_arrive(peer_u32(&tempty[acc], 0));
     }
-    // The tensor stores read shared memory and write the matrices: both end before the block does.
-    if (lane == 0) bulk_wait_all();
-    __syncwarp();
   }
 
   tc_fence_before();
@@ -714,39 +842,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   }
 }
 
-// A and C from the parts of GRAM_PART, added in order.
-struct JoinPartsArgs {
-  const float* parts;
-  int64_t part_elems, pitch;
-  int count, s;
-  __half *a_hi, *a_lo, *c_hi, *c_lo;
-};
-__global__ void __launch_bounds__(PRE_THREADS) join_parts_kernel(const JoinPartsArgs a) {
+// A from the parts of GRAM_PART, added in order.
+__global__ void __launch_bounds__(PRE_THREADS) join_parts_kernel(const float* parts, int64_t part_elems, int count,
+                                                                 __half* hi, __half* lo) {
   grid_dependency_wait();
   launch_dependents();
   const int64_t at = (static_cast<int64_t>(blockIdx.x) * PRE_THREADS + threadIdx.x) * 4;
-  if (at >= a.part_elems) return;
-  float4 v = *reinterpret_cast<const float4*>(a.parts + at);
-  for (int p = 1; p < a.count; ++p) {
-    const float4 w = *reinterpret_cast<const float4*>(a.parts + p * a.part_elems + at);
+  if (at >= part_elems) return;
+  float4 v = *reinterpret_cast<const float4*>(parts + at);
+#pragma unroll 4
+  for (int p = 1; p < count; ++p) {
+    const float4 w = *reinterpret_cast<const float4*>(parts + p * part_elems + at);
     v.x += w.x;
     v.y += w.y;
     v.z += w.z;
     v.w += w.w;
   }
-  const int64_t row_at = at / a.pitch;
-  const int row = static_cast<int>(row_at % a.s), col = static_cast<int>(at - row_at * a.pitch);
-  const float x[4] = {v.x, v.y, v.z, v.w};
-  struct alignas(8) Four { __half e[4]; } ah, al, ch, cl;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    split_half(x[j] * GRAM_TO_A, &ah.e[j], &al.e[j]);
-    split_half(fmaf(x[j], GRAM_TO_C, row == col + j ? C_DIAG : 0.0f), &ch.e[j], &cl.e[j]);
-  }
-  *reinterpret_cast<Four*>(a.a_hi + at) = ah;
-  *reinterpret_cast<Four*>(a.a_lo + at) = al;
-  *reinterpret_cast<Four*>(a.c_hi + at) = ch;
-  *reinterpret_cast<Four*>(a.c_lo + at) = cl;
+  uint2 h, l;
+  split_half2(v.x * GRAM_TO_A, v.y * GRAM_TO_A, &h.x, &l.x);
+  split_half2(v.z * GRAM_TO_A, v.w * GRAM_TO_A, &h.y, &l.y);
+  *reinterpret_cast<uint2*>(hi + at) = h;
+  *reinterpret_cast<uint2*>(lo + at) = l;
 }
 
 // ---------------------------------------------------------------- host side
@@ -764,32 +880,24 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// FP16 [E][rows][cols] with rows `pitch` elements apart, as boxes of box_cols
-// columns (64: 128-byte swizzle, 32: 64-byte swizzle) x box_rows rows.
-bool enc(CUtensorMap* m, const __half* p, int64_t E, int64_t rows, int64_t cols, int64_t pitch, uint32_t box_rows,
-         uint32_t box_cols = 64) {
+// FP16 [E][rows][cols] with rows `pitch` elements apart, as boxes of 64
+// columns x box_rows rows.
+bool enc(CUtensorMap* m, const __half* p, int64_t E, int64_t rows, int64_t cols, int64_t pitch, uint32_t box_rows) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(E)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(pitch) * 2, static_cast<cuuint64_t>(rows * pitch) * 2};
-  const cuuint32_t box[3] = {box_cols, box_rows, 1};
+  const cuuint32_t box[3] = {64, box_rows, 1};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(p), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-// A pair [E, rows, pitch] of the workspace.
-struct Pair {
-  __half* hi;
-  __half* lo;
-  int64_t rows, cols, pitch;
-};
 
 constexpr int64_t MAX_PART_TILES = 128;   // tiles times parts of a split product
 
 struct Layout {
-  size_t partial, x0, x1, a, c, b, parts, total;
+  size_t partial, x0, x1, a, b, parts, total;
   int64_t x_pitch, s_pitch;
 };
 Layout layout(int64_t E, int64_t r, int64_t c) {
@@ -809,7 +917,6 @@ Layout layout(int64_t E, int64_t r, int64_t c) {
   l.x0 = take(2 * x);
   l.x1 = take(2 * x);
   l.a = take(2 * g);
-  l.c = take(2 * g);
   l.b = take(2 * g);
   // The parts of a split product: none where its tiles alone fill the machine.
   const int64_t blocks = (s + TILE - 1) / TILE, tiles = E * blocks * blocks;
@@ -819,24 +926,15 @@ Layout layout(int64_t E, int64_t r, int64_t c) {
 }
 
 template <int MODE, bool P_MN, bool Q_MN>
-cudaError_t launch_product(int64_t E, const Pair& p, const Pair& q, const Pair* out, const Pair* out2, NsArgs args,
-                           int num_pairs, cudaStream_t s, const char** why, int parts = 1) {
-  CUtensorMap m[8];
+cudaError_t launch_product(int64_t E, const Pair& p, const Pair& q, NsArgs args, int num_pairs, cudaStream_t s,
+                           const char** why, int parts = 1) {
+  CUtensorMap m[4];
   if (!enc(&m[0], p.hi, E, p.rows, p.cols, p.pitch, P_MN ? 64 : BM) ||
       !enc(&m[1], p.lo, E, p.rows, p.cols, p.pitch, P_MN ? 64 : BM) ||
       !enc(&m[2], q.hi, E, q.rows, q.cols, q.pitch, Q_MN ? 64 : BM) ||
       !enc(&m[3], q.lo, E, q.rows, q.cols, q.pitch, Q_MN ? 64 : BM)) {
     *why = "cuTensorMapEncodeTiled rejected an operand";
     return cudaErrorInvalidValue;
-  }
-  for (int i = 0; i < 4; ++i) {
-    const Pair* o = i < 2 ? out : out2;
-    if (o == nullptr) {
-      m[4 + i] = m[0];   // not used
-    } else if (!enc(&m[4 + i], i % 2 == 0 ? o->hi : o->lo, E, o->rows, o->cols, o->pitch, 32, 32)) {
-      *why = "cuTensorMapEncodeTiled rejected a result";
-      return cudaErrorInvalidValue;
-    }
   }
   args.m_blocks = (args.m + TILE - 1) / TILE;
   args.n_blocks = (args.n + TILE - 1) / TILE;
@@ -849,7 +947,7 @@ cudaError_t launch_product(int64_t E, const Pair& p, const Pair& q, const Pair* 
   if (err != cudaSuccess) return err;
   const int64_t pairs = std::min<int64_t>(args.tiles, num_pairs);
   return launch_dependent(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(NUM_THREADS), SMEM_BYTES, s, m[0], m[1],
-                          m[2], m[3], m[4], m[5], m[6], m[7], args);
+                          m[2], m[3], args);
 }
 
 // A matrix's X X^T in parts of K, where whole tiles would leave most block
@@ -885,18 +983,22 @@ cudaError_t resident_pairs(int* pairs) {
   return cudaSuccess;
 }
 
+template <typename T, bool MOMENTUM>
+cudaError_t launch_pre(const PreArgs& a, int64_t E, cudaStream_t s) {
+  cudaError_t err = launch_dependent(squares_kernel<T, MOMENTUM>, dim3(a.chunks, static_cast<unsigned>(E)),
+                                     dim3(PRE_THREADS), 0, s, a);
+  if (err != cudaSuccess) return err;
+  // Several rounds a block where there is work for all SMs: its start costs as much as one.
+  const int64_t groups = a.pitch / 8 * a.r;
+  const int64_t rounds = std::max<int64_t>(1, std::min<int64_t>(8, E * groups / (PRE_BLOCKS * PRE_THREADS * PRE_GROUP)));
+  const int64_t per_block = rounds * PRE_GROUP * PRE_THREADS;
+  return launch_dependent(first_x_kernel<T, MOMENTUM>,
+                          dim3(static_cast<unsigned>((groups + per_block - 1) / per_block), static_cast<unsigned>(E)),
+                          dim3(PRE_THREADS), 0, s, a);
+}
 template <typename T>
 cudaError_t launch_pre(const PreArgs& a, int64_t E, cudaStream_t s) {
-  cudaError_t err = launch_dependent(squares_kernel<T>, dim3(a.chunks, static_cast<unsigned>(E)), dim3(PRE_THREADS), 0,
-                                     s, a);
-  if (err != cudaSuccess) return err;
-  const int64_t groups = a.pitch / 8 * a.r;
-  // Several rounds a block where there is work for all SMs: its start (the norm's sum in FP64) costs as much as one.
-  const int64_t rounds = std::max<int64_t>(1, std::min<int64_t>(4, E * groups / (PRE_BLOCKS * PRE_THREADS * PRE_GROUP)));
-  const int64_t per_block = rounds * PRE_GROUP * PRE_THREADS;
-  const int64_t blocks = (groups + per_block - 1) / per_block;
-  return launch_dependent(first_x_kernel<T>, dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(E)),
-                          dim3(PRE_THREADS), 0, s, a);
+  return a.m != nullptr ? launch_pre<T, true>(a, E, s) : launch_pre<T, false>(a, E, s);
 }
 
 }  // namespace
@@ -929,7 +1031,7 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
     return p;
   };
   Pair x = pair(l.x0, r, c, l.x_pitch), next = pair(l.x1, r, c, l.x_pitch);
-  const Pair a = pair(l.a, s, s, l.s_pitch), cc = pair(l.c, s, s, l.s_pitch), b = pair(l.b, s, s, l.s_pitch);
+  const Pair a = pair(l.a, s, s, l.s_pitch), b = pair(l.b, s, s, l.s_pitch);
 
   PreArgs pre{};
   pre.g = o.grad;
@@ -966,41 +1068,45 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
   for (int step = 0; step < o.steps; ++step) {
     NsArgs g = sq;
     g.k = static_cast<int>(tall ? r : c);
+    g.out = a;
     if (parts == 1) {
-      err = tall ? launch_product<GRAM, true, true>(E, x, x, &a, &cc, g, pairs, stream, why)
-                 : launch_product<GRAM, false, false>(E, x, x, &a, &cc, g, pairs, stream, why);
+      err = tall ? launch_product<GRAM, true, true>(E, x, x, g, pairs, stream, why)
+                 : launch_product<GRAM, false, false>(E, x, x, g, pairs, stream, why);
     } else {
       g.parts = reinterpret_cast<float*>(base + l.parts);
       g.part_elems = E * s * l.s_pitch;
       g.k_split = split;
-      err = tall ? launch_product<GRAM_PART, true, true>(E, x, x, nullptr, nullptr, g, pairs, stream, why, parts)
-                 : launch_product<GRAM_PART, false, false>(E, x, x, nullptr, nullptr, g, pairs, stream, why, parts);
+      err = tall ? launch_product<GRAM_PART, true, true>(E, x, x, g, pairs, stream, why, parts)
+                 : launch_product<GRAM_PART, false, false>(E, x, x, g, pairs, stream, why, parts);
       if (err != cudaSuccess) return err;
-      const JoinPartsArgs j{g.parts, g.part_elems, l.s_pitch, parts, static_cast<int>(s), a.hi, a.lo, cc.hi, cc.lo};
       const int64_t blocks = (g.part_elems / 4 + PRE_THREADS - 1) / PRE_THREADS;
-      err = launch_dependent(join_parts_kernel, dim3(static_cast<unsigned>(blocks)), dim3(PRE_THREADS), 0, stream, j);
+      err = launch_dependent(join_parts_kernel, dim3(static_cast<unsigned>(blocks)), dim3(PRE_THREADS), 0, stream,
+                             static_cast<const float*>(g.parts), g.part_elems, parts, a.hi, a.lo);
     }
     if (err != cudaSuccess) return err;
     NsArgs p = sq;
     p.k = static_cast<int>(s);
-    err = launch_product<POLY, false, false>(E, a, cc, &b, nullptr, p, pairs, stream, why);
+    p.out = b;
+    p.a = a;
+    err = launch_product<POLY, false, false>(E, a, a, p, pairs, stream, why);
     if (err != cudaSuccess) return err;
     NsArgs f{};
     f.status = status;
     f.m = static_cast<int>(r);
     f.n = static_cast<int>(c);
     f.k = static_cast<int>(s);
+    f.out = next;
     if (step + 1 < o.steps) {
-      err = tall ? launch_product<APPLY, false, false>(E, x, b, &next, nullptr, f, pairs, stream, why)
-                 : launch_product<APPLY, false, true>(E, b, x, &next, nullptr, f, pairs, stream, why);
+      err = tall ? launch_product<APPLY, false, false>(E, x, b, f, pairs, stream, why)
+                 : launch_product<APPLY, false, true>(E, b, x, f, pairs, stream, why);
     } else {
       f.result = o.result;
       f.result_dtype = o.result_dtype;
       f.update = o.update;
       f.keep = o.keep;
       f.rate = o.rate;
-      err = tall ? launch_product<FINAL, false, false>(E, x, b, nullptr, nullptr, f, pairs, stream, why)
-                 : launch_product<FINAL, false, true>(E, b, x, nullptr, nullptr, f, pairs, stream, why);
+      err = tall ? launch_product<FINAL, false, false>(E, x, b, f, pairs, stream, why)
+                 : launch_product<FINAL, false, true>(E, b, x, f, pairs, stream, why);
     }
     if (err != cudaSuccess) return err;
     std::swap(x, next);
