@@ -49,12 +49,7 @@ namespace {
 
 constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
 constexpr float pow2(int e) { return e == 0 ? 1.0f : e > 0 ? 2.0f * pow2(e - 1) : 0.5f * pow2(e + 1); }
-constexpr int X_EXP = 14, A_EXP = 14, B_EXP = 13;   // stored = value * 2^EXP
-// Accumulators (and POLY's A) to stored values, and what is added on the diagonal.
-constexpr float GRAM_TO_A = pow2(A_EXP - 2 * X_EXP);
-constexpr float POLY_TO_B = NS_C * pow2(B_EXP - 2 * A_EXP), A_TO_B = NS_B * pow2(B_EXP - A_EXP), B_DIAG = NS_A * pow2(B_EXP);
-constexpr float APPLY_TO_X = pow2(-B_EXP), APPLY_TO_RESULT = pow2(-B_EXP - X_EXP);
-
+constexpr int X_EXP = 14, A_EXP = 14, B_EXP = 13, BB_EXP = 12;   // stored = value * 2^EXP
 // ---------------------------------------------------------------- norm, momentum, first X
 
 constexpr int PRE_THREADS = 256;
@@ -357,11 +352,14 @@ __device__ __forceinline__ uint32_t peer_u32(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
   return a;
 }
+// Relaxed: what these two signal is in tensor memory or arrives by TMA, and a
+// release waits for the SM's stores in flight (2 x 14336 x 4096: 14.9 ms with
+// it, 14.1 without).
 __device__ __forceinline__ void peer_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void peer_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
+  asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ uint32_t peer_load(uint32_t addr) {
@@ -423,8 +421,11 @@ struct NsArgs {
   int m_blocks, n_blocks;
   int k_split;          // k-blocks of a part (GRAM_PART), else all
   uint32_t tiles, tiles_per_matrix;
-  Pair out;             // GRAM A, POLY B, APPLY X'
+  int square;           // GRAM: P and Q are the same matrix
+  Pair out;             // GRAM, POLY, APPLY
   Pair a;               // POLY: A
+  float scale;          // of the accumulator: stored result = acc * scale (POLY: + A * a_scale + diag I)
+  float a_scale, diag;
   int64_t pitch;        // GRAM_PART
   float* parts;         // [parts, E, m, pitch]
   int64_t part_elems;   // E * m * pitch
@@ -662,7 +663,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
   auto n_of = [&](const NsTile& t) { return min(TILE, (args.n - t.nb * TILE + 31) & ~31); };
   // A whole tile on the diagonal of M M^T: both operands are the same rows.
   auto same_operand = [&](const NsTile& t) {
-    return (MODE == GRAM || MODE == POLY || MODE == GRAM_PART) && t.mb == t.nb && n_of(t) == TILE;
+    return (MODE == GRAM || MODE == POLY || MODE == GRAM_PART) && args.square && t.mb == t.nb && n_of(t) == TILE;
   };
 
   if (warp == 0) {
@@ -780,12 +781,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
         if (MODE == GRAM || MODE == POLY) {
           if (MODE == GRAM) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) * GRAM_TO_A;
+            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) * args.scale;
           } else {
-            add_pairs(tile_at, a_hi, a_lo, A_TO_B, raw, POLY_TO_B, v);
+            add_pairs(tile_at, a_hi, a_lo, args.a_scale, raw, args.scale, v);
             const int diag = row + lane - col;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] += diag == j ? B_DIAG : 0.0f;
+            for (int j = 0; j < 32; ++j) v[j] += diag == j ? args.diag : 0.0f;
           }
           store_pairs<false>(tile_at, args.out, t.e, row, col, v);
           if (t.nb != t.mb) store_pairs<true>(tile_at, args.out, t.e, row, col, v);
@@ -800,11 +801,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           }
         } else if (MODE == APPLY) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) * APPLY_TO_X;
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) * args.scale;
           store_pairs<false>(tile_at, args.out, t.e, row, col, v);
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) * APPLY_TO_RESULT;
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) * args.scale;
           float* stage = reinterpret_cast<float*>(staging);
           if (args.result_dtype == MOE_F32) store_result<float>(args, stage, row, col, t.e, v);
           else if (args.result_dtype == MOE_F16) store_result<__half>(args, stage, row, col, t.e, v);
@@ -844,7 +845,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
 
 // A from the parts of GRAM_PART, added in order.
 __global__ void __launch_bounds__(PRE_THREADS) join_parts_kernel(const float* parts, int64_t part_elems, int count,
-                                                                 __half* hi, __half* lo) {
+                                                                 float scale, __half* hi, __half* lo) {
   grid_dependency_wait();
   launch_dependents();
   const int64_t at = (static_cast<int64_t>(blockIdx.x) * PRE_THREADS + threadIdx.x) * 4;
@@ -859,8 +860,8 @@ __global__ void __launch_bounds__(PRE_THREADS) join_parts_kernel(const float* pa
     v.w += w.w;
   }
   uint2 h, l;
-  split_half2(v.x * GRAM_TO_A, v.y * GRAM_TO_A, &h.x, &l.x);
-  split_half2(v.z * GRAM_TO_A, v.w * GRAM_TO_A, &h.y, &l.y);
+  split_half2(v.x * scale, v.y * scale, &h.x, &l.x);
+  split_half2(v.z * scale, v.w * scale, &h.y, &l.y);
   *reinterpret_cast<uint2*>(hi + at) = h;
   *reinterpret_cast<uint2*>(lo + at) = l;
 }
@@ -897,7 +898,7 @@ bool enc(CUtensorMap* m, const __half* p, int64_t E, int64_t rows, int64_t cols,
 constexpr int64_t MAX_PART_TILES = 128;   // tiles times parts of a split product
 
 struct Layout {
-  size_t partial, x0, x1, a, b, parts, total;
+  size_t partial, x0, x1, a, b, t, b1, parts, total;
   int64_t x_pitch, s_pitch;
 };
 Layout layout(int64_t E, int64_t r, int64_t c) {
@@ -918,6 +919,8 @@ Layout layout(int64_t E, int64_t r, int64_t c) {
   l.x1 = take(2 * x);
   l.a = take(2 * g);
   l.b = take(2 * g);
+  l.t = take(2 * g);
+  l.b1 = take(2 * g);
   // The parts of a split product: none where its tiles alone fill the machine.
   const int64_t blocks = (s + TILE - 1) / TILE, tiles = E * blocks * blocks;
   l.parts = take(tiles <= MAX_PART_TILES / 2 ? align_up(static_cast<size_t>(MAX_PART_TILES / tiles * E * s * l.s_pitch) * 4, 256) : 0);
@@ -958,6 +961,14 @@ int gram_parts(int64_t E, int64_t s, int64_t l, int num_pairs) {
   const int64_t blocks = (s + TILE - 1) / TILE, tiles = E * blocks * blocks, k_blocks = (l + BK - 1) / BK;
   const int64_t parts = std::min<int64_t>(std::min<int64_t>(num_pairs, MAX_PART_TILES) / tiles, k_blocks / 2);
   return parts < 2 ? 1 : static_cast<int>(parts);
+}
+
+// Two steps at once, X'' = B1 (B X) = (B1 B) X with B1 from X' X'^T = B A B,
+// take three more s x s products instead of a second X X^T and B X: 3 s^2 (l - s)
+// multiplications less a matrix (symmetric products count half), and two
+// launches more, about 10 us or 2e9 of them.
+bool two_steps_pay(int64_t E, int64_t s, int64_t l) {
+  return static_cast<double>(E) * s * s * (l - s) > 2e9;
 }
 
 // Block pairs that the current device runs at once: SMs left single in a
@@ -1032,6 +1043,7 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
   };
   Pair x = pair(l.x0, r, c, l.x_pitch), next = pair(l.x1, r, c, l.x_pitch);
   const Pair a = pair(l.a, s, s, l.s_pitch), b = pair(l.b, s, s, l.s_pitch);
+  const Pair t = pair(l.t, s, s, l.s_pitch), b1 = pair(l.b1, s, s, l.s_pitch);
 
   PreArgs pre{};
   pre.g = o.grad;
@@ -1065,48 +1077,82 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
   sq.status = status;
   sq.m = sq.n = static_cast<int>(s);
   sq.pitch = l.s_pitch;
-  for (int step = 0; step < o.steps; ++step) {
+  // out = X X^T (X^T X)
+  auto gram = [&](const Pair& out) {
     NsArgs g = sq;
     g.k = static_cast<int>(tall ? r : c);
-    g.out = a;
-    if (parts == 1) {
-      err = tall ? launch_product<GRAM, true, true>(E, x, x, g, pairs, stream, why)
-                 : launch_product<GRAM, false, false>(E, x, x, g, pairs, stream, why);
-    } else {
-      g.parts = reinterpret_cast<float*>(base + l.parts);
-      g.part_elems = E * s * l.s_pitch;
-      g.k_split = split;
-      err = tall ? launch_product<GRAM_PART, true, true>(E, x, x, g, pairs, stream, why, parts)
-                 : launch_product<GRAM_PART, false, false>(E, x, x, g, pairs, stream, why, parts);
-      if (err != cudaSuccess) return err;
-      const int64_t blocks = (g.part_elems / 4 + PRE_THREADS - 1) / PRE_THREADS;
-      err = launch_dependent(join_parts_kernel, dim3(static_cast<unsigned>(blocks)), dim3(PRE_THREADS), 0, stream,
-                             static_cast<const float*>(g.parts), g.part_elems, parts, a.hi, a.lo);
-    }
-    if (err != cudaSuccess) return err;
+    g.square = 1;
+    g.out = out;
+    g.scale = pow2(A_EXP - 2 * X_EXP);
+    if (parts == 1)
+      return tall ? launch_product<GRAM, true, true>(E, x, x, g, pairs, stream, why)
+                  : launch_product<GRAM, false, false>(E, x, x, g, pairs, stream, why);
+    g.parts = reinterpret_cast<float*>(base + l.parts);
+    g.part_elems = E * s * l.s_pitch;
+    g.k_split = split;
+    const cudaError_t e = tall ? launch_product<GRAM_PART, true, true>(E, x, x, g, pairs, stream, why, parts)
+                               : launch_product<GRAM_PART, false, false>(E, x, x, g, pairs, stream, why, parts);
+    if (e != cudaSuccess) return e;
+    const int64_t blocks = (g.part_elems / 4 + PRE_THREADS - 1) / PRE_THREADS;
+    return launch_dependent(join_parts_kernel, dim3(static_cast<unsigned>(blocks)), dim3(PRE_THREADS), 0, stream,
+                            static_cast<const float*>(g.parts), g.part_elems, parts, g.scale, out.hi, out.lo);
+  };
+  // out = a I + b A + c A A
+  auto poly = [&](const Pair& in, const Pair& out) {
     NsArgs p = sq;
     p.k = static_cast<int>(s);
-    p.out = b;
-    p.a = a;
-    err = launch_product<POLY, false, false>(E, a, a, p, pairs, stream, why);
-    if (err != cudaSuccess) return err;
+    p.square = 1;
+    p.out = out;
+    p.a = in;
+    p.scale = NS_C * pow2(B_EXP - 2 * A_EXP);
+    p.a_scale = NS_B * pow2(B_EXP - A_EXP);
+    p.diag = NS_A * pow2(B_EXP);
+    return launch_product<POLY, false, false>(E, in, in, p, pairs, stream, why);
+  };
+  // out = P Q of polynomials in the same A: symmetric
+  auto product = [&](const Pair& p, const Pair& q, const Pair& out, int exp) {
+    NsArgs g = sq;
+    g.k = static_cast<int>(s);
+    g.out = out;
+    g.scale = pow2(exp);
+    return launch_product<GRAM, false, false>(E, p, q, g, pairs, stream, why);
+  };
+  const bool by_two = two_steps_pay(E, s, std::max(r, c));
+  for (int left = o.steps; left > 0;) {
+    // An odd step first: the later steps magnify rounding less.
+    const int now = by_two && left % 2 == 0 ? 2 : 1;
+    left -= now;
+    if ((err = gram(a)) != cudaSuccess || (err = poly(a, b)) != cudaSuccess) return err;
+    Pair q = b;
+    int q_exp = B_EXP;
+    if (now == 2) {
+      // X'' = B1 B X with B1 from A1 = X' X'^T = B A B
+      if ((err = product(b, a, t, A_EXP - A_EXP - B_EXP)) != cudaSuccess ||
+          (err = product(t, b, a, A_EXP - A_EXP - B_EXP)) != cudaSuccess || (err = poly(a, b1)) != cudaSuccess ||
+          (err = product(b1, b, t, BB_EXP - 2 * B_EXP)) != cudaSuccess)
+        return err;
+      q = t;
+      q_exp = BB_EXP;
+    }
     NsArgs f{};
     f.status = status;
     f.m = static_cast<int>(r);
     f.n = static_cast<int>(c);
     f.k = static_cast<int>(s);
-    f.out = next;
-    if (step + 1 < o.steps) {
-      err = tall ? launch_product<APPLY, false, false>(E, x, b, f, pairs, stream, why)
-                 : launch_product<APPLY, false, true>(E, b, x, f, pairs, stream, why);
+    if (left > 0) {
+      f.out = next;
+      f.scale = pow2(-q_exp);
+      err = tall ? launch_product<APPLY, false, false>(E, x, q, f, pairs, stream, why)
+                 : launch_product<APPLY, false, true>(E, q, x, f, pairs, stream, why);
     } else {
+      f.scale = pow2(-q_exp - X_EXP);
       f.result = o.result;
       f.result_dtype = o.result_dtype;
       f.update = o.update;
       f.keep = o.keep;
       f.rate = o.rate;
-      err = tall ? launch_product<FINAL, false, false>(E, x, b, f, pairs, stream, why)
-                 : launch_product<FINAL, false, true>(E, b, x, f, pairs, stream, why);
+      err = tall ? launch_product<FINAL, false, false>(E, x, q, f, pairs, stream, why)
+                 : launch_product<FINAL, false, true>(E, q, x, f, pairs, stream, why);
     }
     if (err != cudaSuccess) return err;
     std::swap(x, next);
