@@ -610,7 +610,8 @@ __device__ __forceinline__ void store_result(const NsArgs& a, float* tile, int r
   }
 }
 
-template <int MODE, bool P_MN, bool Q_MN>
+// SINGLE: the product of the hi parts alone.
+template <int MODE, bool P_MN, bool Q_MN, bool SINGLE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     ns_kernel(const __grid_constant__ CUtensorMap p_hi, const __grid_constant__ CUtensorMap p_lo,
               const __grid_constant__ CUtensorMap q_hi, const __grid_constant__ CUtensorMap q_lo,
@@ -682,7 +683,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           if (!ok) break;
           uint8_t* st = smem + stage * STAGE_BYTES;
           const uint32_t bar = peer_u32(&full[stage], 0);
-          peer_arrive_expect_tx(bar, same ? STAGE_BYTES / 2 : STAGE_BYTES);
+          peer_arrive_expect_tx(bar, same || SINGLE ? STAGE_BYTES / 2 : STAGE_BYTES);
           const int k0 = kb * BK;
           auto load = [&](uint8_t* dst, const CUtensorMap* map, bool mn_major, int at) {
             if (!mn_major) {
@@ -693,8 +694,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           };
           load(st, &p_hi, P_MN, m0);
           if (!same) load(st + 2 * OP_BYTES, &q_hi, Q_MN, n0);
-          load(st + OP_BYTES, &p_lo, P_MN, m0);
-          if (!same) load(st + 3 * OP_BYTES, &q_lo, Q_MN, n0);
+          if (!SINGLE) load(st + OP_BYTES, &p_lo, P_MN, m0);
+          if (!same && !SINGLE) load(st + 3 * OP_BYTES, &q_lo, Q_MN, n0);
           ++issued;
           if (++stage == STAGES) {
             stage = 0;
@@ -736,9 +737,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
               auto qd = [&](uint32_t at) {
                 return Q_MN ? sdesc_mnmajor_sw128(at + k * 2048, BOX, 1024) : sdesc_kmajor_sw128(at + k * UMMA_K * 2);
               };
-              pair_umma_f16(d, pd(pl), qd(qh), idesc, (kb > t.kb0 || k > 0) ? 1u : 0u);
-              pair_umma_f16(d, pd(ph), qd(ql), idesc, 1u);
-              pair_umma_f16(d, pd(ph), qd(qh), idesc, 1u);
+              pair_umma_f16(d, pd(ph), qd(qh), idesc, (kb > t.kb0 || k > 0) ? 1u : 0u);
+              if (!SINGLE) {
+                pair_umma_f16(d, pd(pl), qd(qh), idesc, 1u);
+                pair_umma_f16(d, pd(ph), qd(ql), idesc, 1u);
+              }
             }
             pair_commit(&empty[stage]);
             if (++stage == STAGES) {
@@ -928,7 +931,7 @@ Layout layout(int64_t E, int64_t r, int64_t c) {
   return l;
 }
 
-template <int MODE, bool P_MN, bool Q_MN>
+template <int MODE, bool P_MN, bool Q_MN, bool SINGLE = false>
 cudaError_t launch_product(int64_t E, const Pair& p, const Pair& q, NsArgs args, int num_pairs, cudaStream_t s,
                            const char** why, int parts = 1) {
   CUtensorMap m[4];
@@ -945,7 +948,7 @@ cudaError_t launch_product(int64_t E, const Pair& p, const Pair& q, NsArgs args,
                                                    : static_cast<int64_t>(args.m_blocks) * args.n_blocks;
   args.tiles_per_matrix = static_cast<uint32_t>(per);
   args.tiles = static_cast<uint32_t>(E * per * parts);
-  auto kern = ns_kernel<MODE, P_MN, Q_MN>;
+  auto kern = ns_kernel<MODE, P_MN, Q_MN, SINGLE>;
   const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (err != cudaSuccess) return err;
   const int64_t pairs = std::min<int64_t>(args.tiles, num_pairs);
@@ -980,7 +983,7 @@ cudaError_t resident_pairs(int* pairs) {
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
   if (dev < MAX_DEVICES && (*pairs = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
-  auto kern = ns_kernel<POLY, false, false>;
+  auto kern = ns_kernel<POLY, false, false, false>;
   err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
@@ -1119,8 +1122,7 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
   };
   const bool by_two = two_steps_pay(E, s, std::max(r, c));
   for (int left = o.steps; left > 0;) {
-    // An odd step first: the later steps magnify rounding less.
-    const int now = by_two && left % 2 == 0 ? 2 : 1;
+    const int now = by_two && left >= 2 ? 2 : 1;
     left -= now;
     if ((err = gram(a)) != cudaSuccess || (err = poly(a, b)) != cudaSuccess) return err;
     Pair q = b;
@@ -1151,8 +1153,14 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
       f.update = o.update;
       f.keep = o.keep;
       f.rate = o.rate;
-      err = tall ? launch_product<FINAL, false, false>(E, x, q, f, pairs, stream, why)
-                 : launch_product<FINAL, false, true>(E, q, x, f, pairs, stream, why);
+      // A BF16 result of one step (B, at most 3.45): the hi parts' 11 bits leave it off by some 2^-12, an eighth of its
+      // own rounding; a third of the product's time.
+      if (now == 1 && o.result_dtype == MOE_BF16)
+        err = tall ? launch_product<FINAL, false, false, true>(E, x, q, f, pairs, stream, why)
+                   : launch_product<FINAL, false, true, true>(E, q, x, f, pairs, stream, why);
+      else
+        err = tall ? launch_product<FINAL, false, false>(E, x, q, f, pairs, stream, why)
+                   : launch_product<FINAL, false, true>(E, q, x, f, pairs, stream, why);
     }
     if (err != cudaSuccess) return err;
     std::swap(x, next);

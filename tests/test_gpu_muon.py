@@ -2,7 +2,8 @@
 
 Tolerance: how far the FP64 result moves when every product of it is off by the full size of what its operands' 22 bits
 and a truncating FP32 accumulator may lose, with drawn signs (oracle.block.newton_schulz_moved), as a 2-norm over the
-matrix, times 2 for another draw of the signs. A result in 16 bits adds half a step of its type for each entry. FP32
+matrix, times 2 for another draw of the signs. A BF16 result's last product has operands of 11 bits, each off by at
+most half a step of FP16, 2^-11. A result in 16 bits adds half a step of its type for each entry. FP32
 weights add 3 roundings of 2^-24 (keep, rate, the sum)."""
 import numpy as np
 import pytest
@@ -32,7 +33,8 @@ def check_matrices(got, inputs, rng, u=None, steps=5, eps=1e-7):
     g = f64(got)
     for e, m in enumerate(inputs):
         ref = block.newton_schulz(m, steps, eps)
-        move = np.linalg.norm(block.newton_schulz_moved(m, rng, steps, eps) - ref)
+        last = 2.0 ** -11 if got.dtype == torch.bfloat16 else 2.0 ** -22
+        move = np.linalg.norm(block.newton_schulz_moved(m, rng, steps, eps, last) - ref)
         off = np.linalg.norm(g[e] - ref)
         tol = 2 * move + u * np.linalg.norm(ref)
         assert off <= tol, (e, off, tol)
@@ -144,7 +146,8 @@ def test_muon_step(cuda_lib, E, r, c, wdtype, gdtype, nesterov):
                                                      float(np.float32(lr)) * float(np.float32(scale))))
         for e in range(E):
             o = block.newton_schulz(u[e])
-            move = 2 * np.linalg.norm(block.newton_schulz_moved(u[e], rng) - o)
+            last = 2.0 ** -11 if wdtype == "bf16" else 2.0 ** -22
+            move = 2 * np.linalg.norm(block.newton_schulz_moved(u[e], rng, last=last) - o)
             # u itself is rounded once, 2^-24 of it: less than the operands' 2^-22 that `move` has
             ref = keep * w0[e] - rate * o
             eps = torch.finfo(w.dtype).eps / 2 + 3 * 2.0 ** -24
