@@ -936,7 +936,7 @@ moe_status moe_block_join_backward(const void* dout, const void* dnormed, const 
  *   eps         finite, > 0.
  *   workspace   device, moe_orthogonalize_workspace_size(E, rows, cols) bytes,
  *               256-byte aligned, of both calls below: about 8 bytes per
- *               element, 8 min(rows, cols)^2 per matrix, and up to 34 MB for
+ *               element, 16 min(rows, cols)^2 per matrix, and up to 34 MB for
  *               batches of few matrices. Contents need not be initialised. Calls that may overlap need separate ones.
  * Tensors are aligned to their element size. The same bits on every run.
  * ---------------------------------------------------------------------- */

@@ -86,24 +86,33 @@ def newton_schulz(g, steps=5, eps=1e-7):
     return x
 
 
-def newton_schulz_moved(g, rng, steps=5, eps=1e-7, last=2.0 ** -22):
+def newton_schulz_moved(g, rng, steps=5, eps=1e-7):
     """newton_schulz with every product off by what FP16 pairs and a truncating FP32 accumulator may lose, at its full
     size and with signs drawn: an operand by 2^-22 of each entry; an entry of a product over K by 2^-23 of the sum of
     its terms' sizes for each of the 3 K / 16 additions. How far the result moves by it is what rounding may cost."""
     a, b, c = NS
     sign = lambda v: rng.choice((-1.0, 1.0), size=v.shape)
 
-    def product(p, q, off=2.0 ** -22):
-        p, q = (v * (1 + off * sign(v)) for v in (p, q))
+    def product(p, q):
+        p, q = (v * (1 + 2.0 ** -22 * sign(v)) for v in (p, q))
         adds = -(-p.shape[1] // 16) * 3
         v = p @ q
         return v + adds * 2.0 ** -23 * (np.abs(p) @ np.abs(q)) * sign(v)
 
     x = g / (np.sqrt((g * g).sum()) + eps)
     tall = x.shape[0] > x.shape[1]
-    for step in range(steps):
+    for _ in range(steps):
         m = product(x.T, x) if tall else product(x, x.T)
         poly = a * np.eye(len(m)) + product(m, b * np.eye(len(m)) + c * m)
-        off = last if step + 1 == steps else 2.0 ** -22
-        x = product(x, poly, off) if tall else product(poly, x, off)
+        x = product(x, poly) if tall else product(poly, x)
     return x
+
+
+def newton_schulz_last_size(g, steps=5, eps=1e-7):
+    """|B| |X| of the last product B X (X B): its terms' sizes added up."""
+    a, b, c = NS
+    x = newton_schulz(g, steps - 1, eps)
+    tall = x.shape[0] > x.shape[1]
+    m = x.T @ x if tall else x @ x.T
+    poly = np.abs(a * np.eye(len(m)) + b * m + c * (m @ m))
+    return np.abs(x) @ poly if tall else poly @ np.abs(x)

@@ -3,7 +3,8 @@
 Tolerance: how far the FP64 result moves when every product of it is off by the full size of what its operands' 22 bits
 and a truncating FP32 accumulator may lose, with drawn signs (oracle.block.newton_schulz_moved), as a 2-norm over the
 matrix, times 2 for another draw of the signs. A BF16 result's last product has operands of 11 bits, each off by at
-most half a step of FP16, 2^-11. A result in 16 bits adds half a step of its type for each entry. FP32
+most half a step of FP16, 2^-11: each term by (1 + 2^-11)^2 - 1 < 2^-10 (1 + 2^-11), the product by that of the sum of
+its terms' sizes. A result in 16 bits adds half a step of its type for each entry. FP32
 weights add 3 roundings of 2^-24 (keep, rate, the sum)."""
 import numpy as np
 import pytest
@@ -27,18 +28,24 @@ def gradients(rng, E, r, c, dtype, scale=1e-3):
     return torch.tensor(g * scale, dtype=DTYPES[dtype], device=DEV)
 
 
+def last_product(m, dtype, steps=5, eps=1e-7):
+    """What a BF16 result's last product may be off by."""
+    if dtype != torch.bfloat16:
+        return 0.0
+    return 2.0 ** -10 * (1 + 2.0 ** -11) * block.newton_schulz_last_size(m, steps, eps)
+
+
 def check_matrices(got, inputs, rng, u=None, steps=5, eps=1e-7):
     """got [E, r, c] against the FP64 steps on inputs (numpy [E, r, c])."""
     u = torch.finfo(got.dtype).eps / 2 if u is None else u
     g = f64(got)
     for e, m in enumerate(inputs):
         ref = block.newton_schulz(m, steps, eps)
-        last = 2.0 ** -11 if got.dtype == torch.bfloat16 else 2.0 ** -22
-        move = np.linalg.norm(block.newton_schulz_moved(m, rng, steps, eps, last) - ref)
-        off = np.linalg.norm(g[e] - ref)
-        tol = 2 * move + u * np.linalg.norm(ref)
-        assert off <= tol, (e, off, tol)
-        assert (np.abs(g[e] - ref) <= u * np.abs(ref) + 2 * move).all()
+        move = 2 * np.linalg.norm(block.newton_schulz_moved(m, rng, steps, eps) - ref)
+        tol = u * np.abs(ref) + last_product(m, got.dtype, steps, eps) * (1 + u)
+        off = np.abs(g[e] - ref)
+        assert np.linalg.norm(off) <= move + np.linalg.norm(tol), (e, np.linalg.norm(off), move, np.linalg.norm(tol))
+        assert (off <= move + tol).all()
 
 
 # one entry; vectors; under one MMA; ends inside and at tile borders, wide, tall and square; K over many blocks
@@ -146,8 +153,7 @@ def test_muon_step(cuda_lib, E, r, c, wdtype, gdtype, nesterov):
                                                      float(np.float32(lr)) * float(np.float32(scale))))
         for e in range(E):
             o = block.newton_schulz(u[e])
-            last = 2.0 ** -11 if wdtype == "bf16" else 2.0 ** -22
-            move = 2 * np.linalg.norm(block.newton_schulz_moved(u[e], rng, last=last) - o)
+            move = 2 * np.linalg.norm(block.newton_schulz_moved(u[e], rng) - o) + last_product(u[e], w.dtype)
             # u itself is rounded once, 2^-24 of it: less than the operands' 2^-22 that `move` has
             ref = keep * w0[e] - rate * o
             eps = torch.finfo(w.dtype).eps / 2 + 3 * 2.0 ** -24
