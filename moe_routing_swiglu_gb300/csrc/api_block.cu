@@ -132,7 +132,7 @@ moe_status join(const void* branch, size_t branch_bytes, bool combine, const uin
   if (st != MOE_OK) return st;
   const moe::JoinArgs a{branch, residual, out, normed, p->norm_weight, p->next_weight, p->gate, inv, weights, T,
                         static_cast<int>(H), p->gate_kind, p->vec_dtype == MOE_F32, weights_dtype, top_k,
-                        static_cast<uint32_t>(slots), p->residual_scale, p->branch_scale, p->eps};
+                        static_cast<uint32_t>(slots), p->residual_scale, p->branch_scale, p->eps, nullptr};
   const cudaError_t err = moe::launch_join(dtype, a, combine ? 2 : 1, sms, static_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) return api_cuda_fail(err, where);
   return api_ok();
@@ -300,7 +300,8 @@ moe_status moe_block_join_backward(const void* dout, const void* dnormed, const 
   const int arrays = (p->norm_weight != nullptr) + (p->gate_kind == MOE_GATE_CHANNEL) + next;
   const moe::JoinBackwardArgs a{dout, dnormed, branch, joined, p->norm_weight, p->next_weight, p->gate, dbranch,
                                 dresidual, dgate, static_cast<float*>(workspace), T, static_cast<int>(H), p->gate_kind,
-                                p->vec_dtype == MOE_F32, arrays, p->residual_scale, p->branch_scale, p->eps};
+                                p->vec_dtype == MOE_F32, arrays, p->residual_scale, p->branch_scale, p->eps,
+                                nullptr};
   const cudaError_t err =
       moe::launch_join_backward(dtype, a, dnorm_weight, dnext_weight, static_cast<cudaStream_t>(stream));
   if (err != cudaSuccess) return api_cuda_fail(err, "moe_block_join_backward launch");

@@ -257,7 +257,7 @@ cudaError_t launch_grad_clip(const moe_grad_tensor* tensors, int64_t n, const fl
                              cudaStream_t stream);
 // ---- norms before and after a block (block_norm.cu)
 constexpr int64_t BLOCK_NORM_MAX_H = 32768;
-constexpr int64_t JOIN_BACKWARD_BLOCKS = 304;   // blocks whose column sums the workspace holds
+constexpr int64_t JOIN_BACKWARD_SMS = 152;   // that the backward's rows are shared out to
 struct JoinArgs {
   const void* f;             // branch rows [T, H], or expert rows [rows, H]
   const void* x;             // [T, H]
@@ -276,6 +276,7 @@ struct JoinArgs {
   int top_k;
   uint32_t rows;
   float alpha, beta, eps;
+  uint32_t* status;          // set by the launcher
 };
 // branch: 0 y = norm(x), 1 rows of f, 2 the combine of expert rows
 cudaError_t launch_join(moe_dtype dtype, const JoinArgs& a, int branch, int num_sms, cudaStream_t stream);
@@ -297,6 +298,7 @@ struct JoinBackwardArgs {
   int vec_f32;
   int arrays;                // column sums asked for: dw1, a channel gate's, dw2
   float alpha, beta, eps;
+  uint32_t* status;          // set by the launcher
 };
 int64_t join_backward_units(int64_t T, int64_t H);
 cudaError_t launch_join_backward(moe_dtype dtype, const JoinBackwardArgs& a, float* dnorm_weight, float* dnext_weight,
