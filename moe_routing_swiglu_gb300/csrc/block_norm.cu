@@ -172,81 +172,74 @@ __device__ __forceinline__ void load_vector(const void* p, bool f32, const Cols<
 
 // ---------------------------------------------------------------- sums over a row
 
-// N <= 8 sums over a row, for every thread of it. One barrier per call: the
-// two halves of `sm` are used in turn, and a half is written again only after
-// the barrier of the call between, which every reader of the half has passed.
-// In a warp the sums are added by exchanging: with 8 sums a lane gives half of
-// its sums away three times and ends with one of them over 8 lanes, 9 shuffles
-// for the warp's 8 sums in place of 40.
-template <int N>
+// COUNT sums (N of each of R rows), for every thread of the rows. One barrier
+// per call: the two halves of `sm` are used in turn, and a half is written
+// again only after the barrier of the call between, which every reader of the
+// half has passed. In a warp the values, V of them (COUNT rounded up to a power
+// of two), are added by exchanging: a lane gives half of its values away until
+// it holds one, number lane / (32 / V), over 32 / V lanes: for 12 sums 16
+// shuffles in place of 60.
+constexpr int pow2_at_least(int n) { return n <= 1 ? 1 : 2 * pow2_at_least((n + 1) / 2); }
+
+template <int COUNT>
 struct RowSums {
-  static constexpr int PAD = N == 1 ? 1 : 8;
-  float v[2][PAD][MAX_CLUSTER * MAX_WARPS];   // [half][sum][block of the cluster * warps + warp]
+  static constexpr int V = pow2_at_least(COUNT);
+  static constexpr int SLOTS = MAX_CLUSTER * MAX_WARPS;   // block of the cluster * warps + warp, rows side by side in turn
+  float v[2][V][SLOTS];
 };
 
-__device__ __forceinline__ float lanes_sum(float v, int from) {
-  for (int off = from; off > 0; off >>= 1) v += __shfl_xor_sync(FULL_MASK, v, off);
-  return v;
-}
-
-// One value per lane: the warp's sum number lane / 4 (of 8).
-__device__ __forceinline__ float exchange_sums(const float (&s)[8]) {
-  const int lane = threadIdx.x & 31;
-  float a[4], b[2];
+// HAVE values of a lane at distance 16, 8, ... (DIST the first) down to one.
+template <int HAVE, int DIST>
+__device__ __forceinline__ float exchange(const float* v) {
+  if constexpr (HAVE == 1) {
+    float s = v[0];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float keep = lane & 16 ? s[i + 4] : s[i], give = lane & 16 ? s[i] : s[i + 4];
-    a[i] = keep + __shfl_xor_sync(FULL_MASK, give, 16);
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float keep = lane & 8 ? a[i + 2] : a[i], give = lane & 8 ? a[i] : a[i + 2];
-    b[i] = keep + __shfl_xor_sync(FULL_MASK, give, 8);
-  }
-  const float keep = lane & 4 ? b[1] : b[0], give = lane & 4 ? b[0] : b[1];
-  float c = keep + __shfl_xor_sync(FULL_MASK, give, 4);
-  c += __shfl_xor_sync(FULL_MASK, c, 2);
-  return c + __shfl_xor_sync(FULL_MASK, c, 1);
-}
-
-template <int N>
-__device__ __forceinline__ void row_sum(float (&s)[N], RowSums<N>* sm, int& half, int tpr, int cluster, int rank) {
-  static_assert(N == 1 || N == 6, "one sum, or eight slots for six");
-  const int lane = threadIdx.x & 31, warps = tpr >> 5;
-  float mine;
-  if (N == 1) {
-    mine = lanes_sum(s[0], 16);
-    s[0] = mine;
+    for (int off = DIST; off > 0; off >>= 1) s += __shfl_xor_sync(FULL_MASK, s, off);
+    return s;
   } else {
-    const float e[8] = {s[0], s[1 % N], s[2 % N], s[3 % N], s[4 % N], s[5 % N], 0.0f, 0.0f};
-    mine = exchange_sums(e);
+    const bool upper = (threadIdx.x & DIST) != 0;
+    float kept[HAVE / 2];
+#pragma unroll
+    for (int i = 0; i < HAVE / 2; ++i) {
+      const float keep = upper ? v[i + HAVE / 2] : v[i], give = upper ? v[i] : v[i + HAVE / 2];
+      kept[i] = keep + __shfl_xor_sync(FULL_MASK, give, DIST);
+    }
+    return exchange<HAVE / 2, DIST / 2>(kept);
   }
+}
+
+template <int COUNT>
+__device__ __forceinline__ void row_sum(float (&s)[COUNT], RowSums<COUNT>* sm, int& half, int tpr, int cluster, int rank) {
+  constexpr int V = RowSums<COUNT>::V, LANES = 32 / V;   // lanes of a value
+  const int lane = threadIdx.x & 31, which = lane / LANES, part = lane % LANES;
+  float all[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) all[i] = i < COUNT ? s[i < COUNT ? i : 0] : 0.0f;
+  float mine = exchange<V, 16>(all);
   if (tpr > 32 || cluster > 1) {
-    const int slot0 = static_cast<int>(threadIdx.y) * warps;   // rows side by side have slots of their own
-    const int which = N == 1 ? 0 : lane >> 2;
-    const int slot = slot0 + rank * warps + static_cast<int>(threadIdx.x >> 5);
+    const int warps = tpr >> 5, slot0 = static_cast<int>(threadIdx.y) * warps;
+    float* at = &sm->v[half][which][slot0];
+    half ^= 1;
     if (cluster == 1) {
-      if (N == 1 ? lane == 0 : (lane & 3) == 0) sm->v[half][which][slot] = mine;
+      if (part == 0) at[threadIdx.x >> 5] = mine;
       __syncthreads();
     } else {
       cg::cluster_group cl = cg::this_cluster();
-      // N == 1: lane i writes to block i; else the four lanes of a sum share the blocks.
-      for (int to = N == 1 ? lane : lane & 3; to < cluster; to += N == 1 ? 32 : 4)
-        *cl.map_shared_rank(&sm->v[half][which][slot], to) = mine;
+      for (int to = part; to < cluster; to += LANES)
+        *cl.map_shared_rank(at + rank * warps + (threadIdx.x >> 5), to) = mine;
       cl.sync();
     }
     mine = 0.0f;
-    for (int w = N == 1 ? lane : lane & 3; w < cluster * warps; w += N == 1 ? 32 : 4) mine += sm->v[half][which][slot0 + w];
-    half ^= 1;
-    if (N == 1) {
-      s[0] = lanes_sum(mine, 16);
-      return;
-    }
-    mine = lanes_sum(mine, 2);
-  }
-  if (N > 1)
+    for (int w = part; w < cluster * warps; w += LANES) mine += at[w];
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = __shfl_sync(FULL_MASK, mine, 4 * i);
+    for (int off = LANES / 2; off > 0; off >>= 1) mine += __shfl_xor_sync(FULL_MASK, mine, off);
+  }
+  if (V == 1) {
+    s[0] = mine;
+  } else {
+#pragma unroll
+    for (int i = 0; i < COUNT; ++i) s[i] = __shfl_sync(FULL_MASK, mine, i * LANES);
+  }
 }
 
 __device__ __forceinline__ float weight_at(const void* p, int dtype, int64_t i) {
@@ -323,6 +316,17 @@ __device__ __forceinline__ void ring_end(Ring& ring, uint32_t issued, int stages
   __syncthreads();
 }
 
+// n rows of this block's columns: one copy where the block has whole rows.
+template <typename T>
+__device__ __forceinline__ void copy_rows(uint8_t* dst, const T* src, uint32_t n, uint32_t row_bytes, int H, int cluster,
+                                          uint64_t* bar) {
+  if (cluster == 1) {
+    bulk_load(dst, src, row_bytes * n, bar);
+  } else {
+    for (uint32_t r = 0; r < n; ++r) bulk_load(dst + r * row_bytes, src + r * static_cast<int64_t>(H), row_bytes, bar);
+  }
+}
+
 // This thread's columns of a row in a stage.
 template <typename T>
 __device__ __forceinline__ void stage8(const uint8_t* mine, bool any, Eight<T>& v) {
@@ -347,23 +351,29 @@ __device__ __forceinline__ void stage8(const uint8_t* mine, bool any, Eight<T>& 
 
 // Threads that an SM holds: 1024 of 64 registers where that is enough.
 constexpr int join_threads(size_t size, bool vec, int branch, bool element) {
-  return size == 2 && vec && branch < 2 && !element ? 1024 : 512;
+  return size == 2 && vec && branch < 1 && !element ? 1024 : 512;
 }
+// Rows of a thread in a round: two share a round's barriers and index
+// arithmetic, which are most of a row's instructions.
+constexpr int join_rows(bool bulk, int branch) { return bulk && branch != 2 ? 2 : 1; }
+
 template <typename T, bool VEC, bool BULK, int BRANCH, bool ELEMENT>
 __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, ELEMENT) / MAX_TPR)
     join_kernel(const JoinArgs a, int cluster, int stages) {
-  __shared__ RowSums<1> sums;
+  constexpr int R = join_rows(BULK, BRANCH);
+  __shared__ RowSums<R> sums;
   __shared__ Ring ring;
   extern __shared__ __align__(128) uint8_t stage_smem[];
   const int tpr = blockDim.x;
   const int rank = cluster > 1 ? static_cast<int>(blockIdx.x) % cluster : 0;
-  const int64_t unit = blockIdx.x / cluster, units = gridDim.x / cluster;
-  const int64_t step = units * blockDim.y;
+  const uint32_t rows = static_cast<uint32_t>(a.T), round_rows = blockDim.y * R;
+  const uint32_t step = gridDim.x / cluster * round_rows, first_row = blockIdx.x / cluster * round_rows;
   const Cols<VEC> c(threadIdx.x, tpr, rank, a.H);
   const int lane = threadIdx.x & 31;
   const float inv_h = 1.0f / static_cast<float>(a.H);
   const bool post = BRANCH != 0 && a.norm_weight != nullptr;
   const bool next = BRANCH == 0 || a.next_weight != nullptr;
+  const bool token = BRANCH != 0 && a.gate_kind == MOE_GATE_TOKEN;
   int half = 0;
   if (BULK) ring_init(ring, stages);
   if (cluster > 1) cg::this_cluster().sync();   // every block runs before another one writes to its sums
@@ -373,40 +383,40 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
   // The ring: a stage holds x, then f or the expert rows, then the gates, each
   // of this block's columns.
   const int cols = min(tpr * COLS, a.H - rank * tpr * COLS);
-  const size_t row_bytes = static_cast<size_t>(cols) * sizeof(T), block_bytes = row_bytes * blockDim.y;
-  const size_t stage_bytes = block_bytes * (1 + (BRANCH == 2 ? a.top_k : BRANCH) + (ELEMENT ? 1 : 0));
-  uint32_t issued = 0;
-  // Combine: lane j's expert row (and weight) of the round to be issued next
-  // and of the one at work.
-  auto slot_of = [&](int64_t t0) {
-    const int64_t t = min(t0 + threadIdx.y, a.T - 1);
-    return lane < a.top_k && t0 < a.T ? a.inv[t * a.top_k + lane] : 0xFFFFFFFFu;
+  const uint32_t row_bytes = cols * static_cast<uint32_t>(sizeof(T)), block_bytes = row_bytes * round_rows;
+  const uint32_t stage_bytes = block_bytes * (1 + (BRANCH == 2 ? a.top_k : BRANCH) + (ELEMENT ? 1 : 0));
+  // Combine: lane j's expert row of a token's first 32 slots.
+  auto slot_of = [&](uint32_t t) {
+    return lane < a.top_k && t < rows ? a.inv[static_cast<int64_t>(t) * a.top_k + lane] : 0xFFFFFFFFu;
   };
-  uint32_t ahead = BRANCH == 2 && BULK ? slot_of(unit * blockDim.y) : 0;
-  int64_t issue_t0 = unit * blockDim.y;
+  auto weight_of = [&](uint32_t t) {
+    return lane < a.top_k && t < rows ? weight_at(a.weights, a.weights_dtype, static_cast<int64_t>(t) * a.top_k + lane)
+                                      : 0.0f;
+  };
+  uint32_t issued = 0, issue_t0 = first_row;
   Turn fill{0, 0u};
+  uint32_t ahead = BRANCH == 2 && BULK ? slot_of(issue_t0) : 0;   // slots of the round to be issued next
   auto issue = [&]() {   // by the first warp of the block
-    const int64_t t0 = issue_t0;
-    if (t0 >= a.T) return;
-    const int n = static_cast<int>(min(static_cast<int64_t>(blockDim.y), a.T - t0));
+    if (issue_t0 >= rows) return;
     uint8_t* dst = stage_smem + fill.slot * stage_bytes;
     uint64_t* bar = &ring.full[fill.slot];
-    const int64_t at = t0 * a.H + rank * tpr * COLS;
-    const uint32_t bytes = static_cast<uint32_t>(row_bytes * n);
+    const int64_t at = static_cast<int64_t>(issue_t0) * a.H + rank * tpr * COLS;
+    const uint32_t n = min(round_rows, rows - issue_t0);
     const bool good = BRANCH == 2 && ahead < a.rows;
     if (BRANCH == 2) {
-      const uint32_t rows = __popc(__ballot_sync(FULL_MASK, good));
-      if (lane == 0) mbar_arrive_expect_tx(bar, bytes * ((ELEMENT ? 2 : 1) + rows));
+      const uint32_t found = __popc(__ballot_sync(FULL_MASK, good));
+      if (lane == 0) mbar_arrive_expect_tx(bar, row_bytes * ((ELEMENT ? 2 : 1) + found));
       __syncwarp();
       if (good)
         bulk_load(dst + (1 + lane) * row_bytes,
-                  static_cast<const T*>(a.f) + static_cast<int64_t>(ahead) * a.H + rank * tpr * COLS, bytes, bar);
+                  static_cast<const T*>(a.f) + static_cast<int64_t>(ahead) * a.H + rank * tpr * COLS, row_bytes, bar);
     }
     if (lane == 0) {
-      if (BRANCH != 2) mbar_arrive_expect_tx(bar, bytes * (1 + BRANCH + (ELEMENT ? 1 : 0)));
-      bulk_load(dst, static_cast<const T*>(a.x) + at, bytes, bar);
-      if (BRANCH == 1) bulk_load(dst + block_bytes, static_cast<const T*>(a.f) + at, bytes, bar);
-      if (ELEMENT) bulk_load(dst + stage_bytes - block_bytes, static_cast<const T*>(a.gate) + at, bytes, bar);
+      if (BRANCH != 2) mbar_arrive_expect_tx(bar, row_bytes * n * (1 + BRANCH + (ELEMENT ? 1 : 0)));
+      copy_rows<T>(dst, static_cast<const T*>(a.x) + at, n, row_bytes, a.H, cluster, bar);
+      if (BRANCH == 1) copy_rows<T>(dst + block_bytes, static_cast<const T*>(a.f) + at, n, row_bytes, a.H, cluster, bar);
+      if (ELEMENT)
+        copy_rows<T>(dst + stage_bytes - block_bytes, static_cast<const T*>(a.gate) + at, n, row_bytes, a.H, cluster, bar);
     }
     ++issued;
     fill.next(stages);
@@ -430,50 +440,65 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
   load_vector<T, VEC>(a.next_weight, a.vec_f32, c, w2);
 
   // Every thread of a block takes part in every round (the barriers), with a
-  // row past the end as a row that is not stored.
+  // row past the end as a row that is not stored. A round's scalars are loaded
+  // a round ahead.
   Turn turn{0, 0u};
-  const uint8_t* mine = stage_smem + (static_cast<size_t>(threadIdx.y) * cols + threadIdx.x * COLS) * sizeof(T);
+  const uint8_t* mine = stage_smem + threadIdx.y * R * row_bytes + threadIdx.x * (COLS * static_cast<uint32_t>(sizeof(T)));
   const bool row_barrier = tpr > 32 || cluster > 1;
-  for (int64_t t0 = unit * blockDim.y; t0 < a.T; t0 += step) {
-    const bool live = t0 + threadIdx.y < a.T;
-    const int64_t t = live ? t0 + threadIdx.y : a.T - 1;
-    const int64_t at = t * a.H;
-    Eight<T> raw, gv;
-    float x[COLS], f[COLS];
-    float g = a.beta;
-    if (BRANCH != 0 && a.gate_kind == MOE_GATE_TOKEN) g *= token_gate<T>(a.gate, a.vec_f32, t);
-    uint32_t slot = 0;
-    float weight = 0.0f;
-    if (BRANCH == 2 && lane < a.top_k) {
-      slot = a.inv[t * a.top_k + lane];
-      weight = weight_at(a.weights, a.weights_dtype, t * a.top_k + lane);
+  uint32_t t = first_row + threadIdx.y * R;   // this thread's first row
+  auto gate_of = [&](uint32_t row) { return token && row < rows ? token_gate<T>(a.gate, a.vec_f32, row) : 1.0f; };
+  float gate_next[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) gate_next[r] = gate_of(t + r);
+  uint32_t slot_next = BRANCH == 2 ? slot_of(t) : 0;
+  float weight_next = BRANCH == 2 ? weight_of(t) : 0.0f;
+  for (uint32_t t0 = first_row; t0 < rows; t0 += step, t += step) {
+    float g[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      g[r] = a.beta * gate_next[r];
+      gate_next[r] = gate_of(t + step + r);
     }
+    uint32_t slot = slot_next;
+    float weight = weight_next;
+    if (BRANCH == 2) {
+      slot_next = slot_of(t + step);
+      weight_next = weight_of(t + step);
+    }
+    const int64_t at = static_cast<int64_t>(min(t, rows - 1)) * a.H;
+    Eight<T> raw, gv[R];
+    float x[R][COLS], f[R][COLS];
     const uint8_t* stage = mine + turn.slot * stage_bytes;
     if (BULK) {
       ring_wait(ring, turn, a.status);
       turn.next(stages);
-      stage8<T>(stage, c.any(), raw);
-      if (ELEMENT) stage8<T>(stage + stage_bytes - block_bytes, c.any(), gv);
-    } else {
-      load8<T, VEC>(static_cast<const T*>(a.x) + at, c, raw);
-      if (ELEMENT) load8<T, VEC>(static_cast<const T*>(a.gate) + at, c, gv);
     }
-    unpack8(raw, x);
-    if (BRANCH == 1) {
-      if (BULK) stage8<T>(stage + block_bytes, c.any(), raw);
-      else load8<T, VEC>(static_cast<const T*>(a.f) + at, c, raw);
-      unpack8(raw, f);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (BULK) stage8<T>(stage + r * row_bytes, c.any(), raw);
+      else load8<T, VEC>(static_cast<const T*>(a.x) + at, c, raw);
+      unpack8(raw, x[r]);
+      if (ELEMENT) {
+        if (BULK) stage8<T>(stage + stage_bytes - block_bytes + r * row_bytes, c.any(), gv[r]);
+        else load8<T, VEC>(static_cast<const T*>(a.gate) + at, c, gv[r]);
+      }
+      if (BRANCH == 1) {
+        if (BULK) stage8<T>(stage + block_bytes + r * row_bytes, c.any(), raw);
+        else load8<T, VEC>(static_cast<const T*>(a.f) + at, c, raw);
+        unpack8(raw, f[r]);
+      }
     }
     if (BRANCH == 2) {
       // Slot order, as moe_combine; a bad row number makes the token NaN.
 #pragma unroll
-      for (int j = 0; j < COLS; ++j) f[j] = 0.0f;
+      for (int j = 0; j < COLS; ++j) f[0][j] = 0.0f;
       bool bad = false;
       constexpr int G = 4;   // rows whose loads are in flight together
+      const int64_t slot0 = static_cast<int64_t>(min(t, rows - 1)) * a.top_k;
       for (int first = 0; first < a.top_k; first += 32) {
         if (first > 0 && first + lane < a.top_k) {
-          slot = a.inv[t * a.top_k + first + lane];
-          weight = weight_at(a.weights, a.weights_dtype, t * a.top_k + first + lane);
+          slot = a.inv[slot0 + first + lane];
+          weight = weight_at(a.weights, a.weights_dtype, slot0 + first + lane);
         }
         const int here = min(a.top_k - first, 32);
         for (int k0 = 0; k0 < here; k0 += G) {
@@ -498,13 +523,13 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
               float y[COLS];
               unpack8(v[i], y);
 #pragma unroll
-              for (int j = 0; j < COLS; ++j) f[j] = fmaf(w[i], y[j], f[j]);
+              for (int j = 0; j < COLS; ++j) f[0][j] = fmaf(w[i], y[j], f[0][j]);
             }
         }
       }
       if (bad)
 #pragma unroll
-        for (int j = 0; j < COLS; ++j) f[j] = __int_as_float(0x7FC00000);
+        for (int j = 0; j < COLS; ++j) f[0][j] = __int_as_float(0x7FC00000);
     }
     // The first of the round's barriers after which the stage may be copied over.
     bool freed = !BULK;
@@ -514,38 +539,47 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
       if (!barrier) __syncthreads();
       if (issuer) issue();
     };
-    if (BRANCH != 0) {
-      if (post) {
-        float s[1] = {0.0f};
+    auto sum_squares = [&](const float (&v)[R][COLS], float (&s)[R]) {
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        s[r] = 0.0f;
 #pragma unroll
         for (int j = 0; j < COLS; ++j)
-          if (VEC || c.col(j) < c.H) s[0] = fmaf(f[j], f[j], s[0]);
-        if (VEC && !c.any()) s[0] = 0.0f;   // a thread past the row may hold a token's NaN
-        row_sum<1>(s, &sums, half, tpr, cluster, rank);
-        free_stage(row_barrier);
-        g *= rsqrtf(fmaf(s[0], inv_h, a.eps));
+          if (VEC || c.col(j) < c.H) s[r] = fmaf(v[r][j], v[r][j], s[r]);
+        if (VEC && !c.any()) s[r] = 0.0f;   // a thread past the row may hold a token's NaN
       }
-      float gate[COLS];
-      if (ELEMENT) unpack8(gv, gate);
+      row_sum<R>(s, &sums, half, tpr, cluster, rank);
+      free_stage(row_barrier);
+    };
+    float s[R];
+    if (BRANCH != 0) {
+      if (post) {
+        sum_squares(f, s);
 #pragma unroll
-      for (int j = 0; j < COLS; ++j) x[j] = fmaf(a.alpha, x[j], f[j] * g * w1[j] * (ELEMENT ? gate[j] : 1.0f));
-      pack8<T>(x, raw);
-      if (live) store8<T, VEC>(static_cast<T*>(a.out) + at, c, raw);
-      if (next) unpack8(raw, x);
+        for (int r = 0; r < R; ++r) g[r] *= rsqrtf(fmaf(s[r], inv_h, a.eps));
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        float gate[COLS];
+        if (ELEMENT) unpack8(gv[r], gate);
+#pragma unroll
+        for (int j = 0; j < COLS; ++j)
+          x[r][j] = fmaf(a.alpha, x[r][j], f[r][j] * g[r] * w1[j] * (ELEMENT ? gate[j] : 1.0f));
+        pack8<T>(x[r], raw);
+        if (t + r < rows) store8<T, VEC>(static_cast<T*>(a.out) + at + r * static_cast<int64_t>(a.H), c, raw);
+        unpack8(raw, x[r]);
+      }
     }
     if (next) {
-      float s[1] = {0.0f};
+      sum_squares(x, s);
 #pragma unroll
-      for (int j = 0; j < COLS; ++j)
-        if (VEC || c.col(j) < c.H) s[0] = fmaf(x[j], x[j], s[0]);
-      if (VEC && !c.any()) s[0] = 0.0f;
-      row_sum<1>(s, &sums, half, tpr, cluster, rank);
-      free_stage(row_barrier);
-      const float r = rsqrtf(fmaf(s[0], inv_h, a.eps));
+      for (int r = 0; r < R; ++r) {
+        const float rs = rsqrtf(fmaf(s[r], inv_h, a.eps));
 #pragma unroll
-      for (int j = 0; j < COLS; ++j) x[j] = x[j] * r * w2[j];
-      pack8<T>(x, raw);
-      if (live) store8<T, VEC>(static_cast<T*>(a.y) + at, c, raw);
+        for (int j = 0; j < COLS; ++j) x[r][j] = x[r][j] * rs * w2[j];
+        pack8<T>(x[r], raw);
+        if (t + r < rows) store8<T, VEC>(static_cast<T*>(a.y) + at + r * static_cast<int64_t>(a.H), c, raw);
+      }
     }
     free_stage(false);
   }
@@ -561,16 +595,23 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
 // gates): dw1 = gate S, dgate = w1 S.
 //
 // Bound by HBM (join: dout, dy, out, f in, dx, df out). BULK as in the forward.
+constexpr int backward_rows(bool bulk) { return bulk ? 2 : 1; }
+
 template <typename T, bool VEC, bool BULK, bool HAS_F, bool NEXT, bool ELEMENT>
 __global__ void __launch_bounds__(MAX_TPR) join_backward_kernel(const JoinBackwardArgs a, int cluster, int stages) {
-  __shared__ RowSums<6> sums;
+  constexpr int R = backward_rows(BULK);
+  // Sums of a row: out^2, w2 dy out, f^2, dout G f, w2 dy G f, out G f (those that are needed).
+  constexpr int N = HAS_F && NEXT ? 6 : 2;
+  constexpr int AT_FF = HAS_F && NEXT ? 2 : 0, AT_DF = AT_FF + 1, AT_YF = 4, AT_OF = 5;
+  __shared__ RowSums<N * R> sums;
   __shared__ Ring ring;
   extern __shared__ __align__(128) uint8_t stage_smem[];   // the ring; in the end [rows of the block - 1][tpr * COLS] sums
   float* fold = reinterpret_cast<float*>(stage_smem);
   const int tpr = blockDim.x;
   const int rank = cluster > 1 ? static_cast<int>(blockIdx.x) % cluster : 0;
-  const int64_t unit = blockIdx.x / cluster, units = gridDim.x / cluster;
-  const int64_t step = units * blockDim.y;
+  const uint32_t rows = static_cast<uint32_t>(a.T), round_rows = blockDim.y * R;
+  const int64_t unit = blockIdx.x / cluster;
+  const uint32_t step = gridDim.x / cluster * round_rows, first_row = static_cast<uint32_t>(unit) * round_rows;
   const Cols<VEC> c(threadIdx.x, tpr, rank, a.H);
   const float inv_h = 1.0f / static_cast<float>(a.H);
   const bool post = HAS_F && a.norm_weight != nullptr;
@@ -585,29 +626,27 @@ __global__ void __launch_bounds__(MAX_TPR) join_backward_kernel(const JoinBackwa
 
   // A stage: dout, f, out and dy, the gates, of this block's columns.
   const int cols = min(tpr * COLS, a.H - rank * tpr * COLS);
-  const size_t block_bytes = static_cast<size_t>(cols) * sizeof(T) * blockDim.y;
+  const uint32_t row_bytes = cols * static_cast<uint32_t>(sizeof(T)), block_bytes = row_bytes * round_rows;
   constexpr int ARRAYS = 1 + (HAS_F ? 1 : 0) + (NEXT ? 2 : 0) + (ELEMENT ? 1 : 0);
   constexpr int AT_F = 1, AT_O = 1 + (HAS_F ? 1 : 0), AT_Y = AT_O + 1, AT_G = ARRAYS - 1;
-  const size_t stage_bytes = block_bytes * ARRAYS;
-  uint32_t issued = 0;
-  int64_t issue_t0 = unit * blockDim.y;
+  const uint32_t stage_bytes = block_bytes * ARRAYS;
+  uint32_t issued = 0, issue_t0 = first_row;
   Turn fill{0, 0u};
   auto issue = [&]() {
-    const int64_t t0 = issue_t0;
-    if (t0 >= a.T) return;
-    const int n = static_cast<int>(min(static_cast<int64_t>(blockDim.y), a.T - t0));
+    if (issue_t0 >= rows) return;
     uint8_t* dst = stage_smem + fill.slot * stage_bytes;
     uint64_t* bar = &ring.full[fill.slot];
-    const int64_t at = t0 * a.H + rank * tpr * COLS;
-    const uint32_t bytes = static_cast<uint32_t>(static_cast<size_t>(cols) * sizeof(T) * n);
-    mbar_arrive_expect_tx(bar, bytes * (ARRAYS - (has_d ? 0 : 1)));
-    if (has_d) bulk_load(dst, static_cast<const T*>(a.dout) + at, bytes, bar);
-    if (HAS_F) bulk_load(dst + AT_F * block_bytes, static_cast<const T*>(a.f) + at, bytes, bar);
-    if (NEXT) {
-      bulk_load(dst + AT_O * block_bytes, static_cast<const T*>(a.joined) + at, bytes, bar);
-      bulk_load(dst + AT_Y * block_bytes, static_cast<const T*>(a.dnormed) + at, bytes, bar);
-    }
-    if (ELEMENT) bulk_load(dst + AT_G * block_bytes, static_cast<const T*>(a.gate) + at, bytes, bar);
+    const int64_t at = static_cast<int64_t>(issue_t0) * a.H + rank * tpr * COLS;
+    const uint32_t n = min(round_rows, rows - issue_t0);
+    auto copy = [&](int array, const void* src) {
+      copy_rows<T>(dst + array * block_bytes, static_cast<const T*>(src) + at, n, row_bytes, a.H, cluster, bar);
+    };
+    mbar_arrive_expect_tx(bar, row_bytes * n * (ARRAYS - (has_d ? 0 : 1)));
+    if (has_d) copy(0, a.dout);
+    if (HAS_F) copy(AT_F, a.f);
+    if (NEXT) copy(AT_O, a.joined);
+    if (NEXT) copy(AT_Y, a.dnormed);
+    if (ELEMENT) copy(AT_G, a.gate);
     ++issued;
     fill.next(stages);
     issue_t0 += step;
@@ -632,111 +671,128 @@ __global__ void __launch_bounds__(MAX_TPR) join_backward_kernel(const JoinBackwa
   if (NEXT) load_vector<T, VEC>(a.next_weight, a.vec_f32, c, w2);
 
   Turn turn{0, 0u};
-  const uint8_t* mine = stage_smem + (static_cast<size_t>(threadIdx.y) * cols + threadIdx.x * COLS) * sizeof(T);
-  for (int64_t t0 = unit * blockDim.y; t0 < a.T; t0 += step) {
-    const bool live = t0 + threadIdx.y < a.T;
-    const int64_t t = live ? t0 + threadIdx.y : a.T - 1;
-    const int64_t at = t * a.H;
-    const float gt = token ? token_gate<T>(a.gate, a.vec_f32, t) : 1.0f;
-    Eight<T> vd, vf, vo, vy, vg;
+  const uint8_t* mine = stage_smem + threadIdx.y * R * row_bytes + threadIdx.x * (COLS * static_cast<uint32_t>(sizeof(T)));
+  uint32_t t = first_row + threadIdx.y * R;   // this thread's first row
+  auto gate_of = [&](uint32_t row) { return token && row < rows ? token_gate<T>(a.gate, a.vec_f32, row) : 1.0f; };
+  float gate_next[R];
+#pragma unroll
+  for (int r = 0; r < R; ++r) gate_next[r] = gate_of(t + r);
+  for (uint32_t t0 = first_row; t0 < rows; t0 += step, t += step) {
+    float gt[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      gt[r] = gate_next[r];
+      gate_next[r] = gate_of(t + step + r);
+    }
+    const int64_t at = static_cast<int64_t>(min(t, rows - 1)) * a.H;
+    Eight<T> vd[R], vf[R], vo[R], vy[R], vg[R];
+    const uint8_t* stage = mine + turn.slot * stage_bytes;
     if (BULK) {
-      const uint8_t* stage = mine + turn.slot * stage_bytes;
       ring_wait(ring, turn, a.status);
       turn.next(stages);
-      stage8<T>(stage, c.any() && has_d, vd);
-      if (HAS_F) stage8<T>(stage + AT_F * block_bytes, c.any(), vf);
-      if (NEXT) {
-        stage8<T>(stage + AT_O * block_bytes, c.any(), vo);
-        stage8<T>(stage + AT_Y * block_bytes, c.any(), vy);
-      }
-      if (ELEMENT) stage8<T>(stage + AT_G * block_bytes, c.any(), vg);
-    } else {
-      if (has_d) {
-        load8<T, VEC>(static_cast<const T*>(a.dout) + at, c, vd);
-      } else {
-#pragma unroll
-        for (int j = 0; j < COLS; ++j) vd.e[j] = from_f32<T>(0.0f);
-      }
-      if (HAS_F) load8<T, VEC>(static_cast<const T*>(a.f) + at, c, vf);
-      if (NEXT) {
-        load8<T, VEC>(static_cast<const T*>(a.joined) + at, c, vo);
-        load8<T, VEC>(static_cast<const T*>(a.dnormed) + at, c, vy);
-      }
-      if (ELEMENT) load8<T, VEC>(static_cast<const T*>(a.gate) + at, c, vg);
     }
-    float s[6] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    {
+    float s[N * R];
+#pragma unroll
+    for (int i = 0; i < N * R; ++i) s[i] = 0.0f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (BULK) {
+        const uint8_t* row = stage + r * row_bytes;
+        stage8<T>(row, c.any() && has_d, vd[r]);
+        if (HAS_F) stage8<T>(row + AT_F * block_bytes, c.any(), vf[r]);
+        if (NEXT) stage8<T>(row + AT_O * block_bytes, c.any(), vo[r]);
+        if (NEXT) stage8<T>(row + AT_Y * block_bytes, c.any(), vy[r]);
+        if (ELEMENT) stage8<T>(row + AT_G * block_bytes, c.any(), vg[r]);
+      } else {
+        if (has_d) {
+          load8<T, VEC>(static_cast<const T*>(a.dout) + at, c, vd[r]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < COLS; ++j) vd[r].e[j] = from_f32<T>(0.0f);
+        }
+        if (HAS_F) load8<T, VEC>(static_cast<const T*>(a.f) + at, c, vf[r]);
+        if (NEXT) load8<T, VEC>(static_cast<const T*>(a.joined) + at, c, vo[r]);
+        if (NEXT) load8<T, VEC>(static_cast<const T*>(a.dnormed) + at, c, vy[r]);
+        if (ELEMENT) load8<T, VEC>(static_cast<const T*>(a.gate) + at, c, vg[r]);
+      }
       float d[COLS], f[COLS], o[COLS], y[COLS], g[COLS];
-      unpack8(vd, d);
-      if (HAS_F) unpack8(vf, f);
-      if (NEXT) unpack8(vo, o);
-      if (NEXT) unpack8(vy, y);
-      if (ELEMENT) unpack8(vg, g);
+      if (HAS_F) unpack8(vd[r], d);
+      if (HAS_F) unpack8(vf[r], f);
+      if (NEXT) unpack8(vo[r], o);
+      if (NEXT) unpack8(vy[r], y);
+      if (ELEMENT) unpack8(vg[r], g);
+      float* p = s + r * N;
 #pragma unroll
       for (int j = 0; j < COLS; ++j) {
         const float gf = HAS_F ? w1[j] * f[j] * (ELEMENT ? g[j] : 1.0f) : 0.0f;
         if (NEXT) {
           const float wy = w2[j] * y[j];
-          s[0] = fmaf(o[j], o[j], s[0]);
-          s[1] = fmaf(wy, o[j], s[1]);
+          p[0] = fmaf(o[j], o[j], p[0]);
+          p[1] = fmaf(wy, o[j], p[1]);
           if (HAS_F) {
-            s[4] = fmaf(wy, gf, s[4]);
-            s[5] = fmaf(o[j], gf, s[5]);
+            p[AT_YF] = fmaf(wy, gf, p[AT_YF]);
+            p[AT_OF] = fmaf(o[j], gf, p[AT_OF]);
           }
         }
         if (HAS_F) {
-          s[2] = fmaf(f[j], f[j], s[2]);
-          s[3] = fmaf(d[j], gf, s[3]);
+          p[AT_FF] = fmaf(f[j], f[j], p[AT_FF]);
+          p[AT_DF] = fmaf(d[j], gf, p[AT_DF]);
         }
       }
     }
-    row_sum<6>(s, &sums, half, tpr, cluster, rank);
+    row_sum<N * R>(s, &sums, half, tpr, cluster, rank);
     if (BULK) {   // the stage may be copied over
       if (tpr == 32 && cluster == 1) __syncthreads();
       if (issuer) issue();
     }
-    const float r2 = NEXT ? rsqrtf(fmaf(s[0], inv_h, a.eps)) : 0.0f;
-    const float m2 = r2 * r2 * (s[1] * inv_h);                      // r2^2 S2 / H
-    const float r1 = post ? rsqrtf(fmaf(s[2], inv_h, a.eps)) : 1.0f;
-    const float q = s[3] + r2 * (s[4] - m2 * s[5]);
-    const float m1 = post ? r1 * r1 * (q * inv_h) : 0.0f;           // r1^2 Q / H
-    const float b = a.beta * r1;
-    if (token && live && threadIdx.x == 0 && rank == 0) static_cast<float*>(a.dgate)[t] = b * q;
-    float d[COLS];
-    unpack8(vd, d);
-    if (NEXT) {
-      float o[COLS], y[COLS];
-      unpack8(vo, o);
-      unpack8(vy, y);
 #pragma unroll
-      for (int j = 0; j < COLS; ++j) {
-        d[j] = fmaf(r2, fmaf(-o[j], m2, w2[j] * y[j]), d[j]);       // dO
-        if (live) s2[j] = fmaf(y[j], o[j] * r2, s2[j]);
+    for (int r = 0; r < R; ++r) {
+      const float* p = s + r * N;
+      const bool live = t + r < rows;
+      const int64_t to = at + r * static_cast<int64_t>(a.H);
+      const float r2 = NEXT ? rsqrtf(fmaf(p[0], inv_h, a.eps)) : 0.0f;
+      const float m2 = NEXT ? r2 * r2 * (p[1] * inv_h) : 0.0f;        // r2^2 S2 / H
+      const float r1 = post ? rsqrtf(fmaf(p[AT_FF], inv_h, a.eps)) : 1.0f;
+      const float q = HAS_F && NEXT ? p[AT_DF] + r2 * (p[AT_YF] - m2 * p[AT_OF]) : p[AT_DF];
+      const float m1 = post ? r1 * r1 * (q * inv_h) : 0.0f;           // r1^2 Q / H
+      const float b = a.beta * r1;
+      if (token && live && threadIdx.x == 0 && rank == 0) static_cast<float*>(a.dgate)[t + r] = b * q;
+      float d[COLS];
+      unpack8(vd[r], d);
+      if (NEXT) {
+        float o[COLS], y[COLS];
+        unpack8(vo[r], o);
+        unpack8(vy[r], y);
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) {
+          d[j] = fmaf(r2, fmaf(-o[j], m2, w2[j] * y[j]), d[j]);       // dO
+          if (live) s2[j] = fmaf(y[j], o[j] * r2, s2[j]);
+        }
       }
+      if (HAS_F) {
+        float f[COLS], g[COLS];
+        unpack8(vf[r], f);
+        if (ELEMENT) unpack8(vg[r], g);
+        const float bm = b * m1;
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) {
+          const float bd = b * d[j], bdf = bd * f[j];                 // beta r1 dO, and times f
+          f[j] = gt[r] * fmaf(ELEMENT ? w1[j] * g[j] : w1[j], bd, -f[j] * bm);
+          if (live) s1[j] = fmaf(bdf, ELEMENT ? g[j] * gt[r] : gt[r], s1[j]);
+          if (ELEMENT) g[j] = bdf * w1[j];
+        }
+        pack8<T>(f, vf[r]);
+        if (live) store8<T, VEC>(static_cast<T*>(a.dbranch) + to, c, vf[r]);
+        if (ELEMENT) {
+          pack8<T>(g, vg[r]);
+          if (live) store8<T, VEC>(static_cast<T*>(a.dgate) + to, c, vg[r]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) d[j] *= a.alpha;
+      pack8<T>(d, vd[r]);
+      if (live) store8<T, VEC>(static_cast<T*>(a.dresidual) + to, c, vd[r]);
     }
-    if (HAS_F) {
-      float f[COLS], g[COLS];
-      unpack8(vf, f);
-      if (ELEMENT) unpack8(vg, g);
-      const float bm = b * m1;
-#pragma unroll
-      for (int j = 0; j < COLS; ++j) {
-        const float bd = b * d[j], bdf = bd * f[j];                 // beta r1 dO, and times f
-        f[j] = gt * fmaf(ELEMENT ? w1[j] * g[j] : w1[j], bd, -f[j] * bm);
-        if (live) s1[j] = fmaf(bdf, ELEMENT ? g[j] * gt : gt, s1[j]);
-        if (ELEMENT) g[j] = bdf * w1[j];
-      }
-      pack8<T>(f, vf);
-      if (live) store8<T, VEC>(static_cast<T*>(a.dbranch) + at, c, vf);
-      if (ELEMENT) {
-        pack8<T>(g, vg);
-        if (live) store8<T, VEC>(static_cast<T*>(a.dgate) + at, c, vg);
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < COLS; ++j) d[j] *= a.alpha;
-    pack8<T>(d, vd);
-    if (live) store8<T, VEC>(static_cast<T*>(a.dresidual) + at, c, vd);
   }
   if (BULK) ring_end(ring, issued, stages, a.status);
   // The block's rows side by side are added in order, then stored, times the
@@ -814,7 +870,7 @@ __global__ void __launch_bounds__(BLOCK) column_sum_kernel(const float* partial,
 
 // ---------------------------------------------------------------- launches
 
-constexpr size_t SM_STAGE_BYTES = 200 * 1024;   // of an SM's shared memory, for the rings
+constexpr size_t SM_STAGE_BYTES = 180 * 1024;   // of an SM's shared memory, for the rings
 
 template <typename K, typename A>
 cudaError_t launch_rows(K kernel, const RowShape& s, int64_t units, size_t smem, int stages, const A& args,
@@ -839,13 +895,16 @@ cudaError_t launch_rows(K kernel, const RowShape& s, int64_t units, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, args, s.cluster, stages);
 }
 
-// Stages of a ring whose rounds read `arrays` rows of a block's columns, with
-// `resident` blocks on an SM: none where a block has one round only.
-int ring_stages(const RowShape& s, int64_t H, size_t size, int64_t arrays, int64_t resident, int64_t rounds) {
-  const size_t stage = static_cast<size_t>(std::min<int64_t>(H, s.tpr * COLS) * s.rows * arrays) * size;
+// Stages of a ring with `resident` blocks on an SM: none where a block has one
+// round only.
+int ring_stages(size_t stage, int64_t resident, int64_t rounds) {
   const int64_t fit = static_cast<int64_t>(SM_STAGE_BYTES / resident / stage);
   if (rounds < 2 || fit < 2) return 0;
   return static_cast<int>(std::min<int64_t>(std::min<int64_t>(fit, MAX_STAGES), rounds));
+}
+// Bytes of a stage: `arrays` times a round's rows of a block's columns.
+size_t stage_size(const RowShape& s, int64_t H, int rows, int64_t arrays, size_t size) {
+  return static_cast<size_t>(std::min<int64_t>(H, s.tpr * COLS) * s.rows * rows * arrays) * size;
 }
 
 bool vec_ok(moe_dtype dtype, int64_t H, std::initializer_list<const void*> ptrs) {
@@ -870,14 +929,25 @@ cudaError_t launch_join_t(moe_dtype dtype, JoinArgs a, int branch, int num_sms, 
   const bool element = a.gate_kind == MOE_GATE_ELEMENT;
   // The expert rows of one token at a time.
   if (branch == 2) s.rows = 1;
-  const int64_t groups = (a.T + s.rows - 1) / s.rows;
   // One wave: as many blocks as an SM's registers hold, each row after row.
   const int64_t resident = std::max(1, std::min(16, join_threads(sizeof(T), vec, branch, element) / (s.tpr * s.rows)));
-  const int64_t units = std::min<int64_t>(groups, std::max<int64_t>(1, resident * num_sms / s.cluster));
+  const int64_t most = std::max<int64_t>(1, resident * num_sms / s.cluster);
   const int64_t arrays = 1 + (branch == 2 ? a.top_k : branch) + (element ? 1 : 0);
-  const int stages = vec && (branch != 2 || a.top_k <= 32)
-                         ? ring_stages(s, a.H, sizeof(T), arrays, resident, (groups + units - 1) / units) : 0;
-  const size_t smem = static_cast<size_t>(std::min<int64_t>(a.H, s.tpr * COLS) * s.rows * arrays * stages) * sizeof(T);
+  auto rounds_of = [&](int rows, int64_t* units) {
+    const int64_t groups = (a.T + s.rows * rows - 1) / (s.rows * rows);
+    *units = std::min(groups, most);
+    return (groups + *units - 1) / *units;
+  };
+  int64_t units = 0;
+  int stages = 0;
+  size_t smem = 0;
+  if (vec && (branch != 2 || a.top_k <= 32) && rounds_of(1, &units) > 1) {
+    const int rows = join_rows(true, branch);
+    const size_t stage = stage_size(s, a.H, rows, arrays, sizeof(T));
+    stages = ring_stages(stage, resident, rounds_of(rows, &units));
+    smem = stage * stages;
+  }
+  if (stages == 0) rounds_of(1, &units);
   return launch_rows(stages > 0 ? pick_join<T, true, true>(branch, element)
                      : vec      ? pick_join<T, true, false>(branch, element)
                                 : pick_join<T, false, false>(branch, element),
@@ -892,23 +962,34 @@ auto pick_backward(bool has_f, bool next, bool element) {
   return element ? join_backward_kernel<T, VEC, BULK, true, false, true> : join_backward_kernel<T, VEC, BULK, true, false, false>;
 }
 
+// *units: the blocks (of clusters) that have left column sums.
 template <typename T>
-cudaError_t launch_join_backward_t(moe_dtype dtype, const JoinBackwardArgs& a, int64_t units, cudaStream_t stream) {
+cudaError_t launch_join_backward_t(moe_dtype dtype, const JoinBackwardArgs& a, int64_t* units, cudaStream_t stream) {
   const RowShape s = row_shape(a.H);
   const bool vec = vec_ok(dtype, a.H, {a.dout, a.dnormed, a.f, a.joined, a.norm_weight, a.next_weight, a.dbranch,
                                        a.dresidual, a.gate_kind == MOE_GATE_TOKEN ? nullptr : a.gate,
                                        a.gate_kind == MOE_GATE_ELEMENT ? a.dgate : nullptr});
   const bool f = a.f != nullptr, next = a.next_weight != nullptr, element = a.gate_kind == MOE_GATE_ELEMENT;
   const int64_t arrays = 1 + (f ? 1 : 0) + (next ? 2 : 0) + (element ? 1 : 0);
-  const int64_t groups = (a.T + s.rows - 1) / s.rows;
   const int64_t resident = std::max(1, MAX_TPR / (s.tpr * s.rows));
-  const int stages = vec ? ring_stages(s, a.H, sizeof(T), arrays, resident, (groups + units - 1) / units) : 0;
-  const size_t ring = static_cast<size_t>(std::min<int64_t>(a.H, s.tpr * COLS) * s.rows * arrays * stages) * sizeof(T);
-  const size_t fold = static_cast<size_t>(s.rows - 1) * s.tpr * COLS * sizeof(float);
+  const int64_t most = join_backward_units(a.T, a.H);
+  *units = most;
+  int stages = 0;
+  size_t smem = static_cast<size_t>(s.rows - 1) * s.tpr * COLS * sizeof(float);   // the fold in the end
+  if (vec && most * s.rows < a.T) {
+    const int rows = backward_rows(true);
+    const size_t stage = stage_size(s, a.H, rows, arrays, sizeof(T));
+    const int64_t groups = (a.T + s.rows * rows - 1) / (s.rows * rows);
+    stages = ring_stages(stage, resident, (groups + most - 1) / most);
+    if (stages > 0) {
+      *units = std::min(groups, most);
+      smem = std::max(smem, stage * stages);
+    }
+  }
   return launch_rows(stages > 0 ? pick_backward<T, true, true>(f, next, element)
                      : vec      ? pick_backward<T, true, false>(f, next, element)
                                 : pick_backward<T, false, false>(f, next, element),
-                     s, units, std::max(ring, fold), stages, a, stream);
+                     s, *units, smem, stages, a, stream);
 }
 
 }  // namespace
@@ -935,16 +1016,16 @@ cudaError_t launch_join(moe_dtype dtype, const JoinArgs& a, int branch, int num_
 
 cudaError_t launch_join_backward(moe_dtype dtype, const JoinBackwardArgs& a, float* dnorm_weight, float* dnext_weight,
                                  cudaStream_t stream) {
-  const int64_t units = join_backward_units(a.T, a.H);
+  int64_t units = 0;
   cudaError_t err = cudaSuccess;
   if (a.T > 0) {
     JoinBackwardArgs args = a;
     err = device_status_ptr(&args.status);
     if (err != cudaSuccess) return err;
     switch (dtype) {
-      case MOE_F32: err = launch_join_backward_t<float>(dtype, args, units, stream); break;
-      case MOE_F16: err = launch_join_backward_t<__half>(dtype, args, units, stream); break;
-      default: err = launch_join_backward_t<__nv_bfloat16>(dtype, args, units, stream); break;
+      case MOE_F32: err = launch_join_backward_t<float>(dtype, args, &units, stream); break;
+      case MOE_F16: err = launch_join_backward_t<__half>(dtype, args, &units, stream); break;
+      default: err = launch_join_backward_t<__nv_bfloat16>(dtype, args, &units, stream); break;
     }
     if (err != cudaSuccess) return err;
   }
