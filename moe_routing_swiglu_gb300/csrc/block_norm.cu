@@ -56,13 +56,14 @@ struct RowShape {
   int cluster;   // blocks of a row
 };
 
-RowShape row_shape(int64_t H) {
+// chunks: groups of COLS columns that a thread owns.
+RowShape row_shape(int64_t H, int chunks = 1) {
   RowShape s;
   s.cluster = 1;
   while (static_cast<int64_t>(s.cluster) * MAX_TPR * COLS < H) s.cluster *= 2;
   const int64_t per = (H + s.cluster - 1) / s.cluster;
-  s.tpr = static_cast<int>((per + COLS * 32 - 1) / (COLS * 32)) * 32;
-  s.rows = s.tpr >= BLOCK ? 1 : BLOCK / s.tpr;
+  s.tpr = static_cast<int>((per + chunks * COLS * 32 - 1) / (chunks * COLS * 32)) * 32;
+  s.rows = s.tpr >= BLOCK / chunks ? 1 : BLOCK / chunks / s.tpr;
   return s;
 }
 
@@ -73,6 +74,7 @@ RowShape row_shape(int64_t H) {
 template <bool VEC>
 struct Cols {
   int first, step, H;
+  __device__ Cols() {}
   __device__ Cols(int tid, int tpr, int rank, int H_) : H(H_) {
     first = rank * tpr * COLS + (VEC ? tid * COLS : tid);
     step = VEC ? 1 : tpr;
@@ -172,8 +174,8 @@ __device__ __forceinline__ void load_vector(const void* p, bool f32, const Cols<
 
 // ---------------------------------------------------------------- sums over a row
 
-// COUNT sums (N of each of R rows), for every thread of the rows. One barrier
-// per call: the two halves of `sm` are used in turn, and a half is written
+// COUNT sums (N of each of R rows), for every thread of the rows, in two parts
+// with one barrier between them: the two halves of `sm` are used in turn, and a half is written
 // again only after the barrier of the call between, which every reader of the
 // half has passed. In a warp the values, V of them (COUNT rounded up to a power
 // of two), are added by exchanging: a lane gives half of its values away until
@@ -208,27 +210,42 @@ __device__ __forceinline__ float exchange(const float* v) {
   }
 }
 
+// First part: the warp's sums, one per lane, and into `half` of sm.
 template <int COUNT>
-__device__ __forceinline__ void row_sum(float (&s)[COUNT], RowSums<COUNT>* sm, int& half, int tpr, int cluster, int rank) {
+__device__ __forceinline__ float post_sums(const float (&s)[COUNT], RowSums<COUNT>* sm, int half, int tpr, int cluster,
+                                           int rank) {
   constexpr int V = RowSums<COUNT>::V, LANES = 32 / V;   // lanes of a value
   const int lane = threadIdx.x & 31, which = lane / LANES, part = lane % LANES;
   float all[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) all[i] = i < COUNT ? s[i < COUNT ? i : 0] : 0.0f;
-  float mine = exchange<V, 16>(all);
+  const float mine = exchange<V, 16>(all);
   if (tpr > 32 || cluster > 1) {
-    const int warps = tpr >> 5, slot0 = static_cast<int>(threadIdx.y) * warps;
-    float* at = &sm->v[half][which][slot0];
-    half ^= 1;
+    const int warps = tpr >> 5;
+    float* at = &sm->v[half][which][threadIdx.y * warps];
     if (cluster == 1) {
       if (part == 0) at[threadIdx.x >> 5] = mine;
-      __syncthreads();
     } else {
-      cg::cluster_group cl = cg::this_cluster();
       for (int to = part; to < cluster; to += LANES)
-        *cl.map_shared_rank(at + rank * warps + (threadIdx.x >> 5), to) = mine;
-      cl.sync();
+        *cg::this_cluster().map_shared_rank(at + rank * warps + (threadIdx.x >> 5), to) = mine;
     }
+  }
+  return mine;
+}
+// The barrier between the two parts.
+__device__ __forceinline__ void sums_barrier(int cluster) {
+  if (cluster == 1) __syncthreads();
+  else cg::this_cluster().sync();
+}
+// Second part, with the first one's value: the row's sums.
+template <int COUNT>
+__device__ __forceinline__ void take_sums(float (&s)[COUNT], float mine, const RowSums<COUNT>* sm, int half, int tpr,
+                                          int cluster) {
+  constexpr int V = RowSums<COUNT>::V, LANES = 32 / V;
+  const int lane = threadIdx.x & 31, which = lane / LANES, part = lane % LANES;
+  if (tpr > 32 || cluster > 1) {
+    const int warps = tpr >> 5;
+    const float* at = &sm->v[half][which][threadIdx.y * warps];
     mine = 0.0f;
     for (int w = part; w < cluster * warps; w += LANES) mine += at[w];
 #pragma unroll
@@ -240,6 +257,13 @@ __device__ __forceinline__ void row_sum(float (&s)[COUNT], RowSums<COUNT>* sm, i
 #pragma unroll
     for (int i = 0; i < COUNT; ++i) s[i] = __shfl_sync(FULL_MASK, mine, i * LANES);
   }
+}
+template <int COUNT>
+__device__ __forceinline__ void row_sum(float (&s)[COUNT], RowSums<COUNT>* sm, int& half, int tpr, int cluster, int rank) {
+  const float mine = post_sums<COUNT>(s, sm, half, tpr, cluster, rank);
+  if (tpr > 32 || cluster > 1) sums_barrier(cluster);
+  take_sums<COUNT>(s, mine, sm, half, tpr, cluster);
+  half ^= 1;
 }
 
 __device__ __forceinline__ float weight_at(const void* p, int dtype, int64_t i) {
@@ -320,6 +344,7 @@ __device__ __forceinline__ void ring_end(Ring& ring, uint32_t issued, int stages
 template <typename T>
 __device__ __forceinline__ void copy_rows(uint8_t* dst, const T* src, uint32_t n, uint32_t row_bytes, int H, int cluster,
                                           uint64_t* bar) {
+  if (row_bytes == 0) return;
   if (cluster == 1) {
     bulk_load(dst, src, row_bytes * n, bar);
   } else {
@@ -327,17 +352,13 @@ __device__ __forceinline__ void copy_rows(uint8_t* dst, const T* src, uint32_t n
   }
 }
 
-// This thread's columns of a row in a stage.
+// This thread's columns of a row in a stage (a thread past the row's columns is
+// given any others: it adds and stores nothing).
 template <typename T>
-__device__ __forceinline__ void stage8(const uint8_t* mine, bool any, Eight<T>& v) {
-  if (any) {
+__device__ __forceinline__ void stage8(const uint8_t* mine, Eight<T>& v) {
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(v) / 16); ++i)
-      reinterpret_cast<uint4*>(&v)[i] = reinterpret_cast<const uint4*>(mine)[i];
-  } else {
-#pragma unroll
-    for (int j = 0; j < COLS; ++j) v.e[j] = from_f32<T>(0.0f);
-  }
+  for (int i = 0; i < static_cast<int>(sizeof(v) / 16); ++i)
+    reinterpret_cast<uint4*>(&v)[i] = reinterpret_cast<const uint4*>(mine)[i];
 }
 
 // ---------------------------------------------------------------- forward
@@ -382,7 +403,7 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
 
   // The ring: a stage holds x, then f or the expert rows, then the gates, each
   // of this block's columns.
-  const int cols = min(tpr * COLS, a.H - rank * tpr * COLS);
+  const int cols = max(min(tpr * COLS, a.H - rank * tpr * COLS), 0);
   const uint32_t row_bytes = cols * static_cast<uint32_t>(sizeof(T)), block_bytes = row_bytes * round_rows;
   const uint32_t stage_bytes = block_bytes * (1 + (BRANCH == 2 ? a.top_k : BRANCH) + (ELEMENT ? 1 : 0));
   // Combine: lane j's expert row of a token's first 32 slots.
@@ -407,7 +428,7 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
       const uint32_t found = __popc(__ballot_sync(FULL_MASK, good));
       if (lane == 0) mbar_arrive_expect_tx(bar, row_bytes * ((ELEMENT ? 2 : 1) + found));
       __syncwarp();
-      if (good)
+      if (good && cols > 0)
         bulk_load(dst + (1 + lane) * row_bytes,
                   static_cast<const T*>(a.f) + static_cast<int64_t>(ahead) * a.H + rank * tpr * COLS, row_bytes, bar);
     }
@@ -443,7 +464,7 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
   // row past the end as a row that is not stored. A round's scalars are loaded
   // a round ahead.
   Turn turn{0, 0u};
-  const uint8_t* mine = stage_smem + threadIdx.y * R * row_bytes + threadIdx.x * (COLS * static_cast<uint32_t>(sizeof(T)));
+  const uint8_t* mine = stage_smem + threadIdx.y * R * row_bytes + (c.any() ? threadIdx.x * (COLS * static_cast<uint32_t>(sizeof(T))) : 0u);
   const bool row_barrier = tpr > 32 || cluster > 1;
   uint32_t t = first_row + threadIdx.y * R;   // this thread's first row
   auto gate_of = [&](uint32_t row) { return token && row < rows ? token_gate<T>(a.gate, a.vec_f32, row) : 1.0f; };
@@ -475,15 +496,15 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (BULK) stage8<T>(stage + r * row_bytes, c.any(), raw);
+      if (BULK) stage8<T>(stage + r * row_bytes, raw);
       else load8<T, VEC>(static_cast<const T*>(a.x) + at, c, raw);
       unpack8(raw, x[r]);
       if (ELEMENT) {
-        if (BULK) stage8<T>(stage + stage_bytes - block_bytes + r * row_bytes, c.any(), gv[r]);
+        if (BULK) stage8<T>(stage + stage_bytes - block_bytes + r * row_bytes, gv[r]);
         else load8<T, VEC>(static_cast<const T*>(a.gate) + at, c, gv[r]);
       }
       if (BRANCH == 1) {
-        if (BULK) stage8<T>(stage + block_bytes + r * row_bytes, c.any(), raw);
+        if (BULK) stage8<T>(stage + block_bytes + r * row_bytes, raw);
         else load8<T, VEC>(static_cast<const T*>(a.f) + at, c, raw);
         unpack8(raw, f[r]);
       }
@@ -492,10 +513,22 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
       // Slot order, as moe_combine; a bad row number makes the token NaN.
 #pragma unroll
       for (int j = 0; j < COLS; ++j) f[0][j] = 0.0f;
-      bool bad = false;
+      bool bad = __any_sync(FULL_MASK, lane < a.top_k && slot >= a.rows);
+      if (BULK) {
+#pragma unroll 4
+        for (int k = 0; k < a.top_k; ++k) {
+          Eight<T> v;
+          float y[COLS];
+          const float w = __shfl_sync(FULL_MASK, weight, k);
+          stage8<T>(stage + (1 + k) * row_bytes, v);
+          unpack8(v, y);
+#pragma unroll
+          for (int j = 0; j < COLS; ++j) f[0][j] = fmaf(w, y[j], f[0][j]);
+        }
+      }
       constexpr int G = 4;   // rows whose loads are in flight together
       const int64_t slot0 = static_cast<int64_t>(min(t, rows - 1)) * a.top_k;
-      for (int first = 0; first < a.top_k; first += 32) {
+      for (int first = 0; !BULK && first < a.top_k; first += 32) {
         if (first > 0 && first + lane < a.top_k) {
           slot = a.inv[slot0 + first + lane];
           weight = weight_at(a.weights, a.weights_dtype, slot0 + first + lane);
@@ -513,8 +546,7 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
                 bad = true;
                 row = 0;
               }
-              if (BULK) stage8<T>(stage + (1 + k0 + i) * row_bytes, c.any(), v[i]);
-              else load8<T, VEC>(static_cast<const T*>(a.f) + static_cast<int64_t>(row) * a.H, c, v[i]);
+              load8<T, VEC>(static_cast<const T*>(a.f) + static_cast<int64_t>(row) * a.H, c, v[i]);
             }
           }
 #pragma unroll
@@ -595,24 +627,33 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
 // gates): dw1 = gate S, dgate = w1 S.
 //
 // Bound by HBM (join: dout, dy, out, f in, dx, df out). BULK as in the forward.
-constexpr int backward_rows(bool bulk) { return bulk ? 2 : 1; }
-
-template <typename T, bool VEC, bool BULK, bool HAS_F, bool NEXT, bool ELEMENT>
-__global__ void __launch_bounds__(MAX_TPR) join_backward_kernel(const JoinBackwardArgs a, int cluster, int stages) {
-  constexpr int R = backward_rows(BULK);
+// A round's work is in two halves, the sums and, a round later, the results, so
+// that one round's barrier and shuffles run beside another one's arithmetic. A
+// thread owns CHUNKS groups of 8 columns: with two of them a row has half the
+// shuffles, and two blocks of 256 threads share an SM for rows of 4096.
+template <typename T, bool VEC, int CHUNKS, bool BULK, bool HAS_F, bool NEXT, bool ELEMENT>
+__global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel(const JoinBackwardArgs a, int cluster,
+                                                                                 int stages) {
+  static_assert(BULK || CHUNKS == 1, "rows from memory: one group of columns");
   // Sums of a row: out^2, w2 dy out, f^2, dout G f, w2 dy G f, out G f (those that are needed).
   constexpr int N = HAS_F && NEXT ? 6 : 2;
   constexpr int AT_FF = HAS_F && NEXT ? 2 : 0, AT_DF = AT_FF + 1, AT_YF = 4, AT_OF = 5;
-  __shared__ RowSums<N * R> sums;
+  __shared__ RowSums<N> sums;
   __shared__ Ring ring;
   extern __shared__ __align__(128) uint8_t stage_smem[];   // the ring; in the end [rows of the block - 1][tpr * COLS] sums
   float* fold = reinterpret_cast<float*>(stage_smem);
   const int tpr = blockDim.x;
   const int rank = cluster > 1 ? static_cast<int>(blockIdx.x) % cluster : 0;
-  const uint32_t rows = static_cast<uint32_t>(a.T), round_rows = blockDim.y * R;
+  const uint32_t rows = static_cast<uint32_t>(a.T), round_rows = blockDim.y;
   const int64_t unit = blockIdx.x / cluster;
   const uint32_t step = gridDim.x / cluster * round_rows, first_row = static_cast<uint32_t>(unit) * round_rows;
-  const Cols<VEC> c(threadIdx.x, tpr, rank, a.H);
+  const int block_cols = tpr * COLS * CHUNKS;
+  Cols<VEC> c[CHUNKS];
+#pragma unroll
+  for (int k = 0; k < CHUNKS; ++k) {
+    c[k] = Cols<VEC>(threadIdx.x, tpr, 0, a.H);
+    c[k].first += rank * block_cols + k * tpr * COLS;
+  }
   const float inv_h = 1.0f / static_cast<float>(a.H);
   const bool post = HAS_F && a.norm_weight != nullptr;
   const bool token = HAS_F && a.gate_kind == MOE_GATE_TOKEN;
@@ -625,7 +666,7 @@ __global__ void __launch_bounds__(MAX_TPR) join_backward_kernel(const JoinBackwa
   launch_dependents();
 
   // A stage: dout, f, out and dy, the gates, of this block's columns.
-  const int cols = min(tpr * COLS, a.H - rank * tpr * COLS);
+  const int cols = max(min(block_cols, a.H - rank * block_cols), 0);   // a cluster's last block may have none
   const uint32_t row_bytes = cols * static_cast<uint32_t>(sizeof(T)), block_bytes = row_bytes * round_rows;
   constexpr int ARRAYS = 1 + (HAS_F ? 1 : 0) + (NEXT ? 2 : 0) + (ELEMENT ? 1 : 0);
   constexpr int AT_F = 1, AT_O = 1 + (HAS_F ? 1 : 0), AT_Y = AT_O + 1, AT_G = ARRAYS - 1;
@@ -636,17 +677,19 @@ __global__ void __launch_bounds__(MAX_TPR) join_backward_kernel(const JoinBackwa
     if (issue_t0 >= rows) return;
     uint8_t* dst = stage_smem + fill.slot * stage_bytes;
     uint64_t* bar = &ring.full[fill.slot];
-    const int64_t at = static_cast<int64_t>(issue_t0) * a.H + rank * tpr * COLS;
-    const uint32_t n = min(round_rows, rows - issue_t0);
+    const int64_t at = static_cast<int64_t>(issue_t0) * a.H + rank * block_cols;
+    const uint32_t bytes = row_bytes * min(round_rows, rows - issue_t0);   // a cluster's blocks have one row
     auto copy = [&](int array, const void* src) {
-      copy_rows<T>(dst + array * block_bytes, static_cast<const T*>(src) + at, n, row_bytes, a.H, cluster, bar);
+      bulk_load(dst + array * block_bytes, static_cast<const T*>(src) + at, bytes, bar);
     };
-    mbar_arrive_expect_tx(bar, row_bytes * n * (ARRAYS - (has_d ? 0 : 1)));
-    if (has_d) copy(0, a.dout);
-    if (HAS_F) copy(AT_F, a.f);
-    if (NEXT) copy(AT_O, a.joined);
-    if (NEXT) copy(AT_Y, a.dnormed);
-    if (ELEMENT) copy(AT_G, a.gate);
+    mbar_arrive_expect_tx(bar, bytes * (ARRAYS - (has_d ? 0 : 1)));
+    if (bytes > 0) {
+      if (has_d) copy(0, a.dout);
+      if (HAS_F) copy(AT_F, a.f);
+      if (NEXT) copy(AT_O, a.joined);
+      if (NEXT) copy(AT_Y, a.dnormed);
+      if (ELEMENT) copy(AT_G, a.gate);
+    }
     ++issued;
     fill.next(stages);
     issue_t0 += step;
@@ -655,146 +698,201 @@ __global__ void __launch_bounds__(MAX_TPR) join_backward_kernel(const JoinBackwa
   if (issuer)
     for (int i = 0; i < stages; ++i) issue();
 
-  float w1[COLS], w2[COLS];   // w1: with a channel's gate
-  float s1[COLS], s2[COLS];   // column sums S and dw2
+  float w1[CHUNKS][COLS], w2[CHUNKS][COLS];   // w1: with a channel's gate
+  float s1[CHUNKS][COLS], s2[CHUNKS][COLS];   // column sums S and dw2
 #pragma unroll
-  for (int j = 0; j < COLS; ++j) s1[j] = s2[j] = 0.0f;
-  if (HAS_F) {
-    load_vector<T, VEC>(a.norm_weight, a.vec_f32, c, w1);
-    if (channel) {
-      float g[COLS];
-      load_vector<T, VEC>(a.gate, a.vec_f32, c, g);
+  for (int k = 0; k < CHUNKS; ++k) {
 #pragma unroll
-      for (int j = 0; j < COLS; ++j) w1[j] *= g[j];
+    for (int j = 0; j < COLS; ++j) s1[k][j] = s2[k][j] = 0.0f;
+    if (HAS_F) {
+      load_vector<T, VEC>(a.norm_weight, a.vec_f32, c[k], w1[k]);
+      if (channel) {
+        float g[COLS];
+        load_vector<T, VEC>(a.gate, a.vec_f32, c[k], g);
+#pragma unroll
+        for (int j = 0; j < COLS; ++j) w1[k][j] *= g[j];
+      }
     }
+    if (NEXT) load_vector<T, VEC>(a.next_weight, a.vec_f32, c[k], w2[k]);
   }
-  if (NEXT) load_vector<T, VEC>(a.next_weight, a.vec_f32, c, w2);
 
-  Turn turn{0, 0u};
-  const uint8_t* mine = stage_smem + threadIdx.y * R * row_bytes + threadIdx.x * (COLS * static_cast<uint32_t>(sizeof(T)));
-  uint32_t t = first_row + threadIdx.y * R;   // this thread's first row
+  uint32_t mine[CHUNKS];   // this thread's columns in a stage
+#pragma unroll
+  for (int k = 0; k < CHUNKS; ++k)
+    mine[k] = threadIdx.y * row_bytes + (c[k].any() ? (k * tpr + threadIdx.x) * (COLS * static_cast<uint32_t>(sizeof(T))) : 0u);
   auto gate_of = [&](uint32_t row) { return token && row < rows ? token_gate<T>(a.gate, a.vec_f32, row) : 1.0f; };
-  float gate_next[R];
-#pragma unroll
-  for (int r = 0; r < R; ++r) gate_next[r] = gate_of(t + r);
-  for (uint32_t t0 = first_row; t0 < rows; t0 += step, t += step) {
-    float gt[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      gt[r] = gate_next[r];
-      gate_next[r] = gate_of(t + step + r);
-    }
-    const int64_t at = static_cast<int64_t>(min(t, rows - 1)) * a.H;
-    Eight<T> vd[R], vf[R], vo[R], vy[R], vg[R];
-    const uint8_t* stage = mine + turn.slot * stage_bytes;
+  struct Part {   // a thread's chunk of a row
+    Eight<T> d, f, o, y, g;
+  };
+  auto load_part = [&](uint32_t t, int k, int slot, Part& v) {
     if (BULK) {
-      ring_wait(ring, turn, a.status);
-      turn.next(stages);
-    }
-    float s[N * R];
-#pragma unroll
-    for (int i = 0; i < N * R; ++i) s[i] = 0.0f;
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (BULK) {
-        const uint8_t* row = stage + r * row_bytes;
-        stage8<T>(row, c.any() && has_d, vd[r]);
-        if (HAS_F) stage8<T>(row + AT_F * block_bytes, c.any(), vf[r]);
-        if (NEXT) stage8<T>(row + AT_O * block_bytes, c.any(), vo[r]);
-        if (NEXT) stage8<T>(row + AT_Y * block_bytes, c.any(), vy[r]);
-        if (ELEMENT) stage8<T>(row + AT_G * block_bytes, c.any(), vg[r]);
+      const uint8_t* row = stage_smem + slot * stage_bytes + mine[k];
+      if (has_d) {
+        stage8<T>(row, v.d);
       } else {
-        if (has_d) {
-          load8<T, VEC>(static_cast<const T*>(a.dout) + at, c, vd[r]);
-        } else {
 #pragma unroll
-          for (int j = 0; j < COLS; ++j) vd[r].e[j] = from_f32<T>(0.0f);
-        }
-        if (HAS_F) load8<T, VEC>(static_cast<const T*>(a.f) + at, c, vf[r]);
-        if (NEXT) load8<T, VEC>(static_cast<const T*>(a.joined) + at, c, vo[r]);
-        if (NEXT) load8<T, VEC>(static_cast<const T*>(a.dnormed) + at, c, vy[r]);
-        if (ELEMENT) load8<T, VEC>(static_cast<const T*>(a.gate) + at, c, vg[r]);
+        for (int j = 0; j < COLS; ++j) v.d.e[j] = from_f32<T>(0.0f);
       }
-      float d[COLS], f[COLS], o[COLS], y[COLS], g[COLS];
-      if (HAS_F) unpack8(vd[r], d);
-      if (HAS_F) unpack8(vf[r], f);
-      if (NEXT) unpack8(vo[r], o);
-      if (NEXT) unpack8(vy[r], y);
-      if (ELEMENT) unpack8(vg[r], g);
-      float* p = s + r * N;
+      if (HAS_F) stage8<T>(row + AT_F * block_bytes, v.f);
+      if (NEXT) stage8<T>(row + AT_O * block_bytes, v.o);
+      if (NEXT) stage8<T>(row + AT_Y * block_bytes, v.y);
+      if (ELEMENT) stage8<T>(row + AT_G * block_bytes, v.g);
+    } else {
+      const int64_t at = static_cast<int64_t>(min(t, rows - 1)) * a.H;
+      if (has_d) {
+        load8<T, VEC>(static_cast<const T*>(a.dout) + at, c[k], v.d);
+      } else {
 #pragma unroll
-      for (int j = 0; j < COLS; ++j) {
-        const float gf = HAS_F ? w1[j] * f[j] * (ELEMENT ? g[j] : 1.0f) : 0.0f;
-        if (NEXT) {
-          const float wy = w2[j] * y[j];
-          p[0] = fmaf(o[j], o[j], p[0]);
-          p[1] = fmaf(wy, o[j], p[1]);
-          if (HAS_F) {
-            p[AT_YF] = fmaf(wy, gf, p[AT_YF]);
-            p[AT_OF] = fmaf(o[j], gf, p[AT_OF]);
-          }
-        }
-        if (HAS_F) {
-          p[AT_FF] = fmaf(f[j], f[j], p[AT_FF]);
-          p[AT_DF] = fmaf(d[j], gf, p[AT_DF]);
-        }
+        for (int j = 0; j < COLS; ++j) v.d.e[j] = from_f32<T>(0.0f);
       }
+      if (HAS_F) load8<T, VEC>(static_cast<const T*>(a.f) + at, c[k], v.f);
+      if (NEXT) load8<T, VEC>(static_cast<const T*>(a.joined) + at, c[k], v.o);
+      if (NEXT) load8<T, VEC>(static_cast<const T*>(a.dnormed) + at, c[k], v.y);
+      if (ELEMENT) load8<T, VEC>(static_cast<const T*>(a.gate) + at, c[k], v.g);
     }
-    row_sum<N * R>(s, &sums, half, tpr, cluster, rank);
-    if (BULK) {   // the stage may be copied over
-      if (tpr == 32 && cluster == 1) __syncthreads();
-      if (issuer) issue();
-    }
+  };
+  auto add_up = [&](const Part& v, int k, float (&p)[N]) {
+    float d[COLS], f[COLS], o[COLS], y[COLS], g[COLS];
+    if (HAS_F) unpack8(v.d, d);
+    if (HAS_F) unpack8(v.f, f);
+    if (NEXT) unpack8(v.o, o);
+    if (NEXT) unpack8(v.y, y);
+    if (ELEMENT) unpack8(v.g, g);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const float* p = s + r * N;
-      const bool live = t + r < rows;
-      const int64_t to = at + r * static_cast<int64_t>(a.H);
-      const float r2 = NEXT ? rsqrtf(fmaf(p[0], inv_h, a.eps)) : 0.0f;
-      const float m2 = NEXT ? r2 * r2 * (p[1] * inv_h) : 0.0f;        // r2^2 S2 / H
-      const float r1 = post ? rsqrtf(fmaf(p[AT_FF], inv_h, a.eps)) : 1.0f;
-      const float q = HAS_F && NEXT ? p[AT_DF] + r2 * (p[AT_YF] - m2 * p[AT_OF]) : p[AT_DF];
-      const float m1 = post ? r1 * r1 * (q * inv_h) : 0.0f;           // r1^2 Q / H
-      const float b = a.beta * r1;
-      if (token && live && threadIdx.x == 0 && rank == 0) static_cast<float*>(a.dgate)[t + r] = b * q;
-      float d[COLS];
-      unpack8(vd[r], d);
+    for (int j = 0; j < COLS; ++j) {
+      const float gf = HAS_F ? w1[k][j] * f[j] * (ELEMENT ? g[j] : 1.0f) : 0.0f;
       if (NEXT) {
-        float o[COLS], y[COLS];
-        unpack8(vo[r], o);
-        unpack8(vy[r], y);
-#pragma unroll
-        for (int j = 0; j < COLS; ++j) {
-          d[j] = fmaf(r2, fmaf(-o[j], m2, w2[j] * y[j]), d[j]);       // dO
-          if (live) s2[j] = fmaf(y[j], o[j] * r2, s2[j]);
+        const float wy = w2[k][j] * y[j];
+        p[0] = fmaf(o[j], o[j], p[0]);
+        p[1] = fmaf(wy, o[j], p[1]);
+        if (HAS_F) {
+          p[AT_YF] = fmaf(wy, gf, p[AT_YF]);
+          p[AT_OF] = fmaf(o[j], gf, p[AT_OF]);
         }
       }
       if (HAS_F) {
-        float f[COLS], g[COLS];
-        unpack8(vf[r], f);
-        if (ELEMENT) unpack8(vg[r], g);
-        const float bm = b * m1;
-#pragma unroll
-        for (int j = 0; j < COLS; ++j) {
-          const float bd = b * d[j], bdf = bd * f[j];                 // beta r1 dO, and times f
-          f[j] = gt[r] * fmaf(ELEMENT ? w1[j] * g[j] : w1[j], bd, -f[j] * bm);
-          if (live) s1[j] = fmaf(bdf, ELEMENT ? g[j] * gt[r] : gt[r], s1[j]);
-          if (ELEMENT) g[j] = bdf * w1[j];
-        }
-        pack8<T>(f, vf[r]);
-        if (live) store8<T, VEC>(static_cast<T*>(a.dbranch) + to, c, vf[r]);
-        if (ELEMENT) {
-          pack8<T>(g, vg[r]);
-          if (live) store8<T, VEC>(static_cast<T*>(a.dgate) + to, c, vg[r]);
-        }
+        p[AT_FF] = fmaf(f[j], f[j], p[AT_FF]);
+        p[AT_DF] = fmaf(d[j], gf, p[AT_DF]);
       }
+    }
+  };
+  // A row's factors from its sums, and its results.
+  struct Factors {
+    float r2, m2, b, bm;
+  };
+  auto factors_of = [&](uint32_t t, const float (&p)[N], float gt) {
+    Factors x;
+    x.r2 = NEXT ? rsqrtf(fmaf(p[0], inv_h, a.eps)) : 0.0f;
+    x.m2 = NEXT ? x.r2 * x.r2 * (p[1] * inv_h) : 0.0f;              // r2^2 S2 / H
+    const float r1 = post ? rsqrtf(fmaf(p[AT_FF], inv_h, a.eps)) : 1.0f;
+    const float q = HAS_F && NEXT ? p[AT_DF] + x.r2 * (p[AT_YF] - x.m2 * p[AT_OF]) : p[AT_DF];
+    const float b = a.beta * r1;
+    x.b = b * gt;                                                   // beta r1 and a token's gate
+    x.bm = post ? x.b * (r1 * r1 * (q * inv_h)) : 0.0f;             // times r1^2 Q / H
+    if (token && t < rows && threadIdx.x == 0 && rank == 0) static_cast<float*>(a.dgate)[t] = b * q;
+    return x;
+  };
+  auto finish = [&](Part& v, uint32_t t, int k, const Factors& x) {
+    const int64_t to = static_cast<int64_t>(t) * a.H;
+    float d[COLS];
+    unpack8(v.d, d);
+    if (NEXT) {
+      float o[COLS], y[COLS];
+      unpack8(v.o, o);
+      unpack8(v.y, y);
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) {
+        d[j] = fmaf(x.r2, fmaf(-o[j], x.m2, w2[k][j] * y[j]), d[j]);   // dO
+        s2[k][j] = fmaf(y[j], o[j] * x.r2, s2[k][j]);
+      }
+    }
+    if (HAS_F) {
+      float f[COLS], g[COLS];
+      unpack8(v.f, f);
+      if (ELEMENT) unpack8(v.g, g);
+#pragma unroll
+      for (int j = 0; j < COLS; ++j) {
+        const float bd = x.b * d[j];
+        s1[k][j] = fmaf(ELEMENT ? bd * g[j] : bd, f[j], s1[k][j]);
+        const float dg = bd * f[j] * w1[k][j];
+        f[j] = fmaf(ELEMENT ? w1[k][j] * g[j] : w1[k][j], bd, -f[j] * x.bm);
+        if (ELEMENT) g[j] = dg;
+      }
+      pack8<T>(f, v.f);
+      store8<T, VEC>(static_cast<T*>(a.dbranch) + to, c[k], v.f);
+      if (ELEMENT) {
+        pack8<T>(g, v.g);
+        store8<T, VEC>(static_cast<T*>(a.dgate) + to, c[k], v.g);
+      }
+    }
+    if (a.alpha != 1.0f)
 #pragma unroll
       for (int j = 0; j < COLS; ++j) d[j] *= a.alpha;
-      pack8<T>(d, vd[r]);
-      if (live) store8<T, VEC>(static_cast<T*>(a.dresidual) + to, c, vd[r]);
+    pack8<T>(d, v.d);
+    store8<T, VEC>(static_cast<T*>(a.dresidual) + to, c[k], v.d);
+  };
+  if (BULK) {
+    Turn turn{0, 0u};   // of the sums; the results are one turn behind
+    uint32_t t = first_row + threadIdx.y;
+    float share = 0.0f, gate_next = gate_of(t);
+    bool behind = false;
+    for (uint32_t t0 = first_row; t0 < rows || behind; t0 += step, t += step) {
+      const bool ahead = t0 < rows;
+      const float share_before = share, gt = gate_next;
+      const int slot_before = turn.slot == 0 ? stages - 1 : turn.slot - 1;
+      if (ahead) {
+        ring_wait(ring, turn, a.status);
+        float p[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) p[i] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < CHUNKS; ++k) {
+          Part v;
+          load_part(t, k, turn.slot, v);
+          if (k > 0 && !c[k].any()) continue;   // (the first group is whole, or all of the thread is past the row)
+          add_up(v, k, p);
+        }
+        if (!c[0].any())
+#pragma unroll
+          for (int i = 0; i < N; ++i) p[i] = 0.0f;
+        share = post_sums<N>(p, &sums, half, tpr, cluster, rank);
+        turn.next(stages);
+      }
+      if (behind) {
+        float p[N];
+        take_sums<N>(p, share_before, &sums, half ^ 1, tpr, cluster);
+        gate_next = gate_of(t);
+        const Factors x = factors_of(t - step, p, gt);
+        if (t - step < rows) {
+#pragma unroll
+          for (int k = 0; k < CHUNKS; ++k) {
+            Part v;
+            load_part(t - step, k, slot_before, v);
+            finish(v, t - step, k, x);
+          }
+        }
+      }
+      sums_barrier(cluster);
+      if (behind && issuer) issue();   // the results' stage may be copied over
+      behind = ahead;
+      half ^= 1;
+    }
+    ring_end(ring, issued, stages, a.status);
+  } else {
+    uint32_t t = first_row + threadIdx.y;
+    for (uint32_t t0 = first_row; t0 < rows; t0 += step, t += step) {
+      Part v;
+      float p[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) p[i] = 0.0f;
+      const float gt = gate_of(t);
+      load_part(t, 0, 0, v);
+      add_up(v, 0, p);
+      row_sum<N>(p, &sums, half, tpr, cluster, rank);
+      const Factors x = factors_of(t, p, gt);
+      if (t < rows) finish(v, t, 0, x);
     }
   }
-  if (BULK) ring_end(ring, issued, stages, a.status);
   // The block's rows side by side are added in order, then stored, times the
   // vector that the array's column sums are short of.
   float* part = a.partial + unit * a.arrays * static_cast<int64_t>(a.H);
@@ -810,31 +908,35 @@ __global__ void __launch_bounds__(MAX_TPR) join_backward_kernel(const JoinBackwa
 #pragma unroll
         for (int j = 0; j < COLS; ++j) v[j] += fold[((y - 1) * COLS + j) * tpr + threadIdx.x];
   };
-  auto put = [&](const float (&v)[COLS], const void* times) {
-    if (threadIdx.y == 0) {
-      float m[COLS];
-      load_vector<T, VEC>(times, a.vec_f32, c, m);
-      if (VEC) {
-        if (c.any()) {
-          float4* p = reinterpret_cast<float4*>(part + c.first);
-          p[0] = make_float4(v[0] * m[0], v[1] * m[1], v[2] * m[2], v[3] * m[3]);
-          p[1] = make_float4(v[4] * m[4], v[5] * m[5], v[6] * m[6], v[7] * m[7]);
-        }
-      } else {
+  auto put = [&](const float (&v)[CHUNKS][COLS], const void* times) {
+    if (threadIdx.y == 0)
 #pragma unroll
-        for (int j = 0; j < COLS; ++j)
-          if (c.col(j) < c.H) part[c.col(j)] = v[j] * m[j];
+      for (int k = 0; k < CHUNKS; ++k) {
+        float m[COLS];
+        load_vector<T, VEC>(times, a.vec_f32, c[k], m);
+        if (VEC) {
+          if (c[k].any()) {
+            float4* p = reinterpret_cast<float4*>(part + c[k].first);
+            p[0] = make_float4(v[k][0] * m[0], v[k][1] * m[1], v[k][2] * m[2], v[k][3] * m[3]);
+            p[1] = make_float4(v[k][4] * m[4], v[k][5] * m[5], v[k][6] * m[6], v[k][7] * m[7]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < COLS; ++j)
+            if (c[k].col(j) < c[k].H) part[c[k].col(j)] = v[k][j] * m[j];
+        }
       }
-    }
     part += a.H;
   };
   if (HAS_F && (post || channel)) {
-    fold_rows(s1);
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k) fold_rows(s1[k]);
     if (post) put(s1, channel ? a.gate : nullptr);
     if (channel) put(s1, a.norm_weight);
   }
   if (NEXT) {
-    fold_rows(s2);
+#pragma unroll
+    for (int k = 0; k < CHUNKS; ++k) fold_rows(s2[k]);
     put(s2, nullptr);
   }
 }
@@ -870,7 +972,8 @@ __global__ void __launch_bounds__(BLOCK) column_sum_kernel(const float* partial,
 
 // ---------------------------------------------------------------- launches
 
-constexpr size_t SM_STAGE_BYTES = 180 * 1024;   // of an SM's shared memory, for the rings
+// Shared memory of an SM, of which every block takes 1 KB and its static part.
+constexpr size_t SM_SHARED = 228 * 1024, BLOCK_SHARED = 227 * 1024;
 
 template <typename K, typename A>
 cudaError_t launch_rows(K kernel, const RowShape& s, int64_t units, size_t smem, int stages, const A& args,
@@ -895,11 +998,11 @@ cudaError_t launch_rows(K kernel, const RowShape& s, int64_t units, size_t smem,
   return cudaLaunchKernelEx(&cfg, kernel, args, s.cluster, stages);
 }
 
-// Stages of a ring with `resident` blocks on an SM: none where a block has one
-// round only.
-int ring_stages(size_t stage, int64_t resident, int64_t rounds) {
-  const int64_t fit = static_cast<int64_t>(SM_STAGE_BYTES / resident / stage);
-  if (rounds < 2 || fit < 2) return 0;
+// Stages of a ring of `rounds` rounds with `resident` blocks on an SM, each with
+// `fixed` bytes of static shared memory.
+int ring_stages(size_t stage, int64_t resident, size_t fixed, int64_t rounds) {
+  const size_t block = std::min(SM_SHARED / static_cast<size_t>(resident) - 1024, BLOCK_SHARED);
+  const int64_t fit = block > fixed ? static_cast<int64_t>((block - fixed) / stage) : 0;
   return static_cast<int>(std::min<int64_t>(std::min<int64_t>(fit, MAX_STAGES), rounds));
 }
 // Bytes of a stage: `arrays` times a round's rows of a block's columns.
@@ -944,7 +1047,8 @@ cudaError_t launch_join_t(moe_dtype dtype, JoinArgs a, int branch, int num_sms, 
   if (vec && (branch != 2 || a.top_k <= 32) && rounds_of(1, &units) > 1) {
     const int rows = join_rows(true, branch);
     const size_t stage = stage_size(s, a.H, rows, arrays, sizeof(T));
-    stages = ring_stages(stage, resident, rounds_of(rows, &units));
+    stages = ring_stages(stage, resident, sizeof(RowSums<2>) + sizeof(Ring) + 256, rounds_of(rows, &units));
+    if (stages < 2) stages = 0;
     smem = stage * stages;
   }
   if (stages == 0) rounds_of(1, &units);
@@ -954,52 +1058,71 @@ cudaError_t launch_join_t(moe_dtype dtype, JoinArgs a, int branch, int num_sms, 
                      s, units, smem, stages, a, stream);
 }
 
-template <typename T, bool VEC, bool BULK>
+template <typename T, bool VEC, int CHUNKS, bool BULK>
 auto pick_backward(bool has_f, bool next, bool element) {
-  if (!has_f) return join_backward_kernel<T, VEC, BULK, false, true, false>;
+  if (!has_f) return join_backward_kernel<T, VEC, CHUNKS, BULK, false, true, false>;
   if (next)
-    return element ? join_backward_kernel<T, VEC, BULK, true, true, true> : join_backward_kernel<T, VEC, BULK, true, true, false>;
-  return element ? join_backward_kernel<T, VEC, BULK, true, false, true> : join_backward_kernel<T, VEC, BULK, true, false, false>;
+    return element ? join_backward_kernel<T, VEC, CHUNKS, BULK, true, true, true>
+                   : join_backward_kernel<T, VEC, CHUNKS, BULK, true, true, false>;
+  return element ? join_backward_kernel<T, VEC, CHUNKS, BULK, true, false, true>
+                 : join_backward_kernel<T, VEC, CHUNKS, BULK, true, false, false>;
+}
+
+// Rows that share a block pay for two groups of columns a thread with idle
+// lanes: from 1024 columns on.
+int backward_chunks(int64_t H) { return H >= 1024 ? 2 : 1; }
+// One wave of blocks that keep their column sums in registers: 512 threads of
+// them fill an SM (of JOIN_BACKWARD_SMS).
+int backward_resident(const RowShape& s) { return std::max(1, MAX_TPR / (s.tpr * s.rows)); }
+int64_t backward_units(const RowShape& s, int64_t T, int64_t resident) {
+  const int64_t groups = (T + s.rows - 1) / s.rows;
+  return std::min<int64_t>(groups, std::max<int64_t>(1, JOIN_BACKWARD_SMS * resident / s.cluster));
 }
 
 // *units: the blocks (of clusters) that have left column sums.
 template <typename T>
 cudaError_t launch_join_backward_t(moe_dtype dtype, const JoinBackwardArgs& a, int64_t* units, cudaStream_t stream) {
-  const RowShape s = row_shape(a.H);
   const bool vec = vec_ok(dtype, a.H, {a.dout, a.dnormed, a.f, a.joined, a.norm_weight, a.next_weight, a.dbranch,
                                        a.dresidual, a.gate_kind == MOE_GATE_TOKEN ? nullptr : a.gate,
                                        a.gate_kind == MOE_GATE_ELEMENT ? a.dgate : nullptr});
   const bool f = a.f != nullptr, next = a.next_weight != nullptr, element = a.gate_kind == MOE_GATE_ELEMENT;
   const int64_t arrays = 1 + (f ? 1 : 0) + (next ? 2 : 0) + (element ? 1 : 0);
-  const int64_t resident = std::max(1, MAX_TPR / (s.tpr * s.rows));
-  const int64_t most = join_backward_units(a.T, a.H);
-  *units = most;
+  const int chunks = backward_chunks(a.H);
+  RowShape s = row_shape(a.H, chunks);
   int stages = 0;
-  size_t smem = static_cast<size_t>(s.rows - 1) * s.tpr * COLS * sizeof(float);   // the fold in the end
-  if (vec && most * s.rows < a.T) {
-    const int rows = backward_rows(true);
-    const size_t stage = stage_size(s, a.H, rows, arrays, sizeof(T));
-    const int64_t groups = (a.T + s.rows * rows - 1) / (s.rows * rows);
-    stages = ring_stages(stage, resident, (groups + most - 1) / most);
-    if (stages > 0) {
-      *units = std::min(groups, most);
-      smem = std::max(smem, stage * stages);
+  size_t smem = 0;
+  if (vec) {
+    // Three stages hold the rounds at work and one on its way; rather fewer blocks than fewer stages.
+    const size_t stage = static_cast<size_t>(std::min<int64_t>(a.H, s.tpr * COLS * chunks) * s.rows * arrays) * sizeof(T);
+    const size_t fixed = sizeof(RowSums<6>) + sizeof(Ring) + 256;
+    const int64_t groups = (a.T + s.rows - 1) / s.rows;
+    for (int64_t resident = backward_resident(s); resident > 0; resident /= 2) {
+      *units = backward_units(s, a.T, resident);
+      const int64_t rounds = (groups + *units - 1) / *units;
+      stages = rounds < 2 ? 0 : ring_stages(stage, resident, fixed, rounds);
+      if (rounds < 2 || stages >= std::min<int64_t>(rounds, 3)) break;
     }
+    if (stages < 2) stages = 0;
+    smem = stage * stages;
   }
-  return launch_rows(stages > 0 ? pick_backward<T, true, true>(f, next, element)
-                     : vec      ? pick_backward<T, true, false>(f, next, element)
-                                : pick_backward<T, false, false>(f, next, element),
+  if (stages == 0) {
+    s = row_shape(a.H);
+    *units = backward_units(s, a.T, backward_resident(s));
+  }
+  smem = std::max(smem, static_cast<size_t>(s.rows - 1) * s.tpr * COLS * sizeof(float));   // the fold in the end
+  return launch_rows(stages > 0 ? (chunks == 2 ? pick_backward<T, true, 2, true>(f, next, element)
+                                               : pick_backward<T, true, 1, true>(f, next, element))
+                     : vec ? pick_backward<T, true, 1, false>(f, next, element)
+                           : pick_backward<T, false, 1, false>(f, next, element),
                      s, *units, smem, stages, a, stream);
 }
 
 }  // namespace
 
-// One wave: a unit keeps its column sums in registers, 512 threads of them
-// fill an SM (of JOIN_BACKWARD_SMS).
+// An upper bound of the units of a backward, whatever its alignment.
 int64_t join_backward_units(int64_t T, int64_t H) {
-  const RowShape s = row_shape(H);
-  const int64_t groups = (T + s.rows - 1) / s.rows;
-  return std::min<int64_t>(groups, std::max<int64_t>(1, JOIN_BACKWARD_SMS * MAX_TPR / (s.tpr * s.rows * s.cluster)));
+  const RowShape one = row_shape(H), more = row_shape(H, backward_chunks(H));
+  return std::max(backward_units(one, T, backward_resident(one)), backward_units(more, T, backward_resident(more)));
 }
 
 cudaError_t launch_join(moe_dtype dtype, const JoinArgs& a, int branch, int num_sms, cudaStream_t stream) {
