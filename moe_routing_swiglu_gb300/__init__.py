@@ -1108,46 +1108,50 @@ def _rows_of(x: torch.Tensor, name: str) -> tuple[int, int]:
 def _like(t, x: torch.Tensor, name: str, stream) -> torch.Tensor:
     """A row tensor of the call: `t` checked against x, or a new one."""
     if t is None:
-        return _empty(x.shape, x.dtype, x.device, stream)
-    _dev_tensor(t, name)
+        return torch.empty_like(x) if stream is None else _empty(x.shape, x.dtype, x.device, stream)
     if t.dtype != x.dtype or t.shape != x.shape:
         raise MoeError(2, f"{name} must be {tuple(x.shape)} in {x.dtype}")
-    return t
+    return _dev_tensor(t, name)
 
 
 def _vector(t: torch.Tensor, name: str, x: torch.Tensor) -> torch.Tensor:
-    _dev_tensor(t, name)
     if t.shape != x.shape[-1:]:
         raise MoeError(2, f"{name} must hold one value per column")
-    return t
+    return _dev_tensor(t, name)
 
 
 def _join_params(x, norm_weight, gate, next_weight, residual_scale, branch_scale, eps) -> BlockJoinParams:
     """The params of a join of rows like x, its tensors checked against them."""
-    kind, vectors = _GATE_NONE, []
+    kind, vec = _GATE_NONE, None
+    shape, dtype = x.shape, x.dtype
+    vectors = []
     if norm_weight is not None:
-        vectors.append(_vector(norm_weight, "norm_weight", x).dtype)
+        vectors.append(_vector(norm_weight, "norm_weight", x))
     if next_weight is not None:
-        vectors.append(_vector(next_weight, "next_weight", x).dtype)
+        vectors.append(_vector(next_weight, "next_weight", x))
     if gate is not None:
         _dev_tensor(gate, "gate")
-        if gate.shape == x.shape[-1:]:
+        g = gate.shape
+        if g == shape[-1:]:
             kind = _GATE_CHANNEL
-        elif gate.shape == x.shape and (x.shape[-1] != 1 or gate.dtype == x.dtype):
+        elif g == shape and (shape[-1] != 1 or gate.dtype == dtype):
             kind = _GATE_ELEMENT
-            if gate.dtype != x.dtype:
+            if gate.dtype != dtype:
                 raise MoeError(3, "a gate for every element must have the rows' dtype")
-        elif gate.shape == (*x.shape[:-1], 1):
+        elif g == (*shape[:-1], 1):
             kind = _GATE_TOKEN
         else:
-            raise MoeError(2, f"gate must be [H], [.., 1] or [.., H] for rows {tuple(x.shape)}")
+            raise MoeError(2, f"gate must be [H], [.., 1] or [.., H] for rows {tuple(shape)}")
         if kind != _GATE_ELEMENT:
-            vectors.append(gate.dtype)
-    for d in vectors:
-        if d != vectors[0] or (d != torch.float32 and d != x.dtype):
+            vectors.append(gate)
+    for v in vectors:
+        d = v.dtype
+        if vec is None and (d == torch.float32 or d == dtype):
+            vec = d
+        if d != vec:
             raise MoeError(3, "norm_weight, next_weight and a channel or token gate share one dtype: float32 or the rows'")
     return BlockJoinParams(_addr(norm_weight), _addr(next_weight), _addr(gate), kind,
-                           _DTYPE[vectors[0]] if vectors else MOE_F32, residual_scale, branch_scale, eps)
+                           MOE_F32 if vec is None else _DTYPE[vec], residual_scale, branch_scale, eps)
 
 
 def moe_block_norm(x: torch.Tensor, weight: torch.Tensor, *, eps: float = 1e-6, out=None, stream=None) -> torch.Tensor:

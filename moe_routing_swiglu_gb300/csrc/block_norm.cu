@@ -1051,7 +1051,12 @@ cudaError_t launch_join_t(moe_dtype dtype, JoinArgs a, int branch, int num_sms, 
     if (stages < 2) stages = 0;
     smem = stage * stages;
   }
-  if (stages == 0) rounds_of(1, &units);
+  if (stages == 0) {
+    rounds_of(1, &units);
+  } else {   // the only waits that may report
+    const cudaError_t err = device_status_ptr(&a.status);
+    if (err != cudaSuccess) return err;
+  }
   return launch_rows(stages > 0 ? pick_join<T, true, true>(branch, element)
                      : vec      ? pick_join<T, true, false>(branch, element)
                                 : pick_join<T, false, false>(branch, element),
@@ -1081,7 +1086,7 @@ int64_t backward_units(const RowShape& s, int64_t T, int64_t resident) {
 
 // *units: the blocks (of clusters) that have left column sums.
 template <typename T>
-cudaError_t launch_join_backward_t(moe_dtype dtype, const JoinBackwardArgs& a, int64_t* units, cudaStream_t stream) {
+cudaError_t launch_join_backward_t(moe_dtype dtype, JoinBackwardArgs a, int64_t* units, cudaStream_t stream) {
   const bool vec = vec_ok(dtype, a.H, {a.dout, a.dnormed, a.f, a.joined, a.norm_weight, a.next_weight, a.dbranch,
                                        a.dresidual, a.gate_kind == MOE_GATE_TOKEN ? nullptr : a.gate,
                                        a.gate_kind == MOE_GATE_ELEMENT ? a.dgate : nullptr});
@@ -1108,6 +1113,9 @@ cudaError_t launch_join_backward_t(moe_dtype dtype, const JoinBackwardArgs& a, i
   if (stages == 0) {
     s = row_shape(a.H);
     *units = backward_units(s, a.T, backward_resident(s));
+  } else {   // the only waits that may report
+    const cudaError_t err = device_status_ptr(&a.status);
+    if (err != cudaSuccess) return err;
   }
   smem = std::max(smem, static_cast<size_t>(s.rows - 1) * s.tpr * COLS * sizeof(float));   // the fold in the end
   return launch_rows(stages > 0 ? (chunks == 2 ? pick_backward<T, true, 2, true>(f, next, element)
@@ -1127,13 +1135,10 @@ int64_t join_backward_units(int64_t T, int64_t H) {
 
 cudaError_t launch_join(moe_dtype dtype, const JoinArgs& a, int branch, int num_sms, cudaStream_t stream) {
   if (a.T == 0) return cudaSuccess;
-  JoinArgs args = a;
-  const cudaError_t err = device_status_ptr(&args.status);
-  if (err != cudaSuccess) return err;
   switch (dtype) {
-    case MOE_F32: return launch_join_t<float>(dtype, args, branch, num_sms, stream);
-    case MOE_F16: return launch_join_t<__half>(dtype, args, branch, num_sms, stream);
-    default: return launch_join_t<__nv_bfloat16>(dtype, args, branch, num_sms, stream);
+    case MOE_F32: return launch_join_t<float>(dtype, a, branch, num_sms, stream);
+    case MOE_F16: return launch_join_t<__half>(dtype, a, branch, num_sms, stream);
+    default: return launch_join_t<__nv_bfloat16>(dtype, a, branch, num_sms, stream);
   }
 }
 
@@ -1142,13 +1147,10 @@ cudaError_t launch_join_backward(moe_dtype dtype, const JoinBackwardArgs& a, flo
   int64_t units = 0;
   cudaError_t err = cudaSuccess;
   if (a.T > 0) {
-    JoinBackwardArgs args = a;
-    err = device_status_ptr(&args.status);
-    if (err != cudaSuccess) return err;
     switch (dtype) {
-      case MOE_F32: err = launch_join_backward_t<float>(dtype, args, &units, stream); break;
-      case MOE_F16: err = launch_join_backward_t<__half>(dtype, args, &units, stream); break;
-      default: err = launch_join_backward_t<__nv_bfloat16>(dtype, args, &units, stream); break;
+      case MOE_F32: err = launch_join_backward_t<float>(dtype, a, &units, stream); break;
+      case MOE_F16: err = launch_join_backward_t<__half>(dtype, a, &units, stream); break;
+      default: err = launch_join_backward_t<__nv_bfloat16>(dtype, a, &units, stream); break;
     }
     if (err != cudaSuccess) return err;
   }
