@@ -323,7 +323,7 @@ constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
 constexpr int STAGING_BYTES = 32 * 32 * 4;           // per epilogue warp: 32 x 32 FP32, or FP16 hi and lo
 constexpr int SMEM_STAGING = STAGES * STAGE_BYTES;
 constexpr int SMEM_BAR = SMEM_STAGING + NUM_EPI_WARPS * STAGING_BYTES;
-constexpr int NUM_BARS = 2 * STAGES + 6;
+constexpr int NUM_BARS = 2 * STAGES + 5;
 constexpr int SMEM_MISC = SMEM_BAR + 8 * NUM_BARS;   // TMEM address, abort flag, stages issued
 constexpr int SMEM_BYTES = 1024 + SMEM_MISC + 16;
 static_assert(SMEM_BYTES <= 227 * 1024, "shared memory budget");
@@ -334,7 +334,6 @@ constexpr uint32_t ST_MMA_TMEM_EMPTY = 0x43;
 constexpr uint32_t ST_EPI_TMEM_FULL = 0x44;
 constexpr uint32_t ST_MMA_DRAIN = 0x45;
 constexpr uint32_t ST_PRODUCER_DRAIN = 0x46;
-constexpr uint32_t ST_CHAIN_STORED = 0x47;
 
 // A block pair's instructions (cta_group::2): block 0 of the pair issues one
 // MMA for both, each block holding 128 rows of P, half of Q's columns and 128
@@ -611,35 +610,6 @@ __device__ __forceinline__ void store_result(const NsArgs& a, float* tile, int r
   }
 }
 
-// The end of a pair's kernel, by all threads of both blocks.
-__device__ __forceinline__ void pair_teardown(uint64_t* full, uint64_t* drain, volatile int* abort_flag,
-                                              uint32_t* issued_stages, uint32_t rank, uint32_t tmem_base,
-                                              uint32_t* status) {
-  tc_fence_before();
-  __syncthreads();
-  // Every MMA has read its operands, and every commit has arrived, before either block leaves.
-  if (threadIdx.x == 0) mbar_wait_bounded(drain, 0, nullptr, status, ST_MMA_DRAIN, WAIT_LIMIT_NS);
-  __syncwarp();
-  cluster_sync();
-  if (*abort_flag != 0 || peer_load(peer_u32(const_cast<int*>(abort_flag), rank ^ 1u)) != 0) {
-    // A role gave up: the copies that nobody waited for land before the blocks
-    // exit. A stage that one block alone has issued is armed here for the other.
-    if (threadIdx.x == 0 && rank == 0) {
-      const uint32_t mine = *issued_stages, other = peer_load(peer_u32(issued_stages, 1));
-      for (uint32_t n = min(mine, other); n < max(mine, other); ++n) mbar_arrive(&full[n % STAGES]);
-      drain_ring(max(mine, other), STAGES, [&](uint32_t slot, uint32_t parity) {
-        mbar_wait_bounded(&full[slot], parity, nullptr, status, ST_PRODUCER_DRAIN, WAIT_LIMIT_NS);
-      });
-    }
-    __syncthreads();
-  }
-  cluster_sync();   // nothing is left that reads or signals the other block's shared memory
-  if (threadIdx.x >> 5 == 1) {
-    tc_fence_after();
-    pair_tmem_dealloc(tmem_base, TMEM_COLS);
-  }
-}
-
 // SINGLE: the product of the hi parts alone.
 template <int MODE, bool P_MN, bool Q_MN, bool SINGLE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
@@ -851,209 +821,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     }
   }
 
-  pair_teardown(full, drain, abort_flag, issued_stages, rank, tmem_base, args.status);
-}
-
-// ---------------------------------------------------------------- two steps' s x s products in one launch
-
-// For matrices of one tile (s <= 256) that leave a launch short: the products
-// of a two-step group after A = X X^T, one after another by the pair that has
-// the matrix, each reading what the one before has stored.
-//   B = poly(A), T = B A, A = T B (X' X'^T), B1 = poly(A), T = B1 B
-// `stored` (in both blocks) counts the epilogue warps whose results are in
-// memory; the producers wait for all of a product's before the next one's loads.
-constexpr int CHAIN_STEPS = 5;
-struct ChainMaps {
-  CUtensorMap m[4][2];   // A, B, T, B1: hi and lo
-};
-struct ChainArgs {
-  Pair matrix[4];
-  int s;
-  uint32_t matrices;
-  float poly_scale, a_scale, diag, scale[CHAIN_STEPS];
-  uint32_t* status;
-};
-__device__ constexpr uint8_t CHAIN_P[CHAIN_STEPS] = {0, 1, 2, 0, 3}, CHAIN_Q[CHAIN_STEPS] = {0, 0, 1, 0, 1},
-                             CHAIN_OUT[CHAIN_STEPS] = {1, 2, 0, 3, 2};
-
-__device__ __forceinline__ void peer_arrive_release(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// After a wait that has seen a cluster's arrivals: what they have released.
-__device__ __forceinline__ void acquire_stored() {
-  asm volatile("fence.acq_rel.cluster;\n\tfence.proxy.async.global;" ::: "memory");
-}
-
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
-    chain_kernel(const __grid_constant__ ChainMaps maps, const __grid_constant__ ChainArgs args) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + SMEM_BAR);
-  uint64_t* empty = full + STAGES;
-  uint64_t* tfull = empty + STAGES;   // [2]
-  uint64_t* tempty = tfull + 2;       // [2]
-  uint64_t* drain = tempty + 2;
-  uint64_t* stored = drain + 1;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + SMEM_MISC);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + SMEM_MISC + 4);
-  uint32_t* issued_stages = reinterpret_cast<uint32_t*>(smem + SMEM_MISC + 8);
-  const int warp = threadIdx.x >> 5;
-  const int lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const uint32_t pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
-
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
-      mbar_init(&full[s], 2);
-      mbar_init(&empty[s], 1);
-    }
-    for (int a = 0; a < 2; ++a) {
-      mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 2 * NUM_EPI_WARPS);
-    }
-    mbar_init(drain, 1);
-    mbar_init(stored, 2 * NUM_EPI_WARPS);
-    *abort_flag = 0;
-    *issued_stages = 0;
-    fence_mbarrier_init();
-    fence_proxy_async_smem();
-    for (int i = 0; i < 8; ++i) tma_prefetch_desc(&maps.m[i / 2][i % 2]);
-  }
-  __syncwarp();
-  if (warp == 1) pair_tmem_alloc(tmem_holder, TMEM_COLS);
   tc_fence_before();
   __syncthreads();
+  // Every MMA has read its operands, and every commit has arrived, before either block leaves.
+  if (threadIdx.x == 0) mbar_wait_bounded(drain, 0, nullptr, args.status, ST_MMA_DRAIN, WAIT_LIMIT_NS);
+  __syncwarp();
   cluster_sync();
-  tc_fence_after();
-  const uint32_t tmem_base = *tmem_holder;
-  grid_dependency_wait();
-  launch_dependents();
-  const int n_len = (args.s + 31) & ~31;   // columns of a tile, of which each block brings half
-  const int k_blocks = (args.s + BK - 1) / BK;
-
-  if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, issued = 0, n = 0;
-      bool ok = true;
-      const int m0 = static_cast<int>(rank) * BM, n0 = static_cast<int>(rank) * (n_len / 2);
-      for (uint32_t e = pair; ok && e < args.matrices; e += pairs) {
-        for (int step = 0; ok && step < CHAIN_STEPS; ++step, ++n) {
-          if (n > 0) {   // every product: the barrier's phases are told apart by their parity alone
-            ok = mbar_wait_bounded(stored, (n - 1) & 1u, abort_flag, args.status, ST_CHAIN_STORED, WAIT_LIMIT_NS);
-            if (!ok) break;
-            acquire_stored();
-          }
-          const CUtensorMap* p = maps.m[CHAIN_P[step]];
-          const CUtensorMap* q = maps.m[CHAIN_Q[step]];
-          for (int kb = 0; kb < k_blocks; ++kb) {
-            ok = mbar_wait_bounded(&empty[stage], phase ^ 1u, abort_flag, args.status, ST_PRODUCER_EMPTY, WAIT_LIMIT_NS);
-            if (!ok) break;
-            uint8_t* st = smem + stage * STAGE_BYTES;
-            const uint32_t bar = peer_u32(&full[stage], 0);
-            peer_arrive_expect_tx(bar, STAGE_BYTES);
-            pair_load_3d(st, &p[0], bar, kb * BK, m0, static_cast<int>(e));
-            pair_load_3d(st + 2 * OP_BYTES, &q[0], bar, kb * BK, n0, static_cast<int>(e));
-            pair_load_3d(st + OP_BYTES, &p[1], bar, kb * BK, m0, static_cast<int>(e));
-            pair_load_3d(st + 3 * OP_BYTES, &q[1], bar, kb * BK, n0, static_cast<int>(e));
-            ++issued;
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1u;
-            }
-          }
-        }
-      }
-      *issued_stages = issued;
+  if (*abort_flag != 0 || peer_load(peer_u32(const_cast<int*>(abort_flag), rank ^ 1u)) != 0) {
+    // A role gave up: the copies that nobody waited for land before the blocks
+    // exit. A stage that one block alone has issued is armed here for the other.
+    if (threadIdx.x == 0 && rank == 0) {
+      const uint32_t mine = *issued_stages, other = peer_load(peer_u32(issued_stages, 1));
+      for (uint32_t n = min(mine, other); n < max(mine, other); ++n) mbar_arrive(&full[n % STAGES]);
+      drain_ring(max(mine, other), STAGES, [&](uint32_t slot, uint32_t parity) {
+        mbar_wait_bounded(&full[slot], parity, nullptr, args.status, ST_PRODUCER_DRAIN, WAIT_LIMIT_NS);
+      });
     }
-    __syncwarp();
-  } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
-      int stage = 0;
-      uint32_t phase = 0, n = 0;
-      bool ok = true;
-      const uint32_t idesc = idesc_f16_major(false, TILE, n_len, false, false);
-      for (uint32_t e = pair; ok && e < args.matrices; e += pairs) {
-        for (int step = 0; ok && step < CHAIN_STEPS; ++step, ++n) {
-          const uint32_t acc = n & 1u;
-          ok = mbar_wait_bounded(&tempty[acc], ((n >> 1) & 1u) ^ 1u, abort_flag, args.status, ST_MMA_TMEM_EMPTY,
-                                 WAIT_LIMIT_NS);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t d = tmem_base + acc * TILE;
-          for (int kb = 0; kb < k_blocks; ++kb) {
-            ok = mbar_wait_bounded(&full[stage], phase, abort_flag, args.status, ST_MMA_FULL, WAIT_LIMIT_NS);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t ph = smem_u32(smem + stage * STAGE_BYTES);
-            const int n_sub = min(BK / UMMA_K, (args.s - kb * BK + UMMA_K - 1) / UMMA_K);
-            for (int k = 0; k < n_sub; ++k) {
-              auto desc = [&](int operand) { return sdesc_kmajor_sw128(ph + operand * OP_BYTES + k * UMMA_K * 2); };
-              pair_umma_f16(d, desc(0), desc(2), idesc, (kb > 0 || k > 0) ? 1u : 0u);
-              pair_umma_f16(d, desc(1), desc(2), idesc, 1u);
-              pair_umma_f16(d, desc(0), desc(3), idesc, 1u);
-            }
-            pair_commit(&empty[stage]);
-            if (++stage == STAGES) {
-              stage = 0;
-              phase ^= 1u;
-            }
-          }
-          if (!ok) break;
-          pair_commit(&tfull[acc]);
-        }
-      }
-      pair_commit(drain);
-    }
-    __syncwarp();
-  } else {
-    const int quad = warp & 3;
-    const int part = (warp - 2) >> 2;
-    const uint32_t tile_at = smem_u32(smem + SMEM_STAGING + (warp - 2) * STAGING_BYTES);
-    const int row = static_cast<int>(rank) * BM + quad * 32;   // of lane 0
-    uint32_t n = 0;
-    bool ok = true;
-    for (uint32_t e = pair; ok && e < args.matrices; e += pairs) {
-      for (int step = 0; ok && step < CHAIN_STEPS; ++step, ++n) {
-        const uint32_t acc = n & 1u;
-        ok = mbar_wait_bounded(&tfull[acc], (n >> 1) & 1u, abort_flag, args.status, ST_EPI_TMEM_FULL, WAIT_LIMIT_NS);
-        ok = __all_sync(FULL_MASK, ok);
-        if (!ok) break;
-        tc_fence_after();
-        const bool poly = CHAIN_P[step] == 0;
-        const Pair& out = args.matrix[CHAIN_OUT[step]];
-        const uint32_t t_lane = tmem_base + acc * TILE + (static_cast<uint32_t>(quad * 32) << 16);
-        for (int col = 32 * part; col < args.s && row < args.s; col += 64) {
-          uint4 a_hi[4], a_lo[4];
-          if (poly) load_pairs(args.matrix[0], static_cast<int>(e), row, col, a_hi, a_lo);
-          uint32_t raw[32];
-          tmem_ld_32x32b_x32(t_lane + static_cast<uint32_t>(col), raw);
-          tmem_ld_wait();
-          float v[32];
-          if (poly) {
-            add_pairs(tile_at, a_hi, a_lo, args.a_scale, raw, args.poly_scale, v);
-            const int diag = row + lane - col;
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] += diag == j ? args.diag : 0.0f;
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) * args.scale[step];
-          }
-          store_pairs<false>(tile_at, out, static_cast<int>(e), row, col, v);
-        }
-        tc_fence_before();
-        asm volatile("fence.proxy.async.global;" ::: "memory");   // this lane's stores, before others' TMA loads
-        __syncwarp();
-        if (lane == 0) {
-          peer_arrive(peer_u32(&tempty[acc], 0));
-          peer_arrive_release(peer_u32(stored, 0));
-          peer_arrive_release(peer_u32(stored, 1));
-        }
-      }
-    }
+    __syncthreads();
   }
-
-  pair_teardown(full, drain, abort_flag, issued_stages, rank, tmem_base, args.status);
+  cluster_sync();   // nothing is left that reads or signals the other block's shared memory
+  if (warp == 1) {
+    tc_fence_after();
+    pair_tmem_dealloc(tmem_base, TMEM_COLS);
+  }
 }
 
 // A from the parts of GRAM_PART, added in order.
@@ -1330,48 +1120,14 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
     g.scale = pow2(exp);
     return launch_product<GRAM, false, false>(E, p, q, g, pairs, stream, why);
   };
-  // The products of two steps after out = X X^T: T = B1 B, in one launch.
-  auto chain = [&]() {
-    ChainMaps maps;
-    ChainArgs g{};
-    const Pair* m[4] = {&a, &b, &t, &b1};
-    for (int i = 0; i < 4; ++i) {
-      if (!enc(&maps.m[i][0], m[i]->hi, E, s, s, l.s_pitch, BM) || !enc(&maps.m[i][1], m[i]->lo, E, s, s, l.s_pitch, BM)) {
-        *why = "cuTensorMapEncodeTiled rejected an operand";
-        return cudaErrorInvalidValue;
-      }
-      g.matrix[i] = *m[i];
-    }
-    g.s = static_cast<int>(s);
-    g.matrices = static_cast<uint32_t>(E);
-    g.poly_scale = NS_C * pow2(B_EXP - 2 * A_EXP);
-    g.a_scale = NS_B * pow2(B_EXP - A_EXP);
-    g.diag = NS_A * pow2(B_EXP);
-    g.scale[1] = g.scale[2] = pow2(A_EXP - A_EXP - B_EXP);
-    g.scale[4] = pow2(BB_EXP - 2 * B_EXP);
-    g.status = status;
-    const cudaError_t e = cudaFuncSetAttribute(chain_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(chain_kernel, dim3(static_cast<unsigned>(2 * std::min<int64_t>(E, pairs))), dim3(NUM_THREADS),
-                            SMEM_BYTES, stream, maps, g);
-  };
-  // One tile a matrix and not more matrices than pairs: a launch's fixed time, about 6 us, is most of it (one 128 x 2048
-  // matrix, all products apart: 157 us), so five products go in one.
-  const bool chained = s <= TILE && E <= pairs;
-  const bool by_two = chained || two_steps_pay(E, s, std::max(r, c));
+  const bool by_two = two_steps_pay(E, s, std::max(r, c));
   for (int left = o.steps; left > 0;) {
     const int now = by_two && left >= 2 ? 2 : 1;
     left -= now;
-    if ((err = gram(a)) != cudaSuccess) return err;
+    if ((err = gram(a)) != cudaSuccess || (err = poly(a, b)) != cudaSuccess) return err;
     Pair q = b;
     int q_exp = B_EXP;
-    if (now == 2 && chained) {
-      if ((err = chain()) != cudaSuccess) return err;
-      q = t;
-      q_exp = BB_EXP;
-    } else if ((err = poly(a, b)) != cudaSuccess) {
-      return err;
-    } else if (now == 2) {
+    if (now == 2) {
       // X'' = B1 B X with B1 from A1 = X' X'^T = B A B
       if ((err = product(b, a, t, A_EXP - A_EXP - B_EXP)) != cudaSuccess ||
           (err = product(t, b, a, A_EXP - A_EXP - B_EXP)) != cudaSuccess || (err = poly(a, b1)) != cudaSuccess ||
