@@ -1001,9 +1001,8 @@ moe_status moe_muon_step(void* weight, moe_dtype weight_dtype, const void* grad,
  * the scale loader), 0x41 - 0x46 the waits of the Newton-Schulz products (0x41
  * producer, 0x42 MMA for a loaded stage, 0x43 MMA for a drained accumulator,
  * 0x44 epilogue, 0x45 / 0x46 teardown drains), 0x51 / 0x52 the norms around a
- * block waiting for their rows, 0x100
- * moe_selftest_bounded_wait. Synchronises the current device; *code = 0 when
- * no wait has timed out.
+ * block waiting for their rows, 0x100 moe_selftest_bounded_wait. Synchronises
+ * the current device; *code = 0 when no wait has timed out.
  */
 moe_status moe_device_status(uint32_t* code, int32_t clear);
 

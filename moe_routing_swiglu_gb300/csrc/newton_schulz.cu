@@ -931,14 +931,44 @@ Layout layout(int64_t E, int64_t r, int64_t c) {
   return l;
 }
 
+// The tensor maps of a call's matrices, each encoded once (encoding them for
+// every launch was half of a small call's time).
+class Maps {
+ public:
+  explicit Maps(int64_t E) : E_(E) {}
+  // hi and lo of p, two maps; NULL if they cannot be had.
+  const CUtensorMap* of(const Pair& p, uint32_t box_rows) {
+    for (int i = 0; i < n_; ++i)
+      if (entry_[i].p == p.hi && entry_[i].box_rows == box_rows) return entry_[i].m;
+    if (n_ == MAX) return nullptr;
+    Entry& e = entry_[n_];
+    if (!enc(&e.m[0], p.hi, E_, p.rows, p.cols, p.pitch, box_rows) ||
+        !enc(&e.m[1], p.lo, E_, p.rows, p.cols, p.pitch, box_rows))
+      return nullptr;
+    e.p = p.hi;
+    e.box_rows = box_rows;
+    ++n_;
+    return e.m;
+  }
+
+ private:
+  static constexpr int MAX = 8;   // X and X' in two boxes, A, B, T, B1
+  struct Entry {
+    CUtensorMap m[2];
+    const __half* p;
+    uint32_t box_rows;
+  };
+  Entry entry_[MAX];
+  int n_ = 0;
+  int64_t E_;
+};
+
 template <int MODE, bool P_MN, bool Q_MN, bool SINGLE = false>
-cudaError_t launch_product(int64_t E, const Pair& p, const Pair& q, NsArgs args, int num_pairs, cudaStream_t s,
+cudaError_t launch_product(int64_t E, Maps& maps, const Pair& p, const Pair& q, NsArgs args, int num_pairs, cudaStream_t s,
                            const char** why, int parts = 1) {
-  CUtensorMap m[4];
-  if (!enc(&m[0], p.hi, E, p.rows, p.cols, p.pitch, P_MN ? 64 : BM) ||
-      !enc(&m[1], p.lo, E, p.rows, p.cols, p.pitch, P_MN ? 64 : BM) ||
-      !enc(&m[2], q.hi, E, q.rows, q.cols, q.pitch, Q_MN ? 64 : BM) ||
-      !enc(&m[3], q.lo, E, q.rows, q.cols, q.pitch, Q_MN ? 64 : BM)) {
+  const CUtensorMap* pm = maps.of(p, P_MN ? 64 : BM);
+  const CUtensorMap* qm = maps.of(q, Q_MN ? 64 : BM);
+  if (pm == nullptr || qm == nullptr) {
     *why = "cuTensorMapEncodeTiled rejected an operand";
     return cudaErrorInvalidValue;
   }
@@ -948,12 +978,9 @@ cudaError_t launch_product(int64_t E, const Pair& p, const Pair& q, NsArgs args,
                                                    : static_cast<int64_t>(args.m_blocks) * args.n_blocks;
   args.tiles_per_matrix = static_cast<uint32_t>(per);
   args.tiles = static_cast<uint32_t>(E * per * parts);
-  auto kern = ns_kernel<MODE, P_MN, Q_MN, SINGLE>;
-  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  if (err != cudaSuccess) return err;
   const int64_t pairs = std::min<int64_t>(args.tiles, num_pairs);
-  return launch_dependent(kern, dim3(static_cast<unsigned>(2 * pairs)), dim3(NUM_THREADS), SMEM_BYTES, s, m[0], m[1],
-                          m[2], m[3], args);
+  return launch_dependent(ns_kernel<MODE, P_MN, Q_MN, SINGLE>, dim3(static_cast<unsigned>(2 * pairs)), dim3(NUM_THREADS),
+                          SMEM_BYTES, s, pm[0], pm[1], qm[0], qm[1], args);
 }
 
 // A matrix's X X^T in parts of K, where whole tiles would leave most block
@@ -974,26 +1001,46 @@ bool two_steps_pay(int64_t E, int64_t s, int64_t l) {
   return static_cast<double>(E) * s * s * (l - s) > 2e9;
 }
 
+cudaError_t allow_shared_memory() {
+  const void* kernels[] = {
+      reinterpret_cast<const void*>(ns_kernel<GRAM, false, false, false>),
+      reinterpret_cast<const void*>(ns_kernel<GRAM, true, true, false>),
+      reinterpret_cast<const void*>(ns_kernel<GRAM_PART, false, false, false>),
+      reinterpret_cast<const void*>(ns_kernel<GRAM_PART, true, true, false>),
+      reinterpret_cast<const void*>(ns_kernel<POLY, false, false, false>),
+      reinterpret_cast<const void*>(ns_kernel<APPLY, false, false, false>),
+      reinterpret_cast<const void*>(ns_kernel<APPLY, false, true, false>),
+      reinterpret_cast<const void*>(ns_kernel<FINAL, false, false, false>),
+      reinterpret_cast<const void*>(ns_kernel<FINAL, false, true, false>),
+      reinterpret_cast<const void*>(ns_kernel<FINAL, false, false, true>),
+      reinterpret_cast<const void*>(ns_kernel<FINAL, false, true, true>),
+  };
+  for (const void* k : kernels) {
+    const cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
+    if (err != cudaSuccess) return err;
+  }
+  return cudaSuccess;
+}
+
 // Block pairs that the current device runs at once: SMs left single in a
 // cluster of SMs take none, and a pair too many would run after all the others.
+// Once per device, with the kernels' shared memory.
 cudaError_t resident_pairs(int* pairs) {
   constexpr int MAX_DEVICES = 64;
   static std::atomic<int> known[MAX_DEVICES];
   int dev = 0;
   cudaError_t err = cudaGetDevice(&dev);
   if (err != cudaSuccess) return err;
-  if (dev < MAX_DEVICES && (*pairs = known[dev].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
-  auto kern = ns_kernel<POLY, false, false, false>;
-  err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
-  if (err != cudaSuccess) return err;
+  if (dev < MAX_DEVICES && (*pairs = known[dev].load(std::memory_order_acquire)) > 0) return cudaSuccess;
+  if ((err = allow_shared_memory()) != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(NUM_THREADS);
   cfg.dynamicSmemBytes = SMEM_BYTES;
-  err = cudaOccupancyMaxActiveClusters(pairs, kern, &cfg);
+  err = cudaOccupancyMaxActiveClusters(pairs, ns_kernel<POLY, false, false, false>, &cfg);
   if (err != cudaSuccess) return err;
   if (*pairs < 1) return cudaErrorLaunchOutOfResources;
-  if (dev < MAX_DEVICES) known[dev].store(*pairs, std::memory_order_relaxed);
+  if (dev < MAX_DEVICES) known[dev].store(*pairs, std::memory_order_release);
   return cudaSuccess;
 }
 
@@ -1076,6 +1123,7 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
   const int k_blocks = static_cast<int>((std::max(r, c) + BK - 1) / BK);
   const int split = (k_blocks + parts - 1) / parts;
   parts = (k_blocks + split - 1) / split;
+  Maps maps(E);
   NsArgs sq{};
   sq.status = status;
   sq.m = sq.n = static_cast<int>(s);
@@ -1088,13 +1136,13 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
     g.out = out;
     g.scale = pow2(A_EXP - 2 * X_EXP);
     if (parts == 1)
-      return tall ? launch_product<GRAM, true, true>(E, x, x, g, pairs, stream, why)
-                  : launch_product<GRAM, false, false>(E, x, x, g, pairs, stream, why);
+      return tall ? launch_product<GRAM, true, true>(E, maps, x, x, g, pairs, stream, why)
+                  : launch_product<GRAM, false, false>(E, maps, x, x, g, pairs, stream, why);
     g.parts = reinterpret_cast<float*>(base + l.parts);
     g.part_elems = E * s * l.s_pitch;
     g.k_split = split;
-    const cudaError_t e = tall ? launch_product<GRAM_PART, true, true>(E, x, x, g, pairs, stream, why, parts)
-                               : launch_product<GRAM_PART, false, false>(E, x, x, g, pairs, stream, why, parts);
+    const cudaError_t e = tall ? launch_product<GRAM_PART, true, true>(E, maps, x, x, g, pairs, stream, why, parts)
+                               : launch_product<GRAM_PART, false, false>(E, maps, x, x, g, pairs, stream, why, parts);
     if (e != cudaSuccess) return e;
     const int64_t blocks = (g.part_elems / 4 + PRE_THREADS - 1) / PRE_THREADS;
     return launch_dependent(join_parts_kernel, dim3(static_cast<unsigned>(blocks)), dim3(PRE_THREADS), 0, stream,
@@ -1110,7 +1158,7 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
     p.scale = NS_C * pow2(B_EXP - 2 * A_EXP);
     p.a_scale = NS_B * pow2(B_EXP - A_EXP);
     p.diag = NS_A * pow2(B_EXP);
-    return launch_product<POLY, false, false>(E, in, in, p, pairs, stream, why);
+    return launch_product<POLY, false, false>(E, maps, in, in, p, pairs, stream, why);
   };
   // out = P Q of polynomials in the same A: symmetric
   auto product = [&](const Pair& p, const Pair& q, const Pair& out, int exp) {
@@ -1118,7 +1166,7 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
     g.k = static_cast<int>(s);
     g.out = out;
     g.scale = pow2(exp);
-    return launch_product<GRAM, false, false>(E, p, q, g, pairs, stream, why);
+    return launch_product<GRAM, false, false>(E, maps, p, q, g, pairs, stream, why);
   };
   const bool by_two = two_steps_pay(E, s, std::max(r, c));
   for (int left = o.steps; left > 0;) {
@@ -1144,8 +1192,8 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
     if (left > 0) {
       f.out = next;
       f.scale = pow2(-q_exp);
-      err = tall ? launch_product<APPLY, false, false>(E, x, q, f, pairs, stream, why)
-                 : launch_product<APPLY, false, true>(E, q, x, f, pairs, stream, why);
+      err = tall ? launch_product<APPLY, false, false>(E, maps, x, q, f, pairs, stream, why)
+                 : launch_product<APPLY, false, true>(E, maps, q, x, f, pairs, stream, why);
     } else {
       f.scale = pow2(-q_exp - X_EXP);
       f.result = o.result;
@@ -1156,11 +1204,11 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
       // A BF16 result of one step (B, at most 3.45): the hi parts' 11 bits leave it off by some 2^-12, an eighth of its
       // own rounding; a third of the product's time.
       if (now == 1 && o.result_dtype == MOE_BF16)
-        err = tall ? launch_product<FINAL, false, false, true>(E, x, q, f, pairs, stream, why)
-                   : launch_product<FINAL, false, true, true>(E, q, x, f, pairs, stream, why);
+        err = tall ? launch_product<FINAL, false, false, true>(E, maps, x, q, f, pairs, stream, why)
+                   : launch_product<FINAL, false, true, true>(E, maps, q, x, f, pairs, stream, why);
       else
-        err = tall ? launch_product<FINAL, false, false>(E, x, q, f, pairs, stream, why)
-                   : launch_product<FINAL, false, true>(E, q, x, f, pairs, stream, why);
+        err = tall ? launch_product<FINAL, false, false>(E, maps, x, q, f, pairs, stream, why)
+                   : launch_product<FINAL, false, true>(E, maps, q, x, f, pairs, stream, why);
     }
     if (err != cudaSuccess) return err;
     std::swap(x, next);
