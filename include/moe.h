@@ -68,7 +68,8 @@ const char* moe_last_error(void);
  * adds moe_experts_forward_combine, moe_route_dispatch,
  * moe_route_sigmoid_grouped_dispatch and moe_permute_rows to 1.0.0; nothing
  * was removed or changed. The moe_mxfp4_*, moe_experts_mxfp4_*,
- * moe_forward_mxfp4* and moe_grad_* entry points came later under the same
+ * moe_forward_mxfp4*, moe_grad_*, moe_block_*, moe_combine_join,
+ * moe_orthogonalize* and moe_muon_step entry points came later under the same
  * number: a caller that has to know looks the symbols up. */
 int moe_version(void);
 
@@ -972,6 +973,8 @@ typedef struct {
  *   weight     device, [E, rows, cols] in weight_dtype, updated in place.
  *   grad       device, in grad_dtype.
  *   momentum   device, float, updated in place (zeros before the first step).
+ * A matrix whose grad or momentum holds a NaN or an infinity gets NaN weights:
+ * moe_grad_norm tells before the step.
  *   params     host, read during the call only.
  * The tensors and the workspace must not overlap.
  */

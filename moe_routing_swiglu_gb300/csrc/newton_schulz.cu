@@ -1,28 +1,32 @@
 // Orthogonalised updates by Newton-Schulz products, on the tensor cores.
 //
-// For each matrix G [r, c] of a batch (s = min(r, c), the short side):
+// For each matrix G [r, c] of a batch (s = min(r, c) the short, l the long side):
 //   X = G / (|G|_F + eps), then per step, with A = X X^T (X^T X where r > c)
 //   and a, b, c = 3.4445, -4.7750, 2.0315:
 //   X <- B X (X B),  B = a I + b A + c A A
 // which moves every singular value of X from (0, 1] towards the interval
-// [0.7, 1.21] and keeps its singular vectors. Three grouped products a step:
-//   GRAM   A           (symmetric: the tiles on and above the diagonal are
-//          computed, each also stored mirrored)
+// [0.7, 1.21] and keeps its singular vectors. Grouped products:
+//   GRAM   A, and any other product of polynomials in A (symmetric: the tiles
+//          on and above the diagonal are computed, each also stored mirrored)
 //   POLY   B = a I + b A + c A A, the first two terms in the epilogue
 //          (symmetric too)
-//   APPLY  X' = B X, or X B; in the last step its epilogue writes the result
-//          (16-bit, or the weights' update) instead of X'
+//   APPLY  X' = B X, or X B; FINAL the last one, whose epilogue writes the
+//          result (16-bit, or the weights' update) instead of X'
+// Two steps go together where that is less work: X'' = (B1 B) X with B1 from
+// X' X'^T = B A B, so that X' itself is never computed.
 //
 // Precision. The map multiplies small singular values by 3.4 a step, 485 in
-// five, and with them every rounding error made before: 16-bit operands alone
-// (half a step of 2^-11 or 2^-8) leave errors of 5 % and more along the weak
-// directions. Operands are pairs of FP16 instead, v = hi + lo, lo the FP16 of
-// v - hi, and a product is hi hi + hi lo + lo hi: 22 bits, for three MMAs.
-// FP16 rather than BF16 pairs (16 bits) because every value here is bounded:
-// |X| <= 1.21 (its largest singular value: the quintic maps [0, 1.21] into
-// itself), |A| <= 1.47, |B| <= 3.45. Stored times 2^14 (X, A) or 2^13 (B) they
-// stay under FP16's 65504, and lo of an entry as small as
-// 2^-14 is still a normal FP16.
+// five, and with them every rounding error made before; in 16-bit operands that
+// shows along the weak directions. Operands are pairs of FP16 instead, v = hi +
+// lo, lo the FP16 of v - hi, and a product is hi hi + hi lo + lo hi: 22 bits,
+// for three MMAs. FP16 rather than BF16 pairs (16 bits) because every value here
+// is bounded: |X| <= 1.21 (its largest singular value: the quintic maps [0,
+// 1.21] into itself), |A| <= 1.47, |B| <= 3.45, |B1 B| <= 11.9. Stored times 2^14
+// (X, A), 2^13 (B) or 2^12 (B1 B) they stay under FP16's 65504, and lo of an
+// entry as small as 2^-14 is still a normal FP16. What is left is the FP32
+// accumulators' truncation: 1e-6 (2-norm, of the result) for sides of 64, 3e-5
+// to 1e-4 for 768 x 2048 to 2048 x 1408, 3e-4 for 4096 x 14336 with few strong
+// directions, against 1.7e-3 of a BF16 and 2.1e-4 of an F16 result's rounding.
 //
 // Structure: a persistent pair of CTAs on two SMs (cta_group::2) per tile of
 // 256 x 256, K in blocks of 64. Each CTA brings 128 rows of P and half of Q's
@@ -30,15 +34,21 @@
 // with 128 x 256 tiles needs 96 KB, all that an SM takes in from L2 in that
 // time. Warp 0 issues the TMA copies, warp 1 of the first CTA the MMAs, warps
 // 2..9 drain TMEM, whose two 256-column accumulators let one tile's epilogue
-// run under the next one's MMAs. Operands along their rows (K contiguous) are K-major tiles, X as
-// a right-hand side and X^T X read X as it is stored, MN-major. Waits are
-// bounded; one that runs out records a code and the CTA winds down.
+// run under the next one's MMAs. Operands along their rows (K contiguous) are
+// K-major tiles, X as a right-hand side and X^T X read X as it is stored,
+// MN-major. Waits are bounded; one that runs out records a code and the CTA
+// winds down.
+//
+// Bound by the power limit at the large sizes: 2 x 14336 x 4096 takes 8.0 ms on
+// zeros at 2070 MHz and 9.6 ms on random values at about 1600 MHz, 1.7 PFLOP/s
+// of MMAs; 128 x 768 x 2048 4.8 ms, of which 4.0 at that rate. One small matrix
+// is bound by its 22 launches, 7 us each from one's last store to the next
+// one's (one 128 x 2048: 157 us).
 #include <cudaTypedefs.h>
 
 #include <algorithm>
 #include <atomic>
 #include <mutex>
-#include <type_traits>
 
 #include "moe_common.cuh"
 #include "moe_internal.h"
@@ -50,6 +60,7 @@ namespace {
 constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
 constexpr float pow2(int e) { return e == 0 ? 1.0f : e > 0 ? 2.0f * pow2(e - 1) : 0.5f * pow2(e + 1); }
 constexpr int X_EXP = 14, A_EXP = 14, B_EXP = 13, BB_EXP = 12;   // stored = value * 2^EXP
+
 // ---------------------------------------------------------------- norm, momentum, first X
 
 constexpr int PRE_THREADS = 256;
