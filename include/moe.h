@@ -927,8 +927,8 @@ moe_status moe_block_join_backward(const void* dout, const void* dnormed, const 
  * tensor cores with FP16 pairs as operands (22 bits; the last one of a BF16
  * result with 11) and FP32 accumulators: the result is right to about its
  * type's rounding, to some 2^-13 (2-norm over the matrix) where it goes into
- * FP32 weights. A matrix with a NaN or an infinity becomes NaN as a whole, the others of the
- * batch are not touched by it; a matrix of zeros stays zero.
+ * FP32 weights. A matrix with a NaN or an infinity becomes NaN as a whole, the
+ * others of the batch are not touched by it; a matrix of zeros stays zero.
  *
  *   E           0 .. 65535 matrices, dense, one behind the other.
  *   rows, cols  0 .. 65536, either may be the longer (no element: nothing is
@@ -938,7 +938,8 @@ moe_status moe_block_join_backward(const void* dout, const void* dnormed, const 
  *   workspace   device, moe_orthogonalize_workspace_size(E, rows, cols) bytes,
  *               256-byte aligned, of both calls below: about 8 bytes per
  *               element, 16 min(rows, cols)^2 per matrix, and up to 34 MB for
- *               batches of few matrices. Contents need not be initialised. Calls that may overlap need separate ones.
+ *               batches of few matrices. Contents need not be initialised.
+ *               Calls that may overlap need separate ones.
  * Tensors are aligned to their element size. The same bits on every run.
  * ---------------------------------------------------------------------- */
 size_t moe_orthogonalize_workspace_size(int64_t E, int64_t rows, int64_t cols);

@@ -181,13 +181,13 @@ __device__ __forceinline__ void load_vector(const void* p, bool f32, const Cols<
 
 // ---------------------------------------------------------------- sums over a row
 
-// COUNT sums (N of each of R rows), for every thread of the rows, in two parts
-// with one barrier between them: the two halves of `sm` are used in turn, and a half is written
-// again only after the barrier of the call between, which every reader of the
-// half has passed. In a warp the values, V of them (COUNT rounded up to a power
-// of two), are added by exchanging: a lane gives half of its values away until
-// it holds one, number lane / (32 / V), over 32 / V lanes: for 12 sums 16
-// shuffles in place of 60.
+// COUNT sums (of one row, or one of each of two), for every thread of the rows,
+// in two parts with one barrier between them: the two halves of `sm` are used in
+// turn, and a half is written again only after the barrier of the call between,
+// which every reader of the half has passed. In a warp the values, V of them
+// (COUNT rounded up to a power of two), are added by exchanging: a lane gives
+// half of its values away until it holds one, number lane / (32 / V), over 32 / V
+// lanes: for six sums 9 shuffles in place of 30.
 constexpr int pow2_at_least(int n) { return n <= 1 ? 1 : 2 * pow2_at_least((n + 1) / 2); }
 
 template <int COUNT>
@@ -471,7 +471,8 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
   // row past the end as a row that is not stored. A round's scalars are loaded
   // a round ahead.
   Turn turn{0, 0u};
-  const uint8_t* mine = stage_smem + threadIdx.y * R * row_bytes + (c.any() ? threadIdx.x * (COLS * static_cast<uint32_t>(sizeof(T))) : 0u);
+  const uint8_t* mine = stage_smem + threadIdx.y * R * row_bytes +
+                        (c.any() ? threadIdx.x * (COLS * static_cast<uint32_t>(sizeof(T))) : 0u);
   const bool row_barrier = tpr > 32 || cluster > 1;
   uint32_t t = first_row + threadIdx.y * R;   // this thread's first row
   auto gate_of = [&](uint32_t row) { return token && row < rows ? token_gate<T>(a.gate, a.vec_f32, row) : 1.0f; };
@@ -726,7 +727,8 @@ __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel
   uint32_t mine[CHUNKS];   // this thread's columns in a stage
 #pragma unroll
   for (int k = 0; k < CHUNKS; ++k)
-    mine[k] = threadIdx.y * row_bytes + (c[k].any() ? (k * tpr + threadIdx.x) * (COLS * static_cast<uint32_t>(sizeof(T))) : 0u);
+    mine[k] = threadIdx.y * row_bytes +
+              (c[k].any() ? (k * tpr + threadIdx.x) * (COLS * static_cast<uint32_t>(sizeof(T))) : 0u);
   auto gate_of = [&](uint32_t row) { return token && row < rows ? token_gate<T>(a.gate, a.vec_f32, row) : 1.0f; };
   struct Part {   // a thread's chunk of a row
     Eight<T> d, f, o, y, g;
