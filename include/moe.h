@@ -1002,9 +1002,10 @@ moe_status moe_muon_step(void* weight, moe_dtype weight_dtype, const void* grad,
  * accumulator, 0x34 epilogue, 0x35 / 0x36 teardown drains, 0x37 scale loader
  * for a free ring slot, 0x38 scale warps for a free scale buffer, 0x39 for a
  * loaded ring slot, 0x3A MMA for a stage's scales, 0x3B a teardown drain of
- * the scale loader), 0x41 - 0x46 the waits of the Newton-Schulz products (0x41
+ * the scale loader), 0x41 - 0x47 the waits of the Newton-Schulz products (0x41
  * producer, 0x42 MMA for a loaded stage, 0x43 MMA for a drained accumulator,
- * 0x44 epilogue, 0x45 / 0x46 teardown drains), 0x51 / 0x52 the norms around a
+ * 0x44 epilogue, 0x45 / 0x46 teardown drains, 0x47 a product of the one-launch
+ * kernel), 0x51 / 0x52 the norms around a
  * block waiting for their rows, 0x100 moe_selftest_bounded_wait. Synchronises
  * the current device; *code = 0 when no wait has timed out.
  */

@@ -41,9 +41,10 @@
 //
 // Bound by the power limit at the large sizes: 2 x 14336 x 4096 takes 8.0 ms on
 // zeros at 2070 MHz and 9.6 ms on random values at about 1600 MHz, 1.7 PFLOP/s
-// of MMAs; 128 x 768 x 2048 4.8 ms, of which 4.0 at that rate. One small matrix
-// is bound by its 22 launches, 7 us each from one's last store to the next
-// one's (one 128 x 2048: 157 us).
+// of MMAs; 128 x 768 x 2048 4.8 ms, of which 4.0 at that rate. A few small
+// matrices are bound by the 22 launches, 7 us each from one's last store to the
+// next one's; where the short side is at most 128 they have a kernel of their
+// own, which takes all steps in one launch.
 #include <cudaTypedefs.h>
 
 #include <algorithm>
@@ -58,7 +59,7 @@ namespace moe {
 namespace {
 
 constexpr float NS_A = 3.4445f, NS_B = -4.7750f, NS_C = 2.0315f;
-constexpr float pow2(int e) { return e == 0 ? 1.0f : e > 0 ? 2.0f * pow2(e - 1) : 0.5f * pow2(e + 1); }
+__host__ __device__ constexpr float pow2(int e) { return e == 0 ? 1.0f : e > 0 ? 2.0f * pow2(e - 1) : 0.5f * pow2(e + 1); }
 constexpr int X_EXP = 14, A_EXP = 14, B_EXP = 13, BB_EXP = 12;   // stored = value * 2^EXP
 
 // ---------------------------------------------------------------- norm, momentum, first X
@@ -880,6 +881,386 @@ __global__ void __launch_bounds__(PRE_THREADS) join_parts_kernel(const float* pa
   *reinterpret_cast<uint2*>(lo + at) = l;
 }
 
+// ---------------------------------------------------------------- short sides up to 128: one launch
+
+// All steps of a matrix whose short side is at most 128 in one launch: a cluster
+// of 1 to 16 blocks holds X in shared memory, each block the FP16 pairs of up to
+// 192 columns (wide; rows where r > c, transposed as they are loaded), as tiles
+// of 128 rows x 64 columns with 128-byte rows, swizzled: K-major operands of X
+// X^T and an MN-major one of B X alike. A step:
+//   each block's part of A = X X^T goes from TMEM to the blocks that own its
+//   rows, s / C each; the owners add the parts in order and store their rows of
+//   A, as pairs, into every block;
+//   each block has all of B = a I + b A + c A A (over A), and X = B X of its
+//   columns, in place.
+// Rows of X past the short side up to a multiple of 16, and columns past the
+// long side, are zeros and stay zeros; rows past that are never read but as
+// rows of the 128 of an MMA whose results are not read either.
+//
+// Bound by latency: a step is three MMA chains of 24 to 36 instructions, each
+// with a trip through TMEM and registers, and two cluster barriers. 1 x 128 x
+// 2048, 16 blocks: 66 us, of which the parts' way to their owners 11, A's way to
+// all blocks 14, the MMAs of the pairs' lo parts 8; the products above take 144
+// in 22 launches. 512 threads a block are no faster.
+constexpr int CL_THREADS = 256;
+constexpr int CL_STEP = CL_THREADS / 128 * 32;           // columns that a quarter of the accumulator's rows is read in
+constexpr int CL_SIDE = 128, CL_TILES = 3;               // rows, and 64-column tiles of a block at most
+constexpr int CL_BOX = CL_SIDE * 128;                    // bytes of a tile
+constexpr int CL_X = 0;                                  // hi tiles, lo tiles
+constexpr int CL_A = CL_X + 2 * CL_TILES * CL_BOX;       // two hi tiles, two lo tiles
+constexpr int CL_PARTS = CL_A + 4 * CL_BOX;              // the parts of the owned rows, FP32; in the end the warps' staging
+constexpr int CL_PARTS_BYTES = CL_SIDE * CL_SIDE * 4;
+constexpr int CL_MISC = CL_PARTS + CL_PARTS_BYTES;       // barrier, TMEM address, abort flag
+constexpr int CL_BYTES = 1024 + CL_MISC + 16;
+constexpr uint32_t CL_TMEM_A = 0, CL_TMEM_B = 128, CL_TMEM_X = 256;
+constexpr int MAX_CLUSTER = 16;
+static_assert(CL_BYTES <= 227 * 1024, "shared memory budget");
+static_assert(CL_PARTS_BYTES >= CL_THREADS / 32 * STAGING_BYTES, "staging of the last product");
+
+constexpr uint32_t ST_CLUSTER = 0x47;
+
+struct ClusterArgs {
+  PreArgs pre;          // the matrices, their norms' parts
+  NsArgs f;             // FINAL: m, n, scale, result ..
+  int tiles;            // of a block
+  int steps;
+};
+
+// Generic writes of this thread, in any block's shared memory, before later MMAs.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void st_cluster_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+// Byte of the 8 columns of chunk q (of all columns) of a row of 128-byte-swizzled tiles.
+__device__ __forceinline__ uint32_t cl_chunk(int row, int q) {
+  return static_cast<uint32_t>((q >> 3) * CL_BOX + row * 128 + (((q & 7) ^ (row & 7)) << 4));
+}
+// Byte of chunk q (4 columns) of an owned row in a part: the rows of a chunk side
+// by side, because a warp's store takes one chunk of 32 rows (with a row's chunks
+// side by side instead 1 x 128 x 2048 took 77 us, not 66), turned by the chunk so
+// that the owner's reads of a row meet different banks.
+__device__ __forceinline__ uint32_t cl_part(int q, int in, int owned) {
+  return static_cast<uint32_t>(q * owned + (in + (q >> 1)) % owned) * 16;
+}
+// 32 values of a row from column c0 on as pairs into tiles, lo `lo_at` bytes behind hi.
+__device__ __forceinline__ void cl_store_pairs(uint32_t tiles, uint32_t lo_at, int row, int c0, const float (&v)[32]) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    uint32_t h[4], l[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) split_half2(v[q * 8 + 2 * j], v[q * 8 + 2 * j + 1], &h[j], &l[j]);
+    const uint32_t at = tiles + cl_chunk(row, c0 / 8 + q);
+    st_shared_v4(at, h[0], h[1], h[2], h[3]);
+    st_shared_v4(at + lo_at, l[0], l[1], l[2], l[3]);
+  }
+}
+// The last product's block of a tall matrix: lane: a column, v: its 32 rows from j0 on.
+template <typename T>
+__device__ __forceinline__ void store_column(const NsArgs& a, int col, int j0, int e, const float (&v)[32]) {
+  if (col >= a.n) return;
+  T* p = static_cast<T*>(a.result) + (static_cast<int64_t>(e) * a.m + j0) * a.n + col;
+  constexpr int G = 16;
+#pragma unroll
+  for (int r0 = 0; r0 < 32; r0 += G) {
+    T old[G];
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+      if (a.update && j0 + r0 + i < a.m) old[i] = p[static_cast<int64_t>(r0 + i) * a.n];
+#pragma unroll
+    for (int i = 0; i < G; ++i)
+      if (j0 + r0 + i < a.m)
+        p[static_cast<int64_t>(r0 + i) * a.n] =
+            from_f32<T>(a.update ? fmaf(a.keep, to_f32(old[i]), -a.rate * v[r0 + i]) : v[r0 + i]);
+  }
+}
+
+template <typename T, bool MOMENTUM, bool TALL>
+__global__ void __launch_bounds__(CL_THREADS, 1) ns_cluster_kernel(const __grid_constant__ ClusterArgs args, int cluster) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  uint64_t* done = reinterpret_cast<uint64_t*>(smem + CL_MISC);
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + CL_MISC + 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + CL_MISC + 12);
+  __shared__ float2 factors;
+  const PreArgs& pre = args.pre;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = cluster > 1 ? static_cast<int>(blockIdx.x) % cluster : 0;
+  const int64_t e = blockIdx.x / cluster;
+  const int s = TALL ? pre.c : pre.r, l = TALL ? pre.r : pre.c;
+  const int s16 = (s + 15) & ~15, cols = args.tiles * 64, first = rank * cols;
+  if (threadIdx.x == 0) {
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+    fence_proxy_async_smem();
+  }
+  if (warp == 0) {
+    tmem_alloc(tmem_holder, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_holder;
+  if (cluster > 1) cluster_sync();   // every block runs before another one writes into it
+  grid_dependency_wait();
+  launch_dependents();
+
+  // X = u / (norm + eps)
+  if (warp == 1) {
+    double sum = 0.0;
+    for (int i = lane; i < pre.chunks; i += 32) sum += pre.partial[e * pre.chunks + i];
+    sum = warp_sum(sum);
+    if (lane == 0) factors = scale_of(sum, pre.eps);
+  }
+  __syncthreads();
+  const float s1 = factors.x, s2 = factors.y;
+  const T* gp = static_cast<const T*>(pre.g) + e * pre.n;
+  const float* mp = MOMENTUM ? pre.m + e * pre.n : nullptr;
+  const uint32_t x_at = smem_u32(smem + CL_X), a_at = smem_u32(smem + CL_A), parts_at = smem_u32(smem + CL_PARTS);
+  constexpr uint32_t X_LO = CL_TILES * CL_BOX, A_LO = 2 * CL_BOX;
+  if (!TALL) {
+    const int per_row = cols / 8, groups = per_row * s16;
+    for (int i0 = threadIdx.x; i0 < groups; i0 += PRE_GROUP * CL_THREADS) {
+      Eight<T> g[PRE_GROUP];
+      Eight<float> m[PRE_GROUP];
+#pragma unroll
+      for (int k = 0; k < PRE_GROUP; ++k) {
+        const int i = i0 + k * CL_THREADS, row = i / per_row, col = first + (i - row * per_row) * 8;
+        const int n = i < groups && row < s ? max(min(l - col, 8), 0) : 0;
+        const int64_t at = static_cast<int64_t>(row) * l + col;
+        if (pre.vec && l % 8 == 0 && n == 8) {
+          load8<T>(gp + at, g[k]);
+          if (MOMENTUM) load8<float>(mp + at, m[k]);
+        } else {
+          load_some<T>(gp + at, n, g[k]);
+          if (MOMENTUM) load_some<float>(mp + at, n, m[k]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < PRE_GROUP; ++k) {
+        const int i = i0 + k * CL_THREADS, row = i / per_row, q = i - row * per_row;
+        if (i >= groups) continue;
+        uint32_t h[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float u[2];
+#pragma unroll
+          for (int b = 0; b < 2; ++b) {
+            u[b] = to_f32(g[k].e[2 * j + b]);
+            if (MOMENTUM) u[b] = update_of(pre, u[b], m[k].e[2 * j + b]);
+            u[b] = u[b] * s1 * s2;
+          }
+          split_half2(u[0], u[1], &h[j], &lo[j]);
+        }
+        const uint32_t to = x_at + cl_chunk(row, q);
+        st_shared_v4(to, h[0], h[1], h[2], h[3]);
+        st_shared_v4(to + X_LO, lo[0], lo[1], lo[2], lo[3]);
+      }
+    }
+  } else {
+    // A warp takes rows of G (one column of X each), a lane every 32nd element.
+    constexpr int ROWS = 4, PART = CL_SIDE / 32;
+    for (int j0 = warp * ROWS; j0 < cols; j0 += CL_THREADS / 32 * ROWS) {
+      T g[ROWS][PART];
+      float m[ROWS][PART];
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k)
+#pragma unroll
+        for (int b = 0; b < PART; ++b) {
+          const int j = first + j0 + k, i = lane + 32 * b;
+          const int64_t at = static_cast<int64_t>(j) * s + i;
+          const bool in = j < l && i < s;
+          g[k][b] = in ? gp[at] : from_f32<T>(0.0f);
+          if (MOMENTUM) m[k][b] = in ? mp[at] : 0.0f;
+        }
+#pragma unroll
+      for (int k = 0; k < ROWS; ++k)
+#pragma unroll
+        for (int b = 0; b < PART; ++b) {
+          const int j = j0 + k, i = lane + 32 * b;
+          if (i >= s16) continue;
+          float u = to_f32(g[k][b]);
+          if (MOMENTUM) u = update_of(pre, u, m[k][b]);
+          __half h, lo;
+          split_half(u * s1 * s2, &h, &lo);
+          uint8_t* to = smem + CL_X + cl_chunk(i, j >> 3) + (j & 7) * 2;
+          *reinterpret_cast<__half*>(to) = h;
+          *reinterpret_cast<__half*>(to + X_LO) = lo;
+        }
+    }
+  }
+  fence_proxy_async_all();
+  __syncthreads();
+
+  // One product at a time; after a give-up none is issued, and every wait ends at once.
+  uint32_t parity = 0;
+  bool in_flight = false;   // (the issuer's) a product whose end has not been seen
+  auto finish = [&]() {
+    if (mbar_wait_bounded(done, parity, abort_flag, args.f.status, ST_CLUSTER, WAIT_LIMIT_NS)) {
+      parity ^= 1u;
+      in_flight = false;
+    }
+    __syncwarp();
+    tc_fence_after();
+  };
+  // D = P Q over k16 blocks of 16, both pairs.
+  auto mma = [&](uint32_t d, uint32_t p, uint32_t p_lo, uint32_t q, uint32_t q_lo, bool q_mn, int n, int k16) {
+    if (*abort_flag != 0) return;
+    const uint32_t idesc = idesc_f16_major(false, CL_SIDE, n, false, q_mn);
+    for (int k = 0; k < k16; ++k) {
+      const uint32_t at = (k >> 2) * CL_BOX + (k & 3) * UMMA_K * 2;
+      const uint64_t ph = sdesc_kmajor_sw128(p + at), pl = sdesc_kmajor_sw128(p + p_lo + at);
+      const uint64_t qh = q_mn ? sdesc_mnmajor_sw128(q + k * 2048, CL_BOX, 1024) : sdesc_kmajor_sw128(q + at);
+      const uint64_t ql = q_mn ? sdesc_mnmajor_sw128(q + q_lo + k * 2048, CL_BOX, 1024) : sdesc_kmajor_sw128(q + q_lo + at);
+      umma_f16(d, ph, qh, idesc, k > 0 ? 1u : 0u);
+      umma_f16(d, pl, qh, idesc, 1u);
+      umma_f16(d, ph, ql, idesc, 1u);
+    }
+    umma_commit(done);
+    in_flight = true;
+  };
+  const int quad = warp & 3, half = warp >> 2;
+  const int row = quad * 32 + lane;   // of an accumulator
+  const uint32_t t_lane = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+  const bool rows_used = quad * 32 < s16;   // of the warp
+  constexpr float A_SCALE = pow2(A_EXP - 2 * X_EXP);
+  const int owned = s16 / cluster;   // rows of A that this block adds up (cluster divides 16)
+  for (int step = 0; step < args.steps; ++step) {
+    if (threadIdx.x == 0) mma(tmem + CL_TMEM_A, x_at, X_LO, x_at, X_LO, false, s16, cols / 16);
+    finish();
+    if (rows_used) {
+      const int owner = row / owned, in = row - owner * owned;
+      const uint32_t part = cluster > 1 && row < s16 ? peer_u32(smem + CL_PARTS, owner) + rank * owned * 512 : 0;
+      for (int c0 = 32 * half; c0 < s16; c0 += CL_STEP) {
+        uint32_t raw[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(t_lane + CL_TMEM_A + c0, raw);
+        tmem_ld_wait();
+        if (row >= s16) continue;
+        if (cluster == 1) {
+          float v[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) * A_SCALE;
+          cl_store_pairs(a_at, A_LO, row, c0, v);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            st_cluster_v4(part + cl_part(c0 / 4 + q, in, owned), raw[4 * q], raw[4 * q + 1], raw[4 * q + 2], raw[4 * q + 3]);
+        }
+      }
+    }
+    __syncwarp();
+    if (cluster > 1) {
+      cluster_sync();
+      // The owned rows: 8 columns a thread, the parts in order.
+      const int per_row = s16 / 8;
+      for (int i = threadIdx.x; i < owned * per_row; i += CL_THREADS) {
+        const int in = i / per_row, q = i - in * per_row, to_row = rank * owned + in;
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        for (int b = 0; b < cluster; ++b) {
+          const uint8_t* at = smem + CL_PARTS + b * owned * 512;
+          const float4 x = *reinterpret_cast<const float4*>(at + cl_part(2 * q, in, owned));
+          const float4 y = *reinterpret_cast<const float4*>(at + cl_part(2 * q + 1, in, owned));
+          v[0] += x.x;
+          v[1] += x.y;
+          v[2] += x.z;
+          v[3] += x.w;
+          v[4] += y.x;
+          v[5] += y.y;
+          v[6] += y.z;
+          v[7] += y.w;
+        }
+        uint32_t h[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) split_half2(v[2 * j] * A_SCALE, v[2 * j + 1] * A_SCALE, &h[j], &lo[j]);
+        for (int b = 0; b < cluster; ++b) {
+          const uint32_t to = peer_u32(smem + CL_A, b) + cl_chunk(to_row, q);
+          st_cluster_v4(to, h[0], h[1], h[2], h[3]);
+          st_cluster_v4(to + A_LO, lo[0], lo[1], lo[2], lo[3]);
+        }
+      }
+      fence_proxy_async_all();
+      __syncwarp();
+      cluster_sync();
+    }
+    fence_proxy_async_all();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // B over A: A's products are complete before B is stored.
+    if (threadIdx.x == 0) mma(tmem + CL_TMEM_B, a_at, A_LO, a_at, A_LO, false, s16, s16 / 16);
+    finish();
+    if (rows_used)
+      for (int c0 = 32 * half; c0 < s16; c0 += CL_STEP) {
+        uint32_t raw[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(t_lane + CL_TMEM_B + c0, raw);
+        tmem_ld_wait();
+        if (row >= s16) continue;
+        float v[32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint32_t at = a_at + cl_chunk(row, c0 / 8 + q);
+          const uint4 h = ld_shared_v4(at), lo = ld_shared_v4(at + A_LO);
+          const uint32_t hw[4] = {h.x, h.y, h.z, h.w}, lw[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&hw[j]));
+            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&lw[j]));
+            v[q * 8 + 2 * j] = x.x + y.x;
+            v[q * 8 + 2 * j + 1] = x.y + y.y;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          v[j] = fmaf(__uint_as_float(raw[j]), NS_C * pow2(B_EXP - 2 * A_EXP), v[j] * (NS_B * pow2(B_EXP - A_EXP)));
+          if (c0 + j == row) v[j] += NS_A * pow2(B_EXP);
+        }
+        cl_store_pairs(a_at, A_LO, row, c0, v);
+      }
+    fence_proxy_async_all();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (threadIdx.x == 0) mma(tmem + CL_TMEM_X, a_at, A_LO, x_at, X_LO, true, cols, s16 / 16);
+    finish();
+    const bool last = step + 1 == args.steps;
+    if (rows_used)
+      for (int c0 = 32 * half; c0 < cols; c0 += CL_STEP) {
+        uint32_t raw[32];
+        __syncwarp();
+        tmem_ld_32x32b_x32(t_lane + CL_TMEM_X + c0, raw);
+        tmem_ld_wait();
+        const float scale = last ? args.f.scale : pow2(-B_EXP);
+        float v[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(raw[j]) * scale;
+        if (!last) {
+          if (row < s16) cl_store_pairs(x_at, X_LO, row, c0, v);
+        } else if (TALL) {
+          if (args.f.result_dtype == MOE_F32) store_column<float>(args.f, row, first + c0, static_cast<int>(e), v);
+          else if (args.f.result_dtype == MOE_F16) store_column<__half>(args.f, row, first + c0, static_cast<int>(e), v);
+          else store_column<__nv_bfloat16>(args.f, row, first + c0, static_cast<int>(e), v);
+        } else {
+          float* stage = reinterpret_cast<float*>(smem + CL_PARTS + warp * STAGING_BYTES);
+          if (args.f.result_dtype == MOE_F32) store_result<float>(args.f, stage, quad * 32, first + c0, static_cast<int>(e), v);
+          else if (args.f.result_dtype == MOE_F16) store_result<__half>(args.f, stage, quad * 32, first + c0, static_cast<int>(e), v);
+          else store_result<__nv_bfloat16>(args.f, stage, quad * 32, first + c0, static_cast<int>(e), v);
+        }
+      }
+    fence_proxy_async_all();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
+  if (in_flight) mbar_wait_bounded(done, parity, nullptr, args.f.status, ST_CLUSTER, WAIT_LIMIT_NS);
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
+}
+
 // ---------------------------------------------------------------- host side
 
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
@@ -1055,10 +1436,106 @@ cudaError_t resident_pairs(int* pairs) {
   return cudaSuccess;
 }
 
+// Clusters of a size (16 >> i) that the current device runs at once; 0 for none.
+cudaError_t resident_clusters(int i, int* count) {
+  constexpr int MAX_DEVICES = 64;
+  static std::atomic<int> known[MAX_DEVICES][5];   // one more than the count
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  if (dev < MAX_DEVICES && (*count = known[dev][i].load(std::memory_order_acquire) - 1) >= 0) return cudaSuccess;
+  const auto kernel = ns_cluster_kernel<float, false, false>;
+  if ((err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CL_BYTES)) != cudaSuccess ||
+      (err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1)) != cudaSuccess)
+    return err;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim = {static_cast<unsigned>(MAX_CLUSTER >> i), 1, 1};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(MAX_CLUSTER >> i));
+  cfg.blockDim = dim3(CL_THREADS);
+  cfg.dynamicSmemBytes = CL_BYTES;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  if ((err = cudaOccupancyMaxActiveClusters(count, kernel, &cfg)) != cudaSuccess) return err;
+  if (dev < MAX_DEVICES) known[dev][i].store(*count + 1, std::memory_order_release);
+  return cudaSuccess;
+}
+
+// Blocks of a matrix's cluster, and 64-column tiles of a block; 0 blocks: the
+// matrices go through the products above. By the time that either takes, in
+// microseconds for five steps, fitted to sides of 16 to 128 x 64 to 2048 and 1
+// to 1000 matrices: waves of clusters against 22 launches and their tiles.
+// Measured, clusters against products: 1 x 128 x 2048 66 / 144, 8 x 128 x 2048
+// 132 / 152, 16 x 128 x 2048 199 / 181, 128 x 128 x 192 47 / 171, 128 x 64 x 512
+// 139 / 193, 1000 x 64 x 64 148 / 349, 32 x 128 x 1500 206 / 216.
+struct ClusterShape {
+  int blocks, tiles;
+};
+cudaError_t cluster_shape(int64_t E, int64_t s, int64_t l, ClusterShape* best) {
+  *best = {0, 0};
+  if (s > CL_SIDE || l > 64 * CL_TILES * MAX_CLUSTER) return cudaSuccess;
+  const double side = static_cast<double>((s + 15) / 16) / 8, long_side = static_cast<double>(l);
+  double least = 90.0 + 0.026 * long_side + static_cast<double>(E) * (0.2 + 0.00125 * long_side);
+  for (int i = 0; i < 5; ++i) {
+    const int64_t blocks = MAX_CLUSTER >> i, tiles = ((l + blocks - 1) / blocks + 63) / 64;
+    if (tiles > CL_TILES) continue;
+    int count = 0;
+    const cudaError_t err = resident_clusters(i, &count);
+    if (err != cudaSuccess) return err;
+    if (count < 1) continue;
+    constexpr double EXCHANGE[] = {26.0, 18.0, 12.0, 10.0, 0.0};   // of A's parts, by i
+    const double wave = 20.0 + side * (10.0 + 4.0 * static_cast<double>(tiles)) + side * side * EXCHANGE[i];
+    const double time = static_cast<double>((E + count - 1) / count) * wave;
+    if (time < least) {
+      least = time;
+      *best = {static_cast<int>(blocks), static_cast<int>(tiles)};
+    }
+  }
+  return cudaSuccess;
+}
+
+template <typename T, bool MOMENTUM, bool TALL>
+cudaError_t launch_cluster(const ClusterArgs& a, int64_t E, int blocks, cudaStream_t s) {
+  const auto kernel = ns_cluster_kernel<T, MOMENTUM, TALL>;
+  cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CL_BYTES);
+  if (err == cudaSuccess) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (err != cudaSuccess) return err;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(blocks), 1, 1};
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(E * blocks));
+  cfg.blockDim = dim3(CL_THREADS);
+  cfg.dynamicSmemBytes = CL_BYTES;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = blocks > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a, blocks);
+}
+
+template <typename T, bool MOMENTUM>
+cudaError_t launch_squares(const PreArgs& a, int64_t E, cudaStream_t s) {
+  return launch_dependent(squares_kernel<T, MOMENTUM>, dim3(a.chunks, static_cast<unsigned>(E)), dim3(PRE_THREADS), 0, s,
+                          a);
+}
+template <typename T, bool MOMENTUM>
+cudaError_t launch_small(const ClusterArgs& a, int64_t E, int blocks, cudaStream_t s) {
+  const cudaError_t err = launch_squares<T, MOMENTUM>(a.pre, E, s);
+  if (err != cudaSuccess) return err;
+  return a.pre.r > a.pre.c ? launch_cluster<T, MOMENTUM, true>(a, E, blocks, s)
+                           : launch_cluster<T, MOMENTUM, false>(a, E, blocks, s);
+}
+template <typename T>
+cudaError_t launch_small(const ClusterArgs& a, int64_t E, int blocks, cudaStream_t s) {
+  return a.pre.m != nullptr ? launch_small<T, true>(a, E, blocks, s) : launch_small<T, false>(a, E, blocks, s);
+}
+
 template <typename T, bool MOMENTUM>
 cudaError_t launch_pre(const PreArgs& a, int64_t E, cudaStream_t s) {
-  cudaError_t err = launch_dependent(squares_kernel<T, MOMENTUM>, dim3(a.chunks, static_cast<unsigned>(E)),
-                                     dim3(PRE_THREADS), 0, s, a);
+  const cudaError_t err = launch_squares<T, MOMENTUM>(a, E, s);
   if (err != cudaSuccess) return err;
   // Several rounds a block where there is work for all SMs: its start costs as much as one.
   const int64_t groups = a.pitch / 8 * a.r;
@@ -1123,6 +1600,32 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
             reinterpret_cast<uintptr_t>(o.momentum) % 16 == 0;
   pre.mu = o.momentum_decay;
   pre.eps = o.eps;
+  NsArgs f{};   // of the last product
+  f.status = status;
+  f.m = static_cast<int>(r);
+  f.n = static_cast<int>(c);
+  f.k = static_cast<int>(s);
+  f.result = o.result;
+  f.result_dtype = o.result_dtype;
+  f.update = o.update;
+  f.keep = o.keep;
+  f.rate = o.rate;
+  // A result over gradients of another size (or place) would end up on matrices
+  // that are yet to be read: other clusters start later.
+  const size_t from_bytes = static_cast<size_t>(E * pre.n) * dtype_size(static_cast<moe_dtype>(o.grad_dtype));
+  const size_t to_bytes = static_cast<size_t>(E * pre.n) * dtype_size(static_cast<moe_dtype>(o.result_dtype));
+  const uintptr_t from = reinterpret_cast<uintptr_t>(o.grad), to = reinterpret_cast<uintptr_t>(o.result);
+  const bool over = from < to + to_bytes && to < from + from_bytes && (from != to || from_bytes != to_bytes);
+  ClusterShape shape{0, 0};
+  if (!over && (err = cluster_shape(E, s, std::max(r, c), &shape)) != cudaSuccess) return err;
+  if (shape.blocks > 0) {
+    ClusterArgs args{pre, f, shape.tiles, o.steps};
+    args.f.scale = pow2(-B_EXP - X_EXP);
+    return o.grad_dtype == MOE_F32   ? launch_small<float>(args, E, shape.blocks, stream)
+           : o.grad_dtype == MOE_F16 ? launch_small<__half>(args, E, shape.blocks, stream)
+                                     : launch_small<__nv_bfloat16>(args, E, shape.blocks, stream);
+  }
+
   err = o.grad_dtype == MOE_F32   ? launch_pre<float>(pre, E, stream)
         : o.grad_dtype == MOE_F16 ? launch_pre<__half>(pre, E, stream)
                                   : launch_pre<__nv_bfloat16>(pre, E, stream);
@@ -1195,11 +1698,6 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
       q = t;
       q_exp = BB_EXP;
     }
-    NsArgs f{};
-    f.status = status;
-    f.m = static_cast<int>(r);
-    f.n = static_cast<int>(c);
-    f.k = static_cast<int>(s);
     if (left > 0) {
       f.out = next;
       f.scale = pow2(-q_exp);
@@ -1207,11 +1705,6 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
                  : launch_product<APPLY, false, true>(E, maps, q, x, f, pairs, stream, why);
     } else {
       f.scale = pow2(-q_exp - X_EXP);
-      f.result = o.result;
-      f.result_dtype = o.result_dtype;
-      f.update = o.update;
-      f.keep = o.keep;
-      f.rate = o.rate;
       // A BF16 result of one step (B, at most 3.45): the hi parts' 11 bits leave it off by some 2^-12, an eighth of its
       // own rounding; a third of the product's time.
       if (now == 1 && o.result_dtype == MOE_BF16)

@@ -66,6 +66,71 @@ def test_orthogonalize(cuda_lib, E, r, c, dtype, out):
     assert moe.moe_device_status() == 0
 
 
+# short sides up to 128 take one launch: each size of cluster, its blocks' columns whole, ragged and none at all; sides
+# that end inside 16; a long side past what a cluster holds; more clusters than run at once, and too many
+SMALL = [(1, 128, 2048), (1, 2048, 128), (2, 100, 1537), (2, 1537, 100), (1, 128, 3000), (1, 3000, 97), (1, 17, 2999),
+         (1, 17, 3100), (2, 113, 769), (2, 769, 113), (5, 90, 385), (5, 385, 90), (4, 128, 192), (4, 193, 128),
+         (3, 1, 192), (3, 700, 1), (160, 31, 65), (160, 65, 31), (20, 20, 700), (30, 128, 2048), (1, 129, 2048)]
+
+
+@pytest.mark.parametrize("E,r,c", SMALL)
+@pytest.mark.parametrize("dtype,out", [("f32", "f16"), ("bf16", "bf16")])
+def test_short_sides(cuda_lib, E, r, c, dtype, out):
+    moe = cuda_lib
+    rng = np.random.default_rng(E + r * c)
+    g = gradients(rng, E, r, c, dtype)
+    behind = torch.full((E * r * c + 64,), 7.0, dtype=DTYPES[out], device=DEV)
+    o = moe.moe_orthogonalize(g, out=behind[:E * r * c].view(E, r, c))
+    check_matrices(o[:3], f64(g[:3]), rng)
+    check_matrices(o[-1:], f64(g[-1:]), rng)
+    assert (behind[E * r * c:] == 7.0).all()
+    assert torch.equal(o, moe.moe_orthogonalize(g, dtype=DTYPES[out]))
+    assert moe.moe_device_status() == 0
+
+
+@pytest.mark.parametrize("E,r,c", [(40, 64, 300), (40, 300, 64), (3, 128, 1000)])
+@pytest.mark.parametrize("dtype,out,shift", [("bf16", "bf16", 0), ("f32", "bf16", 0), ("f32", "f16", 1), ("f16", "f16", 3)])
+def test_short_sides_over_their_inputs(cuda_lib, E, r, c, dtype, out, shift):
+    """The result over the matrices' own memory, of the same or another element size, at its start or `shift` in."""
+    moe = cuda_lib
+    rng = np.random.default_rng(r)
+    n = E * r * c
+    g = torch.empty(n + 8, dtype=DTYPES[dtype], device=DEV)
+    g[:n] = gradients(rng, E, r, c, dtype).view(-1)
+    inputs = f64(g[:n].view(E, r, c))
+    o = g.view(DTYPES[out])[shift:shift + n].view(E, r, c)
+    moe.moe_orthogonalize(g[:n].view(E, r, c), out=o)
+    check_matrices(o[:2], inputs[:2], rng)
+    check_matrices(o[E // 2:E // 2 + 2], inputs[E // 2:E // 2 + 2], rng)
+    check_matrices(o[-1:], inputs[-1:], rng)
+    assert moe.moe_device_status() == 0
+
+
+@pytest.mark.parametrize("E,r,c", [(1, 128, 2048), (3, 515, 77), (50, 48, 130)])
+@pytest.mark.parametrize("wdtype,gdtype", [("f32", "bf16"), ("bf16", "f32"), ("f16", "f16")])
+def test_short_sides_muon_step(cuda_lib, E, r, c, wdtype, gdtype):
+    """As test_muon_step, at the sizes that take one launch; the matrices at the ends and in the middle."""
+    moe = cuda_lib
+    rng = np.random.default_rng(r + c)
+    w = torch.tensor(rng.normal(size=(E, r, c)) / 8, dtype=DTYPES[wdtype], device=DEV)
+    m = torch.tensor(rng.normal(size=(E, r, c)) * 1e-3, dtype=torch.float32, device=DEV)
+    g = gradients(rng, E, r, c, gdtype)
+    w0, m0, g0 = f64(w), f64(m), f64(g)
+    lr, mu, wd, scale = (float(np.float32(v)) for v in (0.02, 0.9, 0.1, 1.5))
+    moe.moe_muon_step(w, g, m, lr=lr, momentum_decay=mu, weight_decay=wd, update_scale=scale)
+    got_m, got = f64(m), f64(w)
+    assert (np.abs(got_m - (mu * m0 + g0)) <= 2.0 ** -24 * (np.abs(mu * m0 + g0) + 2.0 ** -100)).all()
+    keep, rate = float(np.float32(1 - lr * wd)), float(np.float32(lr * scale))
+    for e in {0, E // 2, E - 1}:
+        u = g0[e] + mu * got_m[e]
+        o = block.newton_schulz(u)
+        move = 2 * np.linalg.norm(block.newton_schulz_moved(u, rng) - o) + last_product(u, w.dtype)
+        eps = torch.finfo(w.dtype).eps / 2 + 3 * 2.0 ** -24
+        tol = eps * (np.abs(keep * w0[e]) + np.abs(rate * o)) + rate * move
+        assert (np.abs(got[e] - (keep * w0[e] - rate * o)) <= tol).all()
+    assert moe.moe_device_status() == 0
+
+
 @pytest.mark.parametrize("steps", [1, 2, 8])
 @pytest.mark.parametrize("r,c", [(60, 200), (200, 60)])
 def test_steps(cuda_lib, steps, r, c):
