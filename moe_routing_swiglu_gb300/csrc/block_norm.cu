@@ -121,6 +121,10 @@ __device__ __forceinline__ void store8(T* row, const Cols<VEC>& c, const Eight<T
     const uint4* q = reinterpret_cast<const uint4*>(&v);
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(v) / 16); ++i) p[i] = q[i];
+  } else if (c.col(COLS - 1) < c.H) {
+    T* p = row + c.first;
+#pragma unroll
+    for (int j = 0; j < COLS; ++j) p[j * c.step] = v.e[j];
   } else {
 #pragma unroll
     for (int j = 0; j < COLS; ++j)
@@ -285,11 +289,11 @@ __device__ __forceinline__ float token_gate(const void* p, bool f32, int64_t t) 
 
 // ---------------------------------------------------------------- rows ahead of their use
 
-// A ring of rounds in shared memory: one thread copies what a round reads, as
-// whole rows by bulk copies (16-byte aligned: VEC rows), several rounds before
-// its turn. An SM needs some 70 KB of loads in flight for its share of HBM's
-// rate; in registers one round ahead is all there is room for (the backward of
-// 8192 x 4096 BF16 rows ran at 1.9 TB/s that way).
+// A ring of rounds in shared memory: one warp copies what a round reads, as whole
+// rows by bulk copies, several rounds before its turn. An SM needs some 70 KB of
+// loads in flight for its share of HBM's rate; in registers one round ahead is
+// all there is room for (the backward of 8192 x 4096 BF16 rows ran at 1.9 TB/s
+// that way).
 constexpr int MAX_STAGES = 8;
 constexpr uint64_t WAIT_LIMIT_NS = 1000000000ull;
 constexpr uint32_t ST_ROWS = 0x51, ST_ROWS_DRAIN = 0x52;
@@ -359,6 +363,68 @@ __device__ __forceinline__ void copy_rows(uint8_t* dst, const T* src, uint32_t n
   }
 }
 
+// Rows that do not lie on 16-byte boundaries come as the 16-byte granules that
+// they touch, to a place with room for that: a round's rows together where a
+// block has whole rows, else row by row. What a granule holds of the rows beside
+// them is not looked at (nor is it waited for: another block may be storing it).
+__host__ __device__ constexpr uint32_t loose_pitch(uint32_t bytes) { return (bytes + 30) & ~15u; }
+// Bytes from row to row in a stage, and of a round's rows.
+__host__ __device__ constexpr uint32_t staged_row(uint32_t row_bytes, int cluster, bool vec) {
+  return vec || cluster == 1 ? row_bytes : loose_pitch(row_bytes);
+}
+__host__ __device__ constexpr uint32_t staged_rows(uint32_t row_bytes, uint32_t rows, int cluster, bool vec) {
+  return vec ? row_bytes * rows : cluster == 1 ? loose_pitch(row_bytes * rows) : loose_pitch(row_bytes) * rows;
+}
+
+// The copy of one such run: `bytes` (0: none) from `src` to `dst`.
+struct LooseRow {
+  const uint8_t* src;
+  uint8_t* dst;
+  uint32_t bytes;
+};
+// The copy of the run at `row` into its place, from a tensor [begin, end). A
+// granule that is not the tensor's as a whole (its first, its last) is not
+// copied; its elements are stored here.
+template <typename T>
+__device__ __forceinline__ LooseRow loose_row(uint8_t* place, const T* row, uint32_t row_bytes, const T* begin,
+                                              const T* end) {
+  const uintptr_t from = reinterpret_cast<uintptr_t>(row), to = from + row_bytes;
+  uintptr_t lo = from & ~uintptr_t{15}, hi = (to + 15) & ~uintptr_t{15};
+  const uintptr_t zero = lo;   // of the place
+  const bool head = lo < reinterpret_cast<uintptr_t>(begin), tail = hi > reinterpret_cast<uintptr_t>(end);
+  if (row_bytes == 0) return {nullptr, nullptr, 0u};
+  if (head || tail) {
+    if (head) lo += 16;
+    if (tail && hi > lo) hi -= 16;
+    const uintptr_t stop = min(lo, to);
+    for (uintptr_t p = from; head && p < stop; p += sizeof(T))
+      *reinterpret_cast<T*>(place + (p - zero)) = *reinterpret_cast<const T*>(p);
+    for (uintptr_t p = max(hi, from); tail && p < to; p += sizeof(T))
+      *reinterpret_cast<T*>(place + (p - zero)) = *reinterpret_cast<const T*>(p);
+    fence_proxy_async_smem();   // before the next round's copies to this place
+  }
+  return {reinterpret_cast<const uint8_t*>(lo), place + (lo - zero), hi > lo ? static_cast<uint32_t>(hi - lo) : 0u};
+}
+__device__ __forceinline__ void loose_load(const LooseRow& r, uint64_t* bar) {
+  if (r.bytes > 0) bulk_load(r.dst, r.src, r.bytes, bar);
+}
+// Where in its place the run from that element on starts.
+__device__ __forceinline__ uint32_t loose_start(const void* tensor, uint32_t element, uint32_t size) {
+  return (static_cast<uint32_t>(reinterpret_cast<uintptr_t>(tensor)) + element * size) & 15u;
+}
+// A thread's columns of such a row (at its first column, `tid` in).
+template <typename T>
+__device__ __forceinline__ void loose8(const uint8_t* row, const Cols<false>& c, int tid, Eight<T>& v) {
+  const T* p = reinterpret_cast<const T*>(row) + tid;
+  if (c.col(COLS - 1) < c.H) {
+#pragma unroll
+    for (int j = 0; j < COLS; ++j) v.e[j] = p[j * c.step];
+  } else {
+#pragma unroll
+    for (int j = 0; j < COLS; ++j) v.e[j] = c.col(j) < c.H ? p[j * c.step] : from_f32<T>(0.0f);
+  }
+}
+
 // This thread's columns of a row in a stage (a thread past the row's columns is
 // given any others: it adds and stores nothing).
 template <typename T>
@@ -374,8 +440,11 @@ __device__ __forceinline__ void stage8(const uint8_t* mine, Eight<T>& v) {
 // ELEMENT: a gate for every element.
 //
 // Bound by HBM: x and f in (combine: top_k rows), out and y out. BULK: rounds
-// come through the ring; else (unaligned rows, calls of one round a block, many
-// slots) they are loaded when their turn comes.
+// come through the ring; else (calls of one round a block, many slots) they are
+// loaded when their turn comes. Loose rows (not VEC) leave the ring and the
+// kernel element by element, 32 neighbours a warp: in FP32 that keeps up with HBM
+// (join of 8192 x 4095 93 us, of 4096 columns 97), in 16 bits issue bounds it (90
+// us, 54; without the ring 148).
 
 // Threads that an SM holds: 1024 of 64 registers where that is enough.
 constexpr int join_threads(size_t size, bool vec, int branch, bool element) {
@@ -411,7 +480,9 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
   // The ring: a stage holds x, then f or the expert rows, then the gates, each
   // of this block's columns.
   const int cols = max(min(tpr * COLS, a.H - rank * tpr * COLS), 0);
-  const uint32_t row_bytes = cols * static_cast<uint32_t>(sizeof(T)), block_bytes = row_bytes * round_rows;
+  const uint32_t row_bytes = cols * static_cast<uint32_t>(sizeof(T));
+  const uint32_t row_pitch = staged_row(row_bytes, cluster, VEC);
+  const uint32_t block_bytes = staged_rows(row_bytes, round_rows, cluster, VEC);
   const uint32_t stage_bytes = block_bytes * (1 + (BRANCH == 2 ? a.top_k : BRANCH) + (ELEMENT ? 1 : 0));
   // Combine: lane j's expert row of a token's first 32 slots.
   auto slot_of = [&](uint32_t t) {
@@ -431,7 +502,31 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
     const int64_t at = static_cast<int64_t>(issue_t0) * a.H + rank * tpr * COLS;
     const uint32_t n = min(round_rows, rows - issue_t0);
     const bool good = BRANCH == 2 && ahead < a.rows;
-    if (BRANCH == 2) {
+    if (!VEC) {   // a lane a run
+      const int64_t total = static_cast<int64_t>(rows) * a.H, mine = at + lane * static_cast<int64_t>(a.H);
+      LooseRow copies[4] = {};
+      auto take = [&](int i, uint32_t offset, const void* tensor, int64_t first, uint32_t bytes, int64_t elements) {
+        const T* p = static_cast<const T*>(tensor);
+        copies[i] = loose_row<T>(dst + offset, p + first, bytes, p, p + elements);
+      };
+      if (static_cast<uint32_t>(lane) < (cluster == 1 ? 1u : n)) {
+        const uint32_t place = lane * row_pitch, bytes = cluster == 1 ? row_bytes * n : row_bytes;
+        take(0, place, a.x, mine, bytes, total);
+        if (BRANCH == 1) take(1, block_bytes + place, a.f, mine, bytes, total);
+        if (ELEMENT) take(2, stage_bytes - block_bytes + place, a.gate, mine, bytes, total);
+      }
+      if (good)
+        take(3, (1 + lane) * block_bytes, a.f, static_cast<int64_t>(ahead) * a.H + rank * tpr * COLS, row_bytes,
+             static_cast<int64_t>(a.rows) * a.H);
+      uint32_t bytes = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) bytes += copies[i].bytes;
+      bytes = __reduce_add_sync(FULL_MASK, bytes);   // after every lane's stores
+      if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) loose_load(copies[i], bar);
+    } else if (BRANCH == 2) {
       const uint32_t found = __popc(__ballot_sync(FULL_MASK, good));
       if (lane == 0) mbar_arrive_expect_tx(bar, row_bytes * ((ELEMENT ? 2 : 1) + found));
       __syncwarp();
@@ -439,7 +534,7 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
         bulk_load(dst + (1 + lane) * row_bytes,
                   static_cast<const T*>(a.f) + static_cast<int64_t>(ahead) * a.H + rank * tpr * COLS, row_bytes, bar);
     }
-    if (lane == 0) {
+    if (VEC && lane == 0) {
       if (BRANCH != 2) mbar_arrive_expect_tx(bar, row_bytes * n * (1 + BRANCH + (ELEMENT ? 1 : 0)));
       copy_rows<T>(dst, static_cast<const T*>(a.x) + at, n, row_bytes, a.H, cluster, bar);
       if (BRANCH == 1) copy_rows<T>(dst + block_bytes, static_cast<const T*>(a.f) + at, n, row_bytes, a.H, cluster, bar);
@@ -471,8 +566,16 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
   // row past the end as a row that is not stored. A round's scalars are loaded
   // a round ahead.
   Turn turn{0, 0u};
-  const uint8_t* mine = stage_smem + threadIdx.y * R * row_bytes +
-                        (c.any() ? threadIdx.x * (COLS * static_cast<uint32_t>(sizeof(T))) : 0u);
+  const uint8_t* mine = stage_smem + threadIdx.y * R * row_pitch +
+                        (VEC && c.any() ? threadIdx.x * (COLS * static_cast<uint32_t>(sizeof(T))) : 0u);
+  // This thread's columns of a row in its stage; `first`: the run's first row.
+  auto staged = [&](const uint8_t* place, const void* tensor, uint32_t first, Eight<T>& v) {
+    if constexpr (VEC)
+      stage8<T>(place, v);
+    else
+      loose8<T>(place + loose_start(tensor, first * static_cast<uint32_t>(a.H) + rank * tpr * COLS, sizeof(T)), c,
+                threadIdx.x, v);
+  };
   const bool row_barrier = tpr > 32 || cluster > 1;
   uint32_t t = first_row + threadIdx.y * R;   // this thread's first row
   auto gate_of = [&](uint32_t row) { return token && row < rows ? token_gate<T>(a.gate, a.vec_f32, row) : 1.0f; };
@@ -504,15 +607,16 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      if (BULK) stage8<T>(stage + r * row_bytes, raw);
+      const uint32_t run = cluster == 1 ? t0 : t + r;
+      if (BULK) staged(stage + r * row_pitch, a.x, run, raw);
       else load8<T, VEC>(static_cast<const T*>(a.x) + at, c, raw);
       unpack8(raw, x[r]);
       if (ELEMENT) {
-        if (BULK) stage8<T>(stage + stage_bytes - block_bytes + r * row_bytes, gv[r]);
+        if (BULK) staged(stage + stage_bytes - block_bytes + r * row_pitch, a.gate, run, gv[r]);
         else load8<T, VEC>(static_cast<const T*>(a.gate) + at, c, gv[r]);
       }
       if (BRANCH == 1) {
-        if (BULK) stage8<T>(stage + block_bytes + r * row_bytes, raw);
+        if (BULK) staged(stage + block_bytes + r * row_pitch, a.f, run, raw);
         else load8<T, VEC>(static_cast<const T*>(a.f) + at, c, raw);
         unpack8(raw, f[r]);
       }
@@ -528,7 +632,8 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
           Eight<T> v;
           float y[COLS];
           const float w = __shfl_sync(FULL_MASK, weight, k);
-          stage8<T>(stage + (1 + k) * row_bytes, v);
+          const uint32_t row = VEC ? 0u : __shfl_sync(FULL_MASK, slot, k);
+          staged(stage + (1 + k) * block_bytes, a.f, row, v);
           unpack8(v, y);
 #pragma unroll
           for (int j = 0; j < COLS; ++j) f[0][j] = fmaf(w, y[j], f[0][j]);
@@ -634,11 +739,14 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, 
 // multiply the same sum, S = sum over rows of beta r1 dO f (times the other
 // gates): dw1 = gate S, dgate = w1 S.
 //
-// Bound by HBM (join: dout, dy, out, f in, dx, df out). BULK as in the forward.
-// A round's work is in two halves, the sums and, a round later, the results, so
-// that one round's barrier and shuffles run beside another one's arithmetic. A
-// thread owns CHUNKS groups of 8 columns: with two of them a row has half the
-// shuffles, and two blocks of 256 threads share an SM for rows of 4096.
+// Bound by HBM (join: dout, dy, out, f in, dx, df out). BULK as in the forward
+// (loose rows of 8192 x 4095 149 us in BF16, 146 in FP32; without the ring 187 and
+// 213; aligned ones 82 and 133). An aligned round's work is in two halves, the
+// sums and, a round later, the results, so that one round's barrier and shuffles
+// run beside another one's arithmetic; loose rows, whose narrow loads are dear,
+// go in one (in two the 149 us were 389). A thread owns CHUNKS groups of 8
+// columns: with two of them a row has half the shuffles, and two blocks of 256
+// threads share an SM for rows of 4096.
 template <typename T, bool VEC, int CHUNKS, bool BULK, bool HAS_F, bool NEXT, bool ELEMENT>
 __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel(const JoinBackwardArgs a, int cluster,
                                                                                  int stages) {
@@ -675,34 +783,56 @@ __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel
 
   // A stage: dout, f, out and dy, the gates, of this block's columns.
   const int cols = max(min(block_cols, a.H - rank * block_cols), 0);   // a cluster's last block may have none
-  const uint32_t row_bytes = cols * static_cast<uint32_t>(sizeof(T)), block_bytes = row_bytes * round_rows;
+  const uint32_t row_bytes = cols * static_cast<uint32_t>(sizeof(T));
+  const uint32_t row_pitch = staged_row(row_bytes, cluster, VEC);
+  const uint32_t block_bytes = staged_rows(row_bytes, round_rows, cluster, VEC);
   constexpr int ARRAYS = 1 + (HAS_F ? 1 : 0) + (NEXT ? 2 : 0) + (ELEMENT ? 1 : 0);
   constexpr int AT_F = 1, AT_O = 1 + (HAS_F ? 1 : 0), AT_Y = AT_O + 1, AT_G = ARRAYS - 1;
   const uint32_t stage_bytes = block_bytes * ARRAYS;
   uint32_t issued = 0, issue_t0 = first_row;
+  const uint32_t lane = threadIdx.x & 31;
   Turn fill{0, 0u};
-  auto issue = [&]() {
+  auto issue = [&]() {   // by the first warp of the block
     if (issue_t0 >= rows) return;
     uint8_t* dst = stage_smem + fill.slot * stage_bytes;
     uint64_t* bar = &ring.full[fill.slot];
     const int64_t at = static_cast<int64_t>(issue_t0) * a.H + rank * block_cols;
-    const uint32_t bytes = row_bytes * min(round_rows, rows - issue_t0);   // a cluster's blocks have one row
-    auto copy = [&](int array, const void* src) {
-      bulk_load(dst + array * block_bytes, static_cast<const T*>(src) + at, bytes, bar);
-    };
-    mbar_arrive_expect_tx(bar, bytes * (ARRAYS - (has_d ? 0 : 1)));
-    if (bytes > 0) {
-      if (has_d) copy(0, a.dout);
-      if (HAS_F) copy(AT_F, a.f);
-      if (NEXT) copy(AT_O, a.joined);
-      if (NEXT) copy(AT_Y, a.dnormed);
-      if (ELEMENT) copy(AT_G, a.gate);
+    const uint32_t n = min(round_rows, rows - issue_t0);   // a cluster's blocks have one row
+    if (!VEC) {   // a lane an array
+      const int64_t total = static_cast<int64_t>(rows) * a.H;
+      const void* const tensors[5] = {has_d ? a.dout : nullptr, HAS_F ? a.f : nullptr, NEXT ? a.joined : nullptr,
+                                      NEXT ? a.dnormed : nullptr, ELEMENT ? a.gate : nullptr};
+      constexpr int PLACES[5] = {0, AT_F, AT_O, AT_Y, AT_G};
+      LooseRow copy{};
+#pragma unroll
+      for (int i = 0; i < 5; ++i)
+        if (lane == i && tensors[i] != nullptr) {
+          const T* p = static_cast<const T*>(tensors[i]);
+          copy = loose_row<T>(dst + PLACES[i] * block_bytes, p + at, row_bytes * n, p, p + total);
+        }
+      const uint32_t bytes = __reduce_add_sync(FULL_MASK, copy.bytes);   // after every lane's stores
+      if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+      __syncwarp();
+      loose_load(copy, bar);
+    } else if (lane == 0) {
+      const uint32_t bytes = row_bytes * n;
+      auto copy = [&](int array, const void* src) {
+        bulk_load(dst + array * block_bytes, static_cast<const T*>(src) + at, bytes, bar);
+      };
+      mbar_arrive_expect_tx(bar, bytes * (ARRAYS - (has_d ? 0 : 1)));
+      if (bytes > 0) {
+        if (has_d) copy(0, a.dout);
+        if (HAS_F) copy(AT_F, a.f);
+        if (NEXT) copy(AT_O, a.joined);
+        if (NEXT) copy(AT_Y, a.dnormed);
+        if (ELEMENT) copy(AT_G, a.gate);
+      }
     }
     ++issued;
     fill.next(stages);
     issue_t0 += step;
   };
-  const bool issuer = BULK && threadIdx.x == 0 && threadIdx.y == 0;
+  const bool issuer = BULK && threadIdx.x < 32 && threadIdx.y == 0;
   if (issuer)
     for (int i = 0; i < stages; ++i) issue();
 
@@ -727,25 +857,34 @@ __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel
   uint32_t mine[CHUNKS];   // this thread's columns in a stage
 #pragma unroll
   for (int k = 0; k < CHUNKS; ++k)
-    mine[k] = threadIdx.y * row_bytes +
-              (c[k].any() ? (k * tpr + threadIdx.x) * (COLS * static_cast<uint32_t>(sizeof(T))) : 0u);
+    mine[k] = threadIdx.y * row_pitch +
+              (VEC && c[k].any() ? (k * tpr + threadIdx.x) * (COLS * static_cast<uint32_t>(sizeof(T))) : 0u);
   auto gate_of = [&](uint32_t row) { return token && row < rows ? token_gate<T>(a.gate, a.vec_f32, row) : 1.0f; };
   struct Part {   // a thread's chunk of a row
     Eight<T> d, f, o, y, g;
   };
-  auto load_part = [&](uint32_t t, int k, int slot, Part& v) {
+  auto load_part = [&](uint32_t t, int k, int slot, Part& v) {   // (threadIdx.y: its row's place in the round)
     if (BULK) {
       const uint8_t* row = stage_smem + slot * stage_bytes + mine[k];
+      auto staged = [&](int array, const void* tensor, Eight<T>& to) {
+        const uint8_t* place = row + array * block_bytes;
+        if constexpr (VEC) {
+          stage8<T>(place, to);
+        } else {
+          const uint32_t element = (t - threadIdx.y) * static_cast<uint32_t>(a.H) + rank * block_cols;
+          loose8<T>(place + loose_start(tensor, element, sizeof(T)), c[k], k * tpr * COLS + threadIdx.x, to);
+        }
+      };
       if (has_d) {
-        stage8<T>(row, v.d);
+        staged(0, a.dout, v.d);
       } else {
 #pragma unroll
         for (int j = 0; j < COLS; ++j) v.d.e[j] = from_f32<T>(0.0f);
       }
-      if (HAS_F) stage8<T>(row + AT_F * block_bytes, v.f);
-      if (NEXT) stage8<T>(row + AT_O * block_bytes, v.o);
-      if (NEXT) stage8<T>(row + AT_Y * block_bytes, v.y);
-      if (ELEMENT) stage8<T>(row + AT_G * block_bytes, v.g);
+      if (HAS_F) staged(AT_F, a.f, v.f);
+      if (NEXT) staged(AT_O, a.joined, v.o);
+      if (NEXT) staged(AT_Y, a.dnormed, v.y);
+      if (ELEMENT) staged(AT_G, a.gate, v.g);
     } else {
       const int64_t at = static_cast<int64_t>(min(t, rows - 1)) * a.H;
       if (has_d) {
@@ -840,7 +979,7 @@ __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel
     pack8<T>(d, v.d);
     store8<T, VEC>(static_cast<T*>(a.dresidual) + to, c[k], v.d);
   };
-  if (BULK) {
+  if (BULK && VEC) {
     Turn turn{0, 0u};   // of the sums; the results are one turn behind
     uint32_t t = first_row + threadIdx.y;
     float share = 0.0f, gate_next = gate_of(t);
@@ -888,19 +1027,30 @@ __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel
     }
     ring_end(ring, issued, stages, a.status);
   } else {
+    // In one go: the narrow loads of a loose row, or memory's, are made once.
+    Turn turn{0, 0u};
     uint32_t t = first_row + threadIdx.y;
+    float gate_next = gate_of(t);
     for (uint32_t t0 = first_row; t0 < rows; t0 += step, t += step) {
       Part v;
       float p[N];
 #pragma unroll
       for (int i = 0; i < N; ++i) p[i] = 0.0f;
-      const float gt = gate_of(t);
-      load_part(t, 0, 0, v);
+      const float gt = gate_next;
+      gate_next = gate_of(t + step);
+      if (BULK) ring_wait(ring, turn, a.status);
+      load_part(t, 0, turn.slot, v);
       add_up(v, 0, p);
       row_sum<N>(p, &sums, half, tpr, cluster, rank);
+      if (BULK) {
+        turn.next(stages);
+        if (tpr == 32 && cluster == 1) __syncthreads();   // else the sums' barrier
+        if (issuer) issue();
+      }
       const Factors x = factors_of(t, p, gt);
       if (t < rows) finish(v, t, 0, x);
     }
+    if (BULK) ring_end(ring, issued, stages, a.status);
   }
   // The block's rows side by side are added in order, then stored, times the
   // vector that the array's column sums are short of.
@@ -1015,8 +1165,9 @@ int ring_stages(size_t stage, int64_t resident, size_t fixed, int64_t rounds) {
   return static_cast<int>(std::min<int64_t>(std::min<int64_t>(fit, MAX_STAGES), rounds));
 }
 // Bytes of a stage: `arrays` times a round's rows of a block's columns.
-size_t stage_size(const RowShape& s, int64_t H, int rows, int64_t arrays, size_t size) {
-  return static_cast<size_t>(std::min<int64_t>(H, s.tpr * COLS) * s.rows * rows * arrays) * size;
+size_t stage_size(const RowShape& s, int64_t H, int cols, int rows, int64_t arrays, size_t size, bool vec) {
+  const uint32_t row = static_cast<uint32_t>(std::min<int64_t>(H, s.tpr * cols) * static_cast<int64_t>(size));
+  return static_cast<size_t>(arrays) * staged_rows(row, static_cast<uint32_t>(s.rows * rows), s.cluster, vec);
 }
 
 bool vec_ok(moe_dtype dtype, int64_t H, std::initializer_list<const void*> ptrs) {
@@ -1053,9 +1204,9 @@ cudaError_t launch_join_t(moe_dtype dtype, JoinArgs a, int branch, int num_sms, 
   int64_t units = 0;
   int stages = 0;
   size_t smem = 0;
-  if (vec && (branch != 2 || a.top_k <= 32) && rounds_of(1, &units) > 1) {
+  if ((branch != 2 || a.top_k <= 32) && rounds_of(1, &units) > 1) {
     const int rows = join_rows(true, branch);
-    const size_t stage = stage_size(s, a.H, rows, arrays, sizeof(T));
+    const size_t stage = stage_size(s, a.H, COLS, rows, arrays, sizeof(T), vec);
     stages = ring_stages(stage, resident, sizeof(RowSums<2>) + sizeof(Ring) + 256, rounds_of(rows, &units));
     if (stages < 2) stages = 0;
     smem = stage * stages;
@@ -1066,7 +1217,8 @@ cudaError_t launch_join_t(moe_dtype dtype, JoinArgs a, int branch, int num_sms, 
     const cudaError_t err = device_status_ptr(&a.status);
     if (err != cudaSuccess) return err;
   }
-  return launch_rows(stages > 0 ? pick_join<T, true, true>(branch, element)
+  return launch_rows(stages > 0 ? (vec ? pick_join<T, true, true>(branch, element)
+                                       : pick_join<T, false, true>(branch, element))
                      : vec      ? pick_join<T, true, false>(branch, element)
                                 : pick_join<T, false, false>(branch, element),
                      s, units, smem, stages, a, stream);
@@ -1101,13 +1253,17 @@ cudaError_t launch_join_backward_t(moe_dtype dtype, JoinBackwardArgs a, int64_t*
                                        a.gate_kind == MOE_GATE_ELEMENT ? a.dgate : nullptr});
   const bool f = a.f != nullptr, next = a.next_weight != nullptr, element = a.gate_kind == MOE_GATE_ELEMENT;
   const int64_t arrays = 1 + (f ? 1 : 0) + (next ? 2 : 0) + (element ? 1 : 0);
-  const int chunks = backward_chunks(a.H);
+  const int chunks = vec ? backward_chunks(a.H) : 1;
   RowShape s = row_shape(a.H, chunks);
   int stages = 0;
   size_t smem = 0;
-  if (vec) {
+  // Short loose rows of 16 bits that L2 holds gain nothing from the ring (16384 x
+  // 518, join: 71 us with it, 64 without; 100000 x 385, past L2, norm: 144 and 182).
+  constexpr int64_t L2_BYTES = int64_t{128} << 20;
+  const bool in_l2 = arrays * a.T * a.H * static_cast<int64_t>(sizeof(T)) < L2_BYTES;
+  if (vec || sizeof(T) == 4 || a.H >= 1024 || !in_l2) {
     // Three stages hold the rounds at work and one on its way; rather fewer blocks than fewer stages.
-    const size_t stage = static_cast<size_t>(std::min<int64_t>(a.H, s.tpr * COLS * chunks) * s.rows * arrays) * sizeof(T);
+    const size_t stage = stage_size(s, a.H, COLS * chunks, 1, arrays, sizeof(T), vec);
     const size_t fixed = sizeof(RowSums<6>) + sizeof(Ring) + 256;
     const int64_t groups = (a.T + s.rows - 1) / s.rows;
     for (int64_t resident = backward_resident(s); resident > 0; resident /= 2) {
@@ -1127,8 +1283,9 @@ cudaError_t launch_join_backward_t(moe_dtype dtype, JoinBackwardArgs a, int64_t*
     if (err != cudaSuccess) return err;
   }
   smem = std::max(smem, static_cast<size_t>(s.rows - 1) * s.tpr * COLS * sizeof(float));   // the fold in the end
-  return launch_rows(stages > 0 ? (chunks == 2 ? pick_backward<T, true, 2, true>(f, next, element)
-                                               : pick_backward<T, true, 1, true>(f, next, element))
+  return launch_rows(stages > 0 ? (!vec          ? pick_backward<T, false, 1, true>(f, next, element)
+                                   : chunks == 2 ? pick_backward<T, true, 2, true>(f, next, element)
+                                                 : pick_backward<T, true, 1, true>(f, next, element))
                      : vec ? pick_backward<T, true, 1, false>(f, next, element)
                            : pick_backward<T, false, 1, false>(f, next, element),
                      s, *units, smem, stages, a, stream);

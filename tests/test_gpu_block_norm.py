@@ -266,6 +266,97 @@ def test_unaligned_rows_match_aligned_ones(cuda_lib):
     check_join(out, y, f64(f), x, p)
 
 
+def shifted(t, by, behind=0):
+    """A copy of t that starts `by` elements into its memory, at the end of it but for `behind`."""
+    room = torch.full((t.numel() + by + behind,), 7.0, dtype=t.dtype, device=DEV)
+    view = room[by:by + t.numel()].view(t.shape)
+    view.copy_(t)
+    return view
+
+
+# odd rows through shared memory, several rounds: many rows a block, one, a cluster's; H under a granule; H even but no
+# multiple of 8; rows of whole granules at odd places
+LOOSE = [(20003, 3), (21001, 63), (5003, 129), (2501, 518), (3001, 1023), (701, 4095), (403, 8191), (301, 16393),
+         (2500, 264), (1301, 2048)]
+
+
+@pytest.mark.parametrize("T,H", LOOSE)
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_rows_off_granules_in_rounds(cuda_lib, T, H, dtype):
+    moe = cuda_lib
+    rng = np.random.default_rng(T + H)
+    kind, post, nxt = PARTS[(T + len(dtype)) % 4]
+    f, x, p = join_case(rng, T, H, dtype, "f32", kind, post, nxt)
+    dout, dy = grads(rng, T, H, dtype), grads(rng, T, H, dtype)
+    f, x, dout, dy = (shifted(t, by) for t, by in ((f, 1), (x, 3), (dout, 0), (dy, 7)))
+    if kind == "element":
+        p["gate"] = shifted(p["gate"], 5)
+    out, y = moe.moe_block_join(f, x, **p)
+    check_join(out, y, f64(f), x, p)
+    joined = shifted(out, 2)
+    check_join_backward(moe, dout, dy, f, joined, p, moe.moe_block_join_backward(dout, f, dnormed=dy, joined=joined, **p))
+    w = p["norm_weight"]
+    y = moe.moe_block_norm(x, w, eps=EPS)
+    ref = block.norm(f64(x), f64(w), EPS)
+    check(y, ref, np.abs(ref))
+    g = moe.moe_block_norm_backward(dy, x, w, eps=EPS, dresidual=dout)
+    dx, dw = block.norm_backward(f64(x), f64(w), f64(dy), EPS)
+    sx, sw = block.norm_backward_size(f64(x), f64(w), np.abs(f64(dy)), EPS)
+    check(g.dx, dx + f64(dout), sx + np.abs(f64(dout)))
+    check(g.dweight, dw, sw, (T + 16) * 2.0 ** -24)
+    assert moe.moe_device_status() == 0
+
+
+@pytest.mark.parametrize("T,k,H", [(20003, 2, 3), (3001, 3, 129), (700, 8, 2047), (400, 3, 8191), (900, 32, 130),
+                                   (900, 8, 2048)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_combined_rows_off_granules_in_rounds(cuda_lib, T, k, H, dtype):
+    moe = cuda_lib
+    rng = np.random.default_rng(T + k)
+    _, x, p = join_case(rng, T, H, dtype, "f32", "element" if k == 3 else "token", True, True)
+    yd = shifted(torch.tensor(rng.normal(size=(T * k, H)), dtype=DTYPES[dtype], device=DEV), 1)
+    x = shifted(x, 3)
+    inv = rng.permutation(T * k)
+    wt = torch.tensor(rng.uniform(size=(T, k)), dtype=torch.float32, device=DEV)
+    terms = f64(wt)[..., None] * f64(yd)[inv].reshape(T, k, H)
+    idx = torch.tensor(inv, dtype=torch.int32, device=DEV)
+    out, y = moe.moe_combine_join(yd, idx, wt, x, **p)
+    check_join(out, y, terms.sum(1), x, p, np.abs(terms).sum(1) * (k * 2.0 ** -24 / REL))
+    idx[5] = T * k   # no such row: the token's rows are NaN, the others as they were
+    o2, y2 = moe.moe_combine_join(yd, idx, wt, x, **p)
+    bad = 5 // k
+    keep = torch.arange(T, device=DEV) != bad
+    assert torch.isnan(o2[bad]).all() and torch.isnan(y2[bad]).all()
+    assert torch.equal(o2[keep], out[keep]) and torch.equal(y2[keep], y[keep])
+    assert moe.moe_device_status() == 0
+
+
+@pytest.mark.parametrize("T,H,dtype", [(5003, 129, "bf16"), (701, 4095, "f16"), (403, 8191, "bf16"), (3001, 1023, "f32")])
+def test_loose_rows_in_place_and_the_rows_behind(cuda_lib, T, H, dtype):
+    """The granules beside a row are being written by other blocks: the same bits as out of place, nothing else written."""
+    moe = cuda_lib
+    rng = np.random.default_rng(H)
+    f, x, p = join_case(rng, T, H, dtype, "f32", "element", True, True)
+    dout, dy = grads(rng, T, H, dtype), grads(rng, T, H, dtype)
+    ref = moe.moe_block_join(f, x, **p)
+    room = torch.full((T * H + 11,), 7.0, dtype=x.dtype, device=DEV)
+    x2, f2 = room[3:3 + T * H].view(T, H), f.clone()
+    x2.copy_(x)
+    moe.moe_block_join(f2, x2, out=x2, normed=f2, **p)
+    assert torch.equal(x2, ref[0]) and torch.equal(f2, ref[1])
+    assert (room[:3] == 7).all() and (room[3 + T * H:] == 7).all()
+    want = moe.moe_block_join_backward(dout, f, dnormed=dy, joined=ref[0], **p)
+    d2, f2, j2, y2 = dout.clone(), f.clone(), ref[0].clone(), dy.clone()
+    got = moe.moe_block_join_backward(d2, f2, dnormed=y2, joined=j2, dresidual=y2, dbranch=f2, **p)
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+    x2.copy_(x)
+    moe.moe_block_norm(x2, p["norm_weight"], out=x2)
+    assert torch.equal(x2, moe.moe_block_norm(x, p["norm_weight"]))
+    assert (room[:3] == 7).all() and (room[3 + T * H:] == 7).all()
+    assert moe.moe_device_status() == 0
+
+
 def test_many_rows_and_far_offsets(cuda_lib):
     """More rows than one wave, and more than 2^31 elements: the last rows against the formula."""
     moe = cuda_lib
