@@ -443,19 +443,20 @@ __device__ __forceinline__ void stage8(const uint8_t* mine, Eight<T>& v) {
 // come through the ring; else (calls of one round a block, many slots) they are
 // loaded when their turn comes. Loose rows (not VEC) leave the ring and the
 // kernel element by element, 32 neighbours a warp: in FP32 that keeps up with HBM
-// (join of 8192 x 4095 93 us, of 4096 columns 97), in 16 bits issue bounds it (90
-// us, 54; without the ring 148).
+// (join of 8192 x 4095 93 us, of 4096 columns 97), in 16 bits as many narrow loads
+// and stores take as long (90 us, 54; without the ring 148).
 
-// Threads that an SM holds: 1024 of 64 registers where that is enough.
-constexpr int join_threads(size_t size, bool vec, int branch, bool element) {
-  return size == 2 && vec && branch < 1 && !element ? 1024 : 512;
+// Threads that an SM holds: 1024 of 64 registers where that is enough (loose rows,
+// 2048 x 8191 BF16: 24 us, 30 with 512).
+constexpr int join_threads(size_t size, int branch, bool element) {
+  return size == 2 && branch < 1 && !element ? 1024 : 512;
 }
 // Rows of a thread in a round: two share a round's barriers and index
 // arithmetic, which are most of a row's instructions.
 constexpr int join_rows(bool bulk, int branch) { return bulk && branch != 2 ? 2 : 1; }
 
 template <typename T, bool VEC, bool BULK, int BRANCH, bool ELEMENT>
-__global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), VEC, BRANCH, ELEMENT) / MAX_TPR)
+__global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), BRANCH, ELEMENT) / MAX_TPR)
     join_kernel(const JoinArgs a, int cluster, int stages) {
   constexpr int R = join_rows(BULK, BRANCH);
   __shared__ RowSums<R> sums;
@@ -792,7 +793,7 @@ __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel
   uint32_t issued = 0, issue_t0 = first_row;
   const uint32_t lane = threadIdx.x & 31;
   Turn fill{0, 0u};
-  auto issue = [&]() {   // by the first warp of the block
+  auto issue = [&]() {   // by the first thread of the block, loose rows by its first warp
     if (issue_t0 >= rows) return;
     uint8_t* dst = stage_smem + fill.slot * stage_bytes;
     uint64_t* bar = &ring.full[fill.slot];
@@ -814,7 +815,7 @@ __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel
       if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
       __syncwarp();
       loose_load(copy, bar);
-    } else if (lane == 0) {
+    } else {
       const uint32_t bytes = row_bytes * n;
       auto copy = [&](int array, const void* src) {
         bulk_load(dst + array * block_bytes, static_cast<const T*>(src) + at, bytes, bar);
@@ -832,7 +833,7 @@ __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel
     fill.next(stages);
     issue_t0 += step;
   };
-  const bool issuer = BULK && threadIdx.x < 32 && threadIdx.y == 0;
+  const bool issuer = BULK && threadIdx.x < (VEC ? 1 : 32) && threadIdx.y == 0;
   if (issuer)
     for (int i = 0; i < stages; ++i) issue();
 
@@ -1193,7 +1194,7 @@ cudaError_t launch_join_t(moe_dtype dtype, JoinArgs a, int branch, int num_sms, 
   // The expert rows of one token at a time.
   if (branch == 2) s.rows = 1;
   // One wave: as many blocks as an SM's registers hold, each row after row.
-  const int64_t resident = std::max(1, std::min(16, join_threads(sizeof(T), vec, branch, element) / (s.tpr * s.rows)));
+  const int64_t resident = std::max(1, std::min(16, join_threads(sizeof(T), branch, element) / (s.tpr * s.rows)));
   const int64_t most = std::max<int64_t>(1, resident * num_sms / s.cluster);
   const int64_t arrays = 1 + (branch == 2 ? a.top_k : branch) + (element ? 1 : 0);
   auto rounds_of = [&](int rows, int64_t* units) {

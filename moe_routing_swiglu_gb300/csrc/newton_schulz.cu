@@ -1457,7 +1457,13 @@ cudaError_t resident_clusters(int i, int* count) {
   cfg.dynamicSmemBytes = CL_BYTES;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  if ((err = cudaOccupancyMaxActiveClusters(count, kernel, &cfg)) != cudaSuccess) return err;
+  err = cudaOccupancyMaxActiveClusters(count, kernel, &cfg);
+  if (err == cudaErrorInvalidClusterSize) {   // a device that does not take clusters of this size
+    cudaGetLastError();
+    *count = 0;
+  } else if (err != cudaSuccess) {
+    return err;
+  }
   if (dev < MAX_DEVICES) known[dev][i].store(*count + 1, std::memory_order_release);
   return cudaSuccess;
 }

@@ -131,6 +131,19 @@ def test_short_sides_muon_step(cuda_lib, E, r, c, wdtype, gdtype):
     assert moe.moe_device_status() == 0
 
 
+def test_short_sides_of_the_most_matrices(cuda_lib):
+    """65535 matrices, past 2^31 bytes: the first, one in the middle and the last."""
+    moe = cuda_lib
+    rng = np.random.default_rng(21)
+    some = gradients(rng, 7, 128, 128, "bf16")
+    g = some[torch.arange(65535, device=DEV) % 7]
+    o = moe.moe_orthogonalize(g, out=g)
+    for e in (0, 40000, 65534):
+        check_matrices(o[e:e + 1], f64(some[e % 7:e % 7 + 1]), rng)
+    assert torch.equal(o[7:14], o[:7]) and torch.equal(o[-7:], o[1:8])
+    assert moe.moe_device_status() == 0
+
+
 @pytest.mark.parametrize("steps", [1, 2, 8])
 @pytest.mark.parametrize("r,c", [(60, 200), (200, 60)])
 def test_steps(cuda_lib, steps, r, c):
