@@ -30,8 +30,8 @@
 // cluster of up to 8 blocks that exchange their sums through distributed shared
 // memory. Short rows share a block.
 //
-// Bound by HBM: norm backward of 8192 x 4096 BF16 rows 50 us (5.4 TB/s over the
-// 268 MB that it has to move), the join's 77 us (5.2 TB/s over 403 MB), the join
+// Bound by HBM: norm backward of 8192 x 4096 BF16 rows 51 us (5.3 TB/s over the
+// 268 MB that it has to move), the join's 78 us (5.2 TB/s over 403 MB), the join
 // of 16384 x 2048 F16 rows 51 us (5.3 TB/s over 268 MB), with the combine of
 // 4096 x 8 expert rows 43 us (4.3 TB/s over 185 MB). A call for 16 tokens takes
 // 3 to 5 us on the GPU, less than its host side.
