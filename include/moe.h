@@ -924,11 +924,11 @@ moe_status moe_block_join_backward(const void* dout, const void* dnormed, const 
  *   X <- 3.4445 X + (-4.7750 A + 2.0315 A A) X
  * (five steps take the singular values that are not much below the largest
  * into about [0.7, 1.2] and keep the singular vectors). Products run on the
- * tensor cores with FP16 pairs as operands (22 bits; the last one of a BF16
- * result with 11) and FP32 accumulators: the result is right to about its
- * type's rounding, to some 2^-13 (2-norm over the matrix) where it goes into
- * FP32 weights. A matrix with a NaN or an infinity becomes NaN as a whole, the
- * others of the batch are not touched by it; a matrix of zeros stays zero.
+ * tensor cores with FP16 pairs as operands (22 bits) and FP32 accumulators:
+ * the result is right to about its type's rounding, to some 2^-13 (2-norm over
+ * the matrix) where it goes into FP32 weights. A matrix with a NaN or an
+ * infinity becomes NaN as a whole, the others of the batch are not touched by
+ * it; a matrix of zeros stays zero.
  *
  *   E           0 .. 65535 matrices, dense, one behind the other.
  *   rows, cols  0 .. 65536, either may be the longer (no element: nothing is

@@ -622,8 +622,7 @@ __device__ __forceinline__ void store_result(const NsArgs& a, float* tile, int r
   }
 }
 
-// SINGLE: the product of the hi parts alone.
-template <int MODE, bool P_MN, bool Q_MN, bool SINGLE>
+template <int MODE, bool P_MN, bool Q_MN>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
     ns_kernel(const __grid_constant__ CUtensorMap p_hi, const __grid_constant__ CUtensorMap p_lo,
               const __grid_constant__ CUtensorMap q_hi, const __grid_constant__ CUtensorMap q_lo,
@@ -695,7 +694,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           if (!ok) break;
           uint8_t* st = smem + stage * STAGE_BYTES;
           const uint32_t bar = peer_u32(&full[stage], 0);
-          peer_arrive_expect_tx(bar, same || SINGLE ? STAGE_BYTES / 2 : STAGE_BYTES);
+          peer_arrive_expect_tx(bar, same ? STAGE_BYTES / 2 : STAGE_BYTES);
           const int k0 = kb * BK;
           auto load = [&](uint8_t* dst, const CUtensorMap* map, bool mn_major, int at) {
             if (!mn_major) {
@@ -706,8 +705,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
           };
           load(st, &p_hi, P_MN, m0);
           if (!same) load(st + 2 * OP_BYTES, &q_hi, Q_MN, n0);
-          if (!SINGLE) load(st + OP_BYTES, &p_lo, P_MN, m0);
-          if (!same && !SINGLE) load(st + 3 * OP_BYTES, &q_lo, Q_MN, n0);
+          load(st + OP_BYTES, &p_lo, P_MN, m0);
+          if (!same) load(st + 3 * OP_BYTES, &q_lo, Q_MN, n0);
           ++issued;
           if (++stage == STAGES) {
             stage = 0;
@@ -750,10 +749,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NUM_THREADS, 1)
                 return Q_MN ? sdesc_mnmajor_sw128(at + k * 2048, BOX, 1024) : sdesc_kmajor_sw128(at + k * UMMA_K * 2);
               };
               pair_umma_f16(d, pd(ph), qd(qh), idesc, (kb > t.kb0 || k > 0) ? 1u : 0u);
-              if (!SINGLE) {
-                pair_umma_f16(d, pd(pl), qd(qh), idesc, 1u);
-                pair_umma_f16(d, pd(ph), qd(ql), idesc, 1u);
-              }
+              pair_umma_f16(d, pd(pl), qd(qh), idesc, 1u);
+              pair_umma_f16(d, pd(ph), qd(ql), idesc, 1u);
             }
             pair_commit(&empty[stage]);
             if (++stage == STAGES) {
@@ -1355,7 +1352,7 @@ class Maps {
   int64_t E_;
 };
 
-template <int MODE, bool P_MN, bool Q_MN, bool SINGLE = false>
+template <int MODE, bool P_MN, bool Q_MN>
 cudaError_t launch_product(int64_t E, Maps& maps, const Pair& p, const Pair& q, NsArgs args, int num_pairs, cudaStream_t s,
                            const char** why, int parts = 1) {
   const CUtensorMap* pm = maps.of(p, P_MN ? 64 : BM);
@@ -1371,7 +1368,7 @@ cudaError_t launch_product(int64_t E, Maps& maps, const Pair& p, const Pair& q, 
   args.tiles_per_matrix = static_cast<uint32_t>(per);
   args.tiles = static_cast<uint32_t>(E * per * parts);
   const int64_t pairs = std::min<int64_t>(args.tiles, num_pairs);
-  return launch_dependent(ns_kernel<MODE, P_MN, Q_MN, SINGLE>, dim3(static_cast<unsigned>(2 * pairs)), dim3(NUM_THREADS),
+  return launch_dependent(ns_kernel<MODE, P_MN, Q_MN>, dim3(static_cast<unsigned>(2 * pairs)), dim3(NUM_THREADS),
                           SMEM_BYTES, s, pm[0], pm[1], qm[0], qm[1], args);
 }
 
@@ -1395,17 +1392,15 @@ bool two_steps_pay(int64_t E, int64_t s, int64_t l) {
 
 cudaError_t allow_shared_memory() {
   const void* kernels[] = {
-      reinterpret_cast<const void*>(ns_kernel<GRAM, false, false, false>),
-      reinterpret_cast<const void*>(ns_kernel<GRAM, true, true, false>),
-      reinterpret_cast<const void*>(ns_kernel<GRAM_PART, false, false, false>),
-      reinterpret_cast<const void*>(ns_kernel<GRAM_PART, true, true, false>),
-      reinterpret_cast<const void*>(ns_kernel<POLY, false, false, false>),
-      reinterpret_cast<const void*>(ns_kernel<APPLY, false, false, false>),
-      reinterpret_cast<const void*>(ns_kernel<APPLY, false, true, false>),
-      reinterpret_cast<const void*>(ns_kernel<FINAL, false, false, false>),
-      reinterpret_cast<const void*>(ns_kernel<FINAL, false, true, false>),
-      reinterpret_cast<const void*>(ns_kernel<FINAL, false, false, true>),
-      reinterpret_cast<const void*>(ns_kernel<FINAL, false, true, true>),
+      reinterpret_cast<const void*>(ns_kernel<GRAM, false, false>),
+      reinterpret_cast<const void*>(ns_kernel<GRAM, true, true>),
+      reinterpret_cast<const void*>(ns_kernel<GRAM_PART, false, false>),
+      reinterpret_cast<const void*>(ns_kernel<GRAM_PART, true, true>),
+      reinterpret_cast<const void*>(ns_kernel<POLY, false, false>),
+      reinterpret_cast<const void*>(ns_kernel<APPLY, false, false>),
+      reinterpret_cast<const void*>(ns_kernel<APPLY, false, true>),
+      reinterpret_cast<const void*>(ns_kernel<FINAL, false, false>),
+      reinterpret_cast<const void*>(ns_kernel<FINAL, false, true>),
   };
   for (const void* k : kernels) {
     const cudaError_t err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_BYTES);
@@ -1429,7 +1424,7 @@ cudaError_t resident_pairs(int* pairs) {
   cfg.gridDim = dim3(2);
   cfg.blockDim = dim3(NUM_THREADS);
   cfg.dynamicSmemBytes = SMEM_BYTES;
-  err = cudaOccupancyMaxActiveClusters(pairs, ns_kernel<POLY, false, false, false>, &cfg);
+  err = cudaOccupancyMaxActiveClusters(pairs, ns_kernel<POLY, false, false>, &cfg);
   if (err != cudaSuccess) return err;
   if (*pairs < 1) return cudaErrorLaunchOutOfResources;
   if (dev < MAX_DEVICES) known[dev].store(*pairs, std::memory_order_release);
@@ -1711,14 +1706,8 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
                  : launch_product<APPLY, false, true>(E, maps, q, x, f, pairs, stream, why);
     } else {
       f.scale = pow2(-q_exp - X_EXP);
-      // A BF16 result of one step (B, at most 3.45): the hi parts' 11 bits leave it off by some 2^-12, an eighth of its
-      // own rounding; a third of the product's time.
-      if (now == 1 && o.result_dtype == MOE_BF16)
-        err = tall ? launch_product<FINAL, false, false, true>(E, maps, x, q, f, pairs, stream, why)
-                   : launch_product<FINAL, false, true, true>(E, maps, q, x, f, pairs, stream, why);
-      else
-        err = tall ? launch_product<FINAL, false, false>(E, maps, x, q, f, pairs, stream, why)
-                   : launch_product<FINAL, false, true>(E, maps, q, x, f, pairs, stream, why);
+      err = tall ? launch_product<FINAL, false, false>(E, maps, x, q, f, pairs, stream, why)
+                 : launch_product<FINAL, false, true>(E, maps, q, x, f, pairs, stream, why);
     }
     if (err != cudaSuccess) return err;
     std::swap(x, next);
