@@ -332,12 +332,23 @@ struct Turn {
   }
 };
 
-// A round's rows are there; a wait that runs out leaves its results undefined.
+// Whether a wait of the block has run out. WARP: asked by a whole warp, whose
+// lanes all get one answer (another warp may be giving up on a later round).
+template <bool WARP>
+__device__ __forceinline__ bool ring_gave_up(const Ring& ring) {
+  const bool gave_up = *const_cast<const volatile int*>(&ring.abort_flag) != 0;
+  return WARP ? __any_sync(FULL_MASK, gave_up) : gave_up;
+}
+
+// A round's rows are there; a wait that runs out leaves the call's results
+// undefined, and no round after it is copied or waited for.
 // Every thread of the block waits here: the clock is read after many tries only.
 __device__ __forceinline__ void ring_wait(Ring& ring, const Turn& turn, uint32_t* status) {
   uint64_t* bar = &ring.full[turn.slot];
-  for (int tries = 0; tries < 256; ++tries)
+  for (int tries = 0; tries < 256; ++tries) {
     if (mbar_try_wait(bar, turn.parity)) return;
+    if (ring_gave_up<false>(ring)) return;
+  }
   mbar_wait_bounded(bar, turn.parity, &ring.abort_flag, status, ST_ROWS, WAIT_LIMIT_NS);
 }
 
@@ -496,8 +507,7 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), BRANCH, ELEME
   uint32_t issued = 0, issue_t0 = first_row;
   Turn fill{0, 0u};
   uint32_t ahead = BRANCH == 2 && BULK ? slot_of(issue_t0) : 0;   // slots of the round to be issued next
-  auto issue = [&]() {   // by the first warp of the block
-    if (issue_t0 >= rows) return;
+  auto arm = [&]() {
     uint8_t* dst = stage_smem + fill.slot * stage_bytes;
     uint64_t* bar = &ring.full[fill.slot];
     const int64_t at = static_cast<int64_t>(issue_t0) * a.H + rank * tpr * COLS;
@@ -542,7 +552,9 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), BRANCH, ELEME
       if (ELEMENT)
         copy_rows<T>(dst + stage_bytes - block_bytes, static_cast<const T*>(a.gate) + at, n, row_bytes, a.H, cluster, bar);
     }
-    ++issued;
+  };
+  auto issue = [&]() {   // by the first warp of the block
+    if (issue_t0 >= rows || !arm_next(issued, ring_gave_up<true>(ring), arm)) return;
     fill.next(stages);
     issue_t0 += step;
     if (BRANCH == 2) ahead = slot_of(issue_t0);
@@ -793,8 +805,7 @@ __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel
   uint32_t issued = 0, issue_t0 = first_row;
   const uint32_t lane = threadIdx.x & 31;
   Turn fill{0, 0u};
-  auto issue = [&]() {   // by the first thread of the block, loose rows by its first warp
-    if (issue_t0 >= rows) return;
+  auto arm = [&]() {
     uint8_t* dst = stage_smem + fill.slot * stage_bytes;
     uint64_t* bar = &ring.full[fill.slot];
     const int64_t at = static_cast<int64_t>(issue_t0) * a.H + rank * block_cols;
@@ -829,7 +840,9 @@ __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel
         if (ELEMENT) copy(AT_G, a.gate);
       }
     }
-    ++issued;
+  };
+  auto issue = [&]() {   // by the first thread of the block, loose rows by its first warp
+    if (issue_t0 >= rows || !arm_next(issued, ring_gave_up<!VEC>(ring), arm)) return;
     fill.next(stages);
     issue_t0 += step;
   };

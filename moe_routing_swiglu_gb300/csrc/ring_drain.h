@@ -13,6 +13,12 @@
 // block's last barrier (no role arms anything after it, and the abort flag is
 // final) and look at that flag, not at the issuing role's own result.
 //
+// Where the threads that wait go on after a give-up (rounds with barriers that
+// every one has to reach), the role that arms the stages must stop by itself: the
+// slot that was given up on still has its copy in flight and its phase open, so
+// that to arm it again would be an arrival too many and a second copy into the
+// same memory, and the drain's parity would be of another phase.
+//
 // No CUDA header: a host test compiles this file alone.
 #pragma once
 #include <cstdint>
@@ -33,6 +39,17 @@ MOE_RING_FN void drain_ring(uint32_t issued, uint32_t depth, Wait wait) {
     const uint32_t n = issued - i;
     wait(n % depth, (n / depth) & 1u);
   }
+}
+
+// Arms the next stage unless a wait of an earlier round was given up, which the
+// caller has read after the barrier that ended that round. `issued` then ends as
+// the number of stages that the drain may wait for. Whether the stage was armed.
+template <typename Arm>
+MOE_RING_FN bool arm_next(uint32_t& issued, bool gave_up, Arm arm) {
+  if (gave_up) return false;
+  arm();
+  ++issued;
+  return true;
 }
 
 }  // namespace moe

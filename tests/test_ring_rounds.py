@@ -1,0 +1,104 @@
+"""The norms around a block copy rows into a ring while every thread of the block waits round after round, and goes on
+when a wait runs out (the rounds have barriers that all must reach). A model of that on the CPU, with the header that
+the kernels arm and drain their stages by: no stage is armed over a copy in flight, none is in flight when the block
+exits. No GPU is made to time out for this."""
+import re
+import shutil
+import subprocess
+
+import pytest
+
+from moe_routing_swiglu_gb300 import _build
+
+MODEL = r"""
+#include <cstdio>
+#include <vector>
+#include "ring_drain.h"
+
+// A barrier's phases end in order; each is armed once, and its copy lands or is late.
+struct Bar { uint32_t armed = 0, ended = 0; };
+
+int main() {
+  long cases = 0, gave_up_cases = 0;
+  for (uint32_t depth = 2; depth <= 6; ++depth)
+    for (uint32_t behind = 0; behind <= 1; ++behind)                   // rounds after whose barrier a stage is free
+      for (uint32_t rounds = 1; rounds <= 2 * depth + 2; ++rounds)
+        for (uint32_t late = 0; late < (1u << rounds); ++late) {        // stages whose copies land with the drain only
+          std::vector<Bar> bar(depth);
+          uint32_t issued = 0, next = 0;
+          bool flag = false, bad = false;
+          auto issue = [&] {
+            if (next >= rounds) return;
+            const bool asked = IGNORE_GIVE_UP ? false : flag;
+            if (!moe::arm_next(issued, asked, [&] {
+                  Bar& b = bar[next % depth];
+                  if (b.armed != b.ended) { bad = true; return; }      // a copy still in flight there
+                  ++b.armed;
+                  if (((late >> next) & 1u) == 0) ++b.ended;
+                })) return;
+            ++next;
+          };
+          for (uint32_t i = 0; i < depth && i < rounds; ++i) issue();
+          for (uint32_t n = 0; n < rounds + behind && !bad; ++n) {
+            if (n < rounds && !flag) {                                  // the wait for round n
+              const Bar& b = bar[n % depth];
+              const bool there = b.armed == n / depth + 1 && b.ended == b.armed;
+              if (!there) flag = true;
+            }
+            if (n >= behind) issue();                                   // after the round's barrier
+          }
+          if (!bad && flag) {
+            moe::drain_ring(issued, depth, [&](uint32_t slot, uint32_t parity) {
+              Bar& b = bar[slot];
+              if (b.armed == 0) { bad = true; return; }
+              if ((b.ended & 1u) == parity) {
+                if (b.armed == b.ended) { bad = true; return; }         // nothing in flight will end it
+                ++b.ended;
+              }
+            });
+            ++gave_up_cases;
+          }
+          for (const Bar& b : bar) bad |= b.armed != b.ended;
+          if (bad) return std::printf("depth %u rounds %u late %x\n", depth, rounds, late), 1;
+          ++cases;
+        }
+  std::printf("%ld %ld\n", cases, gave_up_cases);
+  return 0;
+}
+"""
+
+
+def run_model(tmp_path, ignore):
+    gxx = shutil.which("g++")
+    if gxx is None:
+        pytest.skip("no host compiler")
+    src, exe = tmp_path / "model.cpp", tmp_path / "model"
+    src.write_text(MODEL)
+    subprocess.run([gxx, "-std=c++17", "-O1", "-Wall", "-Werror", f"-DIGNORE_GIVE_UP={ignore}", "-I", str(_build.CSRC),
+                    str(src), "-o", str(exe)], check=True)
+    return subprocess.run([str(exe)], capture_output=True, text=True)
+
+
+def test_no_stage_is_armed_after_a_give_up(tmp_path):
+    run = run_model(tmp_path, 0)
+    assert run.returncode == 0, run.stdout
+    cases, gave_up = map(int, run.stdout.split())
+    assert gave_up > 10000 and cases > gave_up
+
+
+def test_the_model_sees_an_issuer_that_goes_on(tmp_path):
+    assert run_model(tmp_path, 1).returncode == 1
+
+
+def test_the_kernels_arm_through_the_header():
+    """Stages are armed in the `arm` of arm_next only, asked with the block's flag, and every ring ends in its drain."""
+    text = re.sub(r"//[^\n]*", "", (_build.CSRC / "block_norm.cu").read_text())
+    kernels = [text[m.start():] for m in re.finditer(r"__global__ void", text)]
+    kernels = [k[:k.index("\n}\n")] for k in kernels if "ring_wait(" in k[:k.index("\n}\n")]]
+    assert len(kernels) == 2
+    for k in kernels:
+        arm = re.search(r"auto arm = \[&\]\(\) \{\n(.*?)\n  \};\n", k, re.S).group(1)
+        assert k.count("mbar_arrive_expect_tx(") == arm.count("mbar_arrive_expect_tx(") > 0
+        assert k.count("arm_next(") == 1
+        assert re.search(r"if \(issue_t0 >= rows \|\| !arm_next\(issued, ring_gave_up<[^>]*>\(ring\), arm\)\) return;", k)
+        assert "ring_end(ring, issued, stages, a.status);" in k
