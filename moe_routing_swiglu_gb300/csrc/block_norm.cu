@@ -532,9 +532,10 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), BRANCH, ELEME
       uint32_t bytes = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) bytes += copies[i].bytes;
-      bytes = __reduce_add_sync(FULL_MASK, bytes);   // after every lane's stores
+      bytes = __reduce_add_sync(FULL_MASK, bytes);
+      __syncwarp();   // the lanes' stores (loose_row) before the arrive, which the sum alone does not order
       if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-      __syncwarp();
+      __syncwarp();   // the expected bytes before the copies that bring them
 #pragma unroll
       for (int i = 0; i < 4; ++i) loose_load(copies[i], bar);
     } else if (BRANCH == 2) {
@@ -822,9 +823,10 @@ __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel
           const T* p = static_cast<const T*>(tensors[i]);
           copy = loose_row<T>(dst + PLACES[i] * block_bytes, p + at, row_bytes * n, p, p + total);
         }
-      const uint32_t bytes = __reduce_add_sync(FULL_MASK, copy.bytes);   // after every lane's stores
+      const uint32_t bytes = __reduce_add_sync(FULL_MASK, copy.bytes);
+      __syncwarp();   // the lanes' stores (loose_row) before the arrive, which the sum alone does not order
       if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-      __syncwarp();
+      __syncwarp();   // the expected bytes before the copies that bring them
       loose_load(copy, bar);
     } else {
       const uint32_t bytes = row_bytes * n;

@@ -102,3 +102,15 @@ def test_the_kernels_arm_through_the_header():
         assert k.count("arm_next(") == 1
         assert re.search(r"if \(issue_t0 >= rows \|\| !arm_next\(issued, ring_gave_up<[^>]*>\(ring\), arm\)\) return;", k)
         assert "ring_end(ring, issued, stages, a.status);" in k
+
+
+def test_elements_stored_by_hand_are_ordered_before_the_arrive():
+    """loose_row stores the elements of a tensor's partial granules lane by lane, and lane 0 arrives for the warp: only
+    __syncwarp orders the one before the other (a reduction gathers the lanes without ordering their stores)."""
+    text = re.sub(r"//[^\n]*", "", (_build.CSRC / "block_norm.cu").read_text())
+    found = 0
+    for m in re.finditer(r"loose_row<T>\(dst", text):
+        before_arrive = text[m.end():].split("mbar_arrive_expect_tx(", 1)[0]
+        assert re.search(r"__syncwarp\(\);\s*if \(lane == 0\) $", before_arrive)
+        found += 1
+    assert found == 2
