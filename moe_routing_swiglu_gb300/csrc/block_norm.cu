@@ -332,24 +332,16 @@ struct Turn {
   }
 };
 
-// Whether a wait of the block has run out. WARP: asked by a whole warp, whose
-// lanes all get one answer (another warp may be giving up on a later round).
-template <bool WARP>
-__device__ __forceinline__ bool ring_gave_up(const Ring& ring) {
-  const bool gave_up = *const_cast<const volatile int*>(&ring.abort_flag) != 0;
-  return WARP ? __any_sync(FULL_MASK, gave_up) : gave_up;
-}
-
-// A round's rows are there; a wait that runs out leaves the call's results
-// undefined, and no round after it is copied or waited for.
+// Whether a round's rows are there; a wait that runs out leaves the call's
+// results undefined.
 // Every thread of the block waits here: the clock is read after many tries only.
-__device__ __forceinline__ void ring_wait(Ring& ring, const Turn& turn, uint32_t* status) {
+__device__ __forceinline__ bool ring_wait(Ring& ring, const Turn& turn, uint32_t* status) {
   uint64_t* bar = &ring.full[turn.slot];
   for (int tries = 0; tries < 256; ++tries) {
-    if (mbar_try_wait(bar, turn.parity)) return;
-    if (ring_gave_up<false>(ring)) return;
+    if (mbar_try_wait(bar, turn.parity)) return true;
+    if (*static_cast<volatile int*>(&ring.abort_flag) != 0) return false;   // the rounds after a give-up end at once
   }
-  mbar_wait_bounded(bar, turn.parity, &ring.abort_flag, status, ST_ROWS, WAIT_LIMIT_NS);
+  return mbar_wait_bounded(bar, turn.parity, &ring.abort_flag, status, ST_ROWS, WAIT_LIMIT_NS);
 }
 
 // Before the block exits: the copies that nobody waited for (after a give-up).
@@ -507,7 +499,8 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), BRANCH, ELEME
   uint32_t issued = 0, issue_t0 = first_row;
   Turn fill{0, 0u};
   uint32_t ahead = BRANCH == 2 && BULK ? slot_of(issue_t0) : 0;   // slots of the round to be issued next
-  auto arm = [&]() {
+  auto issue = [&]() {   // by the first warp of the block
+    if (issue_t0 >= rows) return;
     uint8_t* dst = stage_smem + fill.slot * stage_bytes;
     uint64_t* bar = &ring.full[fill.slot];
     const int64_t at = static_cast<int64_t>(issue_t0) * a.H + rank * tpr * COLS;
@@ -553,9 +546,7 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), BRANCH, ELEME
       if (ELEMENT)
         copy_rows<T>(dst + stage_bytes - block_bytes, static_cast<const T*>(a.gate) + at, n, row_bytes, a.H, cluster, bar);
     }
-  };
-  auto issue = [&]() {   // by the first warp of the block
-    if (issue_t0 >= rows || !arm_next(issued, ring_gave_up<true>(ring), arm)) return;
+    ++issued;
     fill.next(stages);
     issue_t0 += step;
     if (BRANCH == 2) ahead = slot_of(issue_t0);
@@ -616,7 +607,7 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), BRANCH, ELEME
     float x[R][COLS], f[R][COLS];
     const uint8_t* stage = mine + turn.slot * stage_bytes;
     if (BULK) {
-      ring_wait(ring, turn, a.status);
+      issue_only_after(__all_sync(FULL_MASK, ring_wait(ring, turn, a.status)), issue_t0, rows);
       turn.next(stages);
     }
 #pragma unroll
@@ -806,7 +797,8 @@ __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel
   uint32_t issued = 0, issue_t0 = first_row;
   const uint32_t lane = threadIdx.x & 31;
   Turn fill{0, 0u};
-  auto arm = [&]() {
+  auto issue = [&]() {   // by the first thread of the block, loose rows by its first warp
+    if (issue_t0 >= rows) return;
     uint8_t* dst = stage_smem + fill.slot * stage_bytes;
     uint64_t* bar = &ring.full[fill.slot];
     const int64_t at = static_cast<int64_t>(issue_t0) * a.H + rank * block_cols;
@@ -842,9 +834,7 @@ __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel
         if (ELEMENT) copy(AT_G, a.gate);
       }
     }
-  };
-  auto issue = [&]() {   // by the first thread of the block, loose rows by its first warp
-    if (issue_t0 >= rows || !arm_next(issued, ring_gave_up<!VEC>(ring), arm)) return;
+    ++issued;
     fill.next(stages);
     issue_t0 += step;
   };
@@ -1005,7 +995,7 @@ __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel
       const float share_before = share, gt = gate_next;
       const int slot_before = turn.slot == 0 ? stages - 1 : turn.slot - 1;
       if (ahead) {
-        ring_wait(ring, turn, a.status);
+        issue_only_after(ring_wait(ring, turn, a.status), issue_t0, rows);
         float p[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) p[i] = 0.0f;
@@ -1054,7 +1044,7 @@ __global__ void __launch_bounds__(MAX_TPR / CHUNKS, CHUNKS) join_backward_kernel
       for (int i = 0; i < N; ++i) p[i] = 0.0f;
       const float gt = gate_next;
       gate_next = gate_of(t + step);
-      if (BULK) ring_wait(ring, turn, a.status);
+      if (BULK) issue_only_after(__all_sync(FULL_MASK, ring_wait(ring, turn, a.status)), issue_t0, rows);
       load_part(t, 0, turn.slot, v);
       add_up(v, 0, p);
       row_sum<N>(p, &sums, half, tpr, cluster, rank);

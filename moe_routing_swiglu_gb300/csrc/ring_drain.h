@@ -13,11 +13,12 @@
 // block's last barrier (no role arms anything after it, and the abort flag is
 // final) and look at that flag, not at the issuing role's own result.
 //
-// Where the threads that wait go on after a give-up (rounds with barriers that
-// every one has to reach), the role that arms the stages must stop by itself: the
-// slot that was given up on still has its copy in flight and its phase open, so
-// that to arm it again would be an arrival too many and a second copy into the
-// same memory, and the drain's parity would be of another phase.
+// Where threads go on after a give-up (rounds with barriers that every one has to
+// reach), the role that arms the stages must stop by itself: the slot that was
+// given up on still has its copy in flight and its phase open, so that to arm it
+// again would be an arrival too many and a second copy into the same memory, and
+// the drain's parity would be of another phase. Its own waits tell it that: it
+// arms a slot only after its own wait for the stage before ended with the phase.
 //
 // No CUDA header: a host test compiles this file alone.
 #pragma once
@@ -41,15 +42,10 @@ MOE_RING_FN void drain_ring(uint32_t issued, uint32_t depth, Wait wait) {
   }
 }
 
-// Arms the next stage unless a wait of an earlier round was given up, which the
-// caller has read after the barrier that ended that round. `issued` then ends as
-// the number of stages that the drain may wait for. Whether the stage was armed.
-template <typename Arm>
-MOE_RING_FN bool arm_next(uint32_t& issued, bool gave_up, Arm arm) {
-  if (gave_up) return false;
-  arm();
-  ++issued;
-  return true;
+// What the arming role does with its own wait's result: `next`, the first row of
+// the stage that it would arm next, passes `end` for good after a give-up.
+MOE_RING_FN void issue_only_after(bool waited, uint32_t& next, uint32_t end) {
+  if (!waited) next = end;
 }
 
 }  // namespace moe
