@@ -1140,12 +1140,15 @@ __global__ void __launch_bounds__(BLOCK) column_sum_kernel(const float* partial,
 // Shared memory of an SM, of which every block takes 1 KB and its static part.
 constexpr size_t SM_SHARED = 228 * 1024, BLOCK_SHARED = 227 * 1024;
 
+// `fixed`: at least the kernel's static shared memory.
 template <typename K, typename A>
-cudaError_t launch_rows(K kernel, const RowShape& s, int64_t units, size_t smem, int stages, const A& args,
+cudaError_t launch_rows(K kernel, const RowShape& s, int64_t units, size_t smem, size_t fixed, int stages, const A& args,
                         cudaStream_t stream) {
   if (smem > 32 * 1024) {   // with the static part possibly past the default of 48 KB
-    const cudaError_t err =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // All that a block can have, not this call's size: the attribute is the
+    // kernel's, and a call of another thread may come between it and the launch.
+    const cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 static_cast<int>(BLOCK_SHARED - fixed));
     if (err != cudaSuccess) return err;
   }
   cudaLaunchConfig_t cfg = {};
@@ -1202,6 +1205,7 @@ cudaError_t launch_join_t(moe_dtype dtype, JoinArgs a, int branch, int num_sms, 
   const int64_t resident = std::max(1, std::min(16, join_threads(sizeof(T), branch, element) / (s.tpr * s.rows)));
   const int64_t most = std::max<int64_t>(1, resident * num_sms / s.cluster);
   const int64_t arrays = 1 + (branch == 2 ? a.top_k : branch) + (element ? 1 : 0);
+  constexpr size_t fixed = sizeof(RowSums<2>) + sizeof(Ring) + 256;
   auto rounds_of = [&](int rows, int64_t* units) {
     const int64_t groups = (a.T + s.rows * rows - 1) / (s.rows * rows);
     *units = std::min(groups, most);
@@ -1213,7 +1217,7 @@ cudaError_t launch_join_t(moe_dtype dtype, JoinArgs a, int branch, int num_sms, 
   if ((branch != 2 || a.top_k <= 32) && rounds_of(1, &units) > 1) {
     const int rows = join_rows(true, branch);
     const size_t stage = stage_size(s, a.H, COLS, rows, arrays, sizeof(T), vec);
-    stages = ring_stages(stage, resident, sizeof(RowSums<2>) + sizeof(Ring) + 256, rounds_of(rows, &units));
+    stages = ring_stages(stage, resident, fixed, rounds_of(rows, &units));
     if (stages < 2) stages = 0;
     smem = stage * stages;
   }
@@ -1227,7 +1231,7 @@ cudaError_t launch_join_t(moe_dtype dtype, JoinArgs a, int branch, int num_sms, 
                                        : pick_join<T, false, true>(branch, element))
                      : vec      ? pick_join<T, true, false>(branch, element)
                                 : pick_join<T, false, false>(branch, element),
-                     s, units, smem, stages, a, stream);
+                     s, units, smem, fixed, stages, a, stream);
 }
 
 template <typename T, bool VEC, int CHUNKS, bool BULK>
@@ -1261,6 +1265,7 @@ cudaError_t launch_join_backward_t(moe_dtype dtype, JoinBackwardArgs a, int64_t*
   const int64_t arrays = 1 + (f ? 1 : 0) + (next ? 2 : 0) + (element ? 1 : 0);
   const int chunks = vec ? backward_chunks(a.H) : 1;
   RowShape s = row_shape(a.H, chunks);
+  constexpr size_t fixed = sizeof(RowSums<6>) + sizeof(Ring) + 256;
   int stages = 0;
   size_t smem = 0;
   // Short loose rows of 16 bits that L2 holds gain nothing from the ring (16384 x
@@ -1270,7 +1275,6 @@ cudaError_t launch_join_backward_t(moe_dtype dtype, JoinBackwardArgs a, int64_t*
   if (vec || sizeof(T) == 4 || a.H >= 1024 || !in_l2) {
     // Three stages hold the rounds at work and one on its way; rather fewer blocks than fewer stages.
     const size_t stage = stage_size(s, a.H, COLS * chunks, 1, arrays, sizeof(T), vec);
-    const size_t fixed = sizeof(RowSums<6>) + sizeof(Ring) + 256;
     const int64_t groups = (a.T + s.rows - 1) / s.rows;
     for (int64_t resident = backward_resident(s); resident > 0; resident /= 2) {
       *units = backward_units(s, a.T, resident);
@@ -1294,7 +1298,7 @@ cudaError_t launch_join_backward_t(moe_dtype dtype, JoinBackwardArgs a, int64_t*
                                                  : pick_backward<T, true, 1, true>(f, next, element))
                      : vec ? pick_backward<T, true, 1, false>(f, next, element)
                            : pick_backward<T, false, 1, false>(f, next, element),
-                     s, *units, smem, stages, a, stream);
+                     s, *units, smem, fixed, stages, a, stream);
 }
 
 }  // namespace
