@@ -54,6 +54,7 @@
 #include "moe_common.cuh"
 #include "moe_internal.h"
 #include "ring_drain.h"
+#include "round_sums.h"
 
 namespace moe {
 namespace {
@@ -138,9 +139,9 @@ __device__ __forceinline__ V warp_sum(V v) {
 }
 
 // partial[e][chunk]: the sum of squares of the chunk's u; updates the momentum.
-// A thread's squares are added in FP32 (a norm is off by fewer than 2^-19 of it
-// for any number of them that a chunk has): rounds whose sum FP32 does not hold
-// are added in FP64, of which the SMs have little.
+// A thread's squares are added in FP32, 32 of a round, 16 rounds, then a warp's: 53
+// roundings, which leave a norm off by fewer than 2^-19 of it. The rest is FP64, as
+// are rounds whose sum FP32 does not hold.
 template <typename T, bool MOMENTUM>
 __global__ void __launch_bounds__(PRE_THREADS) squares_kernel(const PreArgs a) {
   __shared__ double sm[PRE_THREADS / 32];
@@ -150,8 +151,7 @@ __global__ void __launch_bounds__(PRE_THREADS) squares_kernel(const PreArgs a) {
   float* mp = MOMENTUM ? a.m + blockIdx.y * a.n : nullptr;
   const int64_t lo = blockIdx.x * a.chunk, hi = min(lo + a.chunk, a.n);
   constexpr int ROUND = PRE_THREADS * 8 * PRE_GROUP;
-  float near = 0.0f;
-  double far = 0.0;
+  RoundSums total;
   for (int64_t i0 = lo; i0 < hi; i0 += ROUND) {
     const int64_t at = i0 + static_cast<int64_t>(threadIdx.x) * 8;
     const bool whole = a.vec && i0 + ROUND <= hi;
@@ -202,24 +202,25 @@ __global__ void __launch_bounds__(PRE_THREADS) squares_kernel(const PreArgs a) {
     }
     // 32 squares that each lose at most 2^-150 do not show in a sum of 2^-60; 2^80 leaves room for the other rounds.
     if (sum >= 0x1p-60f && sum <= 0x1p80f) {
-      near += sum;
+      total.add(sum);
     } else {
       Squares s{0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < PRE_GROUP; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j) s.add(u[k].e[j]);
-      far += s.total();
+      total.far += s.total();
     }
   }
-  near = warp_sum(near);
+  const float near = warp_sum(total.near);
+  double far = total.far;
   if (__any_sync(FULL_MASK, far != 0.0)) far = warp_sum(far);   // NaN != 0 too
   if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = near + far;
   __syncthreads();
   if (threadIdx.x == 0) {
-    double total = 0.0;
-    for (int w = 0; w < PRE_THREADS / 32; ++w) total += sm[w];
-    a.partial[static_cast<int64_t>(blockIdx.y) * a.chunks + blockIdx.x] = total;
+    double sum = 0.0;
+    for (int w = 0; w < PRE_THREADS / 32; ++w) sum += sm[w];
+    a.partial[static_cast<int64_t>(blockIdx.y) * a.chunks + blockIdx.x] = sum;
   }
 }
 
