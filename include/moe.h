@@ -977,7 +977,9 @@ typedef struct {
  * A matrix whose grad or momentum holds a NaN or an infinity gets NaN weights:
  * moe_grad_norm tells before the step.
  *   params     host, read during the call only.
- * The tensors and the workspace must not overlap.
+ * The tensors and the workspace must not overlap. A call that fails leaves them
+ * as they were, unless a launch after its first was rejected (MOE_ERR_CUDA):
+ * then the momentum may have been updated.
  */
 moe_status moe_muon_step(void* weight, moe_dtype weight_dtype, const void* grad, moe_dtype grad_dtype, float* momentum,
                          int64_t E, int64_t rows, int64_t cols, const moe_muon_params* params, void* workspace,

@@ -1497,11 +1497,19 @@ cudaError_t cluster_shape(int64_t E, int64_t s, int64_t l, ClusterShape* best) {
   return cudaSuccess;
 }
 
+template <typename T, bool MOMENTUM>
+cudaError_t launch_squares(const PreArgs& a, int64_t E, cudaStream_t s) {
+  return launch_dependent(squares_kernel<T, MOMENTUM>, dim3(a.chunks, static_cast<unsigned>(E)), dim3(PRE_THREADS), 0, s,
+                          a);
+}
+
+// What can be refused is refused before the squares' launch, which updates the momentum.
 template <typename T, bool MOMENTUM, bool TALL>
 cudaError_t launch_cluster(const ClusterArgs& a, int64_t E, int blocks, cudaStream_t s) {
   const auto kernel = ns_cluster_kernel<T, MOMENTUM, TALL>;
   cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, CL_BYTES);
   if (err == cudaSuccess) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (err == cudaSuccess) err = launch_squares<T, MOMENTUM>(a.pre, E, s);
   if (err != cudaSuccess) return err;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -1519,14 +1527,7 @@ cudaError_t launch_cluster(const ClusterArgs& a, int64_t E, int blocks, cudaStre
 }
 
 template <typename T, bool MOMENTUM>
-cudaError_t launch_squares(const PreArgs& a, int64_t E, cudaStream_t s) {
-  return launch_dependent(squares_kernel<T, MOMENTUM>, dim3(a.chunks, static_cast<unsigned>(E)), dim3(PRE_THREADS), 0, s,
-                          a);
-}
-template <typename T, bool MOMENTUM>
 cudaError_t launch_small(const ClusterArgs& a, int64_t E, int blocks, cudaStream_t s) {
-  const cudaError_t err = launch_squares<T, MOMENTUM>(a.pre, E, s);
-  if (err != cudaSuccess) return err;
   return a.pre.r > a.pre.c ? launch_cluster<T, MOMENTUM, true>(a, E, blocks, s)
                            : launch_cluster<T, MOMENTUM, false>(a, E, blocks, s);
 }
@@ -1628,18 +1629,29 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
                                      : launch_small<__nv_bfloat16>(args, E, shape.blocks, stream);
   }
 
+  // The maps that the products will ask for: one that cannot be had is an error
+  // before the first launch, which updates the momentum.
+  const bool tall = r > c, by_two = two_steps_pay(E, s, std::max(r, c));
+  Maps maps(E);
+  const uint32_t gram_box = tall ? 64 : BM, apply_box = tall ? BM : 64;   // of X along its rows, or across
+  bool have = maps.of(x, gram_box) && maps.of(x, apply_box) && maps.of(a, BM) && maps.of(b, BM);
+  if (by_two && o.steps >= 2) have = have && maps.of(t, BM) && maps.of(b1, BM);
+  if (o.steps > (by_two ? 2 : 1)) have = have && maps.of(next, gram_box) && maps.of(next, apply_box);
+  if (!have) {
+    *why = "cuTensorMapEncodeTiled rejected an operand";
+    return cudaErrorInvalidValue;
+  }
+
   err = o.grad_dtype == MOE_F32   ? launch_pre<float>(pre, E, stream)
         : o.grad_dtype == MOE_F16 ? launch_pre<__half>(pre, E, stream)
                                   : launch_pre<__nv_bfloat16>(pre, E, stream);
   if (err != cudaSuccess) return err;
 
-  const bool tall = r > c;
   // Every part has k-blocks: the last ones may take fewer.
   int parts = gram_parts(E, s, std::max(r, c), pairs);
   const int k_blocks = static_cast<int>((std::max(r, c) + BK - 1) / BK);
   const int split = (k_blocks + parts - 1) / parts;
   parts = (k_blocks + split - 1) / split;
-  Maps maps(E);
   NsArgs sq{};
   sq.status = status;
   sq.m = sq.n = static_cast<int>(s);
@@ -1684,7 +1696,6 @@ cudaError_t launch_newton_schulz(const NewtonSchulz& o, void* scratch, cudaStrea
     g.scale = pow2(exp);
     return launch_product<GRAM, false, false>(E, maps, p, q, g, pairs, stream, why);
   };
-  const bool by_two = two_steps_pay(E, s, std::max(r, c));
   for (int left = o.steps; left > 0;) {
     const int now = by_two && left >= 2 ? 2 : 1;
     left -= now;
