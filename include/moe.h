@@ -956,7 +956,7 @@ moe_status moe_orthogonalize(const void* matrices, moe_dtype dtype, int64_t E, i
                              size_t workspace_bytes, void* stream);
 
 typedef struct {
-  float lr;               /* finite */
+  float lr;               /* finite, as lr * weight_decay and lr * update_scale */
   float momentum_decay;   /* in [0, 1) */
   float weight_decay;     /* finite */
   float update_scale;     /* finite; commonly sqrt(max(1, rows / cols)) */

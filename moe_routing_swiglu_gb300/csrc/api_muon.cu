@@ -97,6 +97,10 @@ moe_status moe_muon_step(void* weight, moe_dtype weight_dtype, const void* grad,
   if (!std::isfinite(p->lr) || !std::isfinite(p->weight_decay) || !std::isfinite(p->update_scale) ||
       !(p->momentum_decay >= 0.0f && p->momentum_decay < 1.0f))
     return api_fail(MOE_ERR_SHAPE, "lr, weight_decay and update_scale must be finite, momentum_decay in [0, 1)");
+  const float keep = static_cast<float>(1.0 - static_cast<double>(p->lr) * p->weight_decay);
+  const float rate = static_cast<float>(static_cast<double>(p->lr) * p->update_scale);
+  if (!std::isfinite(keep) || !std::isfinite(rate))
+    return api_fail(MOE_ERR_SHAPE, "lr * weight_decay and lr * update_scale must be in FP32's range");
   moe_status st = check_common(E, rows, cols, p->steps, p->eps, workspace, workspace_bytes);
   if (st != MOE_OK) return st;
   const size_t n = static_cast<size_t>(E * rows * cols);
@@ -124,8 +128,8 @@ moe_status moe_muon_step(void* weight, moe_dtype weight_dtype, const void* grad,
   o.result = weight;
   o.result_dtype = weight_dtype;
   o.update = 1;
-  o.keep = static_cast<float>(1.0 - static_cast<double>(p->lr) * p->weight_decay);
-  o.rate = static_cast<float>(static_cast<double>(p->lr) * p->update_scale);
+  o.keep = keep;
+  o.rate = rate;
   return launch(o, workspace, stream, "moe_muon_step launch");
 }
 
