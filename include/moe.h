@@ -841,6 +841,7 @@ moe_status moe_block_norm(const void* x, moe_dtype dtype, const void* weight, mo
 /*
  * moe_block_norm_backward - from dy: dx = (dy's gradient of x) + dresidual, and
  * dweight[h] = sum over rows of dy * x / sqrt(mean(x^2) + eps).
+ *   eps         the forward's, at least 2^-80.
  *   dresidual   device, [T, H]: the gradient that reaches x past the block, or
  *               NULL for none.
  *   dx          device, [T, H] out in `dtype`.
@@ -903,6 +904,7 @@ moe_status moe_combine_join(const void* y_dispatched, moe_dtype dtype, const uin
  *             weights are given.
  *   dgate     device, out, exactly when there is a gate: [H] or [T] float, or
  *             [T, H] in `dtype`.
+ *   params    the forward's, with eps at least 2^-80.
  *   branch    the forward's (moe_combine's result for a combined branch).
  *   joined    the forward's out; it and dnormed are read with next_weight only.
  *   workspace moe_block_join_backward_workspace_size(T, H) bytes, 256-byte

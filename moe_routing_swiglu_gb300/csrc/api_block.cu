@@ -53,6 +53,14 @@ moe_status check_eps(float eps) {
   return MOE_OK;
 }
 
+// The backward's factors hold up to the cube of 1 / sqrt(mean + eps) times the
+// gradients, 2^120 of them from this eps on. Below about 2^-128 the square alone
+// is infinite, and the gradient of a row of zeros was NaN.
+moe_status check_backward_eps(float eps) {
+  if (eps < 0x1p-80f) return api_fail(MOE_ERR_SHAPE, "eps must be at least 2^-80 in a backward call");
+  return MOE_OK;
+}
+
 moe_status check_vector(const void* p, int vec_dtype, int dtype) {
   if (vec_dtype != MOE_F32 && vec_dtype != dtype)
     return api_fail(MOE_ERR_DTYPE, "weight vectors must be MOE_F32 or of the rows' dtype");
@@ -192,6 +200,7 @@ moe_status moe_block_norm_backward(const void* dy, const void* x, moe_dtype dtyp
                                    void* dx, float* dweight, void* workspace, size_t workspace_bytes, void* stream) {
   moe_status st = check_rows(dtype, T, H);
   if (st == MOE_OK) st = check_eps(eps);
+  if (st == MOE_OK) st = check_backward_eps(eps);
   if (st != MOE_OK) return st;
   if (weight == nullptr || dweight == nullptr) return api_fail(MOE_ERR_NULL, "weight and dweight must be non-NULL");
   st = check_vector(weight, weight_dtype, dtype);
@@ -261,6 +270,7 @@ moe_status moe_block_join_backward(const void* dout, const void* dnormed, const 
                                    float* dnext_weight, void* workspace, size_t workspace_bytes, void* stream) {
   moe_status st = check_rows(dtype, T, H);
   if (st == MOE_OK) st = check_params(p, dtype, T);
+  if (st == MOE_OK) st = check_backward_eps(p->eps);
   if (st != MOE_OK) return st;
   const bool next = p->next_weight != nullptr, gated = p->gate_kind != MOE_GATE_NONE;
   const bool element = p->gate_kind == MOE_GATE_ELEMENT;
