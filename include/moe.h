@@ -934,9 +934,11 @@ moe_status moe_block_join_backward(const void* dout, const void* dnormed, const 
  *
  *   E           0 .. 65535 matrices, dense, one behind the other.
  *   rows, cols  0 .. 65536, either may be the longer (no element: nothing is
- *               enqueued).
+ *               enqueued); E times the square of max(rows, cols) / 128, rounded
+ *               up, at most 2^31 - 1.
  *   steps       1 .. 100.
- *   eps         finite, > 0.
+ *   eps         finite, > 0. Entries of X under 2^-38 count as zero: a matrix
+ *               whose norm is that far below eps comes out as zeros.
  *   workspace   device, moe_orthogonalize_workspace_size(E, rows, cols) bytes,
  *               256-byte aligned, of both calls below: about 8 bytes per
  *               element, 16 min(rows, cols)^2 per matrix, and up to 34 MB for

@@ -1170,7 +1170,8 @@ def moe_block_norm_backward(dy: torch.Tensor, x: torch.Tensor, weight: torch.Ten
                             dresidual: torch.Tensor | None = None, dx=None, workspace=None,
                             stream=None) -> BlockNormGrads:
     """The gradients of moe_block_norm: dx in x's dtype, with dresidual (the
-    gradient that reaches x past the block) added, and dweight [H] float32."""
+    gradient that reaches x past the block) added, and dweight [H] float32. eps
+    is the forward's, at least 2^-80."""
     lib = load_library()
     T, H = _rows_of(x, "x")
     _vector(weight, "weight", x)
@@ -1245,7 +1246,8 @@ def moe_block_join_backward(dout: torch.Tensor | None, branch: torch.Tensor, *, 
     past the next norm) and, with next_weight, dnormed; `joined` is the
     forward's out. dbranch and dresidual are in the rows' dtype, weight
     gradients float32, dgate of the gate's shape (float32, or the rows' dtype
-    for a gate of every element); None for what the join does not have."""
+    for a gate of every element); None for what the join does not have. eps is
+    the forward's, at least 2^-80."""
     lib = load_library()
     T, H = _rows_of(branch, "branch")
     for t, name in ((dout, "dout"), (dnormed, "dnormed"), (joined, "joined")):

@@ -30,11 +30,12 @@
 // cluster of up to 8 blocks that exchange their sums through distributed shared
 // memory. Short rows share a block.
 //
-// Bound by HBM: norm backward of 8192 x 4096 BF16 rows 51 us (5.3 TB/s over the
-// 268 MB that it has to move), the join's 78 us (5.2 TB/s over 403 MB), the join
-// of 16384 x 2048 F16 rows 51 us (5.3 TB/s over 268 MB), with the combine of
-// 4096 x 8 expert rows 43 us (4.3 TB/s over 185 MB). A call for 16 tokens takes
-// 3 to 5 us on the GPU, less than its host side.
+// Bound by HBM, 8192 x 4096 BF16 rows: the norm 23 us (5.8 TB/s over the 134 MB
+// that it has to move), its backward 51 us (5.3 TB/s over 268 MB), the join's
+// backward 78 us (5.2 TB/s over 403 MB). The join of 16384 x 2048 F16 rows 51 us
+// (5.3 TB/s over 268 MB), with the combine of 4096 x 8 expert rows 43 us (4.3 TB/s
+// over 185 MB). A call for 16 tokens takes 3 to 5 us on the GPU, less than its
+// host side.
 #include <cooperative_groups.h>
 
 #include <algorithm>
@@ -446,11 +447,11 @@ __device__ __forceinline__ void stage8(const uint8_t* mine, Eight<T>& v) {
 // come through the ring; else (calls of one round a block, many slots) they are
 // loaded when their turn comes. Loose rows (not VEC) leave the ring and the
 // kernel element by element, 32 neighbours a warp: in FP32 that keeps up with HBM
-// (join of 8192 x 4095 93 us, of 4096 columns 97), in 16 bits as many narrow loads
-// and stores take as long (90 us, 54; without the ring 148).
+// (join of 8192 x 4095 92 us, of 4096 columns 95), in 16 bits as many narrow loads
+// and stores take as long (87 us, 53; without the ring 148).
 
 // Threads that an SM holds: 1024 of 64 registers where that is enough (loose rows,
-// 2048 x 8191 BF16: 24 us, 30 with 512).
+// 2048 x 8191 BF16: 25 us, 30 with 512).
 constexpr int join_threads(size_t size, int branch, bool element) {
   return size == 2 && branch < 1 && !element ? 1024 : 512;
 }
@@ -745,11 +746,11 @@ __global__ void __launch_bounds__(MAX_TPR, join_threads(sizeof(T), BRANCH, ELEME
 // gates): dw1 = gate S, dgate = w1 S.
 //
 // Bound by HBM (join: dout, dy, out, f in, dx, df out). BULK as in the forward
-// (loose rows of 8192 x 4095 149 us in BF16, 146 in FP32; without the ring 187 and
-// 213; aligned ones 82 and 133). An aligned round's work is in two halves, the
+// (loose rows of 8192 x 4095 144 us in BF16, 138 in FP32; without the ring 187 and
+// 213; aligned ones 77 and 130). An aligned round's work is in two halves, the
 // sums and, a round later, the results, so that one round's barrier and shuffles
 // run beside another one's arithmetic; loose rows, whose narrow loads are dear,
-// go in one (in two the 149 us were 389). A thread owns CHUNKS groups of 8
+// go in one (in two the 144 us were 389). A thread owns CHUNKS groups of 8
 // columns: with two of them a row has half the shuffles, and two blocks of 256
 // threads share an SM for rows of 4096.
 template <typename T, bool VEC, int CHUNKS, bool BULK, bool HAS_F, bool NEXT, bool ELEMENT>

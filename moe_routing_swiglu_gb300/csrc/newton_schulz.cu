@@ -39,11 +39,11 @@
 // MN-major. Waits are bounded; one that runs out records a code and the CTA
 // winds down.
 //
-// Bound by the power limit at the large sizes: 2 x 14336 x 4096 takes 8.0 ms on
-// zeros at 2070 MHz and 9.6 ms on random values at about 1600 MHz, 1.7 PFLOP/s
-// of MMAs; 128 x 768 x 2048 4.8 ms, of which 4.0 at that rate. A few small
-// matrices are bound by the 22 launches, 7 us each from one's last store to the
-// next one's; where the short side is at most 128 they have a kernel of their
+// Bound by the power limit at the large sizes: 2 x 14336 x 4096 takes 8.5 ms on
+// zeros and 11.1 ms on random values, for which the clock falls, 1.6 to 1.7
+// PFLOP/s of MMAs; 128 x 768 x 2048 5.4 ms (4.3 on zeros), of which 4.2 at that
+// rate. A few small matrices are bound by the 22 launches, 7 us each from one's
+// last store to the next one's; where the short side is at most 128 they have a kernel of their
 // own, which takes all steps in one launch.
 #include <cudaTypedefs.h>
 
@@ -897,8 +897,8 @@ __global__ void __launch_bounds__(PRE_THREADS) join_parts_kernel(const float* pa
 //
 // Bound by latency: a step is three MMA chains of 24 to 36 instructions, each
 // with a trip through TMEM and registers, and two cluster barriers. 1 x 128 x
-// 2048, 16 blocks: 66 us, of which the parts' way to their owners 11, A's way to
-// all blocks 14, the MMAs of the pairs' lo parts 8; the products above take 144
+// 2048, 16 blocks: 69 us, of which the parts' way to their owners 11, A's way to
+// all blocks 14, the MMAs of the pairs' lo parts 8; the products above take 159
 // in 22 launches. 512 threads a block are no faster.
 constexpr int CL_THREADS = 256;
 constexpr int CL_STEP = CL_THREADS / 128 * 32;           // columns that a quarter of the accumulator's rows is read in
@@ -935,7 +935,7 @@ __device__ __forceinline__ uint32_t cl_chunk(int row, int q) {
 }
 // Byte of chunk q (4 columns) of an owned row in a part: the rows of a chunk side
 // by side, because a warp's store takes one chunk of 32 rows (with a row's chunks
-// side by side instead 1 x 128 x 2048 took 77 us, not 66), turned by the chunk so
+// side by side instead 1 x 128 x 2048 took 77 us, not 66 at that time), turned by the chunk so
 // that the owner's reads of a row meet different banks.
 __device__ __forceinline__ uint32_t cl_part(int q, int in, int owned) {
   return static_cast<uint32_t>(q * owned + (in + (q >> 1)) % owned) * 16;
@@ -1468,9 +1468,9 @@ cudaError_t resident_clusters(int i, int* count) {
 // matrices go through the products above. By the time that either takes, in
 // microseconds for five steps, fitted to sides of 16 to 128 x 64 to 2048 and 1
 // to 1000 matrices: waves of clusters against 22 launches and their tiles.
-// Measured, clusters against products: 1 x 128 x 2048 66 / 144, 8 x 128 x 2048
-// 132 / 152, 16 x 128 x 2048 199 / 181, 128 x 128 x 192 47 / 171, 128 x 64 x 512
-// 139 / 193, 1000 x 64 x 64 148 / 349, 32 x 128 x 1500 206 / 216.
+// Measured, clusters against products: 1 x 128 x 2048 69 / 159, 8 x 128 x 2048
+// 134 / 166, 16 x 128 x 2048 199 / 197, 128 x 128 x 192 50 / 188, 128 x 64 x 512
+// 141 / 209, 1000 x 64 x 64 149 / 367, 32 x 128 x 1500 209 / 233.
 struct ClusterShape {
   int blocks, tiles;
 };
